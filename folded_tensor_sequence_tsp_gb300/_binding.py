@@ -30,6 +30,8 @@ __all__ = [
     "SCHEMES", "tsp_cost_model", "tsp_cost_model_batched", "tsp_cost_max_batch", "tsp_saved_bytes", "tsp_layer_fwd_train", "tsp_layer_bwd_saved",
     "tsp_rank_shard_bytes", "tsp_pack_rank_shard", "tsp_rank_qkv", "tsp_rank_kv_gather",
     "tsp_rank_attention", "tsp_rank_o_accumulate", "tsp_rank_mlp_step",
+    "tsp_rmsnorm_fwd", "tsp_rmsnorm_fwd_e4m3", "tsp_rmsnorm_workspace_bytes", "tsp_rmsnorm_bwd",
+    "tsp_grad_workspace_bytes", "tsp_grad_norm", "tsp_grad_clip",
 ]
 
 TSP_OK, TSP_ERR_INVALID_ARG, TSP_ERR_UNSUPPORTED, TSP_ERR_CUDA, TSP_ERR_TIMEOUT = range(5)
@@ -77,6 +79,8 @@ SCHEMES = {"dp": 0, "tp": 1, "sp": 2, "tp_sp": 3, "tsp": 4}
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
+_F = ctypes.c_float
 _SIGS = {
     "tsp_plan": (_I, [_I, ctypes.c_int64, _I, _I, _I, ctypes.POINTER(_P)]),
     "tsp_plan_batched": (_I, [_I, ctypes.c_int64, _I, _I, _I, _I, ctypes.POINTER(_P)]),
@@ -127,6 +131,13 @@ _SIGS = {
     "tsp_rank_attention": (_I, [_P, _I] + [_P] * 6),
     "tsp_rank_o_accumulate": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P]),
     "tsp_rank_mlp_step": (_I, [_P] * 9),
+    "tsp_rmsnorm_fwd": (_I, [_L, _I, _P, _P, _I, _P, _F, _P, _P, _P]),
+    "tsp_rmsnorm_fwd_e4m3": (_I, [_L, _I, _P, _P, _I, _P, _F, _I, _P, _P, _P, _P]),
+    "tsp_rmsnorm_workspace_bytes": (ctypes.c_size_t, [_L, _I]),
+    "tsp_rmsnorm_bwd": (_I, [_L, _I, _P, _I, _P, _F] + [_P] * 7),
+    "tsp_grad_workspace_bytes": (ctypes.c_size_t, [_I]),
+    "tsp_grad_norm": (_I, [_I] + [_P] * 6),
+    "tsp_grad_clip": (_I, [_I] + [_P] * 4 + [_F] + [_P] * 3),
 }
 
 
@@ -621,3 +632,162 @@ def tsp_rank_mlp_step(plan, h_r, mlp_shard, residual32, acc_r, out_r, g_r, ws, s
         _dev(residual32, "residual32", n, torch.float32), _dev(acc_r, "acc_r", n, torch.float32),
         _dev(out_r, "out_r", n), _dev(g_r, "g_r", rows * fq), _ws_status(ws), _stream(stream)),
         "tsp_rank_mlp_step")
+
+
+# ------------------------------------------------------------------ around the layer
+# These calls take their sizes from the tensors, and run on the tensors' device: a call
+# on tensors of another device than the current one selects it for the launch.
+
+def _same_device(tensors):
+    """The one CUDA device that the given tensors (None skipped) are on."""
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
+    return device
+
+
+def _launch(name, device, stream, *args):
+    """Call `name` with the stream (default: the device's current one) as last argument."""
+    fn = getattr(load_library(), name)
+    if device is None or device.index == torch.cuda.current_device():
+        status = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(stream))
+    if status != TSP_OK:
+        _check(status, name)
+
+
+_STREAM_DTYPES = (torch.bfloat16, torch.float32)
+
+
+def _matrix(t, name, shape=None, dtypes=(torch.bfloat16,), optional=False):
+    """Pointer of a contiguous [rows, width] tensor of one of `dtypes`."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [rows, width] matrix")
+    return t.data_ptr()
+
+
+def _norm_args(x, weight, residual, h):
+    device = _same_device((x, weight, residual, h))
+    xp = _matrix(x, "x")
+    shape = tuple(x.shape)
+    if weight.dtype != torch.bfloat16 or weight.numel() != shape[1] or not weight.is_contiguous():
+        raise ValueError(f"weight must hold {shape[1]} contiguous bfloat16 values")
+    rp = _matrix(residual, "residual", shape, _STREAM_DTYPES, optional=True)
+    hp = _matrix(h, "h", shape, _STREAM_DTYPES, optional=True)
+    if residual is not None and (h is None or h.dtype != residual.dtype):
+        raise ValueError("a residual needs an h of its type")
+    if residual is None and h is not None:
+        raise ValueError("h is only written with a residual")
+    return device, xp, rp, hp, shape, int(residual is not None and residual.dtype == torch.float32)
+
+
+def tsp_rmsnorm_fwd(x, weight, y, residual=None, h=None, eps=1e-5, stream=None):
+    """h = x + residual and y = h / sqrt(mean(h^2) + eps) * weight, row by row.
+
+    x, y: bfloat16 [rows, width]; residual and h: bfloat16 or float32 [rows, width], both or
+    neither. h may be residual, y may be x."""
+    device, xp, rp, hp, shape, f32 = _norm_args(x, weight, residual, h)
+    yp = _matrix(y, "y", shape)
+    _same_device((x, y))
+    _launch("tsp_rmsnorm_fwd", device, stream, shape[0], shape[1], xp, rp, f32, weight.data_ptr(),
+            eps, hp, yp)
+
+
+def tsp_rmsnorm_fwd_e4m3(x, weight, y, scales, residual=None, h=None, eps=1e-5, group=128,
+                         stream=None):
+    """tsp_rmsnorm_fwd with y in float8_e4m3fn and float32 scales: [rows, 1] with group 0,
+    [rows, ceil(width / 128)] with group 128."""
+    device, xp, rp, hp, shape, f32 = _norm_args(x, weight, residual, h)
+    _same_device((x, y, scales))
+    yp = _matrix(y, "y", shape, (torch.float8_e4m3fn,))
+    groups = -(-shape[1] // group) if group else 1
+    sp = _matrix(scales, "scales", (shape[0], groups), (torch.float32,))
+    _launch("tsp_rmsnorm_fwd_e4m3", device, stream, shape[0], shape[1], xp, rp, f32,
+            weight.data_ptr(), eps, group, hp, yp, sp)
+
+
+def tsp_rmsnorm_workspace_bytes(rows: int, width: int) -> int:
+    return load_library().tsp_rmsnorm_workspace_bytes(rows, width)
+
+
+def tsp_rmsnorm_bwd(h, weight, dy, dx, dw, ws, dh=None, dx16=None, eps=1e-5, stream=None):
+    """The gradients dx of h (plus dh) and dw (float32 [width]) of the weight. h, dh and dx
+    share a type, bfloat16 or float32; dx16 receives a bfloat16 copy of dx."""
+    device = _same_device((h, weight, dy, dx, dw, ws, dh, dx16))
+    hp = _matrix(h, "h", None, _STREAM_DTYPES)
+    shape = tuple(h.shape)
+    if weight.dtype != torch.bfloat16 or weight.numel() != shape[1] or not weight.is_contiguous():
+        raise ValueError(f"weight must hold {shape[1]} contiguous bfloat16 values")
+    if dw.dtype != torch.float32 or dw.numel() != shape[1] or not dw.is_contiguous():
+        raise ValueError(f"dw must hold {shape[1]} contiguous float32 values")
+    _launch("tsp_rmsnorm_bwd", device, stream, shape[0], shape[1], hp, int(h.dtype == torch.float32),
+            weight.data_ptr(), eps, _matrix(dy, "dy", shape),
+            _matrix(dh, "dh", shape, (h.dtype,), optional=True), _matrix(dx, "dx", shape, (h.dtype,)),
+            _matrix(dx16, "dx16", shape, optional=True), dw.data_ptr(),
+            _dev(ws, "ws", tsp_rmsnorm_workspace_bytes(*shape), torch.uint8))
+
+
+def tsp_grad_workspace_bytes(n: int) -> int:
+    return load_library().tsp_grad_workspace_bytes(n)
+
+
+_GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _grad_list(grads, name):
+    for t in grads:
+        if t.dtype not in _GRAD_TYPES:
+            raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    return (_P * len(grads))(*[t.data_ptr() for t in grads])
+
+
+def _grad_args(grads, norm, ws):
+    device = _same_device((*grads, norm, ws))
+    if norm.dtype != torch.float32 or norm.numel() != 1:
+        raise ValueError("norm must be one float32 value")
+    n = len(grads)
+    ptrs = _grad_list(grads, "gradients")
+    sizes = (_L * n)(*[t.numel() for t in grads])
+    types = (_I * n)(*[_GRAD_TYPES[t.dtype] for t in grads])
+    return device, n, ptrs, sizes, types, _dev(ws, "ws", tsp_grad_workspace_bytes(n), torch.uint8)
+
+
+def tsp_grad_norm(grads, norm, ws, stream=None):
+    """norm (one float32 on the device) = the 2-norm over all elements of the tensors."""
+    device, n, ptrs, sizes, types, wp = _grad_args(grads, norm, ws)
+    _launch("tsp_grad_norm", device, stream, n, ptrs, sizes, types, norm.data_ptr(), wp)
+
+
+def tsp_grad_clip(grads, outs, max_norm, norm, ws, stream=None):
+    """The norm, and outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6)); outs[i] may be
+    grads[i]."""
+    device, n, ptrs, sizes, types, wp = _grad_args(grads, norm, ws)
+    if outs is grads:
+        out_ptrs = ptrs
+    else:
+        if len(outs) != n or any(o.shape != g.shape or o.dtype != g.dtype for o, g in zip(outs, grads)):
+            raise ValueError("outs must match the gradients in number, shape and type")
+        if n and _same_device(outs) != device:
+            raise ValueError("outs on another device than the gradients")
+        out_ptrs = _grad_list(outs, "outs")
+    _launch("tsp_grad_clip", device, stream, n, ptrs, out_ptrs, sizes, types, max_norm,
+            norm.data_ptr(), wp)

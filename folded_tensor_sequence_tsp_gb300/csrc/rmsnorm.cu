@@ -1,0 +1,585 @@
+// rmsnorm.cu - root-mean-square norm with the residual's addition, forward (bf16 or
+// e4m3 output) and backward: the step between two blocks of a pre-norm stack.
+//
+// Forward, per row of `width` elements (sums in fp32):
+//     h = x + r            stored in r's type (bf16 or fp32); h = x without a residual
+//     y = h * rstd * w,    rstd = 1 / sqrt(mean(h^2) + eps), from the unrounded h
+//     e4m3: per row or per 128 columns  scale = max|y| / 448,  y8 = e4m3(y / scale)
+// Backward, with g = dy * w and n = width:
+//     dx = rstd * g - h * rstd^3 * (sum(g h) / n)  (+ dh)
+//     dw = sum over rows of dy * h * rstd
+// rstd is taken again from h: the row is in registers for sum(g h) in any case, so a
+// saved rstd would only add traffic.
+//
+// Bound: HBM. A row is read once, stays in registers between its reduction and its
+// outputs, and is written once. Layout of the work: a row of up to 1024 elements per
+// warp (no block barrier), a longer one per CTA; each thread owns the same columns of
+// every row it meets, so the weight is loaded once and dw is summed in registers.
+// CTAs are persistent.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "tsp_device.cuh"
+#include "tsp_internal.h"
+
+namespace tsp {
+namespace {
+
+enum { RES_NONE = 0, RES_BF16 = 1, RES_F32 = 2 };
+constexpr float kE4m3Max = 448.0f;
+constexpr int kMaxWidth = 32768;
+// CTAs of the backward at most: two per SM of this part, a constant so that the order
+// of dw's sum is the same on every device
+constexpr int kBwdCtas = 304;
+
+// VEC consecutive elements as fp32. VEC is 8 (16-byte loads) or 1.
+template <int VEC>
+__device__ __forceinline__ void load_bf16(const __nv_bfloat16* p, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+  } else {
+    v[0] = __bfloat162float(*p);
+  }
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_f32(const float* p, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    v[0] = *p;
+  }
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    uint4 u;
+    u.x = pack_bf16x2(v[0], v[1]);
+    u.y = pack_bf16x2(v[2], v[3]);
+    u.z = pack_bf16x2(v[4], v[5]);
+    u.w = pack_bf16x2(v[6], v[7]);
+    *reinterpret_cast<uint4*>(p) = u;
+  } else {
+    *p = __float2bfloat16_rn(v[0]);
+  }
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_f32(float* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *p = v[0];
+  }
+}
+
+// An element range of a stream kept in bf16 or fp32.
+template <int VEC, int RES>
+__device__ __forceinline__ void load_stream(const void* p, long long i, float (&v)[VEC]) {
+  if constexpr (RES == RES_F32) load_f32<VEC>(static_cast<const float*>(p) + i, v);
+  else load_bf16<VEC>(static_cast<const __nv_bfloat16*>(p) + i, v);
+}
+template <int VEC, int RES>
+__device__ __forceinline__ void store_stream(void* p, long long i, const float (&v)[VEC]) {
+  if constexpr (RES == RES_F32) store_f32<VEC>(static_cast<float*>(p) + i, v);
+  else store_bf16<VEC>(static_cast<__nv_bfloat16*>(p) + i, v);
+}
+
+// Sum over the row's threads, the same bits in every thread. WARP: the row's threads are
+// one warp. Otherwise the whole block, through `part` (one float per warp); the caller
+// alternates between two such arrays, so one barrier per reduction is enough.
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float v, float* part) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (!WARP) {
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) part[warp] = v;
+    __syncthreads();
+    v = (threadIdx.x & 31) < warps ? part[threadIdx.x & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  }
+  return v;
+}
+
+// Largest bit pattern of non-negative floats: NaN above infinity above the numbers.
+template <bool WARP>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* part) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if constexpr (!WARP) {
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) part[warp] = v;
+    __syncthreads();
+    v = __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < warps ? part[threadIdx.x & 31] : 0u);
+  }
+  return v;
+}
+
+// The scale of a group whose largest |y| has the bits `top`. A group of zeros takes 1;
+// the smallest scale is the smallest normal number, so that its reciprocal is finite.
+// NaN or infinity in the group gives a NaN or infinite scale.
+__device__ __forceinline__ float e4m3_scale(uint32_t top) {
+  const float t = __uint_as_float(top);
+  if (top == 0u) return 1.f;
+  if (top > 0x7f800000u) return t;
+  return fmaxf(t / kE4m3Max, 1.17549435e-38f);
+}
+
+__device__ __forceinline__ uint8_t to_e4m3(float v) {
+  return static_cast<uint8_t>(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3));
+}
+
+struct NormParams {
+  const __nv_bfloat16* x;
+  const void* r;
+  const __nv_bfloat16* w;
+  void* h;
+  void* y;        // bf16 or e4m3
+  float* scales;
+  long long rows;
+  int width;
+  int group;      // e4m3: 128, or 0 for one scale per row
+  float eps;
+};
+
+// One row per warp (WARP) or per CTA; NV times VEC elements per thread.
+template <int VEC, int NV, bool WARP, int RES, bool E4M3>
+__global__ void __launch_bounds__(WARP ? 128 : 1024) rmsnorm_fwd_kernel(const NormParams p) {
+  __shared__ float part[2][32];
+  __shared__ uint32_t tops[2][VEC == 1 && E4M3 ? kMaxWidth / 128 : 32];
+  const int lanes = WARP ? 32 : blockDim.x;
+  const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
+  const long long row0 = WARP ? (long long)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  const long long step = (long long)gridDim.x * (WARP ? 4 : 1);
+  const float inv_n = 1.f / (float)p.width;
+  float w[NV][VEC], v[NV][VEC];
+  auto col = [&](int i) { return (i * lanes + tid) * VEC; };
+  auto load = [&](long long row) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = col(i);
+      if (c < p.width) {
+        load_bf16<VEC>(p.x + row * p.width + c, v[i]);
+        if constexpr (RES != RES_NONE) {
+          float r[VEC];
+          load_stream<VEC, RES>(p.r, row * p.width + c, r);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) v[i][e] += r[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (col(i) < p.width) load_bf16<VEC>(p.w + col(i), w[i]);
+  int odd = 0;
+  for (long long row = row0; row < p.rows; row += step, odd ^= 1) {
+    load(row);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+    }
+    const float rstd = 1.f / sqrtf(row_sum<WARP>(ss, part[odd]) * inv_n + p.eps);
+    if constexpr (RES != RES_NONE) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (col(i) < p.width) store_stream<VEC, RES>(p.h, row * p.width + col(i), v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[i][e] = col(i) < p.width ? v[i][e] * rstd * w[i][e] : 0.f;
+    }
+    if constexpr (!E4M3) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (col(i) < p.width)
+          store_bf16<VEC>(static_cast<__nv_bfloat16*>(p.y) + row * p.width + col(i), v[i]);
+    } else {
+      uint8_t* y8 = static_cast<uint8_t*>(p.y) + row * p.width;
+      auto top_of = [&](int i) {
+        uint32_t t = 0;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) t = max(t, __float_as_uint(fabsf(v[i][e])));
+        return t;
+      };
+      auto store8 = [&](int i, float scale) {
+        const float inv = 1.f / scale;
+        if constexpr (VEC == 8) {
+          uint32_t lo = 0, hi = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            lo |= (uint32_t)to_e4m3(v[i][e] * inv) << (8 * e);
+            hi |= (uint32_t)to_e4m3(v[i][4 + e] * inv) << (8 * e);
+          }
+          *reinterpret_cast<uint2*>(y8 + col(i)) = make_uint2(lo, hi);
+        } else {
+          y8[col(i)] = to_e4m3(v[i][0] * inv);
+        }
+      };
+      if (p.group == 0) {
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) t = max(t, top_of(i));
+        const float scale = e4m3_scale(row_max<WARP>(t, tops[odd]));
+        if (tid == 0) p.scales[row] = scale;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (col(i) < p.width) store8(i, scale);
+      } else if constexpr (VEC == 8) {
+        // 16 consecutive threads hold 128 consecutive columns
+        const int groups = (p.width + 127) / 128;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          uint32_t t = top_of(i);
+#pragma unroll
+          for (int o = 8; o; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
+          const float scale = e4m3_scale(t);
+          if (col(i) < p.width) {
+            if ((tid & 15) == 0) p.scales[row * groups + col(i) / 128] = scale;
+            store8(i, scale);
+          }
+        }
+      } else {
+        // 128 consecutive threads hold a group: the largest through shared memory (a
+        // maximum does not depend on the order of the atomics)
+        const int groups = (p.width + 127) / 128;
+        __syncthreads();
+        for (int g = threadIdx.x; g < groups; g += blockDim.x) tops[0][g] = 0u;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (col(i) < p.width) atomicMax(&tops[0][col(i) / 128], top_of(i));
+        __syncthreads();
+        for (int g = threadIdx.x; g < groups; g += blockDim.x)
+          p.scales[row * groups + g] = e4m3_scale(tops[0][g]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (col(i) < p.width) store8(i, e4m3_scale(tops[0][col(i) / 128]));
+      }
+    }
+  }
+}
+
+struct NormBwdParams {
+  const void* h;
+  const __nv_bfloat16* w;
+  const __nv_bfloat16* dy;
+  const void* dh;  // optional, h's type
+  void* dx;        // h's type
+  __nv_bfloat16* dx16;  // optional
+  float* partial;  // [CTAs][width]
+  long long rows;
+  int width;
+  float eps;
+};
+
+// One row per CTA at a time; dw of the CTA's rows in registers, written as one partial row.
+template <int VEC, int NV, int RES>
+__global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormBwdParams p) {
+  __shared__ float part[2][2][32];
+  const int tid = threadIdx.x, lanes = blockDim.x;
+  const float inv_n = 1.f / (float)p.width;
+  auto col = [&](int i) { return (i * lanes + tid) * VEC; };
+  float w[NV][VEC], dw[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) w[i][e] = dw[i][e] = 0.f;
+    if (col(i) < p.width) load_bf16<VEC>(p.w + col(i), w[i]);
+  }
+  int odd = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, odd ^= 1) {
+    float h[NV][VEC], g[NV][VEC];
+    float ss = 0.f, sg = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = col(i);
+      if (c < p.width) {
+        load_stream<VEC, RES>(p.h, row * p.width + c, h[i]);
+        load_bf16<VEC>(p.dy + row * p.width + c, g[i]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) h[i][e] = g[i][e] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        ss = fmaf(h[i][e], h[i][e], ss);
+        sg = fmaf(g[i][e] * w[i][e], h[i][e], sg);
+      }
+    }
+    // both sums behind one barrier
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      sg += __shfl_xor_sync(0xffffffffu, sg, o);
+    }
+    if ((tid & 31) == 0) {
+      part[odd][0][tid >> 5] = ss;
+      part[odd][1][tid >> 5] = sg;
+    }
+    __syncthreads();
+    const bool in = (tid & 31) < (lanes >> 5);
+    ss = in ? part[odd][0][tid & 31] : 0.f;
+    sg = in ? part[odd][1][tid & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      sg += __shfl_xor_sync(0xffffffffu, sg, o);
+    }
+    const float rstd = 1.f / sqrtf(ss * inv_n + p.eps);
+    const float coef = rstd * rstd * (sg * inv_n);  // dx = rstd (g - h coef)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = col(i);
+      if (c >= p.width) continue;
+      float d[VEC];
+      if (p.dh != nullptr) load_stream<VEC, RES>(p.dh, row * p.width + c, d);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float t = rstd * (g[i][e] * w[i][e] - h[i][e] * coef);
+        dw[i][e] = fmaf(g[i][e], h[i][e] * rstd, dw[i][e]);
+        d[e] = p.dh != nullptr ? d[e] + t : t;
+      }
+      store_stream<VEC, RES>(p.dx, row * p.width + c, d);
+      if (p.dx16 != nullptr) store_bf16<VEC>(p.dx16 + row * p.width + c, d);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (col(i) < p.width) store_f32<VEC>(p.partial + (long long)blockIdx.x * p.width + col(i), dw[i]);
+}
+
+// dw[c] = sum of the partial rows, in a fixed order: 8 row groups per column, then their sum.
+__global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float* __restrict__ partial, int n,
+                                                         int width, float* __restrict__ dw) {
+  __shared__ float part[8][33];
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + cx;
+  float s = 0.f;
+  if (c < width)
+    for (int r = ry; r < n; r += 8) s += partial[(long long)r * width + c];
+  part[ry][cx] = s;
+  __syncthreads();
+  if (ry == 0 && c < width) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += part[k][cx];
+    dw[c] = s;
+  }
+}
+
+bool aligned16(std::initializer_list<const void*> ptrs) {
+  for (const void* q : ptrs)
+    if (!al16(q)) return false;
+  return true;
+}
+
+// Threads of a CTA that holds a row of `items` (vectors or elements), NV per thread.
+int row_threads(int items, int nv) { return ((items + nv - 1) / nv + 31) / 32 * 32; }
+
+template <int VEC, int NV, bool WARP, int RES, bool E4M3>
+void launch_fwd_variant(const NormParams& p, cudaStream_t s) {
+  const int threads = WARP ? 128 : row_threads((p.width + VEC - 1) / VEC, NV);
+  const long long blocks = WARP ? (p.rows + 3) / 4 : p.rows;
+  // resident CTAs: 2048 threads per SM
+  const long long cap = (long long)sm_count() * std::max(1, 2048 / threads);
+  rmsnorm_fwd_kernel<VEC, NV, WARP, RES, E4M3>
+      <<<(unsigned)std::min(blocks, cap), threads, 0, s>>>(p);
+}
+
+template <int RES, bool E4M3>
+void launch_fwd_res(const NormParams& p, bool vec, cudaStream_t s) {
+  if (vec) {
+    const int vecs = p.width / 8;
+    if (vecs <= 32) launch_fwd_variant<8, 1, true, RES, E4M3>(p, s);
+    else if (vecs <= 64) launch_fwd_variant<8, 2, true, RES, E4M3>(p, s);
+    else if (vecs <= 128) launch_fwd_variant<8, 4, true, RES, E4M3>(p, s);
+    else if (vecs <= 2048) launch_fwd_variant<8, 2, false, RES, E4M3>(p, s);
+    else launch_fwd_variant<8, 4, false, RES, E4M3>(p, s);
+  } else {
+    if (p.width <= 4096) launch_fwd_variant<1, 8, false, RES, E4M3>(p, s);
+    else launch_fwd_variant<1, 32, false, RES, E4M3>(p, s);
+  }
+}
+
+tsp_status launch_fwd(const NormParams& p, int res, bool e4m3, bool vec, cudaStream_t s) {
+  if (p.rows == 0) return TSP_OK;
+  if (e4m3) {
+    if (res == RES_NONE) launch_fwd_res<RES_NONE, true>(p, vec, s);
+    else if (res == RES_BF16) launch_fwd_res<RES_BF16, true>(p, vec, s);
+    else launch_fwd_res<RES_F32, true>(p, vec, s);
+  } else {
+    if (res == RES_NONE) launch_fwd_res<RES_NONE, false>(p, vec, s);
+    else if (res == RES_BF16) launch_fwd_res<RES_BF16, false>(p, vec, s);
+    else launch_fwd_res<RES_F32, false>(p, vec, s);
+  }
+  cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? TSP_OK : cuda_fail(e, "rmsnorm: launch");
+}
+
+template <int VEC, int NV, int RES>
+void launch_bwd_variant(const NormBwdParams& p, int ctas, cudaStream_t s) {
+  rmsnorm_bwd_kernel<VEC, NV, RES>
+      <<<ctas, row_threads((p.width + VEC - 1) / VEC, NV), 0, s>>>(p);
+}
+
+template <int RES>
+void launch_bwd_res(const NormBwdParams& p, bool vec, int ctas, cudaStream_t s) {
+  if (vec) {
+    const int vecs = p.width / 8;
+    if (vecs <= 128) launch_bwd_variant<8, 1, RES>(p, ctas, s);
+    else if (vecs <= 2048) launch_bwd_variant<8, 2, RES>(p, ctas, s);
+    else launch_bwd_variant<8, 4, RES>(p, ctas, s);
+  } else {
+    if (p.width <= 4096) launch_bwd_variant<1, 8, RES>(p, ctas, s);
+    else launch_bwd_variant<1, 32, RES>(p, ctas, s);
+  }
+}
+
+// Checks shared by the three calls.
+tsp_status check_shape(const char* what, int64_t rows, int width, float eps) {
+  const std::string n(what);
+  if (rows < 0 || rows > (1ll << 31) - 1 || width < 1 || width > kMaxWidth)
+    return fail(TSP_ERR_UNSUPPORTED, n + ": rows in [0, 2^31) and width in [1, 32768] only");
+  if (!(eps > 0.f) || !std::isfinite(eps))
+    return fail(TSP_ERR_INVALID_ARG, n + ": eps must be positive and finite");
+  return TSP_OK;
+}
+tsp_status check_natural(const char* what, const void* ptr, unsigned align, bool optional) {
+  if (!ptr && optional) return TSP_OK;
+  if (!ptr) return fail(TSP_ERR_INVALID_ARG, std::string(what) + ": null pointer");
+  if (reinterpret_cast<uintptr_t>(ptr) % align)
+    return fail(TSP_ERR_INVALID_ARG, std::string(what) + ": pointer not aligned to its element");
+  return TSP_OK;
+}
+
+tsp_status rmsnorm_fwd(const char* what, int64_t rows, int width, const void* x, const void* r,
+                       int r_f32, const void* w, float eps, void* h, void* y, bool e4m3, int group,
+                       float* scales, cudaStream_t s) {
+  TSP_TRY(check_shape(what, rows, width, eps));
+  if (rows == 0) return TSP_OK;
+  const unsigned rs = r_f32 ? 4u : 2u;
+  TSP_TRY(check_natural(what, x, 2, false));
+  TSP_TRY(check_natural(what, w, 2, false));
+  TSP_TRY(check_natural(what, y, e4m3 ? 1u : 2u, false));
+  TSP_TRY(check_natural(what, r, rs, true));
+  TSP_TRY(check_natural(what, h, rs, true));
+  if ((r == nullptr) != (h == nullptr))
+    return fail(TSP_ERR_INVALID_ARG, std::string(what) + ": h is written with a residual and only then");
+  if (e4m3) TSP_TRY(check_natural(what, scales, 4, false));
+  if (y == r || y == h)
+    return fail(TSP_ERR_INVALID_ARG, std::string(what) + ": y aliases the residual stream");
+  if (x == h || (e4m3 && x == y) || (x == r && r == h))
+    return fail(TSP_ERR_INVALID_ARG, std::string(what) + ": x aliases an output");
+  NormParams p{};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.r = r;
+  p.w = static_cast<const __nv_bfloat16*>(w);
+  p.h = h;
+  p.y = y;
+  p.scales = scales;
+  p.rows = rows;
+  p.width = width;
+  p.group = group;
+  p.eps = eps;
+  // 16-byte loads where every row of every buffer starts on 16 bytes (8 for the e4m3
+  // rows, which then follow); single elements otherwise
+  const bool vec = width % 8 == 0 && aligned16({x, r, w, h, y});
+  return launch_fwd(p, r == nullptr ? RES_NONE : r_f32 ? RES_F32 : RES_BF16, e4m3, vec, s);
+}
+
+}  // namespace
+}  // namespace tsp
+
+using namespace tsp;
+
+extern "C" {
+
+tsp_status tsp_rmsnorm_fwd(int64_t rows, int width, const tsp_bf16* x, const void* residual,
+                           int residual_f32, const tsp_bf16* weight, float eps, void* h, tsp_bf16* y,
+                           void* stream) {
+  return rmsnorm_fwd("tsp_rmsnorm_fwd", rows, width, x, residual, residual_f32, weight, eps, h, y,
+                     false, 0, nullptr, static_cast<cudaStream_t>(stream));
+}
+
+tsp_status tsp_rmsnorm_fwd_e4m3(int64_t rows, int width, const tsp_bf16* x, const void* residual,
+                                int residual_f32, const tsp_bf16* weight, float eps, int group,
+                                void* h, uint8_t* y, float* scales, void* stream) {
+  if (group != 0 && group != 128)
+    return fail(TSP_ERR_UNSUPPORTED, "tsp_rmsnorm_fwd_e4m3: group 0 (a row) or 128 columns");
+  return rmsnorm_fwd("tsp_rmsnorm_fwd_e4m3", rows, width, x, residual, residual_f32, weight, eps, h,
+                     y, true, group, scales, static_cast<cudaStream_t>(stream));
+}
+
+size_t tsp_rmsnorm_workspace_bytes(int64_t rows, int width) {
+  if (rows < 0 || width < 1 || width > kMaxWidth) return 0;
+  const int64_t ctas = rows < kBwdCtas ? (rows < 1 ? 1 : rows) : kBwdCtas;
+  return align256((size_t)ctas * (size_t)width * sizeof(float));
+}
+
+tsp_status tsp_rmsnorm_bwd(int64_t rows, int width, const void* h, int h_f32, const tsp_bf16* weight,
+                           float eps, const tsp_bf16* dy, const void* dh, void* dx, tsp_bf16* dx16,
+                           float* dw, void* ws, void* stream) {
+  const char* what = "tsp_rmsnorm_bwd";
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  TSP_TRY(check_shape(what, rows, width, eps));
+  TSP_TRY(check_natural(what, dw, 4, false));
+  TSP_TRY(check_ws(ws, what));
+  if (rows == 0) {
+    cudaError_t e = cudaMemsetAsync(dw, 0, (size_t)width * sizeof(float), s);
+    return e == cudaSuccess ? TSP_OK : cuda_fail(e, what);
+  }
+  const unsigned hs = h_f32 ? 4u : 2u;
+  TSP_TRY(check_natural(what, h, hs, false));
+  TSP_TRY(check_natural(what, dx, hs, false));
+  TSP_TRY(check_natural(what, dh, hs, true));
+  TSP_TRY(check_natural(what, weight, 2, false));
+  TSP_TRY(check_natural(what, dy, 2, false));
+  TSP_TRY(check_natural(what, dx16, 2, true));
+  const void* d16 = dx16;
+  if (dx == h || (d16 && (d16 == h || d16 == dx || d16 == dh)) || (h_f32 && dx == dy))
+    return fail(TSP_ERR_INVALID_ARG, "tsp_rmsnorm_bwd: an output aliases h or another output");
+  NormBwdParams p{};
+  p.h = h;
+  p.w = reinterpret_cast<const __nv_bfloat16*>(weight);
+  p.dy = reinterpret_cast<const __nv_bfloat16*>(dy);
+  p.dh = dh;
+  p.dx = dx;
+  p.dx16 = reinterpret_cast<__nv_bfloat16*>(dx16);
+  p.partial = static_cast<float*>(ws);
+  p.rows = rows;
+  p.width = width;
+  p.eps = eps;
+  const int ctas = (int)std::min<int64_t>(rows, kBwdCtas);
+  const bool vec = width % 8 == 0 && aligned16({h, weight, dy, dh, dx, dx16});
+  if (h_f32) launch_bwd_res<RES_F32>(p, vec, ctas, s);
+  else launch_bwd_res<RES_BF16>(p, vec, ctas, s);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "rmsnorm backward: launch");
+  rmsnorm_dw_kernel<<<(width + 31) / 32, 256, 0, s>>>(p.partial, ctas, width, dw);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? TSP_OK : cuda_fail(e, "rmsnorm backward: dw launch");
+}
+
+}  // extern "C"

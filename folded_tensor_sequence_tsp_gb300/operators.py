@@ -1,0 +1,132 @@
+"""Owners of the operators around a TSP layer, beside TSPLayer: each keeps the workspace
+of its calls, sized once for the largest call, and allocates the outputs that the caller
+does not bring.
+
+One object serves one stream at a time: its calls share its workspace, so calls that may
+overlap (two streams, two captured graphs that replay at the same time) need an object
+each. The workspace is never replaced, so a captured graph stays valid as long as its
+object lives.
+"""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from ._binding import (tsp_grad_clip, tsp_grad_norm, tsp_grad_workspace_bytes, tsp_rmsnorm_bwd,
+                       tsp_rmsnorm_fwd, tsp_rmsnorm_fwd_e4m3, tsp_rmsnorm_workspace_bytes)
+
+__all__ = ["TSPRMSNorm", "TSPGradClip"]
+
+
+def _device(device):
+    device = torch.device(device or "cuda")
+    return device if device.index is not None else torch.device("cuda", torch.cuda.current_device())
+
+
+def _on(stream, device):
+    """Outputs made in here belong to the stream that the call runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+class TSPRMSNorm:
+    """Residual addition and root-mean-square norm of up to `rows` rows of `width`.
+
+    The weight is an argument of each call, so one object serves every norm of a stack
+    with that width."""
+
+    def __init__(self, rows, width, eps=1e-5, device=None):
+        self.rows, self.width, self.eps = rows, width, eps
+        self.device = _device(device)
+        nbytes = tsp_rmsnorm_workspace_bytes(rows, width)
+        if nbytes == 0:
+            raise ValueError(f"TSPRMSNorm: unsupported size {rows} x {width}")
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+
+    def _rows(self, t):
+        if t.dim() < 1 or t.shape[-1] != self.width:
+            raise ValueError(f"expected rows of {self.width}, got shape {tuple(t.shape)}")
+        return t.reshape(-1, self.width) if t.dim() != 2 else t
+
+    @staticmethod
+    def _view(t, width):
+        return None if t is None else t.view(-1, width)
+
+    def forward(self, x, weight, residual=None, y=None, h=None, stream=None):
+        """(y, h): h = x + residual (None without a residual), y = norm(h) * weight in bf16."""
+        with _on(stream, self.device):
+            if y is None:
+                y = torch.empty_like(x)
+            if residual is not None and h is None:
+                h = torch.empty_like(residual)
+        v = lambda t: self._view(t, self.width)  # noqa: E731
+        tsp_rmsnorm_fwd(self._rows(x), weight, v(y), v(residual), v(h), self.eps, stream)
+        return y, h
+
+    def forward_e4m3(self, x, weight, residual=None, group=128, y=None, scales=None, h=None,
+                     stream=None):
+        """(y, scales, h) with y in float8_e4m3fn; scales [rows, 1] for group 0, one per 128
+        columns for group 128."""
+        rows = x.numel() // self.width
+        with _on(stream, self.device):
+            if y is None:
+                y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+            if scales is None:
+                scales = torch.empty((rows, -(-self.width // group) if group else 1),
+                                     dtype=torch.float32, device=x.device)
+            if residual is not None and h is None:
+                h = torch.empty_like(residual)
+        v = lambda t: self._view(t, self.width)  # noqa: E731
+        tsp_rmsnorm_fwd_e4m3(self._rows(x), weight, v(y), scales, v(residual), v(h), self.eps, group,
+                             stream)
+        return y, scales, h
+
+    def backward(self, h, weight, dy, dh=None, dx=None, dx16=None, dw=None, stream=None):
+        """(dx, dw): the gradient of h (dh added when given) in h's type, and the weight's in
+        fp32. h is forward's h, or its x when there was no residual."""
+        if h.numel() > self.rows * self.width:
+            raise ValueError(f"{h.numel() // self.width} rows; the workspace was made for {self.rows}")
+        with _on(stream, self.device):
+            if dx is None:
+                dx = torch.empty_like(h)
+            if dw is None:
+                dw = torch.empty(self.width, dtype=torch.float32, device=h.device)
+        v = lambda t: self._view(t, self.width)  # noqa: E731
+        tsp_rmsnorm_bwd(self._rows(h), weight, v(dy), v(dx), dw, self.ws, v(dh), v(dx16), self.eps,
+                        stream)
+        return dx, dw
+
+
+class TSPGradClip:
+    """Global norm of up to `tensors` gradient tensors (fp32 and bf16 mixed), and clipping."""
+
+    def __init__(self, tensors, device=None):
+        nbytes = tsp_grad_workspace_bytes(tensors)
+        if nbytes == 0:
+            raise ValueError(f"TSPGradClip: unsupported number of tensors {tensors}")
+        self.tensors = tensors
+        self.device = _device(device)
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+
+    def _norm(self, norm, stream):
+        if norm is None:
+            with _on(stream, self.device):
+                norm = torch.empty((), dtype=torch.float32, device=self.device)
+        return norm
+
+    def norm(self, grads, norm=None, stream=None):
+        """The 2-norm over all elements, as one float32 on the device."""
+        norm = self._norm(norm, stream)
+        tsp_grad_norm(grads, norm, self.ws, stream)
+        return norm
+
+    def clip(self, grads, max_norm, outs=None, norm=None, stream=None):
+        """Scale the gradients to a global norm of at most max_norm, in place or into `outs`;
+        returns the norm before scaling, as one float32 on the device."""
+        norm = self._norm(norm, stream)
+        tsp_grad_clip(grads, grads if outs is None else outs, float(max_norm), norm, self.ws, stream)
+        return norm

@@ -612,6 +612,82 @@ tsp_status tsp_cost_model_batched(int scheme, int D, int tp, int64_t S, int batc
 tsp_status tsp_cost_max_batch(int scheme, int D, int tp, int64_t S, int hidden, int heads,
                               int ffn, int layers, double mem_bytes, int64_t* out);
 
+/* ---------------------------------------------------------------------------
+ * Around the layer: the residual norm between two blocks, and gradient clipping.
+ * These calls take sizes instead of a plan.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * tsp_rmsnorm_fwd - the residual's addition and a root-mean-square norm in one pass:
+ *     h = x + residual (rounded once to the residual's type; the norm uses the unrounded sum)
+ *     y = h / sqrt(mean(h^2) + eps) * weight, rounded to bf16
+ * x, y [rows][width]; residual and h [rows][width] in bf16, or in fp32 with residual_f32
+ * (a residual stream kept in fp32). residual and h are both NULL (the norm of x alone) or
+ * both given; h may be the residual itself (updated in place) and y may be x. Sums in
+ * fp32. rows in [0, 2^31) (0: nothing happens), width in [1, 32768], any of them odd; eps
+ * positive and finite. Buffers need their element's alignment; with width % 8 == 0 and
+ * every buffer 16-byte aligned the loads are 16 bytes wide.
+ */
+tsp_status tsp_rmsnorm_fwd(int64_t rows, int width, const tsp_bf16* x, const void* residual,
+                           int residual_f32, const tsp_bf16* weight, float eps, void* h, tsp_bf16* y,
+                           void* stream);
+
+/*
+ * tsp_rmsnorm_fwd_e4m3 - the same with an 8-bit output: y holds e4m3 values (4 exponent
+ * and 3 mantissa bits, largest 448) and scales fp32 factors, so that y * scale stands for
+ * the normed row. group 0: one scale per row, scales [rows]; group 128: one per 128
+ * columns, scales [rows][ceil(width / 128)], the last group may be short. scale = max|y| /
+ * 448 over the group (not below 2^-126; 1 for a group of zeros), y rounded to nearest
+ * even from the fp32 value. A group with a NaN or an infinity has a NaN or infinite scale.
+ * y must not be x; other groups are TSP_ERR_UNSUPPORTED.
+ */
+tsp_status tsp_rmsnorm_fwd_e4m3(int64_t rows, int width, const tsp_bf16* x, const void* residual,
+                                int residual_f32, const tsp_bf16* weight, float eps, int group,
+                                void* h, uint8_t* y, float* scales, void* stream);
+
+/*
+ * tsp_rmsnorm_bwd - the backward of both: from h (the forward's h, or its x when there was
+ * no residual) and the gradient dy of y,
+ *     dx = the gradient of h through y, plus dh when it is given (the gradient that
+ *          reaches h past the norm); it is the gradient of x and of the residual alike
+ *     dw = the gradient of the weight, fp32 [width], overwritten
+ * h, dh and dx are bf16, or all fp32 with h_f32. dx16 (optional) receives dx in bf16 as
+ * well: the gradient of a bf16 block output beside an fp32 stream. dx may be dh, and dx16
+ * (or a bf16 dx) may be dy. dw is summed in a fixed order. rows 0: dw is zeroed. ws:
+ * tsp_rmsnorm_workspace_bytes(rows, width) bytes, 256-byte aligned, scratch of this call.
+ */
+size_t tsp_rmsnorm_workspace_bytes(int64_t rows, int width);
+tsp_status tsp_rmsnorm_bwd(int64_t rows, int width, const void* h, int h_f32, const tsp_bf16* weight,
+                           float eps, const tsp_bf16* dy, const void* dh, void* dx, tsp_bf16* dx16,
+                           float* dw, void* ws, void* stream);
+
+/* Element types of the gradient lists. */
+typedef enum tsp_dtype { TSP_F32 = 0, TSP_BF16 = 1 } tsp_dtype;
+#define TSP_GRAD_MAX_TENSORS 65536
+
+/*
+ * tsp_grad_norm - *norm (device, fp32) = the 2-norm over all elements of n tensors.
+ * grads, sizes (elements) and types (tsp_dtype) are HOST arrays, read during the call;
+ * the tensors are on the device. Empty tensors are skipped. Squares are summed in fp32
+ * over short runs and in fp64 beyond, in a fixed order; gradients of any fp32 magnitude
+ * are covered. An infinite or NaN gradient gives an infinite or NaN norm.
+ *
+ * tsp_grad_clip - the same norm, and outs[i] = grads[i] * min(1, max_norm / (norm +
+ * 1e-6)), rounded once to the tensor's type. outs[i] may be grads[i] (in place; then
+ * nothing is written when the factor is 1); it may not overlap anything else of the list
+ * (TSP_ERR_INVALID_ARG). max_norm >= 0, infinity for no clipping. A NaN norm makes every
+ * output NaN, an infinite norm 0 (NaN where the gradient is infinite).
+ *
+ * ws: tsp_grad_workspace_bytes(n) bytes, 256-byte aligned, scratch of the call. n from 0
+ * (norm 0) to TSP_GRAD_MAX_TENSORS. Both calls only launch kernels: they can be captured,
+ * and a replay takes the addresses and sizes of the capture.
+ */
+size_t tsp_grad_workspace_bytes(int n);
+tsp_status tsp_grad_norm(int n, const void* const* grads, const int64_t* sizes, const int* types,
+                         float* norm, void* ws, void* stream);
+tsp_status tsp_grad_clip(int n, const void* const* grads, void* const* outs, const int64_t* sizes,
+                         const int* types, float max_norm, float* norm, void* ws, void* stream);
+
 /*
  * tsp_device_status - synchronise `stream`, then read and clear the workspace
  * status word. Returns TSP_OK, TSP_ERR_TIMEOUT (a bounded device wait gave up; the
