@@ -18,9 +18,9 @@ from ._binding import (tsp_layer_fwd, tsp_layer_fwd_host, tsp_pack_weights, tsp_
                        tsp_bwd_workspace_bytes, tsp_layer_bwd, tsp_unpack_weight_grads,
                        tsp_saved_bytes, tsp_layer_fwd_train, tsp_layer_bwd_saved)
 
-from .operators import TSPGradClip, TSPRMSNorm
+from .operators import TSPGradClip, TSPPackedAttention, TSPRMSNorm
 
-__all__ = list(_binding_all) + ["TSPLayer", "TSPRMSNorm", "TSPGradClip"]
+__all__ = list(_binding_all) + ["TSPLayer", "TSPPackedAttention", "TSPRMSNorm", "TSPGradClip"]
 
 
 class TSPLayer:

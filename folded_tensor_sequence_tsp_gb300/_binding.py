@@ -30,6 +30,7 @@ __all__ = [
     "SCHEMES", "tsp_cost_model", "tsp_cost_model_batched", "tsp_cost_max_batch", "tsp_saved_bytes", "tsp_layer_fwd_train", "tsp_layer_bwd_saved",
     "tsp_rank_shard_bytes", "tsp_pack_rank_shard", "tsp_rank_qkv", "tsp_rank_kv_gather",
     "tsp_rank_attention", "tsp_rank_o_accumulate", "tsp_rank_mlp_step",
+    "tsp_packed_attention_workspace_bytes", "tsp_status_init", "tsp_packed_attention_fwd",
     "tsp_rmsnorm_fwd", "tsp_rmsnorm_fwd_e4m3", "tsp_rmsnorm_workspace_bytes", "tsp_rmsnorm_bwd",
     "tsp_grad_workspace_bytes", "tsp_grad_norm", "tsp_grad_clip",
 ]
@@ -131,6 +132,9 @@ _SIGS = {
     "tsp_rank_attention": (_I, [_P, _I] + [_P] * 6),
     "tsp_rank_o_accumulate": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P]),
     "tsp_rank_mlp_step": (_I, [_P] * 9),
+    "tsp_packed_attention_workspace_bytes": (ctypes.c_size_t, [_L, _I, _I, _I, _I]),
+    "tsp_status_init": (_I, [_P, _P]),
+    "tsp_packed_attention_fwd": (_I, [_L, _I, _P, _I, _I, _I, _F] + [_P, _L] * 5 + [_P, _P]),
     "tsp_rmsnorm_fwd": (_I, [_L, _I, _P, _P, _I, _P, _F, _P, _P, _P]),
     "tsp_rmsnorm_fwd_e4m3": (_I, [_L, _I, _P, _P, _I, _P, _F, _I, _P, _P, _P, _P]),
     "tsp_rmsnorm_workspace_bytes": (ctypes.c_size_t, [_L, _I]),
@@ -791,3 +795,68 @@ def tsp_grad_clip(grads, outs, max_norm, norm, ws, stream=None):
         out_ptrs = _grad_list(outs, "outs")
     _launch("tsp_grad_clip", device, stream, n, ptrs, out_ptrs, sizes, types, max_norm,
             norm.data_ptr(), wp)
+
+
+# ------------------------------------------------------------------ packed attention
+
+def tsp_packed_attention_workspace_bytes(tokens: int, n_seqs: int, heads: int, kv_heads: int,
+                                         head_dim: int) -> int:
+    return load_library().tsp_packed_attention_workspace_bytes(tokens, n_seqs, heads, kv_heads,
+                                                               head_dim)
+
+
+def tsp_status_init(ws, stream=None):
+    """Zero the status word of a workspace that belongs to no plan."""
+    _launch("tsp_status_init", _same_device((ws,)), stream, _ws_status(ws))
+
+
+def _heads3(t, name, shape=None):
+    """(pointer, row stride) of a bfloat16 [tokens, heads, d] tensor whose rows are contiguous."""
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must have shape {shape or '[tokens, heads, d]'}, got {tuple(t.shape)}")
+    n, h, d = t.shape
+    if t.numel() and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.data_ptr(), t.stride(0) if n > 1 else h * d
+
+
+def _packed_args(q, k, v, starts):
+    qp, ldq = _heads3(q, "q")
+    kp, ldk = _heads3(k, "k")
+    tokens, heads, d = q.shape
+    if k.shape[0] != tokens or k.shape[2] != d:
+        raise ValueError(f"k has shape {tuple(k.shape)} beside q {tuple(q.shape)}")
+    vp, ldv = _heads3(v, "v", tuple(k.shape))
+    if starts.dtype != torch.int32 or starts.dim() != 1 or not starts.is_contiguous() or not starts.numel():
+        raise ValueError("starts must hold n_seqs + 1 contiguous int32 values")
+    n = starts.numel() - 1
+    return (tokens, n, starts.data_ptr(), heads, k.shape[1], d), (qp, ldq, kp, ldk, vp, ldv)
+
+
+def _stat(t, name, heads, tokens):
+    if t.dtype != torch.float32 or tuple(t.shape) != (heads, tokens):
+        raise ValueError(f"{name} must be float32 [{heads}, {tokens}]")
+    if tokens > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+    return t.data_ptr(), max(t.stride(0), tokens) if heads > 1 else tokens
+
+
+def _ws_packed(ws, sizes):
+    tokens, n, _, heads, kv_heads, d = sizes
+    return _dev(ws, "ws", tsp_packed_attention_workspace_bytes(tokens, n, heads, kv_heads, d),
+                torch.uint8)
+
+
+def tsp_packed_attention_fwd(q, k, v, starts, o, ws, lse=None, scale=None, stream=None):
+    """Causal attention of packed sequences: q, o [tokens, heads, d], k, v [tokens, kv_heads, d]
+    (bfloat16, rows may be strided), starts int32 [n_seqs + 1] on the device; lse float32
+    [heads, tokens] receives the row statistics that the backward takes."""
+    device = _same_device((q, k, v, starts, o, ws, lse))
+    sizes, qkv = _packed_args(q, k, v, starts)
+    tokens, heads, d = q.shape
+    op, ldo = _heads3(o, "o", tuple(q.shape))
+    lp, ldl = (None, 0) if lse is None else _stat(lse, "lse", heads, tokens)
+    _launch("tsp_packed_attention_fwd", device, stream, *sizes, d ** -0.5 if scale is None else scale,
+            *qkv, op, ldo, lp, ldl, _ws_packed(ws, sizes))

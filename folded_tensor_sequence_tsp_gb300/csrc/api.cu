@@ -103,6 +103,26 @@ tsp_status make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner,
   return TSP_OK;
 }
 
+tsp_status make_tmap_3d_bf16(CUtensorMap* map, const void* base, const uint64_t (&dims)[3],
+                             const uint64_t (&strides_bytes)[2], const uint32_t (&box)[3]) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(TSP_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
+  cuuint64_t strides[2] = {strides_bytes[0], strides_bytes[1]};
+  cuuint32_t b[3] = {box[0], box[1], box[2]};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), d, strides, b,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    char buf[160];
+    snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled failed (%d) for %llux%llux%llu", (int)r,
+             (unsigned long long)d[0], (unsigned long long)d[1], (unsigned long long)d[2]);
+    return fail(TSP_ERR_CUDA, buf);
+  }
+  return TSP_OK;
+}
+
 int sm_count() {
   static int cached[64] = {0};
   int dev = 0;
@@ -898,6 +918,12 @@ tsp_status tsp_swiglu_down(tsp_plan_t plan, const tsp_bf16* g, const tsp_bf16* w
                      static_cast<cudaStream_t>(stream));
 }
 
+tsp_status tsp_status_init(void* ws, void* stream) {
+  TSP_TRY(check_ws(ws, "tsp_status_init"));
+  cudaError_t e = cudaMemsetAsync(ws, 0, 256, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TSP_OK : cuda_fail(e, "tsp_status_init");
+}
+
 tsp_status tsp_device_status(void* ws, void* stream) {
   TSP_TRY(check_ws(ws, "tsp_device_status"));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -909,6 +935,8 @@ tsp_status tsp_device_status(void* ws, void* stream) {
   e = cudaMemsetAsync(ws, 0, sizeof st, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "tsp_device_status: clear");
+  if (st.site == SITE_PACKED_STARTS)
+    return fail(TSP_ERR_INVALID_ARG, "packed attention: the sequence starts decrease or leave the buffers");
   char buf[160];
   snprintf(buf, sizeof buf, "device wait gave up (site %u, block %u, thread %u)", st.site, st.block,
            st.thread);

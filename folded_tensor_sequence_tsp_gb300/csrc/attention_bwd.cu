@@ -57,6 +57,7 @@
 // longest first.
 #include <type_traits>
 
+#include "attention_math.cuh"
 #include "tsp_device.cuh"
 #include "tsp_internal.h"
 
@@ -131,12 +132,6 @@ __device__ __forceinline__ CtaPos cta_pos(const BwdParams& p) {
   const int tile = rem / in_g;
   const int pair = grp * p.group + (rem - tile * in_g);
   return CtaPos{tile, pair / p.heads, pair % p.heads};
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 template <int HD>

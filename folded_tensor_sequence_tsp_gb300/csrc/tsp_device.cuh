@@ -34,8 +34,13 @@ enum Site : unsigned int {
   SITE_BWD_MMA = 10,
   SITE_BWD_ELEMENTWISE = 11,
   SITE_SMEM_LAYOUT = 12,  // the dynamic shared memory base left no room for the layout
+  SITE_PACKED_STARTS = 13,  // sequence starts that decrease or leave the buffers
+  SITE_PACKED_PRODUCER = 14,
+  SITE_PACKED_MMA = 15,
+  SITE_PACKED_SOFTMAX = 16,
 };
 
+constexpr unsigned int kStatusInvalid = 1;      // == TSP_ERR_INVALID_ARG
 constexpr unsigned int kStatusUnsupported = 2;  // == TSP_ERR_UNSUPPORTED
 constexpr unsigned int kStatusTimeout = 4;      // == TSP_ERR_TIMEOUT
 
@@ -175,6 +180,21 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                            int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Orders this thread's shared-memory writes before later reads by TMA or the tensor core
+// (which use the asynchronous proxy); the other threads learn of it through a barrier.
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // Plain bulk copy global -> shared (both 16-byte aligned, bytes % 16 == 0),

@@ -108,6 +108,10 @@ inline tsp_status check_ws(void* ws, const char* what) {
 tsp_status make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                              uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
 
+// 3D bf16 map of dims {inner (contiguous), middle, outer} with the same swizzle and fill.
+tsp_status make_tmap_3d_bf16(CUtensorMap* map, const void* base, const uint64_t (&dims)[3],
+                             const uint64_t (&strides_bytes)[2], const uint32_t (&box)[3]);
+
 int sm_count();                     // of the current device (cached per device)
 unsigned long long wait_limit_ns();  // bound of the device-side waits
 

@@ -13,10 +13,12 @@ import contextlib
 
 import torch
 
-from ._binding import (tsp_grad_clip, tsp_grad_norm, tsp_grad_workspace_bytes, tsp_rmsnorm_bwd,
-                       tsp_rmsnorm_fwd, tsp_rmsnorm_fwd_e4m3, tsp_rmsnorm_workspace_bytes)
+from ._binding import (TSP_OK, TSPError, tsp_device_status, tsp_grad_clip, tsp_grad_norm,
+                       tsp_grad_workspace_bytes, tsp_last_error, tsp_packed_attention_fwd,
+                       tsp_packed_attention_workspace_bytes, tsp_rmsnorm_bwd, tsp_rmsnorm_fwd,
+                       tsp_rmsnorm_fwd_e4m3, tsp_rmsnorm_workspace_bytes, tsp_status_init)
 
-__all__ = ["TSPRMSNorm", "TSPGradClip"]
+__all__ = ["TSPPackedAttention", "TSPRMSNorm", "TSPGradClip"]
 
 
 def _device(device):
@@ -31,6 +33,64 @@ def _on(stream, device):
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
+
+
+class TSPPackedAttention:
+    """Causal attention over packed sequences with grouped heads: up to `tokens` rows in up to
+    `n_seqs` sequences.
+
+    q [T, heads, d], k and v [T, kv_heads, d] (bfloat16; rows may be strided, as column ranges
+    of one projection are), starts int32 [n + 1] on the device: sequence s owns the rows
+    starts[s] to starts[s + 1]. Rows outside every sequence are left as they were, in every
+    output; outputs made here start as zeros."""
+
+    def __init__(self, tokens, n_seqs, heads, kv_heads, head_dim, scale=None, device=None):
+        self.tokens, self.n_seqs = tokens, n_seqs
+        self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
+        self.scale = head_dim ** -0.5 if scale is None else float(scale)
+        self.device = _device(device)
+        nbytes = tsp_packed_attention_workspace_bytes(tokens, n_seqs, heads, kv_heads, head_dim)
+        if nbytes == 0:
+            raise TSPError(2, tsp_last_error())
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        tsp_status_init(self.ws)
+
+    def _check(self, q, k, starts):
+        if q.shape[1:] != (self.heads, self.head_dim) or k.shape[1:] != (self.kv_heads, self.head_dim):
+            raise ValueError(f"made for {self.heads}/{self.kv_heads} heads of {self.head_dim}, got q "
+                             f"{tuple(q.shape)} and k {tuple(k.shape)}")
+        if q.shape[0] > self.tokens or starts.numel() - 1 > self.n_seqs:
+            raise ValueError(f"made for {self.tokens} tokens in {self.n_seqs} sequences, got "
+                             f"{q.shape[0]} in {starts.numel() - 1}")
+
+    def _zeros(self, stream, *shape, dtype=torch.bfloat16):
+        with _on(stream, self.device):
+            return torch.zeros(shape, dtype=dtype, device=self.device)
+
+    def forward(self, q, k, v, starts, out=None, stream=None):
+        """o [T, heads, d]."""
+        self._check(q, k, starts)
+        if out is None:
+            out = self._zeros(stream, *q.shape)
+        tsp_packed_attention_fwd(q, k, v, starts, out, self.ws, None, self.scale, stream)
+        return out
+
+    def forward_train(self, q, k, v, starts, out=None, lse=None, stream=None):
+        """(o, lse): forward() that also keeps the row statistics [heads, T] for backward()."""
+        self._check(q, k, starts)
+        if out is None:
+            out = self._zeros(stream, *q.shape)
+        if lse is None:
+            lse = self._zeros(stream, self.heads, q.shape[0], dtype=torch.float32)
+        tsp_packed_attention_fwd(q, k, v, starts, out, self.ws, lse, self.scale, stream)
+        return out, lse
+
+    def check(self, stream=None):
+        """Synchronise and raise TSPError if the starts were out of order or a device wait gave up."""
+        with torch.cuda.device(self.device):
+            st = tsp_device_status(self.ws, stream)
+        if st != TSP_OK:
+            raise TSPError(st, tsp_last_error())
 
 
 class TSPRMSNorm:

@@ -613,6 +613,45 @@ tsp_status tsp_cost_max_batch(int scheme, int D, int tp, int64_t S, int hidden, 
                               int ffn, int layers, double mem_bytes, int64_t* out);
 
 /* ---------------------------------------------------------------------------
+ * Packed attention: causal attention over sequences of different lengths that lie back to
+ * back on one token axis, with grouped query heads. It takes sizes instead of a plan; the
+ * plan's own attention (equal lengths, one key head per query head, zigzag rows) is
+ * tsp_causal_attention.
+ *
+ * Shapes: q and o [tokens][heads][d], k and v [tokens][kv_heads][d], bf16, d = 64 or 128,
+ * heads = G kv_heads with 1 <= G <= 128; query head h reads key head h / G. The elements
+ * of a row are contiguous; rows are ld elements apart (a multiple of 8, 16-byte aligned
+ * base), so column ranges of one projection's output can be passed as they are.
+ * starts (device, int32 [n_seqs + 1]): sequence s owns the rows [starts[s], starts[s+1]);
+ * a sequence may be empty. Rows before starts[0] and from starts[n_seqs] on belong to no
+ * sequence: they are not written, whatever they hold, and never read into a result. With
+ * starts on the device a captured call can be replayed with other lengths. Starts that
+ * decrease or leave [0, tokens] write nothing and set TSP_ERR_INVALID_ARG in the status
+ * word (tsp_device_status).
+ * A sequence's results have the same bits whatever is packed beside it. Inside a sequence
+ * a NaN or an infinity in the row of one token may reach the results of tokens up to 127
+ * positions before it (they share a tile, where its weight of 0 multiplies it).
+ * scale multiplies the scores (1/sqrt(d) is customary); positive and finite.
+ * lse (fp32 [heads][ld_lse], one value per head and token): log2 of the sum over the
+ * visible keys of exp(scale q.k), as tsp_causal_attention_lse stores it.
+ *
+ * ws: tsp_packed_attention_workspace_bytes (0 for an unsupported shape), 256-byte aligned,
+ * its status word zeroed once by tsp_status_init. One workspace serves one call at a time.
+ * ------------------------------------------------------------------------- */
+size_t tsp_packed_attention_workspace_bytes(int64_t tokens, int n_seqs, int heads, int kv_heads,
+                                            int head_dim);
+
+/* Zero the status word (the first 256 bytes) of a workspace that belongs to no plan. */
+tsp_status tsp_status_init(void* ws, void* stream);
+
+/* o = attention of every sequence; lse (optional) for the backward. o may not alias an input. */
+tsp_status tsp_packed_attention_fwd(int64_t tokens, int n_seqs, const int32_t* starts, int heads,
+                                    int kv_heads, int head_dim, float scale, const tsp_bf16* q,
+                                    int64_t ld_q, const tsp_bf16* k, int64_t ld_k, const tsp_bf16* v,
+                                    int64_t ld_v, tsp_bf16* o, int64_t ld_o, float* lse,
+                                    int64_t ld_lse, void* ws, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Around the layer: the residual norm between two blocks, and gradient clipping.
  * These calls take sizes instead of a plan.
  * ------------------------------------------------------------------------- */
