@@ -31,7 +31,7 @@ __all__ = [
     "tsp_rank_shard_bytes", "tsp_pack_rank_shard", "tsp_rank_qkv", "tsp_rank_kv_gather",
     "tsp_rank_attention", "tsp_rank_o_accumulate", "tsp_rank_mlp_step",
     "tsp_packed_attention_workspace_bytes", "tsp_status_init", "tsp_packed_attention_fwd",
-    "tsp_rmsnorm_fwd", "tsp_rmsnorm_fwd_e4m3", "tsp_rmsnorm_workspace_bytes", "tsp_rmsnorm_bwd",
+    "tsp_packed_attention_bwd", "tsp_rmsnorm_fwd", "tsp_rmsnorm_fwd_e4m3", "tsp_rmsnorm_workspace_bytes", "tsp_rmsnorm_bwd",
     "tsp_grad_workspace_bytes", "tsp_grad_norm", "tsp_grad_clip",
 ]
 
@@ -135,6 +135,7 @@ _SIGS = {
     "tsp_packed_attention_workspace_bytes": (ctypes.c_size_t, [_L, _I, _I, _I, _I]),
     "tsp_status_init": (_I, [_P, _P]),
     "tsp_packed_attention_fwd": (_I, [_L, _I, _P, _I, _I, _I, _F] + [_P, _L] * 5 + [_P, _P]),
+    "tsp_packed_attention_bwd": (_I, [_L, _I, _P, _I, _I, _I, _F] + [_P, _L] * 9 + [_P, _P]),
     "tsp_rmsnorm_fwd": (_I, [_L, _I, _P, _P, _I, _P, _F, _P, _P, _P]),
     "tsp_rmsnorm_fwd_e4m3": (_I, [_L, _I, _P, _P, _I, _P, _F, _I, _P, _P, _P, _P]),
     "tsp_rmsnorm_workspace_bytes": (ctypes.c_size_t, [_L, _I]),
@@ -860,3 +861,14 @@ def tsp_packed_attention_fwd(q, k, v, starts, o, ws, lse=None, scale=None, strea
     lp, ldl = (None, 0) if lse is None else _stat(lse, "lse", heads, tokens)
     _launch("tsp_packed_attention_fwd", device, stream, *sizes, d ** -0.5 if scale is None else scale,
             *qkv, op, ldo, lp, ldl, _ws_packed(ws, sizes))
+
+
+def tsp_packed_attention_bwd(q, k, v, starts, o, lse, dout, dq, dk, dv, ws, scale=None, stream=None):
+    """Gradients of tsp_packed_attention_fwd from its o and lse and the gradient dout of o."""
+    device = _same_device((q, k, v, starts, o, lse, dout, dq, dk, dv, ws))
+    sizes, qkv = _packed_args(q, k, v, starts)
+    tokens, heads, d = q.shape
+    qs, ks = tuple(q.shape), tuple(k.shape)
+    _launch("tsp_packed_attention_bwd", device, stream, *sizes, d ** -0.5 if scale is None else scale,
+            *qkv, *_heads3(o, "o", qs), *_stat(lse, "lse", heads, tokens), *_heads3(dout, "dout", qs),
+            *_heads3(dq, "dq", qs), *_heads3(dk, "dk", ks), *_heads3(dv, "dv", ks), _ws_packed(ws, sizes))

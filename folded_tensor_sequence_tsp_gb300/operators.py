@@ -14,7 +14,8 @@ import contextlib
 import torch
 
 from ._binding import (TSP_OK, TSPError, tsp_device_status, tsp_grad_clip, tsp_grad_norm,
-                       tsp_grad_workspace_bytes, tsp_last_error, tsp_packed_attention_fwd,
+                       tsp_grad_workspace_bytes, tsp_last_error, tsp_packed_attention_bwd,
+                       tsp_packed_attention_fwd,
                        tsp_packed_attention_workspace_bytes, tsp_rmsnorm_bwd, tsp_rmsnorm_fwd,
                        tsp_rmsnorm_fwd_e4m3, tsp_rmsnorm_workspace_bytes, tsp_status_init)
 
@@ -84,6 +85,15 @@ class TSPPackedAttention:
             lse = self._zeros(stream, self.heads, q.shape[0], dtype=torch.float32)
         tsp_packed_attention_fwd(q, k, v, starts, out, self.ws, lse, self.scale, stream)
         return out, lse
+
+    def backward(self, q, k, v, starts, o, lse, dout, dq=None, dk=None, dv=None, stream=None):
+        """(dq, dk, dv) from forward_train's o and lse and the gradient dout of o."""
+        self._check(q, k, starts)
+        dq = self._zeros(stream, *q.shape) if dq is None else dq
+        dk = self._zeros(stream, *k.shape) if dk is None else dk
+        dv = self._zeros(stream, *v.shape) if dv is None else dv
+        tsp_packed_attention_bwd(q, k, v, starts, o, lse, dout, dq, dk, dv, self.ws, self.scale, stream)
+        return dq, dk, dv
 
     def check(self, stream=None):
         """Synchronise and raise TSPError if the starts were out of order or a device wait gave up."""

@@ -651,6 +651,21 @@ tsp_status tsp_packed_attention_fwd(int64_t tokens, int n_seqs, const int32_t* s
                                     int64_t ld_v, tsp_bf16* o, int64_t ld_o, float* lse,
                                     int64_t ld_lse, void* ws, void* stream);
 
+/*
+ * The gradients of q, k and v from the gradient dout of o; q, k, v, starts and scale as in
+ * the forward, o and lse its results (computed with the same sizes). dq like q, dk and dv
+ * like k; dk and dv sum over the heads of their group, in fp32 and in a fixed order. Each
+ * has its own row stride, so the three may be column ranges of one buffer. No gradient may
+ * alias an input or another gradient. Rows of no sequence are not written.
+ */
+tsp_status tsp_packed_attention_bwd(int64_t tokens, int n_seqs, const int32_t* starts, int heads,
+                                    int kv_heads, int head_dim, float scale, const tsp_bf16* q,
+                                    int64_t ld_q, const tsp_bf16* k, int64_t ld_k, const tsp_bf16* v,
+                                    int64_t ld_v, const tsp_bf16* o, int64_t ld_o, const float* lse,
+                                    int64_t ld_lse, const tsp_bf16* dout, int64_t ld_do, tsp_bf16* dq,
+                                    int64_t ld_dq, tsp_bf16* dk, int64_t ld_dk, tsp_bf16* dv,
+                                    int64_t ld_dv, void* ws, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Around the layer: the residual norm between two blocks, and gradient clipping.
  * These calls take sizes instead of a plan.

@@ -7,6 +7,13 @@ Tolerances, from the arithmetic (u = 2^-8, half a step of bf16 relative to the v
   enters the exponent), the exponential (2^-22) and sums of up to L terms; bounded below by
   F = (2^-20 + 2^-18) of the same magnitude for the sizes here.
 * lse: the exponent's error as above plus 2^-22, absolute, and half an fp32 step.
+* The backward forms P again from lse (relative error E = 4 times the exponent's bound, plus
+  2^-20 for the exponential and lse's own rounding) and rounds P and dS to bf16 once each:
+    dv_j: u |dv| + sum_i (u + E_i) P_ij |dO_i|
+    dS_ij: u |dS| + P_ij (delta_i + d 2^-24 sum_c |dO||v|) + E_i P_ij (|dP_ij| + |Delta_i|)
+  where delta_i bounds Delta's error, which comes from the rounded o of the forward:
+  sum_c |dO_ic| times o's bound. dq and dk: u of the value, and scale times dS's bound
+  against |k| and |q|. fp32 sums over up to L terms add F of the sums of magnitudes.
 """
 import math
 
@@ -103,6 +110,32 @@ def check_forward(c, o, lse, what):
         if lse is not None:
             within(lse[:, rows], elog, 2 * err * math.log2(math.e) + 2.0 ** -21 + 2.0 ** -23 * elog.abs(),
                    f"{what} lse {rows}")
+
+
+def exact_backward(c, q, k, v, do):
+    """Exact dq, dk, dv of one sequence (per query head) and their bounds."""
+    p, _, err = softmax_parts(q, k, c.scale)
+    E = (4 * err + 2.0 ** -20)[..., None]
+    o = p @ v
+    obound = U * o.abs() + (U + F + 4 * err[..., None]) * (p @ v.abs())
+    dp = do @ v.transpose(1, 2)
+    delta = (do * o).sum(-1, keepdim=True)
+    ds = p * (dp - delta)
+    dmag = do.abs() @ v.abs().transpose(1, 2)
+    edelta = (do.abs() * obound).sum(-1, keepdim=True) + c.d * 2.0 ** -24 * (do * o).abs().sum(-1, keepdim=True)
+    eds = (U + F) * ds.abs() + p * (edelta + c.d * 2.0 ** -24 * dmag) + E * p * (dp.abs() + delta.abs())
+    G = c.heads // c.kv
+    group = lambda t: t.unflatten(0, (c.kv, G)).sum(1)  # noqa: E731
+    dq, bq = c.scale * (ds @ k), c.scale * (eds @ k.abs())
+    dk, bk = group(c.scale * (ds.transpose(1, 2) @ q)), group(c.scale * (eds.transpose(1, 2) @ q.abs()))
+    dv, bv = group(p.transpose(1, 2) @ do), group(((U + F + E) * p).transpose(1, 2) @ do.abs())
+    return [(x, b + (U + F) * x.abs() + 2.0 ** -133) for x, b in ((dq, bq), (dk, bk), (dv, bv))]
+
+
+def check_backward(c, grads, what):
+    for rows, q, k, v, do in c.sequences():
+        for name, got, (want, bound) in zip(("dq", "dk", "dv"), grads, exact_backward(c, q, k, v, do)):
+            within(got[rows].transpose(0, 1), want, bound, f"{what} {name} {rows}")
 
 
 @pytest.mark.parametrize("lengths", list(LENGTHS))
@@ -230,3 +263,133 @@ def test_replay_with_other_lengths_on_another_stream():
         graph.replay()
         assert torch.equal(o, wo) and torch.equal(lse, wl)
     op.check()
+
+
+# ------------------------------------------------------------------ backward
+
+@pytest.mark.parametrize("lengths", list(LENGTHS))
+@pytest.mark.parametrize("heads", HEADS, ids=lambda h: "%dof%dx%d" % h)
+def test_backward(lengths, heads):
+    c = Case(LENGTHS[lengths], *heads, before=3, after=5)
+    op = c.op()
+    o, lse = op.forward_train(c.q, c.k, c.v, c.starts)
+    # the three gradients as column ranges of one buffer
+    full = torch.full((c.rows, (c.heads + 2 * c.kv) * c.d), 7.0, dtype=torch.bfloat16, device="cuda")
+    a, b = c.heads * c.d, (c.heads + c.kv) * c.d
+    grads = (full[:, :a].unflatten(1, (c.heads, c.d)), full[:, a:b].unflatten(1, (c.kv, c.d)),
+             full[:, b:].unflatten(1, (c.kv, c.d)))
+    op.backward(c.q, c.k, c.v, c.starts, o, lse, c.do, *grads)
+    op.check()
+    check_backward(c, grads, lengths)
+    assert (full[c.outside()] == 7).all()
+    again = op.backward(c.q, c.k, c.v, c.starts, o, lse, c.do)
+    op.check()
+    inside = ~c.outside()
+    for x, y in zip(grads, again):
+        assert torch.equal(x[inside], y[inside]) and (y[c.outside()] == 0).all()
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 64), (8, 2, 128), (6, 1, 128)], ids=str)
+def test_backward_long_sequence_and_sharp_scores(heads):
+    c = Case([2001, 40], *heads, fused=False, magnitude=2.0)
+    op = c.op()
+    o, lse = op.forward_train(c.q, c.k, c.v, c.starts)
+    grads = op.backward(c.q, c.k, c.v, c.starts, o, lse, c.do)
+    op.check()
+    check_backward(c, grads, "sharp")
+
+
+@pytest.mark.parametrize("heads", [(6, 2, 64), (4, 4, 128), (7, 1, 64)], ids=str)
+def test_backward_of_a_sequence_does_not_see_its_neighbours(heads):
+    lengths = [130, 70, 257, 1, 30]
+    c = Case(lengths, *heads, before=2, after=90)
+    op = c.op()
+    o, lse = op.forward_train(c.q, c.k, c.v, c.starts)
+    grads = op.backward(c.q, c.k, c.v, c.starts, o, lse, c.do)
+    for bad in (math.nan, math.inf):
+        for s in (1, 2):
+            a, b = c.starts_host[s], c.starts_host[s + 1]
+            keep = torch.ones(c.rows, dtype=torch.bool, device="cuda")
+            keep[a:b] = False
+            spoiled = [t.clone() for t in (c.q, c.k, c.v, o, lse.T, c.do)]
+            for t in spoiled:
+                t[~keep] = bad
+                t[c.outside()] = bad
+            q, k, v, o2, lse2, do = spoiled
+            got = op.backward(q, k, v, c.starts, o2, lse2.T.contiguous(), do)
+            for x, y in zip(got, grads):
+                assert torch.equal(x[keep], y[keep])
+                assert torch.isnan(x[a:b]).any()
+    for a, b in zip(c.starts_host, c.starts_host[1:]):
+        alone = torch.tensor([0, b - a], dtype=torch.int32, device="cuda")
+        f = lambda t: t[a:b].contiguous()  # noqa: E731
+        got = op.backward(f(c.q), f(c.k), f(c.v), alone, f(o), lse[:, a:b].contiguous(), f(c.do))
+        for x, y in zip(got, grads):
+            assert torch.equal(x, y[a:b])
+
+
+def test_backward_matches_differences():
+    """The gradients along random directions against central differences of the formula."""
+    c = Case([9, 4], 6, 2, 64, fused=False)
+    op = c.op()
+    o, lse = op.forward_train(c.q, c.k, c.v, c.starts)
+    grads = op.backward(c.q, c.k, c.v, c.starts, o, lse, c.do)
+    step = 1e-5
+    for rows, q, k, v, do in c.sequences():
+        G = c.heads // c.kv
+        shared = lambda t: t[::G]  # noqa: E731  undo the repetition
+        bounds = [b for _, b in exact_backward(c, q, k, v, do)]
+
+        def loss(qq, kk, vv):
+            p, _, _ = softmax_parts(qq, kk.repeat_interleave(G, 0), c.scale)
+            return (do * (p @ vv.repeat_interleave(G, 0))).sum()
+
+        args = [q, shared(k), shared(v)]
+        for i in range(3):
+            for seed in range(4):
+                g = torch.Generator(device="cuda")
+                g.manual_seed(seed)
+                way = torch.randn(args[i].shape, generator=g, device="cuda", dtype=torch.float64)
+                up, down = list(args), list(args)
+                up[i], down[i] = args[i] + step * way, args[i] - step * way
+                want = ((loss(*up) - loss(*down)) / (2 * step)).item()
+                got = (grads[i][rows].transpose(0, 1).double() * way).sum().item()
+                # the differences' own error is of order step^2 and 1e-16 / step
+                assert abs(got - want) <= (bounds[i] * way.abs()).sum().item() + 1e-6
+
+
+def test_backward_in_a_graph_beside_a_live_eager_graph():
+    """Captured forward and backward replay with other lengths while eager results live."""
+    a, b = Case([100, 20, 300], 8, 2, 64, seed=1), Case([7, 380, 33], 8, 2, 64, seed=2)
+    op = a.op()
+
+    def step(q, k, v, starts, do):
+        o, lse = op.forward_train(q, k, v, starts)
+        return (o, lse, *op.backward(q, k, v, starts, o, lse, do))
+
+    want = [step(c.q, c.k, c.v, c.starts, c.do) for c in (a, b)]
+    buf = [t.clone() for t in (a.q, a.k, a.v, a.starts, a.do)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = step(*buf)
+    torch.cuda.current_stream().wait_stream(side)
+    for c, w in ((b, want[1]), (a, want[0])):
+        for x, y in zip(buf, (c.q, c.k, c.v, c.starts, c.do)):
+            x.copy_(y)
+        graph.replay()
+        assert all(torch.equal(x, y) for x, y in zip(out, w))
+    op.check()
+
+
+def test_backward_bad_starts_write_nothing():
+    c = Case([10], 4, 2, 64)
+    op = tsp.TSPPackedAttention(10, 4, 4, 2, 64)
+    o, lse = op.forward_train(c.q, c.k, c.v, c.starts)
+    grads = [torch.full_like(t, 3) for t in (c.q.contiguous(), c.k.contiguous(), c.v.contiguous())]
+    op.backward(c.q, c.k, c.v, torch.tensor([0, 9, 4], dtype=torch.int32, device="cuda"), o, lse, c.do, *grads)
+    with pytest.raises(tsp.TSPError):
+        op.check()
+    assert all((g == 3).all() for g in grads)

@@ -102,3 +102,68 @@ def test_binding_refuses_wrong_tensors(lib):
         tsp.tsp_rmsnorm_fwd(x, x[0], x)
     with pytest.raises(ValueError, match="CUDA"):
         tsp.tsp_grad_norm([x], x, x)
+
+
+def test_packed_attention_refusals(lib):
+    BAD, NO = B.TSP_ERR_INVALID_ARG, B.TSP_ERR_UNSUPPORTED
+    base = dict(tokens=100, n=3, starts=P(0), heads=4, kv=2, d=64, scale=0.1, q=P(1), ldq=256, k=P(2),
+                ldk=128, v=P(3), ldv=128, o=P(4), ldo=256, lse=P(5), ldl=100, do=P(6), lddo=256, dq=P(7),
+                lddq=256, dk=P(8), lddk=128, dv=P(9), lddv=128, ws=P(10))
+
+    def fwd(**kw):
+        a = {**base, **kw}
+        return lib.tsp_packed_attention_fwd(
+            a["tokens"], a["n"], a["starts"], a["heads"], a["kv"], a["d"], a["scale"], a["q"], a["ldq"], a["k"],
+            a["ldk"], a["v"], a["ldv"], a["o"], a["ldo"], a["lse"], a["ldl"], a["ws"], None)
+
+    def bwd(**kw):
+        a = {**base, **kw}
+        return lib.tsp_packed_attention_bwd(
+            a["tokens"], a["n"], a["starts"], a["heads"], a["kv"], a["d"], a["scale"], a["q"], a["ldq"], a["k"],
+            a["ldk"], a["v"], a["ldv"], a["o"], a["ldo"], a["lse"], a["ldl"], a["do"], a["lddo"], a["dq"],
+            a["lddq"], a["dk"], a["lddk"], a["dv"], a["lddv"], a["ws"], None)
+
+    shared = [
+        (dict(tokens=-1), NO, "tokens"), (dict(tokens=(1 << 30) + 1), NO, "tokens"),
+        (dict(n=-1), NO, "sequences"), (dict(n=(1 << 20) + 1), NO, "sequences"),
+        (dict(d=32), NO, "head_dim"), (dict(d=96), NO, "head_dim"), (dict(heads=5), NO, "heads"),
+        (dict(heads=0), NO, "heads"), (dict(kv=0), NO, "heads"), (dict(heads=129, kv=1), NO, "heads"),
+        (dict(heads=65538), NO, "heads"), (dict(heads=65536, kv=65536, tokens=1 << 30), NO, "tiles"),
+        (dict(scale=0.0), BAD, "scale"), (dict(scale=-1.0), BAD, "scale"),
+        (dict(scale=math.nan), BAD, "scale"), (dict(scale=math.inf), BAD, "scale"),
+        (dict(starts=None), BAD, "starts"), (dict(starts=P(0) + 2), BAD, "starts"),
+        (dict(q=None), BAD, "q"), (dict(k=P(2) + 8), BAD, "k"), (dict(ldq=255), BAD, "stride"),
+        (dict(ldq=260), BAD, "stride"), (dict(ldk=120), BAD, "stride"), (dict(ldv=132), BAD, "stride"),
+        (dict(ldo=128), BAD, "stride"), (dict(lse=P(5) + 2), BAD, "lse"), (dict(ldl=99), BAD, "lse"),
+        (dict(ws=None), BAD, "workspace"), (dict(ws=P(10) + 64), BAD, "256-byte")]
+    for call in (fwd, bwd):
+        for kw, code, word in shared:
+            expect(lib, call(**kw), code, word)
+        # nothing to do: no pointer is looked at
+        assert call(tokens=0, q=None, ws=None) == B.TSP_OK
+        assert call(n=0, starts=None, o=None) == B.TSP_OK
+    expect(lib, fwd(o=P(1)), BAD, "alias")
+    expect(lib, fwd(o=P(3)), BAD, "alias")
+    expect(lib, bwd(lse=None), BAD, "lse")
+    for kw in (dict(dq=P(1)), dict(dk=P(2)), dict(dv=P(6)), dict(dq=P(4)), dict(dk=P(9)), dict(dv=P(7))):
+        expect(lib, bwd(**kw), BAD, "alias")
+    expect(lib, bwd(lddk=64), BAD, "stride")
+    expect(lib, bwd(do=None), BAD, "dout")
+
+
+def test_packed_attention_workspace(lib):
+    size = tsp.tsp_packed_attention_workspace_bytes
+    assert size(0, 0, 4, 2, 64) >= 512
+    for tokens, n, heads, kv, d in [(1, 1, 1, 1, 64), (1000, 7, 32, 8, 128), (50, 4096, 130, 2, 128)]:
+        tpt = 128 // (heads // kv)
+        # status, counts, one item per query tile, one per key tile, Delta
+        need = 512 + 16 * (tokens // tpt + n) + 16 * (tokens // 128 + n) + 4 * heads * ((tokens + 127) // 128 * 128)
+        assert need <= size(tokens, n, heads, kv, d) <= need + 4 * 256
+        # a workspace made for more tokens and sequences serves fewer
+        assert size(tokens, n, heads, kv, d) <= size(tokens + 1, n + 1, heads, kv, d)
+    assert size(100, 1, 5, 2, 64) == 0
+
+
+def test_status_init_needs_a_workspace(lib):
+    expect(lib, lib.tsp_status_init(None, None), B.TSP_ERR_INVALID_ARG, "workspace")
+    expect(lib, lib.tsp_status_init(P(0) + 8, None), B.TSP_ERR_INVALID_ARG, "256-byte")
