@@ -19,8 +19,10 @@ from ._binding import (tsp_layer_fwd, tsp_layer_fwd_host, tsp_pack_weights, tsp_
                        tsp_saved_bytes, tsp_layer_fwd_train, tsp_layer_bwd_saved)
 
 from .operators import TSPGradClip, TSPPackedAttention, TSPRMSNorm
+from .stack import TSPStack
 
-__all__ = list(_binding_all) + ["TSPLayer", "TSPPackedAttention", "TSPRMSNorm", "TSPGradClip"]
+__all__ = list(_binding_all) + ["TSPLayer", "TSPPackedAttention", "TSPRMSNorm", "TSPGradClip",
+                                 "TSPStack"]
 
 
 class TSPLayer:

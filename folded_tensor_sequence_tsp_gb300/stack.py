@@ -1,0 +1,130 @@
+"""A stack of pre-norm TSP layers: forward, training forward, backward and clipping.
+
+Per layer, on the sharded activations ([D, S/D, H], or [D, batch, S/D, H]):
+    a = Attn(norm(h) w_attn),  h += a
+    m = MLP(norm(h) w_mlp),    h += m
+and a last norm behind the last layer. The blocks are tsp_attention_fwd / tsp_mlp_fwd,
+which return without a residual; the residual's addition, the rounding of the stream and
+the next norm are one pass (tsp_rmsnorm_fwd). The stream h is kept in fp32 by default. All
+layers share one plan and one workspace.
+"""
+from __future__ import annotations
+
+import torch
+
+from ._binding import (TSP_OK, TSPError, tsp_attention_bwd, tsp_attention_fwd, tsp_bwd_workspace_bytes,
+                       tsp_device_status, tsp_last_error, tsp_mlp_bwd, tsp_mlp_fwd, tsp_pack_weights,
+                       tsp_packed_weight_bytes, tsp_plan, tsp_plan_batched, tsp_workspace_bytes,
+                       tsp_workspace_init)
+from .operators import TSPGradClip, TSPRMSNorm
+
+__all__ = ["TSPStack"]
+
+
+class TSPStack:
+    """weights: one dict per layer with Wq, Wk, Wv, Wo, W1, W3, W2 (bfloat16 CUDA tensors,
+    nn.Linear layout) and the norm weights attn_norm and mlp_norm [hidden]; last_norm [hidden]."""
+
+    def __init__(self, D, S, hidden, heads, ffn, weights, last_norm, eps=1e-5, batch=1,
+                 stream_dtype=torch.float32, device=None):
+        if stream_dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("stream_dtype must be float32 or bfloat16")
+        self.device = torch.device(device or "cuda")
+        self.plan = (tsp_plan(D, S, hidden, heads, ffn) if batch == 1
+                     else tsp_plan_batched(D, S, batch, hidden, heads, ffn))
+        self.stream_dtype = stream_dtype
+        self.wpack = []
+        for w in weights:
+            packed = torch.empty(tsp_packed_weight_bytes(self.plan) // 2, dtype=torch.bfloat16,
+                                 device=self.device)
+            tsp_pack_weights(self.plan, *(w[k] for k in ("Wq", "Wk", "Wv", "Wo", "W1", "W3", "W2")), packed)
+            self.wpack.append(packed)
+        # the norm in front of each block, and the last one
+        self.norms = [w[k] for w in weights for k in ("attn_norm", "mlp_norm")] + [last_norm]
+        self.norm = TSPRMSNorm(self.plan.info.tokens, hidden, eps, device=self.device)
+        self.clipper = TSPGradClip(len(self.wpack) + len(self.norms), device=self.device)
+        self.ws = torch.empty(tsp_workspace_bytes(self.plan), dtype=torch.uint8, device=self.device)
+        tsp_workspace_init(self.plan, self.ws)
+
+    def enable_backward(self):
+        """Grow the workspace to the backward's size (it serves the forward too). Call it before
+        capturing a graph of the forward: growing replaces the workspace."""
+        need = tsp_bwd_workspace_bytes(self.plan)
+        if self.ws.numel() < need:
+            self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            tsp_workspace_init(self.plan, self.ws)
+
+    @property
+    def shape(self):
+        i = self.plan.info
+        return (i.D, i.T, i.hidden) if i.batch == 1 else (i.D, i.batch, i.T, i.hidden)
+
+    def _blocks(self):
+        """(layer, forward, backward) of every block in order."""
+        for layer in range(len(self.wpack)):
+            yield layer, tsp_attention_fwd, tsp_attention_bwd
+            yield layer, tsp_mlp_fwd, tsp_mlp_bwd
+
+    def _run(self, xs, keep):
+        h = xs if self.stream_dtype == xs.dtype else xs.to(self.stream_dtype)
+        y, _ = self.norm.forward(xs, self.norms[0])
+        for i, (layer, forward, _) in enumerate(self._blocks()):
+            block = torch.empty(self.shape, dtype=torch.bfloat16, device=self.device)
+            forward(self.plan, y, self.wpack[layer], block, self.ws)
+            if keep is not None:
+                keep.append((y, h))
+                y, h = self.norm.forward(block, self.norms[i + 1], residual=h)
+            else:
+                # nothing of the last step is kept: the norm goes over the block's output, and
+                # the stream over itself (but for the caller's xs)
+                y, h = self.norm.forward(block, self.norms[i + 1], residual=h, y=block,
+                                         h=None if h is xs else h)
+        if keep is not None:
+            keep.append((y, h))
+        return y
+
+    def forward(self, xs):
+        """The normed output of the stack for the sharded bfloat16 input xs."""
+        return self._run(xs.view(self.shape), None)
+
+    def forward_train(self, xs):
+        """(output, saved): forward() that keeps each block's input and the stream."""
+        self.enable_backward()
+        saved = []
+        return self._run(xs.view(self.shape), saved), saved
+
+    def backward(self, saved, dout):
+        """(dxs, grads) of the output gradient dout: dxs in the stream's type; grads is one
+        packed fp32 weight gradient per layer (see tsp_unpack_weight_grads), then one fp32
+        gradient per norm in the order attn_norm, mlp_norm of every layer, last_norm."""
+        self.enable_backward()
+        info = self.plan.info
+        dpacked = [torch.empty(info.wpack_elems, dtype=torch.float32, device=self.device)
+                   for _ in self.wpack]
+        dnorms = [None] * len(self.norms)
+        f32 = self.stream_dtype == torch.float32
+
+        def through_norm(i, dy, dh):
+            """Gradient of the stream in front of norm i, and its bfloat16 copy for the block."""
+            h = saved[i][1]
+            d16 = torch.empty(self.shape, dtype=torch.bfloat16, device=self.device) if f32 else None
+            dx, dnorms[i] = self.norm.backward(h, self.norms[i], dy, dh=dh, dx=dh, dx16=d16)
+            return dx, d16 if f32 else dx
+
+        dh, dblock = through_norm(len(self.norms) - 1, dout.view(self.shape), None)
+        for i, (layer, _, backward) in reversed(list(enumerate(self._blocks()))):
+            dy = torch.empty(self.shape, dtype=torch.bfloat16, device=self.device)
+            backward(self.plan, saved[i][0], self.wpack[layer], dblock, dy, dpacked[layer], self.ws)
+            dh, dblock = through_norm(i, dy, dh)
+        return dh, dpacked + dnorms
+
+    def clip(self, grads, max_norm):
+        """Scale backward()'s grads in place to a global norm of at most max_norm; returns the
+        norm as one float32 on the device. The packed layout's padding holds zeros."""
+        return self.clipper.clip(grads, max_norm)
+
+    def check(self):
+        """Synchronise and raise TSPError if a bounded device wait gave up."""
+        st = tsp_device_status(self.ws)
+        if st != TSP_OK:
+            raise TSPError(st, tsp_last_error())
