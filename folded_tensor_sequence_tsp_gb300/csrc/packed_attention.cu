@@ -33,11 +33,12 @@
 // infinity in V is not 0: warp 0 overwrites those rows of V with zeros in shared memory
 // before the product may start.
 //
-// The work list is made on the device from `starts` by a small kernel: (sequence, tile
-// pair) items sorted by their number of key tiles, longest first, so that the last CTAs to
-// run are short ones. starts is data, not a launch parameter: a captured graph may be
-// replayed with other lengths. Starts that decrease or leave the buffers give an empty
-// list and an error in the status word.
+// CTAs take (sequence, tile pair) items sorted by their number of key tiles, longest first,
+// so that the last ones to run are short. Up to 128 sequences every CTA finds its own item
+// in `starts` by a search in registers; beyond, a small kernel writes the sorted list first.
+// starts is data, not a launch parameter: a captured graph may be replayed with other
+// lengths. Starts that decrease or leave the buffers give no items and an error in the
+// status word.
 #include <algorithm>
 #include <cmath>
 
@@ -60,17 +61,21 @@ __device__ __forceinline__ uint32_t tm_o(int t) { return t ? 384u : 128u; }
 // ------------------------------------------------------------------ work lists
 constexpr int LIST_THREADS = 1024;
 
-// f(start, len, first token) for every item, spread over the block: the whole block walks
-// each of a few sequences, a warp each of many.
+// f(start, len, first token) for every item: a thread fetches one sequence, then each warp
+// walks its 32 sequences, lane by lane over the items of one.
 template <class F>
 __device__ __forceinline__ void each_item(const int32_t* starts, int n, int tile, F f) {
-  const bool few = n <= 64;
-  const int lane = few ? threadIdx.x : threadIdx.x & 31;
-  const int lanes = few ? LIST_THREADS : 32;
-  for (int i = few ? 0 : threadIdx.x >> 5; i < n; i += few ? 1 : LIST_THREADS / 32) {
-    const int s = starts[i], len = starts[i + 1] - s;
-    for (long long q0 = (long long)lane * tile; q0 < len; q0 += (long long)lanes * tile)
-      f(s, len, (int)q0);
+  const int lane = threadIdx.x & 31;
+  for (int base = 0; base < n; base += LIST_THREADS) {
+    const int i = base + threadIdx.x;
+    const int start = i < n ? starts[i] : 0, end = i < n ? starts[i + 1] : 0;
+    const unsigned some = __ballot_sync(0xffffffffu, end > start);
+    for (unsigned left = some; left; left &= left - 1) {
+      const int from = __ffs(left) - 1;
+      const int s = __shfl_sync(0xffffffffu, start, from);
+      const int len = __shfl_sync(0xffffffffu, end, from) - s;
+      for (long long q0 = (long long)lane * tile; q0 < len; q0 += 32ll * tile) f(s, len, (int)q0);
+    }
   }
 }
 
@@ -146,12 +151,7 @@ struct FwdParams {
   long long ld_o;
   float* lse;  // optional [heads][ld_lse]
   long long ld_lse;
-  const Item* items;
-  const int* count;
-  int max_items;
-  long long tokens;
-  int kv_heads;
-  int group;  // key heads whose CTAs interleave
+  Source src;
   int G, TPT, RU;
   float scale_log2;
   DevStatus* status;
@@ -165,18 +165,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                             const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
   using Geo = Geometry<HD>;
   extern __shared__ uint8_t smem_raw[];
-  // CTA -> group of key heads, item, key head
-  const int per_group = p.max_items * p.group;
-  const int grp = (int)(blockIdx.x / (unsigned)per_group);
-  const int in_g = min(p.group, p.kv_heads - grp * p.group);
-  const int rem = (int)blockIdx.x - grp * per_group;
-  const int at = rem / in_g;
-  if (at >= *p.count) return;  // the grid is an upper bound
-  const int head = grp * p.group + (rem - at * in_g);
-  const Item it = p.items[at];
-  // the list may only be trusted as far as this call's own buffers
-  if (it.start < 0 || it.len <= it.q0 || it.q0 < 0 || (long long)it.start + it.len > p.tokens) return;
-
+  Item it;
+  int head;
+  if (!find_item(p.src, it, head)) return;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;
@@ -217,9 +208,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
+    // the first loads are under way while the CTA sets itself up
+    {
+      const uint32_t q_bytes = (uint32_t)(Geo::BOXES * 128) * (uint32_t)p.RU;
+      mbar_arrive_expect_tx(q_full, (n_b ? 2u : 1u) * q_bytes + Geo::TILE_BYTES);
+#pragma unroll
+      for (int b = 0; b < Geo::BOXES; ++b) {
+        tma_load_3d(sQ + b * BOX_BYTES, &tmQ, q_full, 64 * b, head * p.G, it.start + it.q0);
+        if (n_b)
+          tma_load_3d(sQ + Geo::TILE_BYTES + b * BOX_BYTES, &tmQ, q_full, 64 * b, head * p.G,
+                      it.start + q_b);
+        tma_load_2d(sK0 + b * BOX_BYTES, &tmK, q_full, head * HD + 64 * b, it.start);
+      }
+    }
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, TMEM_COLS);
@@ -235,16 +236,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     // -------------------------------------------------------------- TMA producer
     bool all = true;
     if (lane == 0) {
-      const uint32_t q_bytes = (uint32_t)(Geo::BOXES * 128) * (uint32_t)p.RU;
-      mbar_arrive_expect_tx(q_full, (n_b ? 2u : 1u) * q_bytes + Geo::TILE_BYTES);
-#pragma unroll
-      for (int b = 0; b < Geo::BOXES; ++b) {
-        tma_load_3d(sQ + b * BOX_BYTES, &tmQ, q_full, 64 * b, head * p.G, it.start + it.q0);
-        if (n_b)
-          tma_load_3d(sQ + Geo::TILE_BYTES + b * BOX_BYTES, &tmQ, q_full, 64 * b, head * p.G,
-                      it.start + q_b);
-        tma_load_2d(sK0 + b * BOX_BYTES, &tmK, q_full, head * HD + 64 * b, it.start);
-      }
       int last[STAGES];
 #pragma unroll
       for (int s = 0; s < STAGES; ++s) last[s] = -1;
@@ -494,7 +485,7 @@ tsp_status launch_fwd(const Shape& s, const FwdParams& p, const void* q, int64_t
   const size_t smem = Geometry<HD>::SMEM;
   TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem,
                             "packed attention: cudaFuncSetAttribute"));
-  kernel<<<(unsigned)p.max_items * (unsigned)s.kv_heads, THREADS, smem, stream>>>(tq, tk, tv, p);
+  kernel<<<(unsigned)p.src.max_items * (unsigned)s.kv_heads, THREADS, smem, stream>>>(tq, tk, tv, p);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? TSP_OK : cuda_fail(e, "packed attention: launch");
 }
@@ -544,6 +535,25 @@ Workspace make_workspace(const Shape& s) {
   w.delta = take((size_t)s.heads * (size_t)w.ld_stat * sizeof(float));
   w.total = off;
   return w;
+}
+
+Source make_source(const Shape& s, const int32_t* starts, int tile, bool from_end, int group,
+                   const Item* items, const int* count, int max_items, DevStatus* status) {
+  Source src{};
+  if (s.n_seqs > SEARCH_SEQS) {
+    src.items = items;
+    src.count = count;
+  }
+  src.starts = starts;
+  src.n_seqs = s.n_seqs;
+  src.tile = tile;
+  src.from_end = from_end;
+  src.max_items = max_items;
+  src.kv_heads = s.kv_heads;
+  src.group = group;
+  src.tokens = s.tokens;
+  src.status = status;
+  return src;
 }
 
 int list_shift(long long max_cost) {
@@ -630,22 +640,20 @@ tsp_status tsp_packed_attention_fwd(int64_t tokens, int n_seqs, const int32_t* s
   p.ld_o = ld_o;
   p.lse = lse;
   p.ld_lse = ld_lse;
-  p.items = at<Item>(ws, w.items);
-  p.count = at<int>(ws, w.counts);
-  p.max_items = (int)w.max_fwd;
-  p.tokens = tokens;
-  p.kv_heads = kv_heads;
   // 72 MB of K and V in L2 at a time, as for the plan's attention
-  p.group = head_group(s, 72ll << 20);
+  p.src = make_source(s, starts, 2 * s.TPT, false, head_group(s, 72ll << 20), at<Item>(ws, w.items),
+                      at<int>(ws, w.counts), (int)w.max_fwd, status_of(ws));
   p.G = s.G;
   p.TPT = s.TPT;
   p.RU = s.RU;
   p.scale_log2 = 1.4426950408889634f * scale;
   p.status = status_of(ws);
   p.limit_ns = wait_limit_ns();
-  const ListArgs list{2 * s.TPT, 0, list_shift((tokens + TILE - 1) / TILE), at<Item>(ws, w.items),
-                      at<int>(ws, w.counts), (int)w.max_fwd};
-  TSP_TRY(launch_lists(s, starts, list, ListArgs{}, p.status, st));
+  if (p.src.items != nullptr) {
+    const ListArgs list{2 * s.TPT, 0, list_shift((tokens + TILE - 1) / TILE), at<Item>(ws, w.items),
+                        at<int>(ws, w.counts), (int)w.max_fwd};
+    TSP_TRY(launch_lists(s, starts, list, ListArgs{}, p.status, st));
+  }
   if (head_dim == 64) return launch_fwd<64>(s, p, q, ld_q, k, ld_k, v, ld_v, st);
   return launch_fwd<128>(s, p, q, ld_q, k, ld_k, v, ld_v, st);
 }

@@ -10,8 +10,9 @@
 //
 //   query side (first): a CTA owns one query tile (TPT tokens x G heads, 128 rows) and
 //             streams the key tiles it sees: S = Q K^T, dP = dO V^T, dQ += dS K, with Q and
-//             dO in TMEM as A operands. It also forms Delta from its rows of o and dO, and
-//             leaves it for the key side.
+//             dO in TMEM as A operands. It also forms Delta, from its rows of o and dO, or
+//             from P and dP where one key tile holds all keys of its rows, and leaves it for
+//             the key side.
 //   key side  a CTA owns 128 keys of one key head and streams every query tile that sees
 //             them: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q. A tile's rows
 //             are all heads of the group, so the group's sum needs nothing more: it happens
@@ -61,30 +62,12 @@ struct BwdParams {
   long long ld_lse;
   float* delta;
   long long ld_delta;
-  const Item* items;
-  const int* count;
-  int max_items;
-  long long tokens;
-  int kv_heads, group;
+  Source src;
   int G, TPT, RU;
   float scale_log2, scale;
   DevStatus* status;
   unsigned long long limit_ns;
 };
-
-// The CTA's item and key head; false if it has none (the grid is an upper bound), or if the
-// item does not lie in this call's buffers.
-__device__ __forceinline__ bool find_item(const BwdParams& p, Item& it, int& head) {
-  const int per_group = p.max_items * p.group;
-  const int grp = (int)(blockIdx.x / (unsigned)per_group);
-  const int in_g = min(p.group, p.kv_heads - grp * p.group);
-  const int rem = (int)blockIdx.x - grp * per_group;
-  const int at = rem / in_g;
-  if (at >= *p.count) return false;
-  head = grp * p.group + (rem - at * in_g);
-  it = p.items[at];
-  return it.start >= 0 && it.q0 >= 0 && it.len > it.q0 && (long long)it.start + it.len <= p.tokens;
-}
 
 template <int HD>
 struct KeyGeom {
@@ -109,7 +92,7 @@ struct QueryGeom {
   static constexpr uint32_t TILE_B = 128 * HD * 2;
   static constexpr int KV_STAGES = 3;
   static constexpr uint32_t STAGE = 2 * TILE_B;  // K, V
-  static constexpr size_t USED = 1024 + KV_STAGES * (size_t)STAGE + 1024;
+  static constexpr size_t USED = 1024 + KV_STAGES * (size_t)STAGE + 1280;
   static constexpr size_t SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
   static constexpr uint32_t TM_Q = HD;
   static constexpr uint32_t TM_DO = HD + HD / 2;
@@ -145,7 +128,7 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
   using Geo = KeyGeom<HD>;
   Item it;
   int head;
-  if (!find_item(p, it, head)) return;
+  if (!find_item(p.src, it, head)) return;
   // the tiles start at the first 1024-byte boundary after the small buffers; the check
   // tests that they fit whatever the base's alignment
   extern __shared__ uint8_t smem_raw[];
@@ -206,10 +189,13 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmDO);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
+    // K and V are under way while the CTA sets itself up
+    mbar_arrive_expect_tx(kv_full, 2 * Geo::TILE_B);
+#pragma unroll
+    for (int b = 0; b < Geo::BOXES; ++b) {
+      tma_load_2d(sK + b * BOX_BYTES, &tmK, kv_full, head * HD + 64 * b, it.start + k0);
+      tma_load_2d(sV + b * BOX_BYTES, &tmV, kv_full, head * HD + 64 * b, it.start + k0);
+    }
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, TMEM_COLS);
@@ -231,12 +217,6 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------ producer
-      mbar_arrive_expect_tx(kv_full, 2 * Geo::TILE_B);
-#pragma unroll
-      for (int b = 0; b < Geo::BOXES; ++b) {
-        tma_load_2d(sK + b * BOX_BYTES, &tmK, kv_full, head * HD + 64 * b, it.start + k0);
-        tma_load_2d(sV + b * BOX_BYTES, &tmV, kv_full, head * HD + 64 * b, it.start + k0);
-      }
       int q_last[Geo::QS], o_last[Geo::OS];
       for (int s = 0; s < Geo::QS; ++s) q_last[s] = -1;
       for (int s = 0; s < Geo::OS; ++s) o_last[s] = -1;
@@ -588,20 +568,28 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
 // ============================================================== query side
 template <int HD>
 __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
-    packed_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmK,
+    packed_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
+                         const __grid_constant__ CUtensorMap tmDO,
+                         const __grid_constant__ CUtensorMap tmO,
+                         const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
   using Geo = QueryGeom<HD>;
   constexpr int NS = Geo::KV_STAGES;
   Item it;
   int head;
-  if (!find_item(p, it, head)) return;
+  if (!find_item(p.src, it, head)) return;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sStage = smem;  // stage s: K, V
-  float* sDel = reinterpret_cast<float*>(sStage + NS * Geo::STAGE);  // [128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sDel + 128);
-  uint64_t* a_full = bars;           // Q and dO rows stored in TMEM (8 warps)
+  // the owned rows on their way to TMEM, in the stages that the ring does not use yet
+  uint8_t* sQ = sStage + Geo::STAGE;
+  uint8_t* sDO = sQ + Geo::TILE_B;
+  uint8_t* sO = sStage + 2 * Geo::STAGE;
+  float* sDel = reinterpret_cast<float*>(sStage + NS * Geo::STAGE);  // [2][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sDel + 256);
+  uint64_t* own_full = bars;         // Q, dO and o tiles in shared memory
+  uint64_t* a_full = own_full + 1;   // Q and dO rows stored in TMEM (8 warps)
   uint64_t* kv_full = a_full + 1;    // [NS]
   uint64_t* kv_empty = kv_full + NS; // [NS]
   uint64_t* s_full = kv_empty + NS;  // S(j) in TMEM
@@ -609,7 +597,8 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
   uint64_t* s_free = dp_full + 1;    // S(j) read by the element-wise warps (8)
   uint64_t* ds_full = s_free + 1;    // dS(j) stored (8 warps)
   uint64_t* acc_done = ds_full + 1;
-  uint64_t* tail_ok = acc_done + 1;  // the last K, V tiles are cleared behind the sequence
+  uint64_t* del_full = acc_done + 1; // both halves of a direct Delta stored (8)
+  uint64_t* tail_ok = del_full + 1;  // the last K, V tiles are cleared behind the sequence
   uint64_t* drain = tail_ok + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -617,8 +606,12 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_tiles = (min(it.len, it.q0 + p.TPT) - 1) / TILE + 1;
   const bool ragged = n_tiles * TILE > it.len;
+  // Delta from o, or, where one tile holds all keys, from P and dP themselves: there o is a
+  // mean of few values, and its rounding would be the largest error of dS
+  const bool direct = n_tiles == 1;
 
   if (threadIdx.x == 0) {
+    mbar_init(own_full, 1);
     mbar_init(a_full, 8);
     for (int s = 0; s < NS; ++s) {
       mbar_init(&kv_full[s], 1);
@@ -629,12 +622,22 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
     mbar_init(s_free, 8);
     mbar_init(ds_full, 8);
     mbar_init(acc_done, 1);
+    mbar_init(del_full, 8);
     mbar_init(tail_ok, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
+    // the owned rows and the first keys are under way while the CTA sets itself up
+    mbar_arrive_expect_tx(own_full, (uint32_t)(Geo::BOXES * 128) * (uint32_t)p.RU * (direct ? 2u : 3u));
+    mbar_arrive_expect_tx(&kv_full[0], 2 * Geo::TILE_B);
+#pragma unroll
+    for (int b = 0; b < Geo::BOXES; ++b) {
+      tma_load_3d(sQ + b * BOX_BYTES, &tmQ, own_full, 64 * b, head * p.G, it.start + it.q0);
+      tma_load_3d(sDO + b * BOX_BYTES, &tmDO, own_full, 64 * b, head * p.G, it.start + it.q0);
+      if (!direct) tma_load_3d(sO + b * BOX_BYTES, &tmO, own_full, 64 * b, head * p.G, it.start + it.q0);
+      tma_load_2d(sStage + b * BOX_BYTES, &tmK, &kv_full[0], head * HD + 64 * b, it.start);
+      tma_load_2d(sStage + Geo::TILE_B + b * BOX_BYTES, &tmV, &kv_full[0], head * HD + 64 * b, it.start);
+    }
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, TMEM_COLS);
@@ -653,7 +656,10 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
       int last[NS];
 #pragma unroll
       for (int s = 0; s < NS; ++s) last[s] = -1;
-      for (int j = 0; j < n_tiles; ++j) {
+      last[0] = 0;
+      // the other stages hold the owned rows until these are in TMEM
+      if (n_tiles > 1) all = mbar_wait(a_full, 0, wb, SITE_PACKED_PRODUCER);
+      for (int j = 1; all && j < n_tiles; ++j) {
         const int st = j % NS;
         const uint32_t ph = (uint32_t)((j / NS) & 1);
         if (!mbar_wait(&kv_empty[st], ph ^ 1u, wb, SITE_PACKED_PRODUCER)) {
@@ -671,6 +677,7 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
         last[st] = (int)ph;
       }
       WaitBound wd{p.status, p.limit_ns, nullptr};
+      all = mbar_wait(own_full, 0, wd, SITE_DRAIN) && all;
       for (int s = 0; s < NS; ++s)
         if (last[s] >= 0) all = mbar_wait(&kv_full[s], (uint32_t)last[s], wd, SITE_DRAIN) && all;
     }
@@ -766,32 +773,36 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
     const uint32_t lane_base = tmem + ((uint32_t)(qq * 32) << 16);
     const uint32_t s_t = lane_base + TM_SC + (uint32_t)(g * GCOLS);
     const uint32_t d_t = lane_base + TM_DP + (uint32_t)(g * GCOLS);
-    {
+    bool ok = true;
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool mine = mbar_wait(bar, parity, wb, SITE_PACKED_SOFTMAX);
+      return __all_sync(0xffffffffu, mine) != 0;
+    };
+    float del = 0.f;
+    ok = warp_wait(own_full, 0u);
+    if (ok) {
       // this thread's row of Q (warpgroup 0) or dO (warpgroup 1) into TMEM, two bf16 values
-      // per column; warpgroup 1 also takes its row of o and forms Delta
-      const __nv_bfloat16* src = g == 0 ? p.q + row * p.ld_q + (long long)qh * HD
-                                        : p.dout + row * p.ld_do + (long long)qh * HD;
-      const __nv_bfloat16* os = p.o + row * p.ld_o + (long long)qh * HD;
+      // per column; warpgroup 1 also takes its row of o and forms Delta. Chunk c of row r
+      // lies at chunk c ^ (r % 8) of its 128 bytes (the 128-byte swizzle).
       const uint32_t dst = lane_base + (g == 0 ? Geo::TM_Q : Geo::TM_DO);
-      float del = 0.f;
+      const uint4* src = reinterpret_cast<const uint4*>((g == 0 ? sQ : sDO) + r_local * 128);
+      const uint4* os = reinterpret_cast<const uint4*>(sO + r_local * 128);
 #pragma unroll
-      for (int c = 0; c < HD / 2; c += 32) {
+      for (int b = 0; b < Geo::BOXES; ++b) {
         uint32_t r[32];
-        const uint4* s4 = reinterpret_cast<const uint4*>(src + 2 * c);
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
-          const uint4 v = row_ok ? __ldg(s4 + w) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 v = row_ok ? src[b * (BOX_BYTES / 16) + (w ^ (r_local & 7))] : make_uint4(0u, 0u, 0u, 0u);
           r[4 * w + 0] = v.x;
           r[4 * w + 1] = v.y;
           r[4 * w + 2] = v.z;
           r[4 * w + 3] = v.w;
         }
-        tmem_st32(dst + (uint32_t)c, r);
-        if (g == 1 && row_ok) {
-          const uint4* o4 = reinterpret_cast<const uint4*>(os + 2 * c);
+        tmem_st32(dst + (uint32_t)(32 * b), r);
+        if (g == 1 && row_ok && !direct) {
 #pragma unroll
           for (int w = 0; w < 8; ++w) {
-            const uint4 v = __ldg(o4 + w);
+            const uint4 v = os[b * (BOX_BYTES / 16) + (w ^ (r_local & 7))];
             const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -803,22 +814,17 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
       }
       if (g == 1) {
         sDel[r_local] = del;
-        if (row_ok) p.delta[(long long)qh * p.ld_delta + row] = del;
+        if (row_ok && !direct) p.delta[(long long)qh * p.ld_delta + row] = del;
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(a_full);
     }
-    // both warpgroups hold the row's Delta (the 256 element-wise threads meet)
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    const float del = sDel[r_local];
-    bool ok = true;
-    auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool mine = mbar_wait(bar, parity, wb, SITE_PACKED_SOFTMAX);
-      return __all_sync(0xffffffffu, mine) != 0;
-    };
-    for (int j = 0; j < n_tiles; ++j) {
+    // all eight warps have stored their rows, and Delta with them
+    ok = ok && warp_wait(a_full, 0u);
+    del = sDel[r_local];
+    for (int j = 0; ok && j < n_tiles; ++j) {
       const uint32_t ph = (uint32_t)(j & 1);
       if (!warp_wait(s_full, ph)) {
         ok = false;
@@ -854,6 +860,29 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
         break;
       }
       tc_fence_after();
+      if (direct) {
+        float part = 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t gv[32];
+          tmem_ld32(d_t + (uint32_t)(32 * half), gv);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int c = 32 * half + e;
+            if (kbase + c <= qpos) part = fmaf(pf[c], __uint_as_float(gv[e]), part);
+          }
+        }
+        sDel[g * 128 + r_local] = part;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(del_full);
+        if (!warp_wait(del_full, 0u)) {
+          ok = false;
+          break;
+        }
+        del = sDel[r_local] + sDel[128 + r_local];
+        if (g == 1 && row_ok) p.delta[(long long)qh * p.ld_delta + row] = del;
+      }
       const uint64_t del2 = f2_pack(del, del);
       uint32_t dd[32];
 #pragma unroll
@@ -913,24 +942,23 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
 }
 
 template <int HD>
-tsp_status launch_bwd(const Shape& s, const Workspace& w, void* ws, BwdParams p, const void* k,
-                      int64_t ld_k, const void* v, int64_t ld_v, cudaStream_t stream) {
-  CUtensorMap tq, tdo, tk, tv;
+tsp_status launch_bwd(const Shape& s, const Source& queries, const Source& keys, BwdParams p,
+                      const void* k, int64_t ld_k, const void* v, int64_t ld_v, cudaStream_t stream) {
+  CUtensorMap tq, tdo, to, tk, tv;
   TSP_TRY(make_query_map(&tq, s, p.q, p.ld_q));
   TSP_TRY(make_query_map(&tdo, s, p.dout, p.ld_do));
+  TSP_TRY(make_query_map(&to, s, p.o, p.ld_o));
   const uint64_t cols = (uint64_t)s.kv_heads * HD, rows = (uint64_t)s.tokens;
   TSP_TRY(make_tmap_2d_bf16(&tk, k, cols, rows, (uint64_t)ld_k * 2, 64, TILE));
   TSP_TRY(make_tmap_2d_bf16(&tv, v, cols, rows, (uint64_t)ld_v * 2, 64, TILE));
-  int* counts = at<int>(ws, w.counts);
   {
     auto kernel = packed_bwd_dq_kernel<HD>;
     const size_t smem = QueryGeom<HD>::SMEM;
     TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem,
                               "packed attention backward: cudaFuncSetAttribute"));
-    p.items = at<Item>(ws, w.items);
-    p.count = counts;
-    p.max_items = (int)w.max_query;
-    kernel<<<(unsigned)p.max_items * (unsigned)s.kv_heads, QueryGeom<HD>::THREADS, smem, stream>>>(tk, tv, p);
+    p.src = queries;
+    kernel<<<(unsigned)p.src.max_items * (unsigned)s.kv_heads, QueryGeom<HD>::THREADS, smem, stream>>>(
+        tq, tdo, to, tk, tv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "packed attention backward (query side): launch");
   }
@@ -939,11 +967,9 @@ tsp_status launch_bwd(const Shape& s, const Workspace& w, void* ws, BwdParams p,
     const size_t smem = KeyGeom<HD>::SMEM;
     TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem,
                               "packed attention backward: cudaFuncSetAttribute"));
-    p.items = at<Item>(ws, w.key_items);
-    p.count = counts + 1;
-    p.max_items = (int)w.max_key;
-    kernel<<<(unsigned)p.max_items * (unsigned)s.kv_heads, KeyGeom<HD>::THREADS, smem, stream>>>(tq, tdo, tk,
-                                                                                               tv, p);
+    p.src = keys;
+    kernel<<<(unsigned)p.src.max_items * (unsigned)s.kv_heads, KeyGeom<HD>::THREADS, smem, stream>>>(
+        tq, tdo, tk, tv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "packed attention backward (key side): launch");
   }
@@ -1011,10 +1037,6 @@ extern "C" tsp_status tsp_packed_attention_bwd(
   p.ld_lse = ld_lse;
   p.delta = at<float>(ws, w.delta);
   p.ld_delta = w.ld_stat;
-  p.tokens = tokens;
-  p.kv_heads = kv_heads;
-  // 48 MB of K and V in L2 at a time, as for the plan's backward
-  p.group = head_group(s, 48ll << 20);
   p.G = s.G;
   p.TPT = s.TPT;
   p.RU = s.RU;
@@ -1023,11 +1045,19 @@ extern "C" tsp_status tsp_packed_attention_bwd(
   p.status = status_of(ws);
   p.limit_ns = wait_limit_ns();
   int* counts = at<int>(ws, w.counts);
-  const ListArgs queries{s.TPT, 0, list_shift((tokens + TILE - 1) / TILE), at<Item>(ws, w.items), counts,
-                         (int)w.max_query};
-  const ListArgs keys{TILE, s.TPT, list_shift((tokens + s.TPT - 1) / s.TPT), at<Item>(ws, w.key_items),
-                      counts + 1, (int)w.max_key};
-  TSP_TRY(launch_lists(s, starts, queries, keys, p.status, st));
-  if (head_dim == 64) return launch_bwd<64>(s, w, ws, p, k, ld_k, v, ld_v, st);
-  return launch_bwd<128>(s, w, ws, p, k, ld_k, v, ld_v, st);
+  // 48 MB of K and V in L2 at a time, as for the plan's backward
+  const int group = head_group(s, 48ll << 20);
+  const Source queries = make_source(s, starts, s.TPT, false, group, at<Item>(ws, w.items), counts,
+                                     (int)w.max_query, p.status);
+  const Source keys = make_source(s, starts, TILE, true, group, at<Item>(ws, w.key_items), counts + 1,
+                                  (int)w.max_key, p.status);
+  if (queries.items != nullptr) {
+    const ListArgs a{s.TPT, 0, list_shift((tokens + TILE - 1) / TILE), at<Item>(ws, w.items), counts,
+                     (int)w.max_query};
+    const ListArgs b{TILE, s.TPT, list_shift((tokens + s.TPT - 1) / s.TPT), at<Item>(ws, w.key_items),
+                     counts + 1, (int)w.max_key};
+    TSP_TRY(launch_lists(s, starts, a, b, p.status, st));
+  }
+  if (head_dim == 64) return launch_bwd<64>(s, queries, keys, p, k, ld_k, v, ld_v, st);
+  return launch_bwd<128>(s, queries, keys, p, k, ld_k, v, ld_v, st);
 }

@@ -30,9 +30,9 @@ namespace {
 enum { RES_NONE = 0, RES_BF16 = 1, RES_F32 = 2 };
 constexpr float kE4m3Max = 448.0f;
 constexpr int kMaxWidth = 32768;
-// CTAs of the backward at most: two per SM of this part, a constant so that the order
+// CTAs of the backward at most: three per SM of this part, a constant so that the order
 // of dw's sum is the same on every device
-constexpr int kBwdCtas = 304;
+constexpr int kBwdCtas = 456;
 
 // VEC consecutive elements as fp32. VEC is 8 (16-byte loads) or 1.
 template <int VEC>
@@ -141,6 +141,12 @@ __device__ __forceinline__ float e4m3_scale(uint32_t top) {
 __device__ __forceinline__ uint8_t to_e4m3(float v) {
   return static_cast<uint8_t>(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3));
 }
+// four values, the first in the low byte: one conversion instruction per pair
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
 
 struct NormParams {
   const __nv_bfloat16* x;
@@ -156,8 +162,9 @@ struct NormParams {
 };
 
 // One row per warp (WARP) or per CTA; NV times VEC elements per thread.
-template <int VEC, int NV, bool WARP, int RES, bool E4M3>
-__global__ void __launch_bounds__(WARP ? 128 : 1024) rmsnorm_fwd_kernel(const NormParams p) {
+// MAXT: the largest block, which bounds the registers of a thread.
+template <int VEC, int NV, bool WARP, int RES, bool E4M3, int MAXT>
+__global__ void __launch_bounds__(MAXT) rmsnorm_fwd_kernel(const NormParams p) {
   __shared__ float part[2][32];
   __shared__ uint32_t tops[2][VEC == 1 && E4M3 ? kMaxWidth / 128 : 32];
   const int lanes = WARP ? 32 : blockDim.x;
@@ -224,13 +231,9 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) rmsnorm_fwd_kernel(const No
       auto store8 = [&](int i, float scale) {
         const float inv = 1.f / scale;
         if constexpr (VEC == 8) {
-          uint32_t lo = 0, hi = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            lo |= (uint32_t)to_e4m3(v[i][e] * inv) << (8 * e);
-            hi |= (uint32_t)to_e4m3(v[i][4 + e] * inv) << (8 * e);
-          }
-          *reinterpret_cast<uint2*>(y8 + col(i)) = make_uint2(lo, hi);
+          *reinterpret_cast<uint2*>(y8 + col(i)) =
+              make_uint2(to_e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv),
+                         to_e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv));
         } else {
           y8[col(i)] = to_e4m3(v[i][0] * inv);
         }
@@ -371,22 +374,149 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormBwdParams p
     if (col(i) < p.width) store_f32<VEC>(p.partial + (long long)blockIdx.x * p.width + col(i), dw[i]);
 }
 
-// dw[c] = sum of the partial rows, in a fixed order: 8 row groups per column, then their sum.
-__global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float* __restrict__ partial, int n,
-                                                         int width, float* __restrict__ dw) {
-  __shared__ float part[8][33];
+// The same with the rows staged in shared memory: each thread copies its own 16-byte pieces
+// of the rows ahead (cp.async) and later reads only those, so a wait for its own copies is
+// all the ordering that is needed, and STAGES - 1 rows of every CTA are in flight under the
+// arithmetic and the barrier of the current one.
+template <int BYTES>
+__device__ __forceinline__ void copy_ahead(void* smem, const void* global) {
+  static_assert(BYTES == 16, "one 16-byte piece");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem)), "l"(global) : "memory");
+}
+
+template <int NV, int RES, int STAGES, int MAXT>
+__global__ void __launch_bounds__(MAXT) rmsnorm_bwd_ring_kernel(const NormBwdParams p) {
+  constexpr int SP = RES == RES_F32 ? 2 : 1;  // 16-byte pieces of 8 stream elements
+  extern __shared__ uint4 ring[];             // [STAGES][pieces][threads]
+  __shared__ float part[2][2][32];
+  const int tid = threadIdx.x, lanes = blockDim.x;
+  const bool has_dh = p.dh != nullptr;
+  const int pieces = NV * (SP + 1 + (has_dh ? SP : 0));
+  const float inv_n = 1.f / (float)p.width;
+  auto col = [&](int i) { return (i * lanes + tid) * 8; };
+  auto slot = [&](int stage, int piece) { return ring + ((long long)stage * pieces + piece) * lanes + tid; };
+  const size_t es = RES == RES_F32 ? 4 : 2;
+  auto fetch = [&](long long row, int stage) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (col(i) >= p.width) continue;
+        const long long at = row * p.width + col(i);
+        const char* h = static_cast<const char*>(p.h) + at * es;
+        const char* d = static_cast<const char*>(p.dh) + at * es;
+#pragma unroll
+        for (int u = 0; u < SP; ++u) {
+          copy_ahead<16>(slot(stage, i * SP + u), h + 16 * u);
+          if (has_dh) copy_ahead<16>(slot(stage, NV * (SP + 1) + i * SP + u), d + 16 * u);
+        }
+        copy_ahead<16>(slot(stage, NV * SP + i), p.dy + at);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto stream_of = [&](int stage, int piece, float (&v)[8]) {
+    if constexpr (RES == RES_F32) {
+      const float4 a = *reinterpret_cast<const float4*>(slot(stage, piece));
+      const float4 b = *reinterpret_cast<const float4*>(slot(stage, piece + 1));
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+      load_bf16<8>(reinterpret_cast<const __nv_bfloat16*>(slot(stage, piece)), v);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) fetch(blockIdx.x + (long long)s * gridDim.x, s);
+  float w[NV][8], dw[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[i][e] = dw[i][e] = 0.f;
+    if (col(i) < p.width) load_bf16<8>(p.w + col(i), w[i]);
+  }
+  int odd = 0, stage = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, odd ^= 1) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+    float h[NV][8], g[NV][8];
+    float ss = 0.f, sg = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (col(i) < p.width) {
+        stream_of(stage, i * SP, h[i]);
+        load_bf16<8>(reinterpret_cast<const __nv_bfloat16*>(slot(stage, NV * SP + i)), g[i]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i][e] = g[i][e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        ss = fmaf(h[i][e], h[i][e], ss);
+        sg = fmaf(g[i][e] * w[i][e], h[i][e], sg);
+      }
+    }
+    // the stage of the row before is read to its end: the row furthest ahead goes there
+    {
+      const int into = stage == 0 ? STAGES - 1 : stage - 1;
+      fetch(row + (long long)(STAGES - 1) * gridDim.x, into);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      sg += __shfl_xor_sync(0xffffffffu, sg, o);
+    }
+    if ((tid & 31) == 0) {
+      part[odd][0][tid >> 5] = ss;
+      part[odd][1][tid >> 5] = sg;
+    }
+    __syncthreads();
+    const bool in = (tid & 31) < (lanes >> 5);
+    ss = in ? part[odd][0][tid & 31] : 0.f;
+    sg = in ? part[odd][1][tid & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      sg += __shfl_xor_sync(0xffffffffu, sg, o);
+    }
+    const float rstd = 1.f / sqrtf(ss * inv_n + p.eps);
+    const float coef = rstd * rstd * (sg * inv_n);  // dx = rstd (g - h coef)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = col(i);
+      if (c >= p.width) continue;
+      float d[8];
+      if (has_dh) stream_of(stage, NV * (SP + 1) + i * SP, d);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float t = rstd * (g[i][e] * w[i][e] - h[i][e] * coef);
+        dw[i][e] = fmaf(g[i][e], h[i][e] * rstd, dw[i][e]);
+        d[e] = has_dh ? d[e] + t : t;
+      }
+      store_stream<8, RES>(p.dx, row * p.width + c, d);
+      if (p.dx16 != nullptr) store_bf16<8>(p.dx16 + row * p.width + c, d);
+    }
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (col(i) < p.width) store_f32<8>(p.partial + (long long)blockIdx.x * p.width + col(i), dw[i]);
+}
+
+// dw[c] = sum of the partial rows, in a fixed order: 32 row groups per column, then their
+// sum.
+__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* __restrict__ partial, int n,
+                                                          int width, float* __restrict__ dw) {
+  __shared__ float part[32][33];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + cx;
   float s = 0.f;
   if (c < width)
-    for (int r = ry; r < n; r += 8) s += partial[(long long)r * width + c];
+    for (int r = ry; r < n; r += 32) s += partial[(long long)r * width + c];
   part[ry][cx] = s;
   __syncthreads();
-  if (ry == 0 && c < width) {
+  // column ry's 32 sums, one per lane
+  s = part[cx][ry];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += part[k][cx];
-    dw[c] = s;
-  }
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (cx == 0 && blockIdx.x * 32 + ry < width) dw[blockIdx.x * 32 + ry] = s;
 }
 
 bool aligned16(std::initializer_list<const void*> ptrs) {
@@ -404,8 +534,13 @@ void launch_fwd_variant(const NormParams& p, cudaStream_t s) {
   const long long blocks = WARP ? (p.rows + 3) / 4 : p.rows;
   // resident CTAs: 2048 threads per SM
   const long long cap = (long long)sm_count() * std::max(1, 2048 / threads);
-  rmsnorm_fwd_kernel<VEC, NV, WARP, RES, E4M3>
-      <<<(unsigned)std::min(blocks, cap), threads, 0, s>>>(p);
+  const unsigned grid = (unsigned)std::min(blocks, cap);
+  if constexpr (WARP) {
+    rmsnorm_fwd_kernel<VEC, NV, true, RES, E4M3, 128><<<grid, threads, 0, s>>>(p);
+  } else {
+    if (threads <= 256) rmsnorm_fwd_kernel<VEC, NV, false, RES, E4M3, 256><<<grid, threads, 0, s>>>(p);
+    else rmsnorm_fwd_kernel<VEC, NV, false, RES, E4M3, 1024><<<grid, threads, 0, s>>>(p);
+  }
 }
 
 template <int RES, bool E4M3>
@@ -444,17 +579,41 @@ void launch_bwd_variant(const NormBwdParams& p, int ctas, cudaStream_t s) {
       <<<ctas, row_threads((p.width + VEC - 1) / VEC, NV), 0, s>>>(p);
 }
 
+template <int NV, int RES, int STAGES, int MAXT>
+tsp_status launch_bwd_ring(const NormBwdParams& p, int ctas, int threads, size_t smem, cudaStream_t s) {
+  auto kernel = rmsnorm_bwd_ring_kernel<NV, RES, STAGES, MAXT>;
+  TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem,
+                            "rmsnorm backward: cudaFuncSetAttribute"));
+  kernel<<<ctas, threads, smem, s>>>(p);
+  return TSP_OK;
+}
+
 template <int RES>
-void launch_bwd_res(const NormBwdParams& p, bool vec, int ctas, cudaStream_t s) {
-  if (vec) {
-    const int vecs = p.width / 8;
-    if (vecs <= 128) launch_bwd_variant<8, 1, RES>(p, ctas, s);
-    else if (vecs <= 2048) launch_bwd_variant<8, 2, RES>(p, ctas, s);
-    else launch_bwd_variant<8, 4, RES>(p, ctas, s);
-  } else {
+tsp_status launch_bwd_res(const NormBwdParams& p, bool vec, int ctas, cudaStream_t s) {
+  if (!vec) {
     if (p.width <= 4096) launch_bwd_variant<1, 8, RES>(p, ctas, s);
     else launch_bwd_variant<1, 32, RES>(p, ctas, s);
+    return TSP_OK;
   }
+  const int vecs = p.width / 8;
+  const int nv = vecs <= 128 ? 1 : 2;
+  const int threads = row_threads(vecs, nv);
+  // shared memory of a staged row: whole 16-byte pieces of every thread
+  const size_t row = (size_t)threads * nv * 16 * ((RES == RES_F32 ? 2 : 1) * (p.dh ? 2 : 1) + 1);
+  // three stages where three CTAs fit an SM with them, else two; a row too wide for two
+  // stages is loaded straight into registers
+  const bool three = 3 * row <= 74 * 1024;
+  const size_t smem = (three ? 3 : 2) * row;
+  if (threads <= 1024 && smem <= 220 * 1024) {
+    if (nv == 1) return launch_bwd_ring<1, RES, 3, 256>(p, ctas, threads, 3 * row, s);
+    if (threads <= 256) {
+      if (three) return launch_bwd_ring<2, RES, 3, 256>(p, ctas, threads, smem, s);
+      return launch_bwd_ring<2, RES, 2, 256>(p, ctas, threads, smem, s);
+    }
+    return launch_bwd_ring<2, RES, 2, 1024>(p, ctas, threads, 2 * row, s);
+  }
+  launch_bwd_variant<8, 4, RES>(p, ctas, s);
+  return TSP_OK;
 }
 
 // Checks shared by the three calls.
@@ -573,11 +732,10 @@ tsp_status tsp_rmsnorm_bwd(int64_t rows, int width, const void* h, int h_f32, co
   p.eps = eps;
   const int ctas = (int)std::min<int64_t>(rows, kBwdCtas);
   const bool vec = width % 8 == 0 && aligned16({h, weight, dy, dh, dx, dx16});
-  if (h_f32) launch_bwd_res<RES_F32>(p, vec, ctas, s);
-  else launch_bwd_res<RES_BF16>(p, vec, ctas, s);
+  TSP_TRY(h_f32 ? launch_bwd_res<RES_F32>(p, vec, ctas, s) : launch_bwd_res<RES_BF16>(p, vec, ctas, s));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "rmsnorm backward: launch");
-  rmsnorm_dw_kernel<<<(width + 31) / 32, 256, 0, s>>>(p.partial, ctas, width, dw);
+  rmsnorm_dw_kernel<<<(width + 31) / 32, 1024, 0, s>>>(p.partial, ctas, width, dw);
   e = cudaGetLastError();
   return e == cudaSuccess ? TSP_OK : cuda_fail(e, "rmsnorm backward: dw launch");
 }
