@@ -644,28 +644,36 @@ def tsp_rank_mlp_step(plan, h_r, mlp_shard, residual32, acc_r, out_r, g_r, ws, s
 # on tensors of another device than the current one selects it for the launch.
 
 def _same_device(tensors):
-    """The one CUDA device that the given tensors (None skipped) are on."""
-    device = None
+    """Index of the one CUDA device that the given tensors (None skipped) are on."""
+    device = -1
     for t in tensors:
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        try:
+            d = t.get_device()
+        except AttributeError:
+            d = -1
+        if d < 0:
             raise ValueError("expected CUDA tensors")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}")
+        if d != device:
+            if device >= 0:
+                raise ValueError(f"tensors on cuda:{device} and cuda:{d}")
+            device = d
     return device
 
 
 def _launch(name, device, stream, *args):
     """Call `name` with the stream (default: the device's current one) as last argument."""
-    fn = getattr(load_library(), name)
-    if device is None or device.index == torch.cuda.current_device():
-        status = fn(*args, _stream(stream))
+    fn = getattr(_lib or load_library(), name)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if device == torch.cuda.current_device():
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            status = fn(*args, _stream(stream))
+            status = fn(*args, raw)
     if status != TSP_OK:
         _check(status, name)
 
@@ -681,15 +689,16 @@ def _matrix(t, name, shape=None, dtypes=(torch.bfloat16,), optional=False):
         raise ValueError(f"{name} is required")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.dim() != 2 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [rows, width] matrix")
+    own = t.shape
+    if len(own) != 2 or (shape is not None and own != shape):
+        raise ValueError(f"{name} must have shape {shape or '[rows, width]'}, got {tuple(own)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _norm_args(x, weight, residual, h):
-    device = _same_device((x, weight, residual, h))
+def _norm_args(x, weight, residual, h, *outs):
+    device = _same_device((x, weight, residual, h, *outs))
     xp = _matrix(x, "x")
     shape = tuple(x.shape)
     if weight.dtype != torch.bfloat16 or weight.numel() != shape[1] or not weight.is_contiguous():
@@ -708,9 +717,8 @@ def tsp_rmsnorm_fwd(x, weight, y, residual=None, h=None, eps=1e-5, stream=None):
 
     x, y: bfloat16 [rows, width]; residual and h: bfloat16 or float32 [rows, width], both or
     neither. h may be residual, y may be x."""
-    device, xp, rp, hp, shape, f32 = _norm_args(x, weight, residual, h)
+    device, xp, rp, hp, shape, f32 = _norm_args(x, weight, residual, h, y)
     yp = _matrix(y, "y", shape)
-    _same_device((x, y))
     _launch("tsp_rmsnorm_fwd", device, stream, shape[0], shape[1], xp, rp, f32, weight.data_ptr(),
             eps, hp, yp)
 
@@ -719,8 +727,7 @@ def tsp_rmsnorm_fwd_e4m3(x, weight, y, scales, residual=None, h=None, eps=1e-5, 
                          stream=None):
     """tsp_rmsnorm_fwd with y in float8_e4m3fn and float32 scales: [rows, 1] with group 0,
     [rows, ceil(width / 128)] with group 128."""
-    device, xp, rp, hp, shape, f32 = _norm_args(x, weight, residual, h)
-    _same_device((x, y, scales))
+    device, xp, rp, hp, shape, f32 = _norm_args(x, weight, residual, h, y, scales)
     yp = _matrix(y, "y", shape, (torch.float8_e4m3fn,))
     groups = -(-shape[1] // group) if group else 1
     sp = _matrix(scales, "scales", (shape[0], groups), (torch.float32,))
@@ -756,30 +763,25 @@ def tsp_grad_workspace_bytes(n: int) -> int:
 _GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
-def _grad_list(grads, name):
-    for t in grads:
-        if t.dtype not in _GRAD_TYPES:
-            raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    return (_P * len(grads))(*[t.data_ptr() for t in grads])
-
-
 def _grad_args(grads, norm, ws):
     device = _same_device((*grads, norm, ws))
     if norm.dtype != torch.float32 or norm.numel() != 1:
         raise ValueError("norm must be one float32 value")
     n = len(grads)
-    ptrs = _grad_list(grads, "gradients")
-    sizes = (_L * n)(*[t.numel() for t in grads])
-    types = (_I * n)(*[_GRAD_TYPES[t.dtype] for t in grads])
-    return device, n, ptrs, sizes, types, _dev(ws, "ws", tsp_grad_workspace_bytes(n), torch.uint8)
+    types = [_GRAD_TYPES.get(t.dtype) for t in grads]
+    if None in types:
+        raise ValueError("gradients must be float32 or bfloat16")
+    if not all([t.is_contiguous() for t in grads]):
+        raise ValueError("gradients must be contiguous")
+    return (device, n, (_L * n)(*[t.data_ptr() for t in grads]), [t.numel() for t in grads], types,
+            _dev(ws, "ws", tsp_grad_workspace_bytes(n), torch.uint8))
 
 
 def tsp_grad_norm(grads, norm, ws, stream=None):
     """norm (one float32 on the device) = the 2-norm over all elements of the tensors."""
     device, n, ptrs, sizes, types, wp = _grad_args(grads, norm, ws)
-    _launch("tsp_grad_norm", device, stream, n, ptrs, sizes, types, norm.data_ptr(), wp)
+    _launch("tsp_grad_norm", device, stream, n, ptrs, (_L * n)(*sizes), (_I * n)(*types),
+            norm.data_ptr(), wp)
 
 
 def tsp_grad_clip(grads, outs, max_norm, norm, ws, stream=None):
@@ -789,13 +791,14 @@ def tsp_grad_clip(grads, outs, max_norm, norm, ws, stream=None):
     if outs is grads:
         out_ptrs = ptrs
     else:
-        if len(outs) != n or any(o.shape != g.shape or o.dtype != g.dtype for o, g in zip(outs, grads)):
-            raise ValueError("outs must match the gradients in number, shape and type")
         if n and _same_device(outs) != device:
             raise ValueError("outs on another device than the gradients")
-        out_ptrs = _grad_list(outs, "outs")
-    _launch("tsp_grad_clip", device, stream, n, ptrs, out_ptrs, sizes, types, max_norm,
-            norm.data_ptr(), wp)
+        if ([t.numel() for t in outs] != sizes or [_GRAD_TYPES.get(t.dtype) for t in outs] != types
+                or not all([t.is_contiguous() for t in outs])):
+            raise ValueError("outs must be contiguous and match the gradients in number, size and type")
+        out_ptrs = (_L * n)(*[t.data_ptr() for t in outs])
+    _launch("tsp_grad_clip", device, stream, n, ptrs, out_ptrs, (_L * n)(*sizes), (_I * n)(*types),
+            max_norm, norm.data_ptr(), wp)
 
 
 # ------------------------------------------------------------------ packed attention
@@ -815,25 +818,28 @@ def _heads3(t, name, shape=None):
     """(pointer, row stride) of a bfloat16 [tokens, heads, d] tensor whose rows are contiguous."""
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must have shape {shape or '[tokens, heads, d]'}, got {tuple(t.shape)}")
-    n, h, d = t.shape
-    if t.numel() and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+    own = t.shape
+    if len(own) != 3 or (shape is not None and own != shape):
+        raise ValueError(f"{name} must have shape {shape or '[tokens, heads, d]'}, got {tuple(own)}")
+    n, h, d = own
+    row, head, one = t.stride()
+    if n and h and d and (one != 1 or (h > 1 and head != d)):
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.data_ptr(), t.stride(0) if n > 1 else h * d
+    return t.data_ptr(), row if n > 1 else h * d
 
 
 def _packed_args(q, k, v, starts):
     qp, ldq = _heads3(q, "q")
     kp, ldk = _heads3(k, "k")
-    tokens, heads, d = q.shape
-    if k.shape[0] != tokens or k.shape[2] != d:
-        raise ValueError(f"k has shape {tuple(k.shape)} beside q {tuple(q.shape)}")
-    vp, ldv = _heads3(v, "v", tuple(k.shape))
-    if starts.dtype != torch.int32 or starts.dim() != 1 or not starts.is_contiguous() or not starts.numel():
-        raise ValueError("starts must hold n_seqs + 1 contiguous int32 values")
+    qs, ks = q.shape, k.shape
+    tokens, heads, d = qs
+    if ks[0] != tokens or ks[2] != d:
+        raise ValueError(f"k has shape {tuple(ks)} beside q {tuple(qs)}")
+    vp, ldv = _heads3(v, "v", ks)
     n = starts.numel() - 1
-    return (tokens, n, starts.data_ptr(), heads, k.shape[1], d), (qp, ldq, kp, ldk, vp, ldv)
+    if starts.dtype != torch.int32 or starts.dim() != 1 or n < 0 or not starts.is_contiguous():
+        raise ValueError("starts must hold n_seqs + 1 contiguous int32 values")
+    return (tokens, n, starts.data_ptr(), heads, ks[1], d), (qp, ldq, kp, ldk, vp, ldv), qs, ks
 
 
 def _stat(t, name, heads, tokens):
@@ -855,9 +861,9 @@ def tsp_packed_attention_fwd(q, k, v, starts, o, ws, lse=None, scale=None, strea
     (bfloat16, rows may be strided), starts int32 [n_seqs + 1] on the device; lse float32
     [heads, tokens] receives the row statistics that the backward takes."""
     device = _same_device((q, k, v, starts, o, ws, lse))
-    sizes, qkv = _packed_args(q, k, v, starts)
-    tokens, heads, d = q.shape
-    op, ldo = _heads3(o, "o", tuple(q.shape))
+    sizes, qkv, qs, _ = _packed_args(q, k, v, starts)
+    tokens, heads, d = qs
+    op, ldo = _heads3(o, "o", qs)
     lp, ldl = (None, 0) if lse is None else _stat(lse, "lse", heads, tokens)
     _launch("tsp_packed_attention_fwd", device, stream, *sizes, d ** -0.5 if scale is None else scale,
             *qkv, op, ldo, lp, ldl, _ws_packed(ws, sizes))
@@ -866,9 +872,8 @@ def tsp_packed_attention_fwd(q, k, v, starts, o, ws, lse=None, scale=None, strea
 def tsp_packed_attention_bwd(q, k, v, starts, o, lse, dout, dq, dk, dv, ws, scale=None, stream=None):
     """Gradients of tsp_packed_attention_fwd from its o and lse and the gradient dout of o."""
     device = _same_device((q, k, v, starts, o, lse, dout, dq, dk, dv, ws))
-    sizes, qkv = _packed_args(q, k, v, starts)
-    tokens, heads, d = q.shape
-    qs, ks = tuple(q.shape), tuple(k.shape)
+    sizes, qkv, qs, ks = _packed_args(q, k, v, starts)
+    tokens, heads, d = qs
     _launch("tsp_packed_attention_bwd", device, stream, *sizes, d ** -0.5 if scale is None else scale,
             *qkv, *_heads3(o, "o", qs), *_stat(lse, "lse", heads, tokens), *_heads3(dout, "dout", qs),
             *_heads3(dq, "dq", qs), *_heads3(dk, "dk", ks), *_heads3(dv, "dv", ks), _ws_packed(ws, sizes))

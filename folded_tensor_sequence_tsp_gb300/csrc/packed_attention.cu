@@ -53,6 +53,7 @@ constexpr int QT = TILE, KT = TILE;
 constexpr int STAGES = 2;
 constexpr int THREADS = 320;
 constexpr uint32_t TMEM_COLS = 512;
+constexpr int ITEMS = 4;  // items between the producer and the epilogue
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
 
 __device__ __forceinline__ uint32_t tm_s(int t) { return t ? 256u : 0u; }
@@ -141,7 +142,7 @@ struct Geometry {
   static constexpr int BOXES = HD / 64;
   static constexpr uint32_t TILE_BYTES = 128 * HD * 2;
   // Q_A, Q_B, K_0, then the ring: K slots 0/1 and V slots 0/1
-  static constexpr size_t USED = 1024 + (size_t)(3 + 2 * STAGES) * TILE_BYTES + 256;
+  static constexpr size_t USED = 1024 + (size_t)(3 + 2 * STAGES) * TILE_BYTES + 512;
   // all 512 TMEM columns: alone on its SM
   static constexpr size_t SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
 };
@@ -158,6 +159,21 @@ struct FwdParams {
   unsigned long long limit_ns;
 };
 
+// Tiles of an item: key tiles of query tile A and of B (0: B has no query).
+struct Tiles {
+  int a, b, n;
+  bool ragged;  // the last key tile reads on behind the sequence
+};
+__device__ __forceinline__ Tiles tiles_of(const Item& it, int tpt) {
+  const int q_b = it.q0 + tpt;
+  Tiles t;
+  t.a = (min(it.len, q_b) + KT - 1) / KT;
+  t.b = q_b < it.len ? (min(it.len, q_b + tpt) + KT - 1) / KT : 0;
+  t.n = max(t.a, t.b);
+  t.ragged = t.n * KT > it.len;
+  return t;
+}
+
 template <int HD>
 __global__ void __launch_bounds__(THREADS, 1)
     packed_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -165,36 +181,37 @@ __global__ void __launch_bounds__(THREADS, 1)
                             const __grid_constant__ CUtensorMap tmV, const FwdParams p) {
   using Geo = Geometry<HD>;
   extern __shared__ uint8_t smem_raw[];
-  Item it;
-  int head;
-  if (!find_item(p.src, it, head)) return;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;
   uint8_t* sK0 = sQ + 2 * Geo::TILE_BYTES;
   uint8_t* sK = sK0 + Geo::TILE_BYTES;
   uint8_t* sV = sK + STAGES * Geo::TILE_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + STAGES * Geo::TILE_BYTES);
-  uint64_t* q_full = bars;                // Q_A, Q_B, K_0
-  uint64_t* kv_full = q_full + 1;         // [STAGES] stage j % 2: V_j and K_{j+1}
-  uint64_t* kv_empty = kv_full + STAGES;  // [STAGES]
-  uint64_t* s_full = kv_empty + STAGES;   // [2] per tile: S(j) in TMEM
-  uint64_t* p_full = s_full + 2;          // [2] per tile: P(j) in TMEM (4 warps)
-  uint64_t* o_done = p_full + 2;          // [2] per tile: its last O += P V complete
-  uint64_t* tail_ok = o_done + 2;         // the last V tile is cleared behind the sequence
-  uint64_t* drain = tail_ok + 1;
+  Item* items = reinterpret_cast<Item*>(sV + STAGES * Geo::TILE_BYTES);  // [ITEMS]
+  uint64_t* item_full = reinterpret_cast<uint64_t*>(items + ITEMS);      // [ITEMS]
+  uint64_t* item_empty = item_full + ITEMS;  // [ITEMS] read by the MMA lane and 8 warps
+  uint64_t* q_full = item_empty + ITEMS;     // Q_A, Q_B, K_0 of the item
+  uint64_t* q_empty = q_full + 1;            // its scores are all computed
+  uint64_t* kv_full = q_empty + 1;           // [STAGES] V_j and K_{j+1}
+  uint64_t* kv_empty = kv_full + STAGES;     // [STAGES]
+  uint64_t* s_full = kv_empty + STAGES;      // [2] per tile: S(j) in TMEM
+  uint64_t* p_full = s_full + 2;             // [2] per tile: P(j) in TMEM (4 warps)
+  uint64_t* o_done = p_full + 2;             // [2] per tile: the item's last O += P V complete
+  // the last V tile is cleared behind the sequence: two in turn, because the producer may
+  // clear the next item's before the MMA lane has waited for this one's
+  uint64_t* tail_ok = o_done + 2;            // [2]
+  uint64_t* drain = tail_ok + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int q_b = it.q0 + p.TPT;  // tile B's first token
-  const int n_a = (min(it.len, q_b) + KT - 1) / KT;
-  const int n_b = q_b < it.len ? (min(it.len, q_b + p.TPT) + KT - 1) / KT : 0;
-  const int n_tiles = max(n_a, n_b);
-  const bool ragged = n_tiles * KT > it.len;
-
   if (threadIdx.x == 0) {
+    for (int s = 0; s < ITEMS; ++s) {
+      mbar_init(&item_full[s], 1);
+      mbar_init(&item_empty[s], 9);
+    }
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 1);
@@ -204,28 +221,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&p_full[t], 4);
       mbar_init(&o_done[t], 1);
     }
-    mbar_init(tail_ok, 1);
+    mbar_init(&tail_ok[0], 1);
+    mbar_init(&tail_ok[1], 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    // the first loads are under way while the CTA sets itself up
-    {
-      const uint32_t q_bytes = (uint32_t)(Geo::BOXES * 128) * (uint32_t)p.RU;
-      mbar_arrive_expect_tx(q_full, (n_b ? 2u : 1u) * q_bytes + Geo::TILE_BYTES);
-#pragma unroll
-      for (int b = 0; b < Geo::BOXES; ++b) {
-        tma_load_3d(sQ + b * BOX_BYTES, &tmQ, q_full, 64 * b, head * p.G, it.start + it.q0);
-        if (n_b)
-          tma_load_3d(sQ + Geo::TILE_BYTES + b * BOX_BYTES, &tmQ, q_full, 64 * b, head * p.G,
-                      it.start + q_b);
-        tma_load_2d(sK0 + b * BOX_BYTES, &tmK, q_full, head * HD + 64 * b, it.start);
-      }
-    }
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
+  // the producer looks its first item up before the CTA meets
+  Item next{};
+  Walk walk;
+  if (warp == 0) walk.next(p.src, next);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -233,52 +245,87 @@ __global__ void __launch_bounds__(THREADS, 1)
   WaitBound wb{p.status, p.limit_ns, abort_flag};
 
   if (warp == 0) {
-    // -------------------------------------------------------------- TMA producer
-    bool all = true;
-    if (lane == 0) {
-      int last[STAGES];
-#pragma unroll
-      for (int s = 0; s < STAGES; ++s) last[s] = -1;
-      for (int j = 0; j < n_tiles; ++j) {
-        const int st = j % STAGES;
-        const uint32_t ph = (uint32_t)((j / STAGES) & 1);
-        if (!mbar_wait(&kv_empty[st], ph ^ 1u, wb, SITE_PACKED_PRODUCER)) {
-          all = false;
-          break;
+    // -------------------------------------------------------------- producer
+    WaitBound wd{p.status, p.limit_ns, nullptr};
+    bool ok = true;
+    uint32_t n_items = 0, c = 0, n_tail = 0;  // items, key tiles and ragged items so far
+    while (ok) {
+      const Item it = next;
+      const int slot = (int)(n_items % ITEMS);
+      const Tiles tl = tiles_of(it, p.TPT);
+      if (lane == 0) {
+        ok = mbar_wait(&item_empty[slot], ((n_items / ITEMS) & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+        if (ok) {
+          items[slot] = it;
+          mbar_arrive(&item_full[slot]);
         }
-        const bool has_k = j + 1 < n_tiles;
-        mbar_arrive_expect_tx(&kv_full[st], (has_k ? 2u : 1u) * Geo::TILE_BYTES);
+        if (ok && it.head >= 0) {
+          ok = mbar_wait(q_empty, (n_items & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+          if (ok) {
+            const uint32_t q_bytes = (uint32_t)(Geo::BOXES * 128) * (uint32_t)p.RU;
+            mbar_arrive_expect_tx(q_full, (tl.b ? 2u : 1u) * q_bytes + Geo::TILE_BYTES);
+#pragma unroll
+            for (int b = 0; b < Geo::BOXES; ++b) {
+              tma_load_3d(sQ + b * BOX_BYTES, &tmQ, q_full, 64 * b, it.head * p.G, it.start + it.q0);
+              if (tl.b)
+                tma_load_3d(sQ + Geo::TILE_BYTES + b * BOX_BYTES, &tmQ, q_full, 64 * b, it.head * p.G,
+                            it.start + it.q0 + p.TPT);
+              tma_load_2d(sK0 + b * BOX_BYTES, &tmK, q_full, it.head * HD + 64 * b, it.start);
+            }
+          }
+          for (int j = 0; ok && j < tl.n; ++j, ++c) {
+            const int st = (int)(c % STAGES);
+            ok = mbar_wait(&kv_empty[st], ((c / STAGES) & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+            if (!ok) break;
+            const bool has_k = j + 1 < tl.n;
+            mbar_arrive_expect_tx(&kv_full[st], (has_k ? 2u : 1u) * Geo::TILE_BYTES);
+#pragma unroll
+            for (int b = 0; b < Geo::BOXES; ++b) {
+              tma_load_2d(sV + st * Geo::TILE_BYTES + b * BOX_BYTES, &tmV, &kv_full[st],
+                          it.head * HD + 64 * b, it.start + j * KT);
+              if (has_k)
+                tma_load_2d(sK + st * Geo::TILE_BYTES + b * BOX_BYTES, &tmK, &kv_full[st],
+                            it.head * HD + 64 * b, it.start + (j + 1) * KT);
+            }
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      c = __shfl_sync(0xffffffffu, c, 0);
+      if (!ok || it.head < 0) break;
+      // the next item is looked up while the last loads are on their way
+      walk.next(p.src, next);
+      if (tl.ragged) {
+        const uint32_t last = c - 1;
+        const int st = (int)(last % STAGES);
+        // every lane reads the phase itself: the tile is then visible to its writes
+        ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[st], (last / STAGES) & 1u, wb,
+                                               SITE_PACKED_PRODUCER)) != 0;
+        if (!ok) break;
+        const int keep = it.len - (tl.n - 1) * KT;  // rows of the sequence in the tile
 #pragma unroll
         for (int b = 0; b < Geo::BOXES; ++b) {
-          tma_load_2d(sV + st * Geo::TILE_BYTES + b * BOX_BYTES, &tmV, &kv_full[st],
-                      head * HD + 64 * b, it.start + j * KT);
-          if (has_k)
-            tma_load_2d(sK + st * Geo::TILE_BYTES + b * BOX_BYTES, &tmK, &kv_full[st],
-                        head * HD + 64 * b, it.start + (j + 1) * KT);
+          uint4* rows = reinterpret_cast<uint4*>(sV + st * Geo::TILE_BYTES + b * BOX_BYTES);
+          for (int i = keep * 8 + lane; i < 128 * 8; i += 32) rows[i] = make_uint4(0u, 0u, 0u, 0u);
         }
-        last[st] = (int)ph;
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail_ok[n_tail & 1u]);
+        ++n_tail;
       }
-      WaitBound wd{p.status, p.limit_ns, nullptr};
-      all = mbar_wait(q_full, 0, wd, SITE_DRAIN) && all;
-      for (int s = 0; s < STAGES; ++s)
-        if (last[s] >= 0) all = mbar_wait(&kv_full[s], (uint32_t)last[s], wd, SITE_DRAIN) && all;
+      ++n_items;
     }
-    // every load of the CTA has landed; the last V tile still waits for tail_ok
-    all = __shfl_sync(0xffffffffu, all ? 1 : 0, 0) != 0;
-    if (ragged && all) {
-      const int st = (n_tiles - 1) % STAGES;
-      // every lane reads the phase itself: the tile is then visible to its writes
-      WaitBound wd{p.status, p.limit_ns, nullptr};
-      mbar_wait(&kv_full[st], (uint32_t)(((n_tiles - 1) / STAGES) & 1), wd, SITE_DRAIN);
-      const int keep = it.len - (n_tiles - 1) * KT;  // rows of the sequence in the tile
-#pragma unroll
-      for (int b = 0; b < Geo::BOXES; ++b) {
-        uint4* rows = reinterpret_cast<uint4*>(sV + st * Geo::TILE_BYTES + b * BOX_BYTES);
-        for (int i = keep * 8 + lane; i < 128 * 8; i += 32) rows[i] = make_uint4(0u, 0u, 0u, 0u);
+    // copies in flight land before the CTA ends: the last use of each barrier that was armed
+    // (after a wait that gave up, of every one that may have been; those waits are bounded)
+    if (lane == 0) {
+      if (n_items > 0) mbar_wait(q_full, (n_items - 1) & 1u, wd, SITE_DRAIN);
+      for (uint32_t b = c > STAGES ? c - STAGES : 0; b < c; ++b)
+        mbar_wait(&kv_full[b % STAGES], (b / STAGES) & 1u, wd, SITE_DRAIN);
+      if (!ok) {
+        const unsigned long long t0 = global_ns();  // what a stopped item may still have in flight
+        while (global_ns() - t0 < 1000000ull) {
+        }
       }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tail_ok);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -291,9 +338,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t q_hi = (uint32_t)(dq0 >> 32), k_hi = (uint32_t)(dk0 >> 32);
       const uint32_t v_hi = (uint32_t)(dv0 >> 32);
       constexpr uint32_t TILE16 = Geo::TILE_BYTES >> 4;
-      auto issue_s = [&](int t, int j) {
+      // S_t = Q_t K^T with K in `slot` (0: the item's first key tile, 1 + stage otherwise)
+      auto issue_s = [&](int t, uint32_t slot) {
         const uint32_t a_lo = (uint32_t)dq0 + (uint32_t)t * TILE16;
-        const uint32_t b_lo = (uint32_t)dk0 + (j == 0 ? 0u : (uint32_t)(1 + (j - 1) % STAGES) * TILE16);
+        const uint32_t b_lo = (uint32_t)dk0 + slot * TILE16;
         const uint32_t d = tmem + tm_s(t);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
@@ -302,49 +350,66 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         mma_commit(&s_full[t]);
       };
-      auto issue_pv = [&](int t, int j) {
-        const uint32_t b_lo = (uint32_t)dv0 + (uint32_t)(j % STAGES) * TILE16;
+      auto issue_pv = [&](int t, uint32_t stage, bool first) {
+        const uint32_t b_lo = (uint32_t)dv0 + stage * TILE16;
         const uint32_t d = tmem + tm_o(t), a = tmem + tm_s(t);
-        const uint32_t first = j > 0 ? 1u : 0u;
 #pragma unroll
         for (int kk = 0; kk < KT / 16; ++kk)
           mma_ts_w(d, a + (uint32_t)(kk * 8), b_lo + (uint32_t)(kk * (2048 >> 4)), v_hi, idesc_o,
-                   kk > 0 ? 1u : first);
+                   kk > 0 ? 1u : (first ? 0u : 1u));
       };
-      bool ok = mbar_wait_poll(q_full, 0, wb, SITE_PACKED_MMA);
-      if (ok) {
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return mbar_wait_poll(bar, parity & 1u, wb, SITE_PACKED_MMA);
+      };
+      bool ok = true;
+      uint32_t n_items = 0, c = 0, n_tail = 0;
+      uint32_t cp[2] = {0, 0};  // P tiles taken so far
+      while (ok) {
+        const int slot = (int)(n_items % ITEMS);
+        ok = wait(&item_full[slot], n_items / ITEMS);
+        if (!ok) break;
+        const Item it = items[slot];
+        mbar_arrive(&item_empty[slot]);
+        if (it.head < 0) break;
+        const Tiles tl = tiles_of(it, p.TPT);
+        ok = wait(q_full, n_items);
+        if (!ok) break;
         tc_fence_after();
         issue_s(0, 0);
-        if (n_b > 0) issue_s(1, 0);
-        ok = mbar_wait_poll(&kv_full[0], 0, wb, SITE_PACKED_MMA);
-      }
-      for (int j = 0; ok && j < n_tiles; ++j) {
-        if (ragged && j == n_tiles - 1 && !mbar_wait_poll(tail_ok, 0, wb, SITE_PACKED_MMA)) break;
-        for (int t = 0; t < 2; ++t) {
-          const int nt = t ? n_b : n_a;
-          if (j < nt) {
-            if (!mbar_wait_poll(&p_full[t], (uint32_t)(j & 1), wb, SITE_PACKED_MMA)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            issue_pv(t, j);
-            if (j + 1 < nt) {
-              issue_s(t, j + 1);
-            } else {
-              mma_commit(&o_done[t]);
-            }
+        if (tl.b > 0) issue_s(1, 0);
+        if (tl.n == 1) mma_commit(q_empty);
+        ok = wait(&kv_full[c % STAGES], c / STAGES);
+        for (int j = 0; ok && j < tl.n; ++j, ++c) {
+          const uint32_t st = c % STAGES;
+          if (tl.ragged && j == tl.n - 1) {
+            ok = wait(&tail_ok[n_tail & 1u], n_tail >> 1);
+            ++n_tail;
+            if (!ok) break;
           }
-          // while tile A's products run, wait for the next stage
-          if (t == 0 && j + 1 < n_tiles &&
-              !mbar_wait_poll(&kv_full[(j + 1) % STAGES], (uint32_t)(((j + 1) / STAGES) & 1), wb,
-                              SITE_PACKED_MMA)) {
-            ok = false;
-            break;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int nt = t ? tl.b : tl.a;
+            if (ok && j < nt) {
+              ok = wait(&p_full[t], cp[t]);
+              ++cp[t];
+              if (ok) {
+                tc_fence_after();
+                issue_pv(t, st, j == 0);
+                if (j + 1 < nt) {
+                  issue_s(t, 1 + st);
+                } else {
+                  mma_commit(&o_done[t]);
+                }
+              }
+            }
+            // while tile A's products run, wait for the next stage
+            if (ok && t == 0 && j + 1 < tl.n) ok = wait(&kv_full[(c + 1) % STAGES], (c + 1) / STAGES);
           }
+          if (!ok) break;
+          mma_commit(&kv_empty[st]);
+          if (j + 2 == tl.n) mma_commit(q_empty);  // the item's last scores are issued
         }
-        if (!ok) break;
-        mma_commit(&kv_empty[j % STAGES]);
+        ++n_items;
       }
       mma_commit(drain);
       WaitBound wd{p.status, p.limit_ns, nullptr};
@@ -355,102 +420,127 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int t = (warp - 2) >> 2;
     const int q = warp & 3;
     const int r_local = q * 32 + lane;
-    const int tok = r_local / p.G;
-    const int my_q0 = t ? q_b : it.q0;
-    const bool row_ok = r_local < p.RU && my_q0 + tok < it.len;
-    const int pos = row_ok ? my_q0 + tok : -1;
     const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
     const uint32_t s_tmem = lane_base + tm_s(t);
     const uint32_t o_tmem = lane_base + tm_o(t);
-    const int my_tiles = t ? n_b : n_a;
-    float m_ref = -INFINITY;  // reference maximum (scaled, log2 units)
-    float l = 0.f;
-    bool ok = true;
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
       const WaitBound wbs{p.status, p.limit_ns, abort_flag};
-      const bool mine = mbar_wait(bar, parity, wbs, SITE_PACKED_SOFTMAX);
+      const bool mine = mbar_wait(bar, parity & 1u, wbs, SITE_PACKED_SOFTMAX);
       return __all_sync(0xffffffffu, mine) != 0;
     };
-    for (int j = 0; j < my_tiles; ++j) {
-      // S(j) complete also means O += P(j-1) V_{j-1} is complete (in-order MMAs)
-      if (!warp_wait(&s_full[t], (uint32_t)(j & 1))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      float sc[KT];
+    uint32_t n_items = 0;
+    uint32_t ph = 0;  // phase bits: 1 of s_full, 2 of o_done
+    while (true) {
+      const int slot = (int)(n_items % ITEMS);
+      if (!warp_wait(&item_full[slot], n_items / ITEMS)) break;
+      ++n_items;
+      // what the epilogue needs of the item is read again there, instead of being held in
+      // registers across the key loop; only then is the slot released
+      int my_tiles, pos;
       {
-        uint32_t ra[32], rb[32], rc[32], rd[32];
-        tmem_ld32(s_tmem + 0, ra);
-        tmem_ld32(s_tmem + 32, rb);
-        tmem_ld32(s_tmem + 64, rc);
-        tmem_ld32(s_tmem + 96, rd);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          sc[e] = __uint_as_float(ra[e]);
-          sc[32 + e] = __uint_as_float(rb[e]);
-          sc[64 + e] = __uint_as_float(rc[e]);
-          sc[96 + e] = __uint_as_float(rd[e]);
+        const Item it = items[slot];
+        if (it.head < 0) break;
+        const Tiles tl = tiles_of(it, p.TPT);
+        const int at = it.q0 + (t ? p.TPT : 0) + r_local / p.G;
+        my_tiles = t ? tl.b : tl.a;
+        pos = r_local < p.RU && at < it.len ? at : -1;
+      }
+      if (my_tiles == 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[slot]);
+        continue;
+      }
+      float m_ref = -INFINITY;  // reference maximum (scaled, log2 units)
+      float l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < my_tiles; ++j, ph ^= 1u) {
+        // S(j) complete also means O += P(j-1) V_{j-1} is complete (in-order MMAs)
+        if (!warp_wait(&s_full[t], ph)) {
+          ok = false;
+          break;
         }
-      }
-      const int kv0 = j * KT;
-      if (kv0 + KT - 1 > pos) {
-#pragma unroll
-        for (int e = 0; e < KT; ++e)
-          if (kv0 + e > pos) sc[e] = -INFINITY;
-      }
-      float m4[4] = {sc[0], sc[1], sc[2], sc[3]};
-#pragma unroll
-      for (int e = 4; e + 8 <= KT; e += 8) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m4[k] = max3f(m4[k], sc[e + k], sc[e + 4 + k]);
-      }
-      const float mraw = max3f(max3f(m4[0], m4[1], sc[KT - 4]), max3f(m4[2], m4[3], sc[KT - 3]),
-                               fmaxf(sc[KT - 2], sc[KT - 1]));
-      const float mx = mraw * p.scale_log2;  // scale > 0 keeps the order
-      float factor = 1.f;
-      const bool rescale = mx > m_ref + RESCALE_THRESHOLD;
-      if (rescale) {
-        factor = ex2(m_ref - mx);  // 0 when m_ref is still -inf
-        m_ref = mx;
-      }
-      const float neg_ref = m_ref == -INFINITY ? 0.f : -m_ref;
-      l *= factor;
-      l += exp_tile<KT>(sc, s_tmem, p.scale_log2, neg_ref);
-      // rescale O before P(j) is handed over; after the exponentials, when the scores are
-      // no longer live
-      if (j > 0 && __any_sync(0xffffffffu, rescale && factor != 1.f)) {
-#pragma unroll 1
-        for (int c = 0; c < HD; c += 16) {
-          uint32_t r[16];
-          tmem_ld16(o_tmem + c, r);
+        tc_fence_after();
+        float sc[KT];
+        {
+          uint32_t ra[32], rb[32], rc[32], rd[32];
+          tmem_ld32(s_tmem + 0, ra);
+          tmem_ld32(s_tmem + 32, rb);
+          tmem_ld32(s_tmem + 64, rc);
+          tmem_ld32(s_tmem + 96, rd);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * factor);
-          tmem_st16(o_tmem + c, r);
+          for (int e = 0; e < 32; ++e) {
+            sc[e] = __uint_as_float(ra[e]);
+            sc[32 + e] = __uint_as_float(rb[e]);
+            sc[64 + e] = __uint_as_float(rc[e]);
+            sc[96 + e] = __uint_as_float(rd[e]);
+          }
         }
+        const int kv0 = j * KT;
+        if (kv0 + KT - 1 > pos) {
+#pragma unroll
+          for (int e = 0; e < KT; ++e)
+            if (kv0 + e > pos) sc[e] = -INFINITY;
+        }
+        float m4[4] = {sc[0], sc[1], sc[2], sc[3]};
+#pragma unroll
+        for (int e = 4; e + 8 <= KT; e += 8) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) m4[u] = max3f(m4[u], sc[e + u], sc[e + 4 + u]);
+        }
+        const float mraw = max3f(max3f(m4[0], m4[1], sc[KT - 4]), max3f(m4[2], m4[3], sc[KT - 3]),
+                                 fmaxf(sc[KT - 2], sc[KT - 1]));
+        const float mx = mraw * p.scale_log2;  // scale > 0 keeps the order
+        float factor = 1.f;
+        const bool rescale = mx > m_ref + RESCALE_THRESHOLD;
+        if (rescale) {
+          factor = ex2(m_ref - mx);  // 0 when m_ref is still -inf
+          m_ref = mx;
+        }
+        const float neg_ref = m_ref == -INFINITY ? 0.f : -m_ref;
+        l *= factor;
+        l += exp_tile<KT>(sc, s_tmem, p.scale_log2, neg_ref);
+        // rescale O before P(j) is handed over; after the exponentials, when the scores are
+        // no longer live
+        if (j > 0 && __any_sync(0xffffffffu, rescale && factor != 1.f)) {
+#pragma unroll 1
+          for (int e0 = 0; e0 < HD; e0 += 16) {
+            uint32_t r[16];
+            tmem_ld16(o_tmem + e0, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * factor);
+            tmem_st16(o_tmem + e0, r);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t]);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[t]);
-    }
-    // ------------------------------------------------------------ epilogue
-    if (ok && my_tiles > 0 && warp_wait(&o_done[t], 0u)) {
+      if (!ok || !warp_wait(&o_done[t], ph >> 1)) break;
+      ph ^= 2u;
+      // ---------------------------------------------------------- epilogue
+      // P of the next item is handed over after these loads, and only then may its first
+      // product overwrite O
       tc_fence_after();
-      const long long row = (long long)it.start + (pos < 0 ? 0 : pos);
-      const int qh = head * p.G + (r_local - tok * p.G);
+      const bool row_ok = pos >= 0;
+      const Item it = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[slot]);
+      const int tok = r_local / p.G;
+      const long long row = (long long)it.start + (row_ok ? pos : 0);
+      const int qh = it.head * p.G + (r_local - tok * p.G);
       const float inv = 1.f / l;
       if (p.lse != nullptr && row_ok) p.lse[(long long)qh * p.ld_lse + row] = m_ref + log2f(l);
       __nv_bfloat16* dst = p.o + row * p.ld_o + (long long)qh * HD;
 #pragma unroll
-      for (int c = 0; c < HD; c += 32) {
+      for (int e0 = 0; e0 < HD; e0 += 32) {
         uint32_t r[32];
-        tmem_ld32(o_tmem + c, r);
+        tmem_ld32(o_tmem + e0, r);
         tmem_ld_wait();
         if (row_ok) {
-          uint4* d4 = reinterpret_cast<uint4*>(dst + c);
+          uint4* d4 = reinterpret_cast<uint4*>(dst + e0);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint4 w;
@@ -462,6 +552,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
+      tc_fence_before();
     }
   }
 
@@ -485,7 +576,8 @@ tsp_status launch_fwd(const Shape& s, const FwdParams& p, const void* q, int64_t
   const size_t smem = Geometry<HD>::SMEM;
   TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem,
                             "packed attention: cudaFuncSetAttribute"));
-  kernel<<<(unsigned)p.src.max_items * (unsigned)s.kv_heads, THREADS, smem, stream>>>(tq, tk, tv, p);
+  const unsigned grid = (unsigned)std::min<long long>((long long)p.src.max_items * s.kv_heads, sm_count());
+  kernel<<<grid, THREADS, smem, stream>>>(tq, tk, tv, p);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? TSP_OK : cuda_fail(e, "packed attention: launch");
 }

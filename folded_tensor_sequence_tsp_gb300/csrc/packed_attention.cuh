@@ -16,7 +16,7 @@ struct Item {
   int start;  // the sequence's first row
   int len;    // and its tokens
   int q0;
-  int unused;
+  int head;  // key head (set by find_item)
 };
 
 struct Shape {
@@ -130,24 +130,46 @@ static __device__ __forceinline__ bool search_item(const Source& src, int idx, I
   return true;
 }
 
-// The CTA's item and key head; false if it has none (the grid is an upper bound), or if the
-// item does not lie in this call's buffers.
-static __device__ __forceinline__ bool find_item(const Source& src, Item& it, int& head) {
-  const int per_group = src.max_items * src.group;
-  const int grp = (int)(blockIdx.x / (unsigned)per_group);
+// Work `rem` of head group `grp` as an item and its key head, by a whole warp; false if there
+// is none (the number of works is an upper bound), or if the item does not lie in this call's
+// buffers.
+static __device__ __forceinline__ bool find_item(const Source& src, int grp, int rem, Item& it) {
   const int in_g = min(src.group, src.kv_heads - grp * src.group);
-  const int rem = (int)blockIdx.x - grp * per_group;
   const int at = rem / in_g;
-  head = grp * src.group + (rem - at * in_g);
   if (src.items == nullptr) {
     if (!search_item(src, at, it)) return false;
   } else {
     if (at >= *src.count) return false;
     it = src.items[at];
   }
+  it.head = grp * src.group + (rem - at * in_g);
   return it.start >= 0 && it.q0 >= 0 && it.len > it.q0 &&
          (long long)it.start + it.len <= src.tokens;
 }
+
+// The items of a persistent CTA, one after the other. The works of a head group are dealt to
+// the CTAs in rounds that run forth and back, so that a list in falling cost gives every CTA
+// about the same sum; a new group begins with a new round.
+struct Walk {
+  int grp = 0, round = 0;
+  // Moves on to the next item (the first call: to the first); false at the end.
+  __device__ __forceinline__ bool next(const Source& src, Item& it) {
+    while (grp * src.group < src.kv_heads) {
+      const long long works = (long long)src.max_items * min(src.group, src.kv_heads - grp * src.group);
+      const unsigned c = (round & 1) ? gridDim.x - 1u - blockIdx.x : blockIdx.x;
+      const long long w = (long long)round * gridDim.x + c;
+      if ((long long)round * gridDim.x >= works) {
+        ++grp;
+        round = 0;
+        continue;
+      }
+      ++round;
+      if (w < works && find_item(src, grp, (int)w, it)) return true;
+    }
+    it.head = -1;
+    return false;
+  }
+};
 #endif
 
 tsp_status make_shape(const char* what, int64_t tokens, int n_seqs, int heads, int kv_heads,

@@ -127,8 +127,12 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
                           const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
   using Geo = KeyGeom<HD>;
   Item it;
-  int head;
-  if (!find_item(p.src, it, head)) return;
+  {
+    const int per_group = p.src.max_items * p.src.group;
+    const int grp = (int)blockIdx.x / per_group;
+    if (!find_item(p.src, grp, (int)blockIdx.x - grp * per_group, it)) return;
+  }
+  const int head = it.head;
   // the tiles start at the first 1024-byte boundary after the small buffers; the check
   // tests that they fit whatever the base's alignment
   extern __shared__ uint8_t smem_raw[];
@@ -576,8 +580,12 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
   using Geo = QueryGeom<HD>;
   constexpr int NS = Geo::KV_STAGES;
   Item it;
-  int head;
-  if (!find_item(p.src, it, head)) return;
+  {
+    const int per_group = p.src.max_items * p.src.group;
+    const int grp = (int)blockIdx.x / per_group;
+    if (!find_item(p.src, grp, (int)blockIdx.x - grp * per_group, it)) return;
+  }
+  const int head = it.head;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));

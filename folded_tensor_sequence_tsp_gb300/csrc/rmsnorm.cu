@@ -282,6 +282,134 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_fwd_kernel(const NormParams p) {
   }
 }
 
+// Longer rows, staged in shared memory: each thread copies its own 16-byte pieces of the
+// rows ahead (cp.async) and later reads only those, so a wait for its own copies is all the
+// ordering that is needed, and STAGES - 1 rows of every CTA are in flight under the
+// arithmetic and the barriers of the current one.
+__device__ __forceinline__ void copy_ahead(void* smem, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem)), "l"(global) : "memory");
+}
+
+template <int RES, bool E4M3, int STAGES, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 4 : 1) rmsnorm_fwd_ring_kernel(const NormParams p) {
+  constexpr int NV = 2;
+  constexpr int SP = RES == RES_NONE ? 0 : RES == RES_F32 ? 2 : 1;  // 16-byte pieces of 8 stream elements
+  constexpr int PIECES = NV * (1 + SP);
+  extern __shared__ uint4 ring[];  // [STAGES][PIECES][threads]
+  __shared__ float part[2][32];
+  __shared__ uint32_t tops[2][32];
+  const int tid = threadIdx.x, lanes = blockDim.x;
+  const float inv_n = 1.f / (float)p.width;
+  auto col = [&](int i) { return (i * lanes + tid) * 8; };
+  auto slot = [&](int stage, int piece) { return ring + (stage * PIECES + piece) * lanes + tid; };
+  auto fetch = [&](long long row, int stage) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (col(i) >= p.width) continue;
+        const long long at = row * p.width + col(i);
+        copy_ahead(slot(stage, i), p.x + at);
+#pragma unroll
+        for (int u = 0; u < SP; ++u)
+          copy_ahead(slot(stage, NV + i * SP + u),
+                     static_cast<const char*>(p.r) + at * (RES == RES_F32 ? 4 : 2) + 16 * u);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) fetch(blockIdx.x + (long long)s * gridDim.x, s);
+  uint4 w[NV];  // bf16: unpacked where it is used
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    w[i] = col(i) < p.width ? *reinterpret_cast<const uint4*>(p.w + col(i)) : make_uint4(0u, 0u, 0u, 0u);
+  int odd = 0, stage = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, odd ^= 1) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+    float v[NV][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (col(i) < p.width) {
+        load_bf16<8>(reinterpret_cast<const __nv_bfloat16*>(slot(stage, i)), v[i]);
+        if constexpr (RES != RES_NONE) {
+          float r[8];
+          if constexpr (RES == RES_F32) {
+            const float4 a = *reinterpret_cast<const float4*>(slot(stage, NV + i * SP));
+            const float4 b = *reinterpret_cast<const float4*>(slot(stage, NV + i * SP + 1));
+            r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w;
+            r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
+          } else {
+            load_bf16<8>(reinterpret_cast<const __nv_bfloat16*>(slot(stage, NV + i * SP)), r);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][e] += r[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+    }
+    // this stage is read; the one before it takes the row furthest ahead
+    fetch(row + (long long)(STAGES - 1) * gridDim.x, stage == 0 ? STAGES - 1 : stage - 1);
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    const float rstd = 1.f / sqrtf(row_sum<false>(ss, part[odd]) * inv_n + p.eps);
+    if constexpr (RES != RES_NONE) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (col(i) < p.width) store_stream<8, RES>(p.h, row * p.width + col(i), v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[i][2 * e] *= rstd * bf16_lo(u[e]);
+        v[i][2 * e + 1] *= rstd * bf16_hi(u[e]);
+      }
+    }
+    if constexpr (!E4M3) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (col(i) < p.width)
+          store_bf16<8>(static_cast<__nv_bfloat16*>(p.y) + row * p.width + col(i), v[i]);
+    } else {
+      uint8_t* y8 = static_cast<uint8_t*>(p.y) + row * p.width;
+      uint32_t top[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        top[i] = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top[i] = max(top[i], __float_as_uint(fabsf(v[i][e])));
+      }
+      if (p.group == 0) {
+        const uint32_t t = row_max<false>(max(top[0], top[1]), tops[odd]);
+        top[0] = top[1] = t;
+        if (tid == 0) p.scales[row] = e4m3_scale(t);
+      } else {
+        // 16 consecutive threads hold 128 consecutive columns
+        const int groups = (p.width + 127) / 128;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+          for (int o = 8; o; o >>= 1) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+          if (col(i) < p.width && (tid & 15) == 0) p.scales[row * groups + col(i) / 128] = e4m3_scale(top[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const float inv = 1.f / e4m3_scale(top[i]);
+        if (col(i) < p.width)
+          *reinterpret_cast<uint2*>(y8 + col(i)) =
+              make_uint2(to_e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv),
+                         to_e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv));
+      }
+    }
+  }
+}
+
 struct NormBwdParams {
   const void* h;
   const __nv_bfloat16* w;
@@ -374,16 +502,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormBwdParams p
     if (col(i) < p.width) store_f32<VEC>(p.partial + (long long)blockIdx.x * p.width + col(i), dw[i]);
 }
 
-// The same with the rows staged in shared memory: each thread copies its own 16-byte pieces
-// of the rows ahead (cp.async) and later reads only those, so a wait for its own copies is
-// all the ordering that is needed, and STAGES - 1 rows of every CTA are in flight under the
-// arithmetic and the barrier of the current one.
-template <int BYTES>
-__device__ __forceinline__ void copy_ahead(void* smem, const void* global) {
-  static_assert(BYTES == 16, "one 16-byte piece");
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem)), "l"(global) : "memory");
-}
-
+// The same with the rows staged in shared memory, as in the forward's ring kernel.
 template <int NV, int RES, int STAGES, int MAXT>
 __global__ void __launch_bounds__(MAXT) rmsnorm_bwd_ring_kernel(const NormBwdParams p) {
   constexpr int SP = RES == RES_F32 ? 2 : 1;  // 16-byte pieces of 8 stream elements
@@ -406,10 +525,10 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_bwd_ring_kernel(const NormBwdPar
         const char* d = static_cast<const char*>(p.dh) + at * es;
 #pragma unroll
         for (int u = 0; u < SP; ++u) {
-          copy_ahead<16>(slot(stage, i * SP + u), h + 16 * u);
-          if (has_dh) copy_ahead<16>(slot(stage, NV * (SP + 1) + i * SP + u), d + 16 * u);
+          copy_ahead(slot(stage, i * SP + u), h + 16 * u);
+          if (has_dh) copy_ahead(slot(stage, NV * (SP + 1) + i * SP + u), d + 16 * u);
         }
-        copy_ahead<16>(slot(stage, NV * SP + i), p.dy + at);
+        copy_ahead(slot(stage, NV * SP + i), p.dy + at);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -530,45 +649,59 @@ int row_threads(int items, int nv) { return ((items + nv - 1) / nv + 31) / 32 * 
 
 template <int VEC, int NV, bool WARP, int RES, bool E4M3>
 void launch_fwd_variant(const NormParams& p, cudaStream_t s) {
+  constexpr int MAXT = WARP ? 128 : 1024;
   const int threads = WARP ? 128 : row_threads((p.width + VEC - 1) / VEC, NV);
   const long long blocks = WARP ? (p.rows + 3) / 4 : p.rows;
   // resident CTAs: 2048 threads per SM
   const long long cap = (long long)sm_count() * std::max(1, 2048 / threads);
-  const unsigned grid = (unsigned)std::min(blocks, cap);
-  if constexpr (WARP) {
-    rmsnorm_fwd_kernel<VEC, NV, true, RES, E4M3, 128><<<grid, threads, 0, s>>>(p);
-  } else {
-    if (threads <= 256) rmsnorm_fwd_kernel<VEC, NV, false, RES, E4M3, 256><<<grid, threads, 0, s>>>(p);
-    else rmsnorm_fwd_kernel<VEC, NV, false, RES, E4M3, 1024><<<grid, threads, 0, s>>>(p);
-  }
+  rmsnorm_fwd_kernel<VEC, NV, WARP, RES, E4M3, MAXT>
+      <<<(unsigned)std::min(blocks, cap), threads, 0, s>>>(p);
+}
+
+template <int RES, bool E4M3, int STAGES, int MAXT>
+tsp_status launch_fwd_ring(const NormParams& p, int threads, cudaStream_t s) {
+  auto kernel = rmsnorm_fwd_ring_kernel<RES, E4M3, STAGES, MAXT>;
+  const size_t smem = (size_t)STAGES * 2 * (1 + (RES == RES_NONE ? 0 : RES == RES_F32 ? 2 : 1)) * 16 * threads;
+  TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem,
+                            "rmsnorm: cudaFuncSetAttribute"));
+  // resident CTAs: by registers (four of 256 threads, one of 1024) and by shared memory
+  const long long per_sm = std::min<long long>(std::max(1, 1024 / threads), (220 * 1024) / (long long)smem);
+  const long long cap = (long long)sm_count() * std::max<long long>(1, per_sm);
+  kernel<<<(unsigned)std::min<long long>(p.rows, cap), threads, smem, s>>>(p);
+  return TSP_OK;
 }
 
 template <int RES, bool E4M3>
-void launch_fwd_res(const NormParams& p, bool vec, cudaStream_t s) {
+tsp_status launch_fwd_res(const NormParams& p, bool vec, cudaStream_t s) {
   if (vec) {
     const int vecs = p.width / 8;
+    const int threads = row_threads(vecs, 2);
     if (vecs <= 32) launch_fwd_variant<8, 1, true, RES, E4M3>(p, s);
     else if (vecs <= 64) launch_fwd_variant<8, 2, true, RES, E4M3>(p, s);
     else if (vecs <= 128) launch_fwd_variant<8, 4, true, RES, E4M3>(p, s);
-    else if (vecs <= 2048) launch_fwd_variant<8, 2, false, RES, E4M3>(p, s);
+    else if (threads <= 256) return launch_fwd_ring<RES, E4M3, 3, 256>(p, threads, s);
+    else if (threads <= 1024) return launch_fwd_ring<RES, E4M3, 2, 1024>(p, threads, s);
     else launch_fwd_variant<8, 4, false, RES, E4M3>(p, s);
   } else {
     if (p.width <= 4096) launch_fwd_variant<1, 8, false, RES, E4M3>(p, s);
     else launch_fwd_variant<1, 32, false, RES, E4M3>(p, s);
   }
+  return TSP_OK;
 }
 
 tsp_status launch_fwd(const NormParams& p, int res, bool e4m3, bool vec, cudaStream_t s) {
   if (p.rows == 0) return TSP_OK;
+  tsp_status st;
   if (e4m3) {
-    if (res == RES_NONE) launch_fwd_res<RES_NONE, true>(p, vec, s);
-    else if (res == RES_BF16) launch_fwd_res<RES_BF16, true>(p, vec, s);
-    else launch_fwd_res<RES_F32, true>(p, vec, s);
+    st = res == RES_NONE ? launch_fwd_res<RES_NONE, true>(p, vec, s)
+         : res == RES_BF16 ? launch_fwd_res<RES_BF16, true>(p, vec, s)
+                           : launch_fwd_res<RES_F32, true>(p, vec, s);
   } else {
-    if (res == RES_NONE) launch_fwd_res<RES_NONE, false>(p, vec, s);
-    else if (res == RES_BF16) launch_fwd_res<RES_BF16, false>(p, vec, s);
-    else launch_fwd_res<RES_F32, false>(p, vec, s);
+    st = res == RES_NONE ? launch_fwd_res<RES_NONE, false>(p, vec, s)
+         : res == RES_BF16 ? launch_fwd_res<RES_BF16, false>(p, vec, s)
+                           : launch_fwd_res<RES_F32, false>(p, vec, s);
   }
+  if (st != TSP_OK) return st;
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? TSP_OK : cuda_fail(e, "rmsnorm: launch");
 }

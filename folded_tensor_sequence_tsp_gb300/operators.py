@@ -118,13 +118,12 @@ class TSPRMSNorm:
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
 
     def _rows(self, t):
+        """t as a [rows, width] matrix (None stays None)."""
+        if t is None or (t.dim() == 2 and t.shape[1] == self.width):
+            return t
         if t.dim() < 1 or t.shape[-1] != self.width:
             raise ValueError(f"expected rows of {self.width}, got shape {tuple(t.shape)}")
-        return t.reshape(-1, self.width) if t.dim() != 2 else t
-
-    @staticmethod
-    def _view(t, width):
-        return None if t is None else t.view(-1, width)
+        return t.view(-1, self.width)
 
     def forward(self, x, weight, residual=None, y=None, h=None, stream=None):
         """(y, h): h = x + residual (None without a residual), y = norm(h) * weight in bf16."""
@@ -133,8 +132,8 @@ class TSPRMSNorm:
                 y = torch.empty_like(x)
             if residual is not None and h is None:
                 h = torch.empty_like(residual)
-        v = lambda t: self._view(t, self.width)  # noqa: E731
-        tsp_rmsnorm_fwd(self._rows(x), weight, v(y), v(residual), v(h), self.eps, stream)
+        v = self._rows
+        tsp_rmsnorm_fwd(v(x), weight, v(y), v(residual), v(h), self.eps, stream)
         return y, h
 
     def forward_e4m3(self, x, weight, residual=None, group=128, y=None, scales=None, h=None,
@@ -150,8 +149,8 @@ class TSPRMSNorm:
                                      dtype=torch.float32, device=x.device)
             if residual is not None and h is None:
                 h = torch.empty_like(residual)
-        v = lambda t: self._view(t, self.width)  # noqa: E731
-        tsp_rmsnorm_fwd_e4m3(self._rows(x), weight, v(y), scales, v(residual), v(h), self.eps, group,
+        v = self._rows
+        tsp_rmsnorm_fwd_e4m3(v(x), weight, v(y), scales, v(residual), v(h), self.eps, group,
                              stream)
         return y, scales, h
 
@@ -165,8 +164,8 @@ class TSPRMSNorm:
                 dx = torch.empty_like(h)
             if dw is None:
                 dw = torch.empty(self.width, dtype=torch.float32, device=h.device)
-        v = lambda t: self._view(t, self.width)  # noqa: E731
-        tsp_rmsnorm_bwd(self._rows(h), weight, v(dy), v(dx), dw, self.ws, v(dh), v(dx16), self.eps,
+        v = self._rows
+        tsp_rmsnorm_bwd(v(h), weight, v(dy), v(dx), dw, self.ws, v(dh), v(dx16), self.eps,
                         stream)
         return dx, dw
 
