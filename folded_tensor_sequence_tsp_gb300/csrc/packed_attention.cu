@@ -315,14 +315,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       ++n_items;
     }
-    // copies in flight land before the CTA ends: the last use of each barrier that was armed
-    // (after a wait that gave up, of every one that may have been; those waits are bounded)
     if (lane == 0) {
+      walk.end(p.src);
+      // copies in flight land before the CTA ends: the last use of each barrier that was armed
+      // (after a wait that gave up, a millisecond for what its item may have left)
       if (n_items > 0) mbar_wait(q_full, (n_items - 1) & 1u, wd, SITE_DRAIN);
       for (uint32_t b = c > STAGES ? c - STAGES : 0; b < c; ++b)
         mbar_wait(&kv_full[b % STAGES], (b / STAGES) & 1u, wd, SITE_DRAIN);
       if (!ok) {
-        const unsigned long long t0 = global_ns();  // what a stopped item may still have in flight
+        const unsigned long long t0 = global_ns();
         while (global_ns() - t0 < 1000000ull) {
         }
       }
@@ -533,24 +534,20 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int qh = it.head * p.G + (r_local - tok * p.G);
       const float inv = 1.f / l;
       if (p.lse != nullptr && row_ok) p.lse[(long long)qh * p.ld_lse + row] = m_ref + log2f(l);
-      __nv_bfloat16* dst = p.o + row * p.ld_o + (long long)qh * HD;
+      __nv_bfloat16* dst[4];
+      group_rows(row_ok ? p.o + row * p.ld_o + (long long)qh * HD : nullptr, dst);
 #pragma unroll
       for (int e0 = 0; e0 < HD; e0 += 32) {
-        uint32_t r[32];
+        uint32_t r[32], w[16];
         tmem_ld32(o_tmem + e0, r);
         tmem_ld_wait();
-        if (row_ok) {
-          uint4* d4 = reinterpret_cast<uint4*>(dst + e0);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint4 w;
-            w.x = pack_bf16x2(__uint_as_float(r[8 * v + 0]) * inv, __uint_as_float(r[8 * v + 1]) * inv);
-            w.y = pack_bf16x2(__uint_as_float(r[8 * v + 2]) * inv, __uint_as_float(r[8 * v + 3]) * inv);
-            w.z = pack_bf16x2(__uint_as_float(r[8 * v + 4]) * inv, __uint_as_float(r[8 * v + 5]) * inv);
-            w.w = pack_bf16x2(__uint_as_float(r[8 * v + 6]) * inv, __uint_as_float(r[8 * v + 7]) * inv);
-            d4[v] = w;
-          }
-        }
+        for (int e = 0; e < 16; ++e)
+          w[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * inv, __uint_as_float(r[2 * e + 1]) * inv);
+        store_rows(w, dst);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (dst[k] != nullptr) dst[k] += 32;
       }
       tc_fence_before();
     }
@@ -630,7 +627,7 @@ Workspace make_workspace(const Shape& s) {
 }
 
 Source make_source(const Shape& s, const int32_t* starts, int tile, bool from_end, int group,
-                   const Item* items, const int* count, int max_items, DevStatus* status) {
+                   const Item* items, const int* count, int max_items, void* ws, int counter) {
   Source src{};
   if (s.n_seqs > SEARCH_SEQS) {
     src.items = items;
@@ -644,7 +641,8 @@ Source make_source(const Shape& s, const int32_t* starts, int tile, bool from_en
   src.kv_heads = s.kv_heads;
   src.group = group;
   src.tokens = s.tokens;
-  src.status = status;
+  src.next = at<unsigned>(ws, COUNTERS) + 2 * counter;
+  src.status = status_of(ws);
   return src;
 }
 
@@ -734,7 +732,7 @@ tsp_status tsp_packed_attention_fwd(int64_t tokens, int n_seqs, const int32_t* s
   p.ld_lse = ld_lse;
   // 72 MB of K and V in L2 at a time, as for the plan's attention
   p.src = make_source(s, starts, 2 * s.TPT, false, head_group(s, 72ll << 20), at<Item>(ws, w.items),
-                      at<int>(ws, w.counts), (int)w.max_fwd, status_of(ws));
+                      at<int>(ws, w.counts), (int)w.max_fwd, ws, 0);
   p.G = s.G;
   p.TPT = s.TPT;
   p.RU = s.RU;

@@ -10,6 +10,7 @@ namespace packed {
 
 constexpr int TILE = 128;                  // rows of a tensor-core tile, and keys per key tile
 constexpr uint32_t BOX_BYTES = 128 * 128;  // 128 rows x 64 bf16 in shared memory
+constexpr size_t COUNTERS = 128;           // byte offset in the workspace's first 256 bytes
 
 // One CTA's share of a sequence: the tile (or pair of tiles) that begins at token q0.
 struct Item {
@@ -30,6 +31,7 @@ struct Shape {
 
 // Workspace (byte offsets from its 256-byte aligned start).
 struct Workspace {
+  // the first 256 bytes: the status word, and from COUNTERS on two words per kernel for Walk
   size_t counts;  // int[2]: items in each list
   size_t items;   // forward, or query side of the backward
   size_t key_items;
@@ -65,6 +67,8 @@ struct Source {
   int kv_heads;
   int group;     // key heads whose CTAs interleave
   long long tokens;
+  unsigned* next;  // [2] in the workspace: works handed out beyond the first of each CTA, and
+                   // CTAs that are done; both 0 before and after a launch
   DevStatus* status;
 };
 
@@ -147,29 +151,74 @@ static __device__ __forceinline__ bool find_item(const Source& src, int grp, int
          (long long)it.start + it.len <= src.tokens;
 }
 
-// The items of a persistent CTA, one after the other. The works of a head group are dealt to
-// the CTAs in rounds that run forth and back, so that a list in falling cost gives every CTA
-// about the same sum; a new group begins with a new round.
+// The items of a persistent CTA, one after the other, by a whole warp. The first work is the
+// CTA's own number; the others are drawn from a counter, so the CTAs that finish early take
+// what is left. The list falls in cost, hence what is left last is short.
 struct Walk {
-  int grp = 0, round = 0;
-  // Moves on to the next item (the first call: to the first); false at the end.
-  __device__ __forceinline__ bool next(const Source& src, Item& it) {
-    while (grp * src.group < src.kv_heads) {
-      const long long works = (long long)src.max_items * min(src.group, src.kv_heads - grp * src.group);
-      const unsigned c = (round & 1) ? gridDim.x - 1u - blockIdx.x : blockIdx.x;
-      const long long w = (long long)round * gridDim.x + c;
-      if ((long long)round * gridDim.x >= works) {
-        ++grp;
-        round = 0;
-        continue;
+  bool begun = false;
+  // Moves on to the next item (the first call: to the first); head -1 at the end.
+  __device__ __forceinline__ void next(const Source& src, Item& it) {
+    const long long works = (long long)src.max_items * src.kv_heads;
+    const int per_group = src.max_items * src.group;
+    while (true) {
+      unsigned w = blockIdx.x;
+      if (begun) {
+        if ((threadIdx.x & 31) == 0) w = gridDim.x + atomicAdd(src.next, 1u);
+        w = __shfl_sync(0xffffffffu, w, 0);
       }
-      ++round;
-      if (w < works && find_item(src, grp, (int)w, it)) return true;
+      begun = true;
+      if (w >= works) break;
+      const int grp = (int)(w / (unsigned)per_group);
+      if (find_item(src, grp, (int)w - grp * per_group, it)) return;
     }
     it.head = -1;
-    return false;
+  }
+  // Once per CTA, after its last next(), by one thread: the last CTA leaves the counters at 0.
+  __device__ __forceinline__ void end(const Source& src) {
+    __threadfence();
+    if (atomicAdd(src.next + 1, 1u) == gridDim.x - 1u) {
+      src.next[0] = 0u;
+      src.next[1] = 0u;
+    }
   }
 };
+
+// Stores one accumulator row per lane (32 columns as 16 packed bf16 pairs), 16 bytes at a
+// time. Lane by lane that would touch 32 lines per instruction; a 4 x 4 exchange of 16-byte
+// chunks inside groups of four lanes first lets four lanes write 64 contiguous bytes of one
+// row. `dst[k]` is the first of the 32 columns of row k of the lane's group of four, or
+// nullptr where that row is not written.
+static __device__ __forceinline__ void store_rows(uint32_t (&v)[16], __nv_bfloat16* const (&dst)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int bit = 0; bit < 2; ++bit) {
+    const bool up = (lane >> bit) & 1;
+#pragma unroll
+    for (int pair = 0; pair < 2; ++pair) {
+      // chunks (0,1), (2,3) with the neighbour; then (0,2), (1,3) with the next but one
+      const int lo = bit == 0 ? 2 * pair : pair, hi = lo + (1 << bit);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t give = up ? v[4 * lo + e] : v[4 * hi + e];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1 << bit);
+        if (up) v[4 * lo + e] = got;
+        else v[4 * hi + e] = got;
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (dst[k] != nullptr)
+      reinterpret_cast<uint4*>(dst[k])[lane & 3] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+}
+
+// The row pointers of the lane's group of four, from each lane's own (nullptr: not written).
+static __device__ __forceinline__ void group_rows(__nv_bfloat16* mine, __nv_bfloat16* (&dst)[4]) {
+  const unsigned long long m = reinterpret_cast<unsigned long long>(mine);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    dst[k] = reinterpret_cast<__nv_bfloat16*>(__shfl_sync(0xffffffffu, m, ((threadIdx.x & 31) & ~3) + k));
+}
 #endif
 
 tsp_status make_shape(const char* what, int64_t tokens, int n_seqs, int heads, int kv_heads,
@@ -179,7 +228,7 @@ Workspace make_workspace(const Shape& s);
 tsp_status launch_lists(const Shape& s, const int32_t* starts, const ListArgs& a, const ListArgs& b,
                         DevStatus* status, cudaStream_t stream);
 Source make_source(const Shape& s, const int32_t* starts, int tile, bool from_end, int group,
-                   const Item* items, const int* count, int max_items, DevStatus* status);
+                   const Item* items, const int* count, int max_items, void* ws, int counter);
 int list_shift(long long max_cost);
 // Query heads grouped by key head: box of 64 columns x G heads x TPT tokens.
 tsp_status make_query_map(CUtensorMap* map, const Shape& s, const void* base, int64_t ld);

@@ -54,10 +54,8 @@ struct BwdParams {
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
   long long ld_dq, ld_dk, ld_dv;
-  const __nv_bfloat16* q;
   const __nv_bfloat16* o;
-  const __nv_bfloat16* dout;
-  long long ld_q, ld_o, ld_do;
+  long long ld_o;
   const float* lse;
   long long ld_lse;
   float* delta;
@@ -69,16 +67,19 @@ struct BwdParams {
   unsigned long long limit_ns;
 };
 
+constexpr int ITEMS = 4;  // items between the producer and the slowest reader
+
 template <int HD>
 struct KeyGeom {
   static constexpr int THREADS = 352;  // TMA, MMA, 2 x 4 element-wise warps, statistics
+  static constexpr int READERS = 10;   // of an item: MMA lane, statistics, 8 warps
   static constexpr int BOXES = HD / 64;
   static constexpr uint32_t TILE_B = 128 * HD * 2;
   // Q tiles (with lse) and dO tiles (with Delta) in separate rings: a Q tile is read last
   // by dK, a full tile after its scores, so it gets the deeper ring
   static constexpr int QS = 3;
   static constexpr int OS = 2;
-  static constexpr uint32_t SMALL = (QS + OS) * 512 + 256;
+  static constexpr uint32_t SMALL = (QS + OS) * 512 + ITEMS * 16 + 384;
   static constexpr uint32_t TILES_OFF = (SMALL + 1023) / 1024 * 1024;
   static constexpr size_t USED = TILES_OFF + (size_t)(2 + QS + OS) * TILE_B;
   static constexpr size_t SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
@@ -88,15 +89,35 @@ static_assert(KeyGeom<128>::USED <= 227 * 1024, "key-side shared memory");
 template <int HD>
 struct QueryGeom {
   static constexpr int THREADS = 320;
+  static constexpr int READERS = 9;  // of an item: MMA lane, 8 warps
   static constexpr int BOXES = HD / 64;
   static constexpr uint32_t TILE_B = 128 * HD * 2;
-  static constexpr int KV_STAGES = 3;
-  static constexpr uint32_t STAGE = 2 * TILE_B;  // K, V
-  static constexpr size_t USED = 1024 + KV_STAGES * (size_t)STAGE + 1280;
+  // a V tile is read last by dP, a K tile by dQ, which comes a phase later
+  static constexpr int KS = 3;
+  static constexpr int VS = 2;
+  static constexpr uint32_t SMALL = 1024 + ITEMS * 16 + 384;  // Delta, items, barriers
+  static constexpr uint32_t TILES_OFF = (SMALL + 1023) / 1024 * 1024;
+  static constexpr size_t USED = TILES_OFF + (size_t)(2 + KS + VS) * TILE_B;  // Q, dO, K, V
   static constexpr size_t SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
   static constexpr uint32_t TM_Q = HD;
   static constexpr uint32_t TM_DO = HD + HD / 2;
 };
+static_assert(QueryGeom<128>::USED <= 227 * 1024, "query-side shared memory");
+
+// Offset of the tiles behind `small` bytes of a shared-memory base of any alignment; 0 if the
+// allocation, made for `most`, has no room for them.
+__device__ __forceinline__ uint32_t tiles_offset(const uint8_t* base, uint32_t small, uint32_t most) {
+  const uint32_t at = smem_addr(base);
+  const uint32_t off = ((at + small + 1023u) & ~1023u) - at;
+  return off > most ? 0u : off;
+}
+
+// A millisecond, for copies that a wait which gave up may have left in flight.
+__device__ __forceinline__ void let_copies_land() {
+  const unsigned long long t0 = global_ns();
+  while (global_ns() - t0 < 1000000ull) {
+  }
+}
 
 // K-major operand offset (>> 4) of the kk-th 16-wide K step of a [rows][HD] tile stored as
 // 64-column boxes.
@@ -126,60 +147,56 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
                           const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
   using Geo = KeyGeom<HD>;
-  Item it;
-  {
-    const int per_group = p.src.max_items * p.src.group;
-    const int grp = (int)blockIdx.x / per_group;
-    if (!find_item(p.src, grp, (int)blockIdx.x - grp * per_group, it)) return;
-  }
-  const int head = it.head;
-  // the tiles start at the first 1024-byte boundary after the small buffers; the check
-  // tests that they fit whatever the base's alignment
+  constexpr uint32_t QS = Geo::QS, OS = Geo::OS;
   extern __shared__ uint8_t smem_raw[];
   float* sLse = reinterpret_cast<float*>(smem_raw);  // [QS][128]
-  float* sDel = sLse + Geo::QS * 128;                // [OS][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sDel + Geo::OS * 128);
-  uint64_t* kv_full = bars;                // [1]
-  uint64_t* q_full = kv_full + 1;          // [QS] Q tile (TMA) and its lse (statistics warp)
-  uint64_t* q_empty = q_full + Geo::QS;    // [QS]
-  uint64_t* o_full = q_empty + Geo::QS;    // [OS] dO tile and its Delta
-  uint64_t* o_empty = o_full + Geo::OS;    // [OS]
-  uint64_t* s_full = o_empty + Geo::OS;    // scores of the current tile written
-  uint64_t* g_full = s_full + 1;           // dP^T of the current tile written
-  uint64_t* p_ready = g_full + 1;          // packed P^T stored (8 warps)
-  uint64_t* g_taken = p_ready + 1;         // dP^T loaded into registers (8 warps)
-  uint64_t* ds_ready = g_taken + 1;        // packed dS^T stored (8 warps)
-  uint64_t* acc_done = ds_ready + 1;
-  uint64_t* tail_q = acc_done + 1;         // the last Q tile is cleared behind the sequence
-  uint64_t* tail_o = tail_q + 1;           // and the last dO tile
-  uint64_t* drain = tail_o + 1;
+  float* sDel = sLse + QS * 128;                     // [OS][128]
+  Item* items = reinterpret_cast<Item*>(sDel + OS * 128);           // [ITEMS]
+  uint64_t* item_full = reinterpret_cast<uint64_t*>(items + ITEMS); // [ITEMS]
+  uint64_t* item_empty = item_full + ITEMS;  // [ITEMS]
+  uint64_t* kv_full = item_empty + ITEMS;    // the item's K and V
+  uint64_t* kv_empty = kv_full + 1;          // its S^T and dP^T are all computed
+  uint64_t* q_full = kv_empty + 1;           // [QS] Q tile landed
+  uint64_t* q_ready = q_full + QS;           // [QS] and its lse stored, its end cleared
+  uint64_t* q_empty = q_ready + QS;          // [QS]
+  uint64_t* o_full = q_empty + QS;           // [OS] dO tile landed
+  uint64_t* o_ready = o_full + OS;           // [OS] and its Delta stored, its end cleared
+  uint64_t* o_empty = o_ready + OS;          // [OS]
+  uint64_t* s_full = o_empty + OS;           // scores of the current tile written
+  uint64_t* g_full = s_full + 1;             // dP^T of the current tile written
+  uint64_t* p_ready = g_full + 1;            // packed P^T stored (8 warps)
+  uint64_t* g_taken = p_ready + 1;           // dP^T loaded into registers (8 warps)
+  uint64_t* ds_ready = g_taken + 1;          // packed dS^T stored (8 warps)
+  uint64_t* acc_done = ds_ready + 1;         // the item's dK and dV complete
+  uint64_t* drain = acc_done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const uint32_t base = smem_addr(smem_raw);
-  const uint32_t tiles_off = ((base + Geo::SMALL + 1023u) & ~1023u) - base;
-  if (tiles_off > Geo::TILES_OFF) {  // uniform
+  const uint32_t tiles_off = tiles_offset(smem_raw, Geo::SMALL, Geo::TILES_OFF);
+  if (tiles_off == 0) {  // uniform
     if (threadIdx.x == 0) record_error(p.status, kStatusUnsupported, SITE_SMEM_LAYOUT);
     return;
   }
   uint8_t* sK = smem_raw + tiles_off;
   uint8_t* sV = sK + Geo::TILE_B;
-  uint8_t* sQ0 = sV + Geo::TILE_B;               // [QS]
-  uint8_t* sO0 = sQ0 + Geo::QS * Geo::TILE_B;    // [OS]
+  uint8_t* sQ0 = sV + Geo::TILE_B;        // [QS]
+  uint8_t* sO0 = sQ0 + QS * Geo::TILE_B;  // [OS]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int k0 = it.q0;              // first key
-  const int first = k0 / p.TPT;      // the first query tile that sees a key
-  const int n_inner = (it.len - 1) / p.TPT + 1 - first;
-  const bool ragged = (first + n_inner) * p.TPT > it.len;
-
   if (threadIdx.x == 0) {
+    for (int s = 0; s < ITEMS; ++s) {
+      mbar_init(&item_full[s], 1);
+      mbar_init(&item_empty[s], Geo::READERS);
+    }
     mbar_init(kv_full, 1);
-    for (int s = 0; s < Geo::QS; ++s) {
-      mbar_init(&q_full[s], 2);
+    mbar_init(kv_empty, 1);
+    for (uint32_t s = 0; s < QS; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_ready[s], 1);
       mbar_init(&q_empty[s], 1);
     }
-    for (int s = 0; s < Geo::OS; ++s) {
-      mbar_init(&o_full[s], 2);
+    for (uint32_t s = 0; s < OS; ++s) {
+      mbar_init(&o_full[s], 1);
+      mbar_init(&o_ready[s], 1);
       mbar_init(&o_empty[s], 1);
     }
     mbar_init(s_full, 1);
@@ -188,26 +205,24 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
     mbar_init(g_taken, 8);
     mbar_init(ds_ready, 8);
     mbar_init(acc_done, 1);
-    mbar_init(tail_q, 1);
-    mbar_init(tail_o, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    // K and V are under way while the CTA sets itself up
-    mbar_arrive_expect_tx(kv_full, 2 * Geo::TILE_B);
-#pragma unroll
-    for (int b = 0; b < Geo::BOXES; ++b) {
-      tma_load_2d(sK + b * BOX_BYTES, &tmK, kv_full, head * HD + 64 * b, it.start + k0);
-      tma_load_2d(sV + b * BOX_BYTES, &tmV, kv_full, head * HD + 64 * b, it.start + k0);
-    }
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmDO);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
+  Item next{};
+  Walk walk;
+  if (warp == 0) walk.next(p.src, next);
   if (p.RU < 128) {
     // rows that no TMA box writes: zeros for the whole run
-    for (int s = 0; s < Geo::QS + Geo::OS; ++s)
+    for (uint32_t s = 0; s < QS + OS; ++s)
       clear_rows(sQ0 + s * Geo::TILE_B, Geo::BOXES, p.RU, threadIdx.x, Geo::THREADS);
     fence_proxy_async();
   }
@@ -216,98 +231,132 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   WaitBound wb{p.status, p.limit_ns, abort_flag};
-  const uint32_t box_rows = (uint32_t)(Geo::BOXES * 128) * (uint32_t)p.RU;
+  // streamed query tiles of an item: from the first that sees one of its keys
+  auto first_of = [&](const Item& it) { return it.q0 / p.TPT; };
+  auto inner_of = [&](const Item& it) { return (it.len - 1) / p.TPT + 1 - it.q0 / p.TPT; };
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ producer
-      int q_last[Geo::QS], o_last[Geo::OS];
-      for (int s = 0; s < Geo::QS; ++s) q_last[s] = -1;
-      for (int s = 0; s < Geo::OS; ++s) o_last[s] = -1;
-      bool ok = true;
-      for (int idx = 0; idx < n_inner; ++idx) {
-        const int r0 = it.start + (first + idx) * p.TPT;
-        const int qs = idx % Geo::QS, os = idx % Geo::OS;
-        const uint32_t qph = (uint32_t)((idx / Geo::QS) & 1), oph = (uint32_t)((idx / Geo::OS) & 1);
-        ok = mbar_wait(&q_empty[qs], qph ^ 1u, wb, SITE_PACKED_PRODUCER);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&q_full[qs], box_rows);
+    // -------------------------------------------------------------- producer
+    const uint32_t box_rows = (uint32_t)(Geo::BOXES * 128) * (uint32_t)p.RU;
+    bool ok = true;
+    uint32_t n_items = 0, c = 0;  // items and streamed tiles so far
+    while (ok) {
+      const Item it = next;
+      const int slot = (int)(n_items % ITEMS);
+      if (lane == 0) {
+        ok = mbar_wait(&item_empty[slot], ((n_items / ITEMS) & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+        if (ok) {
+          items[slot] = it;
+          mbar_arrive(&item_full[slot]);
+        }
+        if (ok && it.head >= 0) {
+          ok = mbar_wait(kv_empty, (n_items & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+          if (ok) {
+            mbar_arrive_expect_tx(kv_full, 2 * Geo::TILE_B);
 #pragma unroll
-        for (int b = 0; b < Geo::BOXES; ++b)
-          tma_load_3d(sQ0 + qs * Geo::TILE_B + b * BOX_BYTES, &tmQ, &q_full[qs], 64 * b, head * p.G, r0);
-        q_last[qs] = (int)qph;
-        ok = mbar_wait(&o_empty[os], oph ^ 1u, wb, SITE_PACKED_PRODUCER);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&o_full[os], box_rows);
+            for (int b = 0; b < Geo::BOXES; ++b) {
+              tma_load_2d(sK + b * BOX_BYTES, &tmK, kv_full, it.head * HD + 64 * b, it.start + it.q0);
+              tma_load_2d(sV + b * BOX_BYTES, &tmV, kv_full, it.head * HD + 64 * b, it.start + it.q0);
+            }
+          }
+          const int n = inner_of(it);
+          int r0 = it.start + first_of(it) * p.TPT;
+          for (int j = 0; ok && j < n; ++j, ++c, r0 += p.TPT) {
+            const uint32_t qs = c % QS, os = c % OS;
+            ok = mbar_wait(&q_empty[qs], ((c / QS) & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&q_full[qs], box_rows);
 #pragma unroll
-        for (int b = 0; b < Geo::BOXES; ++b)
-          tma_load_3d(sO0 + os * Geo::TILE_B + b * BOX_BYTES, &tmDO, &o_full[os], 64 * b, head * p.G, r0);
-        o_last[os] = (int)oph;
+            for (int b = 0; b < Geo::BOXES; ++b)
+              tma_load_3d(sQ0 + qs * Geo::TILE_B + b * BOX_BYTES, &tmQ, &q_full[qs], 64 * b,
+                          it.head * p.G, r0);
+            ok = mbar_wait(&o_empty[os], ((c / OS) & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&o_full[os], box_rows);
+#pragma unroll
+            for (int b = 0; b < Geo::BOXES; ++b)
+              tma_load_3d(sO0 + os * Geo::TILE_B + b * BOX_BYTES, &tmDO, &o_full[os], 64 * b,
+                          it.head * p.G, r0);
+          }
+        }
       }
-      // copies in flight land before the CTA ends. After a wait that gave up, the
-      // statistics warp may have left a phase without its arrival: these waits then end
-      // at their bound.
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok || it.head < 0) break;
+      ++n_items;
+      walk.next(p.src, next);
+    }
+    if (lane == 0) {
+      walk.end(p.src);
+      // copies in flight land before the CTA ends
       WaitBound wd{p.status, p.limit_ns, nullptr};
-      mbar_wait(kv_full, 0, wd, SITE_DRAIN);
-      for (int s = 0; s < Geo::QS; ++s)
-        if (q_last[s] >= 0) mbar_wait(&q_full[s], (uint32_t)q_last[s], wd, SITE_DRAIN);
-      for (int s = 0; s < Geo::OS; ++s)
-        if (o_last[s] >= 0) mbar_wait(&o_full[s], (uint32_t)o_last[s], wd, SITE_DRAIN);
+      if (n_items > 0) mbar_wait(kv_full, (n_items - 1) & 1u, wd, SITE_DRAIN);
+      for (uint32_t b = c > QS ? c - QS : 0; b < c; ++b)
+        mbar_wait(&q_full[b % QS], (b / QS) & 1u, wd, SITE_DRAIN);
+      for (uint32_t b = c > OS ? c - OS : 0; b < c; ++b)
+        mbar_wait(&o_full[b % OS], (b / OS) & 1u, wd, SITE_DRAIN);
+      if (!ok) let_copies_land();
     }
   } else if (warp == 10) {
     // -------------------------------------------------------------- statistics
-    // lse and Delta of each streamed tile: row r = token * G + head; four rows per lane,
-    // fetched a tile ahead
-    const float* lse_h = p.lse + (long long)head * p.G * p.ld_lse + it.start;
-    const float* del_h = p.delta + (long long)head * p.G * p.ld_delta + it.start;
-    float ls[4], de[4];
-    auto fetch = [&](int idx) {
-      const int t0 = (first + idx) * p.TPT;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int r = u * 32 + lane, tok = r / p.G, g = r - tok * p.G;
-        const bool is = r < p.RU && t0 + tok < it.len;
-        ls[u] = is ? lse_h[(long long)g * p.ld_lse + t0 + tok] : INFINITY;
-        de[u] = is ? del_h[(long long)g * p.ld_delta + t0 + tok] : 0.f;
-      }
-    };
-    fetch(0);
+    // lse and Delta of each streamed tile, row r = token * G + head, four rows per lane,
+    // fetched a tile ahead; and zeros behind the sequence in its last Q and dO tiles
     bool ok = true;
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, wb, SITE_PACKED_PRODUCER)) != 0;
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, wb, SITE_PACKED_PRODUCER)) != 0;
     };
-    for (int idx = 0; ok && idx < n_inner; ++idx) {
-      const int qs = idx % Geo::QS, os = idx % Geo::OS;
-      const uint32_t qph = (uint32_t)((idx / Geo::QS) & 1), oph = (uint32_t)((idx / Geo::OS) & 1);
-      ok = warp_wait(&q_empty[qs], qph ^ 1u);
-      if (!ok) break;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) sLse[qs * 128 + u * 32 + lane] = ls[u];
+    uint32_t n_items = 0, c = 0;
+    while (ok) {
+      const int slot = (int)(n_items % ITEMS);
+      if (!warp_wait(&item_full[slot], n_items / ITEMS)) break;
+      ++n_items;
+      const Item it = items[slot];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[qs]);
-      ok = warp_wait(&o_empty[os], oph ^ 1u);
-      if (!ok) break;
+      if (lane == 0) mbar_arrive(&item_empty[slot]);
+      if (it.head < 0) break;
+      const int n = inner_of(it);
+      const float* lse_h = p.lse + (long long)it.head * p.G * p.ld_lse + it.start;
+      const float* del_h = p.delta + (long long)it.head * p.G * p.ld_delta + it.start;
+      float ls[4], de[4];
+      auto fetch = [&](int t0) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) sDel[os * 128 + u * 32 + lane] = de[u];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&o_full[os]);
-      if (idx + 1 < n_inner) fetch(idx + 1);
-    }
-    if (ok && ragged) {
-      const int last = n_inner - 1;
-      const int keep = (it.len - (first + last) * p.TPT) * p.G;  // rows of the sequence
-      const int qs = last % Geo::QS, os = last % Geo::OS;
-      if (warp_wait(&q_full[qs], (uint32_t)((last / Geo::QS) & 1))) {
-        clear_rows(sQ0 + qs * Geo::TILE_B, Geo::BOXES, keep, lane, 32);
-        fence_proxy_async();
+        for (int u = 0; u < 4; ++u) {
+          const int r = u * 32 + lane, tok = r / p.G, g = r - tok * p.G;
+          const bool is = r < p.RU && t0 + tok < it.len;
+          ls[u] = is ? lse_h[(long long)g * p.ld_lse + t0 + tok] : INFINITY;
+          de[u] = is ? del_h[(long long)g * p.ld_delta + t0 + tok] : 0.f;
+        }
+      };
+      int t0 = first_of(it) * p.TPT;
+      fetch(t0);
+      for (int j = 0; ok && j < n; ++j, ++c, t0 += p.TPT) {
+        const uint32_t qs = c % QS, os = c % OS;
+        const int keep = (it.len - t0) * p.G;  // rows of the sequence, if the tile is its last
+        const bool ragged = j == n - 1 && keep < p.RU;
+        ok = warp_wait(&q_empty[qs], (c / QS) ^ 1u);
+        if (!ok) break;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sLse[qs * 128 + u * 32 + lane] = ls[u];
+        ok = warp_wait(&q_full[qs], c / QS);
+        if (!ok) break;
+        if (ragged) {
+          clear_rows(sQ0 + qs * Geo::TILE_B, Geo::BOXES, keep, lane, 32);
+          fence_proxy_async();
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(tail_q);
-        if (warp_wait(&o_full[os], (uint32_t)((last / Geo::OS) & 1))) {
+        if (lane == 0) mbar_arrive(&q_ready[qs]);
+        ok = warp_wait(&o_empty[os], (c / OS) ^ 1u);
+        if (!ok) break;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sDel[os * 128 + u * 32 + lane] = de[u];
+        if (j + 1 < n) fetch(t0 + p.TPT);
+        ok = warp_wait(&o_full[os], c / OS);
+        if (!ok) break;
+        if (ragged) {
           clear_rows(sO0 + os * Geo::TILE_B, Geo::BOXES, keep, lane, 32);
           fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(tail_o);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_ready[os]);
       }
     }
   } else if (warp == 1) {
@@ -324,88 +373,94 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
       const uint32_t k_lo = (uint32_t)dk0, k_hi = (uint32_t)(dk0 >> 32);
       const uint32_t v_lo = (uint32_t)dv0, v_hi = (uint32_t)(dv0 >> 32);
       const uint32_t kq_hi = (uint32_t)(dq0 >> 32), mn_hi = (uint32_t)(dq0_mn >> 32);
-      auto issue_s = [&](int j) {
-        const uint32_t q_lo = (uint32_t)dq0 + (uint32_t)(j % Geo::QS) * (Geo::TILE_B / 16);
+      // c: streamed tiles so far, over all items
+      auto issue_s = [&](uint32_t c) {
+        const uint32_t q_lo = (uint32_t)dq0 + (c % QS) * (Geo::TILE_B / 16);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ss_w(tmem + tm_s(j), k_lo + kmajor_step(kk), k_hi, q_lo + kmajor_step(kk), kq_hi,
+          mma_ss_w(tmem + tm_s((int)c), k_lo + kmajor_step(kk), k_hi, q_lo + kmajor_step(kk), kq_hi,
                    idesc_s, kk > 0 ? 1u : 0u);
         mma_commit(s_full);
       };
-      auto issue_g = [&](int j) {
-        const uint32_t o_lo = (uint32_t)do0 + (uint32_t)(j % Geo::OS) * (Geo::TILE_B / 16);
+      auto issue_g = [&](uint32_t c) {
+        const uint32_t o_lo = (uint32_t)do0 + (c % OS) * (Geo::TILE_B / 16);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ss_w(tmem + tm_g(j), v_lo + kmajor_step(kk), v_hi, o_lo + kmajor_step(kk), kq_hi,
+          mma_ss_w(tmem + tm_g((int)c), v_lo + kmajor_step(kk), v_hi, o_lo + kmajor_step(kk), kq_hi,
                    idesc_s, kk > 0 ? 1u : 0u);
         mma_commit(g_full);
       };
-      auto issue_dv = [&](int j) {
-        const uint32_t o_lo = (uint32_t)do0_mn + (uint32_t)(j % Geo::OS) * (Geo::TILE_B / 16);
+      auto issue_dv = [&](uint32_t c, bool first) {
+        const uint32_t o_lo = (uint32_t)do0_mn + (c % OS) * (Geo::TILE_B / 16);
 #pragma unroll
         for (int kk = 0; kk < TILE / 16; ++kk)
-          mma_ts_w(tmem + 0, tmem + packed_step(tm_s(j), kk), o_lo + (uint32_t)(kk * 128), mn_hi,
-                   idesc_acc, (j == 0 && kk == 0) ? 0u : 1u);
+          mma_ts_w(tmem + 0, tmem + packed_step(tm_s((int)c), kk), o_lo + (uint32_t)(kk * 128), mn_hi,
+                   idesc_acc, (first && kk == 0) ? 0u : 1u);
       };
-      auto issue_dk = [&](int j) {
-        const uint32_t q_lo = (uint32_t)dq0_mn + (uint32_t)(j % Geo::QS) * (Geo::TILE_B / 16);
+      auto issue_dk = [&](uint32_t c, bool first) {
+        const uint32_t q_lo = (uint32_t)dq0_mn + (c % QS) * (Geo::TILE_B / 16);
 #pragma unroll
         for (int kk = 0; kk < TILE / 16; ++kk)
-          mma_ts_w(tmem + HD, tmem + packed_step(tm_s(j) + 32, kk), q_lo + (uint32_t)(kk * 128),
-                   mn_hi, idesc_acc, (j == 0 && kk == 0) ? 0u : 1u);
+          mma_ts_w(tmem + HD, tmem + packed_step(tm_s((int)c) + 32, kk), q_lo + (uint32_t)(kk * 128),
+                   mn_hi, idesc_acc, (first && kk == 0) ? 0u : 1u);
       };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return mbar_wait_poll(bar, parity, wb, SITE_PACKED_MMA);
+        return mbar_wait_poll(bar, parity & 1u, wb, SITE_PACKED_MMA);
       };
-      // tile j's Q (dO) is in shared memory, and cleared where it is the ragged last one
-      auto wait_q = [&](int j) {
-        return wait(&q_full[j % Geo::QS], (uint32_t)((j / Geo::QS) & 1)) &&
-               (!ragged || j != n_inner - 1 || wait(tail_q, 0));
-      };
-      auto wait_o = [&](int j) {
-        return wait(&o_full[j % Geo::OS], (uint32_t)((j / Geo::OS) & 1)) &&
-               (!ragged || j != n_inner - 1 || wait(tail_o, 0));
-      };
-      bool ok = wait(kv_full, 0) && wait_q(0);
-      if (ok) {
-        tc_fence_after();
-        issue_s(0);
-      }
-      ok = ok && wait_o(0);
-      if (ok) {
-        tc_fence_after();
-        issue_g(0);
-      }
-      // per tile j: dV(j) once P^T(j) is stored; S^T(j+1) into the dP^T(j) region once the
-      // element-wise warps hold dP^T(j); dK(j) once dS^T(j) is stored; dP^T(j+1) into the
-      // region of tile j, after dV(j) and dK(j) have read it (in issue order)
-      for (int j = 0; ok && j < n_inner; ++j) {
-        const uint32_t ph = (uint32_t)(j & 1);
-        const bool more = j + 1 < n_inner;
-        ok = wait(p_ready, ph);
+      auto wait_q = [&](uint32_t c) { return wait(&q_ready[c % QS], c / QS); };
+      auto wait_o = [&](uint32_t c) { return wait(&o_ready[c % OS], c / OS); };
+      bool ok = true;
+      uint32_t n_items = 0, c = 0;
+      while (ok) {
+        const int slot = (int)(n_items % ITEMS);
+        ok = wait(&item_full[slot], n_items / ITEMS);
+        if (!ok) break;
+        const Item it = items[slot];
+        mbar_arrive(&item_empty[slot]);
+        if (it.head < 0) break;
+        const int n = inner_of(it);
+        // S^T(c) goes over the dP^T(c - 1) of the item before, once that is in registers
+        ok = wait(kv_full, n_items) && wait_q(c) && (c == 0 || wait(g_taken, c - 1));
         if (!ok) break;
         tc_fence_after();
-        issue_dv(j);
-        if (more) {
-          ok = wait(g_taken, ph) && wait_q(j + 1);
-          if (!ok) break;
-          tc_fence_after();
-          issue_s(j + 1);
-        }
-        ok = wait(ds_ready, ph);
+        issue_s(c);
+        ok = wait_o(c);
         if (!ok) break;
         tc_fence_after();
-        issue_dk(j);
-        mma_commit(&q_empty[j % Geo::QS]);
-        mma_commit(&o_empty[j % Geo::OS]);
-        if (more) {
-          ok = wait_o(j + 1);
+        issue_g(c);
+        if (n == 1) mma_commit(kv_empty);
+        // per tile: dV once P^T is stored; the next S^T into the dP^T region once the
+        // element-wise warps hold dP^T; dK once dS^T is stored; the next dP^T into the
+        // region of this tile, after dV and dK have read it (in issue order)
+        for (int j = 0; j < n; ++j, ++c) {
+          const bool more = j + 1 < n;
+          ok = wait(p_ready, c);
           if (!ok) break;
           tc_fence_after();
-          issue_g(j + 1);
+          issue_dv(c, j == 0);
+          if (more) {
+            ok = wait(g_taken, c) && wait_q(c + 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(c + 1);
+          }
+          ok = wait(ds_ready, c);
+          if (!ok) break;
+          tc_fence_after();
+          issue_dk(c, j == 0);
+          mma_commit(&q_empty[c % QS]);
+          mma_commit(&o_empty[c % OS]);
+          if (more) {
+            ok = wait_o(c + 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_g(c + 1);
+            if (j + 2 == n) mma_commit(kv_empty);
+          }
         }
+        if (ok) mma_commit(acc_done);
+        ++n_items;
       }
-      if (ok) mma_commit(acc_done);
       mma_commit(drain);
       WaitBound wd{p.status, p.limit_ns, nullptr};
       mbar_wait(drain, 0, wd, SITE_DRAIN);
@@ -414,150 +469,159 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
     // -------------------------------------------------------------- element-wise
     const int g = (warp - 2) >> 2;  // query rows [64g, 64g + 64) of every tile
     const int qq = warp & 3;        // TMEM lane quarter
-    const int kp = k0 + qq * 32 + lane;  // this thread's key, as a position of the sequence
     const uint32_t lane_base = tmem + ((uint32_t)(qq * 32) << 16);
     const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
-    bool ok = true;
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool mine = mbar_wait(bar, parity, wb, SITE_PACKED_SOFTMAX);
+      const bool mine = mbar_wait(bar, parity & 1u, wb, SITE_PACKED_SOFTMAX);
       return __all_sync(0xffffffffu, mine) != 0;
     };
-    for (int j = 0; j < n_inner; ++j) {
-      const uint32_t ph = (uint32_t)(j & 1);
-      const int qs = j % Geo::QS, os = j % Geo::OS;
-      if (!warp_wait(s_full, ph) || !warp_wait(&q_full[qs], (uint32_t)((j / Geo::QS) & 1))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t s_t = lane_base + tm_s(j) + (uint32_t)(GCOLS * g);
-      const uint32_t g_t = lane_base + tm_g(j) + (uint32_t)(GCOLS * g);
-      uint32_t sv[2][32];
-      tmem_ld32(s_t, sv[0]);
-      tmem_ld32(s_t + 32, sv[1]);
-      const float4* sl4 = reinterpret_cast<const float4*>(sLse + qs * 128 + g * GCOLS);
-      // row c of the tile is the query at token t0 + c / G: it sees this key iff
-      // c >= (kp - t0) G
-      const int t0 = (first + j) * p.TPT;
-      const bool masked = t0 < k0 + TILE - 1;
-      const int c_min = max(kp - t0, 0) * p.G - g * GCOLS;
-      tmem_ld_wait();
-      // P^T = exp2(s * scale_log2 - lse[q]), kept in fp32 for dS^T and stored as bf16
-      float pf[64];
-      uint32_t pp[32];
-      auto p_chunk = [&](const uint32_t (&s)[32], int c0, auto mask_tag) {
-        constexpr bool MASK = decltype(mask_tag)::value;
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 l4 = sl4[(c0 + e) >> 2];
-          const uint64_t nl[2] = {f2_pack(-l4.x, -l4.y), f2_pack(-l4.z, -l4.w)};
-#pragma unroll
-          for (int u = 0; u < 4; u += 2) {
-            float x0, x1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e + u]), __uint_as_float(s[e + u + 1])),
-                             scale2, nl[u >> 1]),
-                      x0, x1);
-            float p0 = ex2(x0), p1 = ex2(x1);
-            if constexpr (MASK) {
-              p0 = c0 + e + u >= c_min ? p0 : 0.f;
-              p1 = c0 + e + u + 1 >= c_min ? p1 : 0.f;
-            }
-            pf[c0 + e + u] = p0;
-            pf[c0 + e + u + 1] = p1;
-            pp[(c0 + e + u) >> 1] = pack_bf16x2(p0, p1);
-          }
+    uint32_t n_items = 0, c = 0;
+    while (true) {
+      const int slot = (int)(n_items % ITEMS);
+      if (!warp_wait(&item_full[slot], n_items / ITEMS)) break;
+      const Item it = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[slot]);
+      if (it.head < 0) break;
+      const int n = inner_of(it);
+      const int kp = it.q0 + qq * 32 + lane;  // this thread's key, as a position of the sequence
+      int t0 = first_of(it) * p.TPT;
+      bool ok = true;
+      for (int j = 0; j < n; ++j, ++c, t0 += p.TPT) {
+        const uint32_t qs = c % QS, os = c % OS;
+        // the scores' completion tells that the Q tile was ready; its lse came with it
+        if (!warp_wait(s_full, c) || !warp_wait(&q_ready[qs], c / QS)) {
+          ok = false;
+          break;
         }
-      };
-      if (masked) {
-        p_chunk(sv[0], 0, std::true_type{});
-        p_chunk(sv[1], 32, std::true_type{});
-      } else {
-        p_chunk(sv[0], 0, std::false_type{});
-        p_chunk(sv[1], 32, std::false_type{});
-      }
-      tmem_st32(s_t, pp);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_ready);
-      if (!warp_wait(g_full, ph) || !warp_wait(&o_full[os], (uint32_t)((j / Geo::OS) & 1))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      uint32_t gv[2][32];
-      tmem_ld32(g_t, gv[0]);
-      tmem_ld32(g_t + 32, gv[1]);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(g_taken);
-      // dS^T = P^T (dP^T - Delta[q])
-      const float4* sd4 = reinterpret_cast<const float4*>(sDel + os * 128 + g * GCOLS);
-      auto ds_chunk = [&](int c, auto mask_tag) {
-        constexpr bool MASK = decltype(mask_tag)::value;
-        uint32_t dd[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 d4 = sd4[(32 * c + e) >> 2];
-          const uint64_t dl[2] = {f2_pack(d4.x, d4.y), f2_pack(d4.z, d4.w)};
-#pragma unroll
-          for (int u = 0; u < 4; u += 2) {
-            float d0, d1;
-            f2_unpack(f2_mul(f2_pack(pf[32 * c + e + u], pf[32 * c + e + u + 1]),
-                             f2_sub(f2_pack(__uint_as_float(gv[c][e + u]),
-                                            __uint_as_float(gv[c][e + u + 1])),
-                                    dl[u >> 1])),
-                      d0, d1);
-            if constexpr (MASK) {  // 0 times a dP that is not finite is not 0
-              d0 = 32 * c + e + u >= c_min ? d0 : 0.f;
-              d1 = 32 * c + e + u + 1 >= c_min ? d1 : 0.f;
+        tc_fence_after();
+        const uint32_t s_t = lane_base + tm_s((int)c) + (uint32_t)(GCOLS * g);
+        const uint32_t g_t = lane_base + tm_g((int)c) + (uint32_t)(GCOLS * g);
+        uint32_t sv[2][32];
+        tmem_ld32(s_t, sv[0]);
+        tmem_ld32(s_t + 32, sv[1]);
+        const float4* sl4 = reinterpret_cast<const float4*>(sLse + qs * 128 + g * GCOLS);
+        // row e of the tile is the query at token t0 + e / G: it sees this key iff
+        // e >= (kp - t0) G
+        const bool masked = t0 < it.q0 + TILE - 1;
+        const int c_min = max(kp - t0, 0) * p.G - g * GCOLS;
+        tmem_ld_wait();
+        // P^T = exp2(s * scale_log2 - lse[q]), kept in fp32 for dS^T and stored as bf16
+        float pf[64];
+        uint32_t pp[32];
+        auto p_chunk = [&](const uint32_t (&s)[32], int c0, auto mask_tag) {
+          constexpr bool MASK = decltype(mask_tag)::value;
+  #pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 l4 = sl4[(c0 + e) >> 2];
+            const uint64_t nl[2] = {f2_pack(-l4.x, -l4.y), f2_pack(-l4.z, -l4.w)};
+  #pragma unroll
+            for (int u = 0; u < 4; u += 2) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e + u]), __uint_as_float(s[e + u + 1])),
+                               scale2, nl[u >> 1]),
+                        x0, x1);
+              float p0 = ex2(x0), p1 = ex2(x1);
+              if constexpr (MASK) {
+                p0 = c0 + e + u >= c_min ? p0 : 0.f;
+                p1 = c0 + e + u + 1 >= c_min ? p1 : 0.f;
+              }
+              pf[c0 + e + u] = p0;
+              pf[c0 + e + u + 1] = p1;
+              pp[(c0 + e + u) >> 1] = pack_bf16x2(p0, p1);
             }
-            dd[(e + u) >> 1] = pack_bf16x2(d0, d1);
           }
+        };
+        if (masked) {
+          p_chunk(sv[0], 0, std::true_type{});
+          p_chunk(sv[1], 32, std::true_type{});
+        } else {
+          p_chunk(sv[0], 0, std::false_type{});
+          p_chunk(sv[1], 32, std::false_type{});
         }
-        tmem_st16(s_t + 32 + 16 * c, dd);
-      };
-      if (masked) {
-        ds_chunk(0, std::true_type{});
-        ds_chunk(1, std::true_type{});
-      } else {
-        ds_chunk(0, std::false_type{});
-        ds_chunk(1, std::false_type{});
+        tmem_st32(s_t, pp);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready);
+        if (!warp_wait(g_full, c) || !warp_wait(&o_ready[os], c / OS)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t gv[2][32];
+        tmem_ld32(g_t, gv[0]);
+        tmem_ld32(g_t + 32, gv[1]);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(g_taken);
+        // dS^T = P^T (dP^T - Delta[q])
+        const float4* sd4 = reinterpret_cast<const float4*>(sDel + os * 128 + g * GCOLS);
+        auto ds_chunk = [&](int h, auto mask_tag) {
+          constexpr bool MASK = decltype(mask_tag)::value;
+          uint32_t dd[16];
+  #pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 d4 = sd4[(32 * h + e) >> 2];
+            const uint64_t dl[2] = {f2_pack(d4.x, d4.y), f2_pack(d4.z, d4.w)};
+  #pragma unroll
+            for (int u = 0; u < 4; u += 2) {
+              float d0, d1;
+              f2_unpack(f2_mul(f2_pack(pf[32 * h + e + u], pf[32 * h + e + u + 1]),
+                               f2_sub(f2_pack(__uint_as_float(gv[h][e + u]),
+                                              __uint_as_float(gv[h][e + u + 1])),
+                                      dl[u >> 1])),
+                        d0, d1);
+              if constexpr (MASK) {  // 0 times a dP that is not finite is not 0
+                d0 = 32 * h + e + u >= c_min ? d0 : 0.f;
+                d1 = 32 * h + e + u + 1 >= c_min ? d1 : 0.f;
+              }
+              dd[(e + u) >> 1] = pack_bf16x2(d0, d1);
+            }
+          }
+          tmem_st16(s_t + 32 + 16 * h, dd);
+        };
+        if (masked) {
+          ds_chunk(0, std::true_type{});
+          ds_chunk(1, std::true_type{});
+        } else {
+          ds_chunk(0, std::false_type{});
+          ds_chunk(1, std::false_type{});
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_ready);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ds_ready);
-    }
-    // ------------------------------------------------------------ epilogue
-    if (ok && warp_wait(acc_done, 0u)) {
+      if (!ok || !warp_wait(acc_done, n_items)) break;
+      ++n_items;
+      // ---------------------------------------------------------- epilogue
+      // P^T of the next item is handed over after these loads, and only then may its first
+      // products overwrite dV and dK
       tc_fence_after();
       const bool row_ok = kp < it.len;
       const long long row = (long long)it.start + (row_ok ? kp : 0);
-      __nv_bfloat16* dvp = p.dv + row * p.ld_dv + head * HD;
-      __nv_bfloat16* dkp = p.dk + row * p.ld_dk + head * HD;
+      auto store = [&](__nv_bfloat16* base, long long ld, uint32_t column, float f) {
+        __nv_bfloat16* dst[4];
+        group_rows(row_ok ? base + row * ld + it.head * HD + g * (HD / 2) : nullptr, dst);
 #pragma unroll
-      for (int c = g * (HD / 2); c < (g + 1) * (HD / 2); c += 32) {
-        uint32_t a[32], b[32];
-        tmem_ld32(lane_base + (uint32_t)c, a);
-        tmem_ld32(lane_base + (uint32_t)(HD + c), b);
-        tmem_ld_wait();
-        if (row_ok) {
-          uint4* v4 = reinterpret_cast<uint4*>(dvp + c);
-          uint4* k4 = reinterpret_cast<uint4*>(dkp + c);
-          auto pair = [](const uint32_t* r, float f) {
-            return pack_bf16x2(__uint_as_float(r[0]) * f, __uint_as_float(r[1]) * f);
-          };
+        for (int e0 = 0; e0 < HD / 2; e0 += 32) {
+          uint32_t r[32], w[16];
+          tmem_ld32(lane_base + column + (uint32_t)(g * (HD / 2) + e0), r);
+          tmem_ld_wait();
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            v4[w] = make_uint4(pair(a + 8 * w, 1.f), pair(a + 8 * w + 2, 1.f), pair(a + 8 * w + 4, 1.f),
-                               pair(a + 8 * w + 6, 1.f));
-            k4[w] = make_uint4(pair(b + 8 * w, p.scale), pair(b + 8 * w + 2, p.scale),
-                               pair(b + 8 * w + 4, p.scale), pair(b + 8 * w + 6, p.scale));
-          }
+          for (int e = 0; e < 16; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
+          store_rows(w, dst);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (dst[k] != nullptr) dst[k] += 32;
         }
-      }
+      };
+      store(p.dv, p.ld_dv, 0u, 1.f);
+      store(p.dk, p.ld_dk, (uint32_t)HD, p.scale);
+      tc_fence_before();
     }
   }
 
@@ -574,195 +638,253 @@ template <int HD>
 __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
     packed_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmDO,
-                         const __grid_constant__ CUtensorMap tmO,
                          const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
   using Geo = QueryGeom<HD>;
-  constexpr int NS = Geo::KV_STAGES;
-  Item it;
-  {
-    const int per_group = p.src.max_items * p.src.group;
-    const int grp = (int)blockIdx.x / per_group;
-    if (!find_item(p.src, grp, (int)blockIdx.x - grp * per_group, it)) return;
-  }
-  const int head = it.head;
+  constexpr uint32_t KS = Geo::KS, VS = Geo::VS;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  uint8_t* sStage = smem;  // stage s: K, V
-  // the owned rows on their way to TMEM, in the stages that the ring does not use yet
-  uint8_t* sQ = sStage + Geo::STAGE;
-  uint8_t* sDO = sQ + Geo::TILE_B;
-  uint8_t* sO = sStage + 2 * Geo::STAGE;
-  float* sDel = reinterpret_cast<float*>(sStage + NS * Geo::STAGE);  // [2][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sDel + 256);
-  uint64_t* own_full = bars;         // Q, dO and o tiles in shared memory
-  uint64_t* a_full = own_full + 1;   // Q and dO rows stored in TMEM (8 warps)
-  uint64_t* kv_full = a_full + 1;    // [NS]
-  uint64_t* kv_empty = kv_full + NS; // [NS]
-  uint64_t* s_full = kv_empty + NS;  // S(j) in TMEM
-  uint64_t* dp_full = s_full + 1;    // dP(j) in TMEM
-  uint64_t* s_free = dp_full + 1;    // S(j) read by the element-wise warps (8)
-  uint64_t* ds_full = s_free + 1;    // dS(j) stored (8 warps)
-  uint64_t* acc_done = ds_full + 1;
-  uint64_t* del_full = acc_done + 1; // both halves of a direct Delta stored (8)
-  uint64_t* tail_ok = del_full + 1;  // the last K, V tiles are cleared behind the sequence
-  uint64_t* drain = tail_ok + 1;
+  float* sDel = reinterpret_cast<float*>(smem_raw);                  // [2][128] halves of Delta
+  Item* items = reinterpret_cast<Item*>(sDel + 256);                 // [ITEMS]
+  uint64_t* item_full = reinterpret_cast<uint64_t*>(items + ITEMS);  // [ITEMS]
+  uint64_t* item_empty = item_full + ITEMS;  // [ITEMS]
+  uint64_t* own_full = item_empty + ITEMS;   // the item's Q and dO tiles in shared memory
+  uint64_t* own_empty = own_full + 1;        // and read (8 warps)
+  uint64_t* a_full = own_empty + 1;          // Q and dO rows stored in TMEM (8 warps)
+  uint64_t* del_full = a_full + 1;           // both halves of Delta stored (8 warps)
+  uint64_t* k_full = del_full + 1;           // [KS]
+  uint64_t* k_empty = k_full + KS;           // [KS]
+  uint64_t* v_full = k_empty + KS;           // [VS]
+  uint64_t* v_empty = v_full + VS;           // [VS]
+  uint64_t* s_full = v_empty + VS;           // S in TMEM
+  uint64_t* dp_full = s_full + 1;            // dP in TMEM
+  uint64_t* s_free = dp_full + 1;            // S read by the element-wise warps (8)
+  uint64_t* ds_full = s_free + 1;            // dS stored (8 warps)
+  uint64_t* acc_done = ds_full + 1;          // the item's dQ complete
+  uint64_t* tail_ok = acc_done + 1;          // [2] the last K and V tiles are cleared behind the
+                                             // sequence (in turn, as in the forward)
+  uint64_t* drain = tail_ok + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t tiles_off = tiles_offset(smem_raw, Geo::SMALL, Geo::TILES_OFF);
+  if (tiles_off == 0) {  // uniform
+    if (threadIdx.x == 0) record_error(p.status, kStatusUnsupported, SITE_SMEM_LAYOUT);
+    return;
+  }
+  uint8_t* sQ = smem_raw + tiles_off;
+  uint8_t* sDO = sQ + Geo::TILE_B;
+  uint8_t* sK = sDO + Geo::TILE_B;      // [KS]
+  uint8_t* sV = sK + KS * Geo::TILE_B;  // [VS]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n_tiles = (min(it.len, it.q0 + p.TPT) - 1) / TILE + 1;
-  const bool ragged = n_tiles * TILE > it.len;
-  // Delta from o, or, where one tile holds all keys, from P and dP themselves: there o is a
-  // mean of few values, and its rounding would be the largest error of dS
-  const bool direct = n_tiles == 1;
-
   if (threadIdx.x == 0) {
+    for (int s = 0; s < ITEMS; ++s) {
+      mbar_init(&item_full[s], 1);
+      mbar_init(&item_empty[s], Geo::READERS);
+    }
     mbar_init(own_full, 1);
+    mbar_init(own_empty, 8);
     mbar_init(a_full, 8);
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+    mbar_init(del_full, 8);
+    for (uint32_t s = 0; s < KS; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (uint32_t s = 0; s < VS; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
     mbar_init(s_free, 8);
     mbar_init(ds_full, 8);
     mbar_init(acc_done, 1);
-    mbar_init(del_full, 8);
-    mbar_init(tail_ok, 1);
+    mbar_init(&tail_ok[0], 1);
+    mbar_init(&tail_ok[1], 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    // the owned rows and the first keys are under way while the CTA sets itself up
-    mbar_arrive_expect_tx(own_full, (uint32_t)(Geo::BOXES * 128) * (uint32_t)p.RU * (direct ? 2u : 3u));
-    mbar_arrive_expect_tx(&kv_full[0], 2 * Geo::TILE_B);
-#pragma unroll
-    for (int b = 0; b < Geo::BOXES; ++b) {
-      tma_load_3d(sQ + b * BOX_BYTES, &tmQ, own_full, 64 * b, head * p.G, it.start + it.q0);
-      tma_load_3d(sDO + b * BOX_BYTES, &tmDO, own_full, 64 * b, head * p.G, it.start + it.q0);
-      if (!direct) tma_load_3d(sO + b * BOX_BYTES, &tmO, own_full, 64 * b, head * p.G, it.start + it.q0);
-      tma_load_2d(sStage + b * BOX_BYTES, &tmK, &kv_full[0], head * HD + 64 * b, it.start);
-      tma_load_2d(sStage + Geo::TILE_B + b * BOX_BYTES, &tmV, &kv_full[0], head * HD + 64 * b, it.start);
-    }
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmDO);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
+  Item next{};
+  Walk walk;
+  if (warp == 0) walk.next(p.src, next);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   WaitBound wb{p.status, p.limit_ns, abort_flag};
+  auto tiles_of = [&](const Item& it) { return (min(it.len, it.q0 + p.TPT) - 1) / TILE + 1; };
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
-    bool all = true;
-    if (lane == 0) {
-      int last[NS];
-#pragma unroll
-      for (int s = 0; s < NS; ++s) last[s] = -1;
-      last[0] = 0;
-      // the other stages hold the owned rows until these are in TMEM
-      if (n_tiles > 1) all = mbar_wait(a_full, 0, wb, SITE_PACKED_PRODUCER);
-      for (int j = 1; all && j < n_tiles; ++j) {
-        const int st = j % NS;
-        const uint32_t ph = (uint32_t)((j / NS) & 1);
-        if (!mbar_wait(&kv_empty[st], ph ^ 1u, wb, SITE_PACKED_PRODUCER)) {
-          all = false;
-          break;
+    const uint32_t box_rows = (uint32_t)(Geo::BOXES * 128) * (uint32_t)p.RU;
+    bool ok = true;
+    uint32_t n_items = 0, c = 0, n_tail = 0;  // items, key tiles and ragged items so far
+    while (ok) {
+      const Item it = next;
+      const int slot = (int)(n_items % ITEMS);
+      const int n = tiles_of(it);
+      if (lane == 0) {
+        ok = mbar_wait(&item_empty[slot], ((n_items / ITEMS) & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+        if (ok) {
+          items[slot] = it;
+          mbar_arrive(&item_full[slot]);
         }
-        mbar_arrive_expect_tx(&kv_full[st], 2 * Geo::TILE_B);
-        uint8_t* sk = sStage + st * Geo::STAGE;
+        if (ok && it.head >= 0) {
+          ok = mbar_wait(own_empty, (n_items & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+          if (ok) {
+            mbar_arrive_expect_tx(own_full, 2 * box_rows);
 #pragma unroll
-        for (int b = 0; b < Geo::BOXES; ++b) {
-          tma_load_2d(sk + b * BOX_BYTES, &tmK, &kv_full[st], head * HD + 64 * b, it.start + j * TILE);
-          tma_load_2d(sk + Geo::TILE_B + b * BOX_BYTES, &tmV, &kv_full[st], head * HD + 64 * b,
-                      it.start + j * TILE);
+            for (int b = 0; b < Geo::BOXES; ++b) {
+              tma_load_3d(sQ + b * BOX_BYTES, &tmQ, own_full, 64 * b, it.head * p.G, it.start + it.q0);
+              tma_load_3d(sDO + b * BOX_BYTES, &tmDO, own_full, 64 * b, it.head * p.G, it.start + it.q0);
+            }
+          }
+          for (int j = 0; ok && j < n; ++j, ++c) {
+            const uint32_t ks = c % KS, vs = c % VS;
+            ok = mbar_wait(&k_empty[ks], ((c / KS) & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&k_full[ks], Geo::TILE_B);
+#pragma unroll
+            for (int b = 0; b < Geo::BOXES; ++b)
+              tma_load_2d(sK + ks * Geo::TILE_B + b * BOX_BYTES, &tmK, &k_full[ks],
+                          it.head * HD + 64 * b, it.start + j * TILE);
+            ok = mbar_wait(&v_empty[vs], ((c / VS) & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&v_full[vs], Geo::TILE_B);
+#pragma unroll
+            for (int b = 0; b < Geo::BOXES; ++b)
+              tma_load_2d(sV + vs * Geo::TILE_B + b * BOX_BYTES, &tmV, &v_full[vs],
+                          it.head * HD + 64 * b, it.start + j * TILE);
+          }
         }
-        last[st] = (int)ph;
       }
-      WaitBound wd{p.status, p.limit_ns, nullptr};
-      all = mbar_wait(own_full, 0, wd, SITE_DRAIN) && all;
-      for (int s = 0; s < NS; ++s)
-        if (last[s] >= 0) all = mbar_wait(&kv_full[s], (uint32_t)last[s], wd, SITE_DRAIN) && all;
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      c = __shfl_sync(0xffffffffu, c, 0);
+      if (!ok || it.head < 0) break;
+      ++n_items;
+      walk.next(p.src, next);
+      if (n * TILE > it.len) {
+        const uint32_t last = c - 1;
+        const uint32_t ks = last % KS, vs = last % VS;
+        // every lane reads the phases itself: the tiles are then visible to its writes
+        ok = mbar_wait(&k_full[ks], (last / KS) & 1u, wb, SITE_PACKED_PRODUCER) &&
+             mbar_wait(&v_full[vs], (last / VS) & 1u, wb, SITE_PACKED_PRODUCER);
+        ok = __all_sync(0xffffffffu, ok) != 0;
+        if (!ok) break;
+        const int keep = it.len - (n - 1) * TILE;
+        clear_rows(sK + ks * Geo::TILE_B, Geo::BOXES, keep, lane, 32);
+        clear_rows(sV + vs * Geo::TILE_B, Geo::BOXES, keep, lane, 32);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail_ok[n_tail & 1u]);
+        ++n_tail;
+      }
     }
-    all = __shfl_sync(0xffffffffu, all ? 1 : 0, 0) != 0;
-    if (ragged && all) {
-      const int st = (n_tiles - 1) % NS;
+    if (lane == 0) {
+      walk.end(p.src);
+      // copies in flight land before the CTA ends
       WaitBound wd{p.status, p.limit_ns, nullptr};
-      mbar_wait(&kv_full[st], (uint32_t)(((n_tiles - 1) / NS) & 1), wd, SITE_DRAIN);
-      const int keep = it.len - (n_tiles - 1) * TILE;
-      clear_rows(sStage + st * Geo::STAGE, 2 * Geo::BOXES, keep, lane, 32);  // K, then V
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tail_ok);
+      if (n_items > 0) mbar_wait(own_full, (n_items - 1) & 1u, wd, SITE_DRAIN);
+      for (uint32_t b = c > KS ? c - KS : 0; b < c; ++b)
+        mbar_wait(&k_full[b % KS], (b / KS) & 1u, wd, SITE_DRAIN);
+      for (uint32_t b = c > VS ? c - VS : 0; b < c; ++b)
+        mbar_wait(&v_full[b % VS], (b / VS) & 1u, wd, SITE_DRAIN);
+      if (!ok) let_copies_land();
     }
   } else if (warp == 1) {
     if (lane == 0) {
       // ------------------------------------------------------------ MMA issuer
       const uint32_t idesc_s = make_idesc_bf16(TILE, TILE, false);
       const uint32_t idesc_acc = make_idesc_bf16(TILE, HD, true);
-      const uint64_t dst0 = make_sdesc_sw128(smem_addr(sStage), 16, 1024);
-      const uint64_t dst0_mn = make_sdesc_sw128(smem_addr(sStage), BOX_BYTES, 1024);
-      const uint32_t st_lo = (uint32_t)dst0, st_hi = (uint32_t)(dst0 >> 32);
-      const uint32_t mn_lo = (uint32_t)dst0_mn, mn_hi = (uint32_t)(dst0_mn >> 32);
-      auto issue_s = [&](int st) {
-        const uint32_t k_lo = st_lo + (uint32_t)st * Geo::STAGE / 16;
+      const uint64_t dk = make_sdesc_sw128(smem_addr(sK), 16, 1024);
+      const uint64_t dk_mn = make_sdesc_sw128(smem_addr(sK), BOX_BYTES, 1024);
+      const uint64_t dv = make_sdesc_sw128(smem_addr(sV), 16, 1024);
+      const uint32_t k_hi = (uint32_t)(dk >> 32), mn_hi = (uint32_t)(dk_mn >> 32);
+      // c: key tiles so far, over all items
+      auto issue_s = [&](uint32_t c) {
+        const uint32_t lo = (uint32_t)dk + (c % KS) * (Geo::TILE_B / 16);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ts_w(tmem + TM_SC, tmem + Geo::TM_Q + (uint32_t)(kk * 8), k_lo + kmajor_step(kk),
-                   st_hi, idesc_s, kk > 0 ? 1u : 0u);
+          mma_ts_w(tmem + TM_SC, tmem + Geo::TM_Q + (uint32_t)(kk * 8), lo + kmajor_step(kk), k_hi,
+                   idesc_s, kk > 0 ? 1u : 0u);
         mma_commit(s_full);
       };
-      auto issue_dp = [&](int st) {
-        const uint32_t v_lo = st_lo + ((uint32_t)st * Geo::STAGE + Geo::TILE_B) / 16;
+      auto issue_dp = [&](uint32_t c) {
+        const uint32_t lo = (uint32_t)dv + (c % VS) * (Geo::TILE_B / 16);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ts_w(tmem + TM_DP, tmem + Geo::TM_DO + (uint32_t)(kk * 8), v_lo + kmajor_step(kk),
-                   st_hi, idesc_s, kk > 0 ? 1u : 0u);
+          mma_ts_w(tmem + TM_DP, tmem + Geo::TM_DO + (uint32_t)(kk * 8), lo + kmajor_step(kk), k_hi,
+                   idesc_s, kk > 0 ? 1u : 0u);
         mma_commit(dp_full);
+        mma_commit(&v_empty[c % VS]);
       };
-      auto issue_dq = [&](int st, bool first) {
-        const uint32_t k_lo = mn_lo + (uint32_t)st * Geo::STAGE / 16;
+      auto issue_dq = [&](uint32_t c, bool first) {
+        const uint32_t lo = (uint32_t)dk_mn + (c % KS) * (Geo::TILE_B / 16);
 #pragma unroll
         for (int kk = 0; kk < TILE / 16; ++kk)
-          mma_ts_w(tmem + 0, packed_step(tmem + TM_DP, kk), k_lo + (uint32_t)(kk * 128), mn_hi,
-                   idesc_acc, (first && kk == 0) ? 0u : 1u);
+          mma_ts_w(tmem + 0, packed_step(tmem + TM_DP, kk), lo + (uint32_t)(kk * 128), mn_hi, idesc_acc,
+                   (first && kk == 0) ? 0u : 1u);
+        mma_commit(&k_empty[c % KS]);
       };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return mbar_wait_poll(bar, parity, wb, SITE_PACKED_MMA);
+        return mbar_wait_poll(bar, parity & 1u, wb, SITE_PACKED_MMA);
       };
-      auto wait_kv = [&](int j) {
-        return wait(&kv_full[j % NS], (uint32_t)((j / NS) & 1)) &&
-               (!ragged || j != n_tiles - 1 || wait(tail_ok, 0));
-      };
-      bool ok = wait(a_full, 0) && wait_kv(0);
-      if (ok) {
-        tc_fence_after();
-        issue_s(0);
-        issue_dp(0);
-      }
-      for (int j = 0; ok && j < n_tiles; ++j) {
-        const int st = j % NS;
-        const uint32_t ph = (uint32_t)(j & 1);
-        if (j + 1 < n_tiles) {
-          // next scores as soon as the element-wise warps hold this tile's
-          ok = wait_kv(j + 1) && wait(s_free, ph);
-          if (!ok) break;
-          tc_fence_after();
-          issue_s((j + 1) % NS);
-        }
-        ok = wait(ds_full, ph);
+      bool ok = true;
+      uint32_t n_items = 0, c = 0, n_tail = 0;
+      while (ok) {
+        const int slot = (int)(n_items % ITEMS);
+        ok = wait(&item_full[slot], n_items / ITEMS);
+        if (!ok) break;
+        const Item it = items[slot];
+        mbar_arrive(&item_empty[slot]);
+        if (it.head < 0) break;
+        const int n = tiles_of(it);
+        const bool ragged = n * TILE > it.len;
+        // K (and with the ragged last tile also V) of the item's tile j, at c, is in place
+        auto wait_k = [&](int j, uint32_t at) {
+          if (!wait(&k_full[at % KS], at / KS)) return false;
+          if (!ragged || j != n - 1) return true;
+          const uint32_t turn = n_tail++;
+          return wait(&tail_ok[turn & 1u], turn >> 1);
+        };
+        // S over the last tile's S of the item before, once that is in registers
+        ok = wait(a_full, n_items) && wait_k(0, c) && (c == 0 || wait(s_free, c - 1));
         if (!ok) break;
         tc_fence_after();
-        issue_dq(st, j == 0);
-        mma_commit(&kv_empty[st]);
-        if (j + 1 < n_tiles) issue_dp((j + 1) % NS);
+        issue_s(c);
+        ok = wait(&v_full[c % VS], c / VS);
+        if (!ok) break;
+        issue_dp(c);
+        for (int j = 0; j < n; ++j, ++c) {
+          const bool more = j + 1 < n;
+          if (more) {
+            // next scores as soon as the element-wise warps hold this tile's
+            ok = wait_k(j + 1, c + 1) && wait(s_free, c);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(c + 1);
+          }
+          ok = wait(ds_full, c);
+          if (!ok) break;
+          tc_fence_after();
+          issue_dq(c, j == 0);
+          if (more) {
+            ok = wait(&v_full[(c + 1) % VS], (c + 1) / VS);
+            if (!ok) break;
+            issue_dp(c + 1);
+          }
+        }
+        if (ok) mma_commit(acc_done);
+        ++n_items;
       }
-      if (ok) mma_commit(acc_done);
       mma_commit(drain);
       WaitBound wd{p.status, p.limit_ns, nullptr};
       mbar_wait(drain, 0, wd, SITE_DRAIN);
@@ -773,171 +895,237 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
     const int qq = warp & 3;
     const int r_local = qq * 32 + lane;
     const int tok = r_local / p.G;
-    const bool row_ok = r_local < p.RU && it.q0 + tok < it.len;
-    const int qpos = row_ok ? it.q0 + tok : -1;
-    const long long row = (long long)it.start + (row_ok ? qpos : 0);
-    const int qh = row_ok ? head * p.G + (r_local - tok * p.G) : 0;
-    const float lse = row_ok ? p.lse[(long long)qh * p.ld_lse + row] : INFINITY;
     const uint32_t lane_base = tmem + ((uint32_t)(qq * 32) << 16);
     const uint32_t s_t = lane_base + TM_SC + (uint32_t)(g * GCOLS);
     const uint32_t d_t = lane_base + TM_DP + (uint32_t)(g * GCOLS);
-    bool ok = true;
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool mine = mbar_wait(bar, parity, wb, SITE_PACKED_SOFTMAX);
+      const bool mine = mbar_wait(bar, parity & 1u, wb, SITE_PACKED_SOFTMAX);
       return __all_sync(0xffffffffu, mine) != 0;
     };
-    float del = 0.f;
-    ok = warp_wait(own_full, 0u);
-    if (ok) {
-      // this thread's row of Q (warpgroup 0) or dO (warpgroup 1) into TMEM, two bf16 values
-      // per column; warpgroup 1 also takes its row of o and forms Delta. Chunk c of row r
-      // lies at chunk c ^ (r % 8) of its 128 bytes (the 128-byte swizzle).
+    // this thread's row in an item
+    struct Row {
+      int n;     // key tiles of the item; 0: no item is left
+      int pos;   // position in the sequence, -1: no query
+      int qh;    // query head
+      long long row;
+      float lse;
+    };
+    // 16-byte pieces of o per lane: half a row, but of the four rows of its group of lanes
+    // the pieces 4 s + lane % 4, so that four lanes read 64 contiguous bytes
+    constexpr int OW = HD / 16;
+    const int quad = (lane & ~3) + qq * 32;  // the group's first row in the tile
+    uint32_t n_items = 0, c = 0;
+    // Takes the next item: its Q (warpgroup 0) or dO (warpgroup 1) row into TMEM, two bf16
+    // values per column, as A operands; and this thread's pieces of o on the way to registers
+    // (o[4 s + k]: piece 4 s + lane % 4 of the half row g of row quad + k). The item's Q and dO columns are free: the products of the item before that
+    // read them are complete (dP of its last tile was). Chunk w of row r lies at chunk
+    // w ^ (r % 8) of its 128 bytes in shared memory (the 128-byte swizzle).
+    auto take = [&](Row& r, uint4 (&o)[OW]) {
+      r.n = 0;
+      const int slot = (int)(n_items % ITEMS);
+      if (!warp_wait(&item_full[slot], n_items / ITEMS)) return false;
+      const Item it = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[slot]);
+      if (it.head < 0) return true;
+      const bool row_ok = r_local < p.RU && it.q0 + tok < it.len;
+      r.n = tiles_of(it);
+      r.pos = row_ok ? it.q0 + tok : -1;
+      r.qh = row_ok ? it.head * p.G + (r_local - tok * p.G) : 0;
+      r.row = (long long)it.start + (row_ok ? r.pos : 0);
+      r.lse = row_ok ? p.lse[(long long)r.qh * p.ld_lse + r.row] : INFINITY;
+      if (r.n > 1) {
+        const __nv_bfloat16* mine = row_ok ? p.o + r.row * p.ld_o + (long long)r.qh * HD + g * (HD / 2) : nullptr;
+        __nv_bfloat16* rows[4];
+        group_rows(const_cast<__nv_bfloat16*>(mine), rows);
+#pragma unroll
+        for (int w = 0; w < OW; ++w) {
+          const uint4* from = reinterpret_cast<const uint4*>(rows[w & 3]) + (w & ~3) + (lane & 3);
+          o[w] = rows[w & 3] != nullptr ? __ldg(from) : make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      if (!warp_wait(own_full, n_items)) return false;
       const uint32_t dst = lane_base + (g == 0 ? Geo::TM_Q : Geo::TM_DO);
       const uint4* src = reinterpret_cast<const uint4*>((g == 0 ? sQ : sDO) + r_local * 128);
-      const uint4* os = reinterpret_cast<const uint4*>(sO + r_local * 128);
 #pragma unroll
       for (int b = 0; b < Geo::BOXES; ++b) {
-        uint32_t r[32];
+        uint32_t u[32];
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
           const uint4 v = row_ok ? src[b * (BOX_BYTES / 16) + (w ^ (r_local & 7))] : make_uint4(0u, 0u, 0u, 0u);
-          r[4 * w + 0] = v.x;
-          r[4 * w + 1] = v.y;
-          r[4 * w + 2] = v.z;
-          r[4 * w + 3] = v.w;
+          u[4 * w + 0] = v.x;
+          u[4 * w + 1] = v.y;
+          u[4 * w + 2] = v.z;
+          u[4 * w + 3] = v.w;
         }
-        tmem_st32(dst + (uint32_t)(32 * b), r);
-        if (g == 1 && row_ok && !direct) {
-#pragma unroll
-          for (int w = 0; w < 8; ++w) {
-            const uint4 v = os[b * (BOX_BYTES / 16) + (w ^ (r_local & 7))];
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              del = fmaf(bf16_lo(u[e]), bf16_lo(r[4 * w + e]), del);
-              del = fmaf(bf16_hi(u[e]), bf16_hi(r[4 * w + e]), del);
-            }
-          }
-        }
-      }
-      if (g == 1) {
-        sDel[r_local] = del;
-        if (row_ok && !direct) p.delta[(long long)qh * p.ld_delta + row] = del;
+        tmem_st32(dst + (uint32_t)(32 * b), u);
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(a_full);
-    }
-    // all eight warps have stored their rows, and Delta with them
-    ok = ok && warp_wait(a_full, 0u);
-    del = sDel[r_local];
-    for (int j = 0; ok && j < n_tiles; ++j) {
-      const uint32_t ph = (uint32_t)(j & 1);
-      if (!warp_wait(s_full, ph)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      // ---- P of this query row for the group's 64 key columns
-      float pf[64];
-      {
-        uint32_t s0[32], s1[32];
-        tmem_ld32(s_t, s0);
-        tmem_ld32(s_t + 32, s1);
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free);
+      return true;
+    };
+    // This thread's half of Delta from o and dO (more than one key tile), and the release of
+    // the item's tiles in shared memory.
+    auto half_delta = [&](const Row& r, const uint4 (&o)[OW]) {
+      if (r.n == 0) return;
+      if (r.n > 1) {
+        float part[4] = {0.f, 0.f, 0.f, 0.f};  // of rows quad + k
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          pf[c] = ex2(fmaf(__uint_as_float(s0[c]), p.scale_log2, -lse));
-          pf[32 + c] = ex2(fmaf(__uint_as_float(s1[c]), p.scale_log2, -lse));
+        for (int w = 0; w < OW; ++w) {
+          const int row = quad + (w & 3);
+          const int piece = g * OW + (w & ~3) + (lane & 3);  // of the row's HD / 8
+          const uint4 d = *reinterpret_cast<const uint4*>(sDO + (piece >> 3) * BOX_BYTES + row * 128 +
+                                                          16 * ((piece & 7) ^ (row & 7)));
+          const uint32_t a[4] = {o[w].x, o[w].y, o[w].z, o[w].w}, b[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            part[w & 3] = fmaf(bf16_lo(a[e]), bf16_lo(b[e]), part[w & 3]);
+            part[w & 3] = fmaf(bf16_hi(a[e]), bf16_hi(b[e]), part[w & 3]);
+          }
         }
-      }
-      const int kbase = j * TILE + g * GCOLS;
-      // some key of the group is in the future of some row of the CTA
-      const bool masked = kbase + GCOLS - 1 > qpos;
-      if (masked) {
+        float del = 0.f;
 #pragma unroll
-        for (int c = 0; c < 64; ++c) pf[c] = kbase + c <= qpos ? pf[c] : 0.f;
+        for (int k = 0; k < 4; ++k) {
+          part[k] += __shfl_xor_sync(0xffffffffu, part[k], 1);
+          part[k] += __shfl_xor_sync(0xffffffffu, part[k], 2);
+          if ((lane & 3) == k) del = part[k];
+        }
+        sDel[g * 128 + r_local] = r.pos < 0 ? 0.f : del;
       }
-      // ---- dS = P (dP - Delta)
-      if (!warp_wait(dp_full, ph)) {
-        ok = false;
-        break;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(own_empty);
+        if (r.n > 1) mbar_arrive(del_full);
       }
-      tc_fence_after();
-      if (direct) {
-        float part = 0.f;
+    };
+    Row cur;
+    bool ok;
+    {
+      uint4 o[OW];
+      ok = take(cur, o);
+      if (ok) half_delta(cur, o);
+    }
+    while (ok && cur.n > 0) {
+      float del = 0.f;
+      for (int j = 0; j < cur.n; ++j, ++c) {
+        if (!warp_wait(s_full, c)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // ---- P of this query row for the group's 64 key columns
+        float pf[64];
+        {
+          uint32_t s0[32], s1[32];
+          tmem_ld32(s_t, s0);
+          tmem_ld32(s_t + 32, s1);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            pf[e] = ex2(fmaf(__uint_as_float(s0[e]), p.scale_log2, -cur.lse));
+            pf[32 + e] = ex2(fmaf(__uint_as_float(s1[e]), p.scale_log2, -cur.lse));
+          }
+        }
+        const int kbase = j * TILE + g * GCOLS;
+        // some key of the group is in the row's future
+        const bool masked = kbase + GCOLS - 1 > cur.pos;
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) pf[e] = kbase + e <= cur.pos ? pf[e] : 0.f;
+        }
+        // ---- dS = P (dP - Delta)
+        if (!warp_wait(dp_full, c)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (cur.n == 1) {
+          // one tile holds all keys: Delta from P and dP themselves. There o is a mean of few
+          // values, and its rounding would be the largest error of dS.
+          float part = 0.f;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t gv[32];
+            tmem_ld32(d_t + (uint32_t)(32 * half), gv);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (kbase + 32 * half + e <= cur.pos)
+                part = fmaf(pf[32 * half + e], __uint_as_float(gv[e]), part);
+          }
+          sDel[g * 128 + r_local] = part;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(del_full);
+        }
+        if (j == 0) {
+          if (!warp_wait(del_full, n_items)) {
+            ok = false;
+            break;
+          }
+          del = sDel[r_local] + sDel[128 + r_local];
+          if (g == 1 && cur.pos >= 0) p.delta[(long long)cur.qh * p.ld_delta + cur.row] = del;
+        }
+        const uint64_t del2 = f2_pack(del, del);
+        uint32_t dd[32];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t gv[32];
           tmem_ld32(d_t + (uint32_t)(32 * half), gv);
           tmem_ld_wait();
+          if (masked) {  // 0 times a dP that is not finite is not 0
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int c = 32 * half + e;
-            if (kbase + c <= qpos) part = fmaf(pf[c], __uint_as_float(gv[e]), part);
+            for (int e = 0; e < 32; ++e)
+              if (kbase + 32 * half + e > cur.pos) gv[e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const int at = 32 * half + e;
+            float d0, d1;
+            f2_unpack(f2_mul(f2_pack(pf[at], pf[at + 1]),
+                             f2_sub(f2_pack(__uint_as_float(gv[e]), __uint_as_float(gv[e + 1])), del2)),
+                      d0, d1);
+            dd[at >> 1] = pack_bf16x2(d0, d1);
           }
         }
-        sDel[g * 128 + r_local] = part;
+        tmem_st32(d_t, dd);
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(del_full);
-        if (!warp_wait(del_full, 0u)) {
-          ok = false;
-          break;
-        }
-        del = sDel[r_local] + sDel[128 + r_local];
-        if (g == 1 && row_ok) p.delta[(long long)qh * p.ld_delta + row] = del;
+        if (lane == 0) mbar_arrive(ds_full);
       }
-      const uint64_t del2 = f2_pack(del, del);
-      uint32_t dd[32];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t gv[32];
-        tmem_ld32(d_t + (uint32_t)(32 * half), gv);
-        tmem_ld_wait();
-        if (masked) {  // 0 times a dP that is not finite is not 0
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (kbase + 32 * half + e > qpos) gv[e] = 0u;
-        }
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const int c = 32 * half + e;
-          float d0, d1;
-          f2_unpack(f2_mul(f2_pack(pf[c], pf[c + 1]),
-                           f2_sub(f2_pack(__uint_as_float(gv[e]), __uint_as_float(gv[e + 1])), del2)),
-                    d0, d1);
-          dd[c >> 1] = pack_bf16x2(d0, d1);
-        }
-      }
-      tmem_st32(d_t, dd);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
-    }
-    // ------------------------------------------------------------ epilogue
-    if (ok && warp_wait(acc_done, 0u)) {
+      if (!ok) break;
+      // the next item's rows go to TMEM before this one's epilogue, so that its first
+      // products run under it; its first dQ waits for the dS that comes after the epilogue
+      const uint32_t done = n_items++;
+      Row nxt;
+      uint4 o[OW];
+      ok = take(nxt, o);
+      if (!ok || !warp_wait(acc_done, done)) break;
+      // ---------------------------------------------------------- epilogue
       tc_fence_after();
-      __nv_bfloat16* dqp = p.dq + row * p.ld_dq + (long long)qh * HD;
+      __nv_bfloat16* dst[4];
+      group_rows(cur.pos >= 0 ? p.dq + cur.row * p.ld_dq + (long long)cur.qh * HD + g * (HD / 2) : nullptr, dst);
 #pragma unroll
-      for (int c = g * (HD / 2); c < (g + 1) * (HD / 2); c += 32) {
-        uint32_t a[32];
-        tmem_ld32(lane_base + (uint32_t)c, a);
+      for (int e0 = 0; e0 < HD / 2; e0 += 32) {
+        uint32_t a[32], w[16];
+        tmem_ld32(lane_base + (uint32_t)(g * (HD / 2) + e0), a);
         tmem_ld_wait();
-        if (row_ok) {
-          uint4* q4 = reinterpret_cast<uint4*>(dqp + c);
-          auto pair = [&](int e) {
-            return pack_bf16x2(__uint_as_float(a[e]) * p.scale, __uint_as_float(a[e + 1]) * p.scale);
-          };
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            q4[w] = make_uint4(pair(8 * w), pair(8 * w + 2), pair(8 * w + 4), pair(8 * w + 6));
-        }
+        for (int e = 0; e < 16; ++e)
+          w[e] = pack_bf16x2(__uint_as_float(a[2 * e]) * p.scale, __uint_as_float(a[2 * e + 1]) * p.scale);
+        store_rows(w, dst);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (dst[k] != nullptr) dst[k] += 32;
       }
+      tc_fence_before();
+      half_delta(nxt, o);
+      cur = nxt;
     }
   }
 
@@ -951,11 +1139,11 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
 
 template <int HD>
 tsp_status launch_bwd(const Shape& s, const Source& queries, const Source& keys, BwdParams p,
-                      const void* k, int64_t ld_k, const void* v, int64_t ld_v, cudaStream_t stream) {
-  CUtensorMap tq, tdo, to, tk, tv;
-  TSP_TRY(make_query_map(&tq, s, p.q, p.ld_q));
-  TSP_TRY(make_query_map(&tdo, s, p.dout, p.ld_do));
-  TSP_TRY(make_query_map(&to, s, p.o, p.ld_o));
+                      const void* q, int64_t ld_q, const void* dout, int64_t ld_do, const void* k,
+                      int64_t ld_k, const void* v, int64_t ld_v, cudaStream_t stream) {
+  CUtensorMap tq, tdo, tk, tv;
+  TSP_TRY(make_query_map(&tq, s, q, ld_q));
+  TSP_TRY(make_query_map(&tdo, s, dout, ld_do));
   const uint64_t cols = (uint64_t)s.kv_heads * HD, rows = (uint64_t)s.tokens;
   TSP_TRY(make_tmap_2d_bf16(&tk, k, cols, rows, (uint64_t)ld_k * 2, 64, TILE));
   TSP_TRY(make_tmap_2d_bf16(&tv, v, cols, rows, (uint64_t)ld_v * 2, 64, TILE));
@@ -965,8 +1153,8 @@ tsp_status launch_bwd(const Shape& s, const Source& queries, const Source& keys,
     TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem,
                               "packed attention backward: cudaFuncSetAttribute"));
     p.src = queries;
-    kernel<<<(unsigned)p.src.max_items * (unsigned)s.kv_heads, QueryGeom<HD>::THREADS, smem, stream>>>(
-        tq, tdo, to, tk, tv, p);
+    const unsigned grid = (unsigned)std::min<long long>((long long)queries.max_items * s.kv_heads, sm_count());
+    kernel<<<grid, QueryGeom<HD>::THREADS, smem, stream>>>(tq, tdo, tk, tv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "packed attention backward (query side): launch");
   }
@@ -976,8 +1164,8 @@ tsp_status launch_bwd(const Shape& s, const Source& queries, const Source& keys,
     TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem,
                               "packed attention backward: cudaFuncSetAttribute"));
     p.src = keys;
-    kernel<<<(unsigned)p.src.max_items * (unsigned)s.kv_heads, KeyGeom<HD>::THREADS, smem, stream>>>(
-        tq, tdo, tk, tv, p);
+    const unsigned grid = (unsigned)std::min<long long>((long long)keys.max_items * s.kv_heads, sm_count());
+    kernel<<<grid, KeyGeom<HD>::THREADS, smem, stream>>>(tq, tdo, tk, tv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "packed attention backward (key side): launch");
   }
@@ -1035,12 +1223,8 @@ extern "C" tsp_status tsp_packed_attention_bwd(
   p.ld_dq = ld_dq;
   p.ld_dk = ld_dk;
   p.ld_dv = ld_dv;
-  p.q = in(q);
   p.o = in(o);
-  p.dout = in(dout);
-  p.ld_q = ld_q;
   p.ld_o = ld_o;
-  p.ld_do = ld_do;
   p.lse = lse;
   p.ld_lse = ld_lse;
   p.delta = at<float>(ws, w.delta);
@@ -1056,9 +1240,9 @@ extern "C" tsp_status tsp_packed_attention_bwd(
   // 48 MB of K and V in L2 at a time, as for the plan's backward
   const int group = head_group(s, 48ll << 20);
   const Source queries = make_source(s, starts, s.TPT, false, group, at<Item>(ws, w.items), counts,
-                                     (int)w.max_query, p.status);
+                                     (int)w.max_query, ws, 1);
   const Source keys = make_source(s, starts, TILE, true, group, at<Item>(ws, w.key_items), counts + 1,
-                                  (int)w.max_key, p.status);
+                                  (int)w.max_key, ws, 2);
   if (queries.items != nullptr) {
     const ListArgs a{s.TPT, 0, list_shift((tokens + TILE - 1) / TILE), at<Item>(ws, w.items), counts,
                      (int)w.max_query};
@@ -1066,6 +1250,6 @@ extern "C" tsp_status tsp_packed_attention_bwd(
                      counts + 1, (int)w.max_key};
     TSP_TRY(launch_lists(s, starts, a, b, p.status, st));
   }
-  if (head_dim == 64) return launch_bwd<64>(s, queries, keys, p, k, ld_k, v, ld_v, st);
-  return launch_bwd<128>(s, queries, keys, p, k, ld_k, v, ld_v, st);
+  if (head_dim == 64) return launch_bwd<64>(s, queries, keys, p, q, ld_q, dout, ld_do, k, ld_k, v, ld_v, st);
+  return launch_bwd<128>(s, queries, keys, p, q, ld_q, dout, ld_do, k, ld_k, v, ld_v, st);
 }

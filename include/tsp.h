@@ -636,12 +636,12 @@ tsp_status tsp_cost_max_batch(int scheme, int D, int tp, int64_t S, int hidden, 
  * visible keys of exp(scale q.k), as tsp_causal_attention_lse stores it.
  *
  * ws: tsp_packed_attention_workspace_bytes (0 for an unsupported shape), 256-byte aligned,
- * its status word zeroed once by tsp_status_init. One workspace serves one call at a time.
+ * initialised once by tsp_status_init. One workspace serves one call at a time.
  * ------------------------------------------------------------------------- */
 size_t tsp_packed_attention_workspace_bytes(int64_t tokens, int n_seqs, int heads, int kv_heads,
                                             int head_dim);
 
-/* Zero the status word (the first 256 bytes) of a workspace that belongs to no plan. */
+/* Zero the first 256 bytes (status word, counters) of a workspace that belongs to no plan. */
 tsp_status tsp_status_init(void* ws, void* stream);
 
 /* o = attention of every sequence; lse (optional) for the backward. o may not alias an input. */
