@@ -230,23 +230,28 @@ __global__ void __launch_bounds__(THREADS, 1)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, TMEM_COLS);
-    tmem_relinquish();
+  uint32_t tmem = 0;
+  if (warp == 0) {
+    __syncwarp();
+    start_arrive<THREADS>();
+  } else {
+    if (warp == 1) {
+      tmem_alloc(tmem_slot, TMEM_COLS);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    start_sync<THREADS>();
+    tc_fence_after();
+    tmem = *tmem_slot;
   }
-  // the producer looks its first item up before the CTA meets
-  Item next{};
-  Walk walk;
-  if (warp == 0) walk.next(p.src, next);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   WaitBound wb{p.status, p.limit_ns, abort_flag};
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
     WaitBound wd{p.status, p.limit_ns, nullptr};
+    Item next{};
+    Walk walk;
+    walk.next(p.src, next);
     bool ok = true;
     uint32_t n_items = 0, c = 0, n_tail = 0;  // items, key tiles and ragged items so far
     while (ok) {

@@ -183,6 +183,18 @@ struct Walk {
   }
 };
 
+// The start of a persistent CTA: warp 0 has set up the barriers and goes on to its first
+// loads, the others meet (tensor memory allocated, shared memory cleared) and see what warp 0
+// wrote before.
+template <int THREADS>
+static __device__ __forceinline__ void start_arrive() {
+  asm volatile("barrier.cta.arrive 1, %0;" ::"n"(THREADS) : "memory");
+}
+template <int THREADS>
+static __device__ __forceinline__ void start_sync() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
 // Stores one accumulator row per lane (32 columns as 16 packed bf16 pairs), 16 bytes at a
 // time. Lane by lane that would touch 32 lines per instruction; a 4 x 4 exchange of 16-byte
 // chunks inside groups of four lanes first lets four lanes write 64 contiguous bytes of one

@@ -92,12 +92,12 @@ struct QueryGeom {
   static constexpr int READERS = 9;  // of an item: MMA lane, 8 warps
   static constexpr int BOXES = HD / 64;
   static constexpr uint32_t TILE_B = 128 * HD * 2;
-  // a V tile is read last by dP, a K tile by dQ, which comes a phase later
-  static constexpr int KS = 3;
-  static constexpr int VS = 2;
+  // a stage holds the item's Q and dO on their way to TMEM, or K and V of one key tile
+  static constexpr int NS = 3;
+  static constexpr uint32_t STAGE = 2 * TILE_B;
   static constexpr uint32_t SMALL = 1024 + ITEMS * 16 + 384;  // Delta, items, barriers
   static constexpr uint32_t TILES_OFF = (SMALL + 1023) / 1024 * 1024;
-  static constexpr size_t USED = TILES_OFF + (size_t)(2 + KS + VS) * TILE_B;  // Q, dO, K, V
+  static constexpr size_t USED = TILES_OFF + (size_t)NS * STAGE;
   static constexpr size_t SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
   static constexpr uint32_t TM_Q = HD;
   static constexpr uint32_t TM_DO = HD + HD / 2;
@@ -213,23 +213,26 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, TMEM_COLS);
-    tmem_relinquish();
+  uint32_t tmem = 0;
+  if (warp == 0) {
+    __syncwarp();
+    start_arrive<Geo::THREADS>();
+  } else {
+    if (warp == 1) {
+      tmem_alloc(tmem_slot, TMEM_COLS);
+      tmem_relinquish();
+    }
+    if (p.RU < 128) {
+      // rows that no TMA box writes: zeros for the whole run
+      for (uint32_t s = 0; s < QS + OS; ++s)
+        clear_rows(sQ0 + s * Geo::TILE_B, Geo::BOXES, p.RU, threadIdx.x - 32, Geo::THREADS - 32);
+      fence_proxy_async();
+    }
+    tc_fence_before();
+    start_sync<Geo::THREADS>();
+    tc_fence_after();
+    tmem = *tmem_slot;
   }
-  Item next{};
-  Walk walk;
-  if (warp == 0) walk.next(p.src, next);
-  if (p.RU < 128) {
-    // rows that no TMA box writes: zeros for the whole run
-    for (uint32_t s = 0; s < QS + OS; ++s)
-      clear_rows(sQ0 + s * Geo::TILE_B, Geo::BOXES, p.RU, threadIdx.x, Geo::THREADS);
-    fence_proxy_async();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   WaitBound wb{p.status, p.limit_ns, abort_flag};
   // streamed query tiles of an item: from the first that sees one of its keys
   auto first_of = [&](const Item& it) { return it.q0 / p.TPT; };
@@ -238,6 +241,9 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
   if (warp == 0) {
     // -------------------------------------------------------------- producer
     const uint32_t box_rows = (uint32_t)(Geo::BOXES * 128) * (uint32_t)p.RU;
+    Item next{};
+    Walk walk;
+    walk.next(p.src, next);
     bool ok = true;
     uint32_t n_items = 0, c = 0;  // items and streamed tiles so far
     while (ok) {
@@ -479,13 +485,16 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
     while (true) {
       const int slot = (int)(n_items % ITEMS);
       if (!warp_wait(&item_full[slot], n_items / ITEMS)) break;
-      const Item it = items[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&item_empty[slot]);
-      if (it.head < 0) break;
-      const int n = inner_of(it);
-      const int kp = it.q0 + qq * 32 + lane;  // this thread's key, as a position of the sequence
-      int t0 = first_of(it) * p.TPT;
+      // what the epilogue needs of the item is read again there, and only then is the slot
+      // released: the loop below has no registers to spare
+      int n, t0, kp;
+      {
+        const Item it = items[slot];
+        if (it.head < 0) break;
+        n = inner_of(it);
+        t0 = first_of(it) * p.TPT;
+        kp = it.q0 + qq * 32 + lane;  // this thread's key, as a position of the sequence
+      }
       bool ok = true;
       for (int j = 0; j < n; ++j, ++c, t0 += p.TPT) {
         const uint32_t qs = c % QS, os = c % OS;
@@ -503,7 +512,7 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
         const float4* sl4 = reinterpret_cast<const float4*>(sLse + qs * 128 + g * GCOLS);
         // row e of the tile is the query at token t0 + e / G: it sees this key iff
         // e >= (kp - t0) G
-        const bool masked = t0 < it.q0 + TILE - 1;
+        const bool masked = t0 < kp - (qq * 32 + lane) + TILE - 1;
         const int c_min = max(kp - t0, 0) * p.G - g * GCOLS;
         tmem_ld_wait();
         // P^T = exp2(s * scale_log2 - lse[q]), kept in fp32 for dS^T and stored as bf16
@@ -600,6 +609,9 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
       // P^T of the next item is handed over after these loads, and only then may its first
       // products overwrite dV and dK
       tc_fence_after();
+      const Item it = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[slot]);
       const bool row_ok = kp < it.len;
       const long long row = (long long)it.start + (row_ok ? kp : 0);
       auto store = [&](__nv_bfloat16* base, long long ld, uint32_t column, float f) {
@@ -641,21 +653,17 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
                          const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
   using Geo = QueryGeom<HD>;
-  constexpr uint32_t KS = Geo::KS, VS = Geo::VS;
+  constexpr uint32_t NS = Geo::NS;
   extern __shared__ uint8_t smem_raw[];
   float* sDel = reinterpret_cast<float*>(smem_raw);                  // [2][128] halves of Delta
   Item* items = reinterpret_cast<Item*>(sDel + 256);                 // [ITEMS]
   uint64_t* item_full = reinterpret_cast<uint64_t*>(items + ITEMS);  // [ITEMS]
   uint64_t* item_empty = item_full + ITEMS;  // [ITEMS]
-  uint64_t* own_full = item_empty + ITEMS;   // the item's Q and dO tiles in shared memory
-  uint64_t* own_empty = own_full + 1;        // and read (8 warps)
-  uint64_t* a_full = own_empty + 1;          // Q and dO rows stored in TMEM (8 warps)
+  uint64_t* a_full = item_empty + ITEMS;     // Q and dO rows stored in TMEM, their stage read (8)
   uint64_t* del_full = a_full + 1;           // both halves of Delta stored (8 warps)
-  uint64_t* k_full = del_full + 1;           // [KS]
-  uint64_t* k_empty = k_full + KS;           // [KS]
-  uint64_t* v_full = k_empty + KS;           // [VS]
-  uint64_t* v_empty = v_full + VS;           // [VS]
-  uint64_t* s_full = v_empty + VS;           // S in TMEM
+  uint64_t* full = del_full + 1;             // [NS] stage landed
+  uint64_t* empty = full + NS;               // [NS] stage consumed
+  uint64_t* s_full = empty + NS;             // S in TMEM
   uint64_t* dp_full = s_full + 1;            // dP in TMEM
   uint64_t* s_free = dp_full + 1;            // S read by the element-wise warps (8)
   uint64_t* ds_full = s_free + 1;            // dS stored (8 warps)
@@ -670,10 +678,7 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
     if (threadIdx.x == 0) record_error(p.status, kStatusUnsupported, SITE_SMEM_LAYOUT);
     return;
   }
-  uint8_t* sQ = smem_raw + tiles_off;
-  uint8_t* sDO = sQ + Geo::TILE_B;
-  uint8_t* sK = sDO + Geo::TILE_B;      // [KS]
-  uint8_t* sV = sK + KS * Geo::TILE_B;  // [VS]
+  uint8_t* sStage = smem_raw + tiles_off;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -681,17 +686,11 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
       mbar_init(&item_full[s], 1);
       mbar_init(&item_empty[s], Geo::READERS);
     }
-    mbar_init(own_full, 1);
-    mbar_init(own_empty, 8);
     mbar_init(a_full, 8);
     mbar_init(del_full, 8);
-    for (uint32_t s = 0; s < KS; ++s) {
-      mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
-    }
-    for (uint32_t s = 0; s < VS; ++s) {
-      mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
+    for (uint32_t s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
@@ -708,25 +707,32 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, TMEM_COLS);
-    tmem_relinquish();
+  uint32_t tmem = 0;
+  if (warp == 0) {
+    __syncwarp();
+    start_arrive<Geo::THREADS>();
+  } else {
+    if (warp == 1) {
+      tmem_alloc(tmem_slot, TMEM_COLS);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    start_sync<Geo::THREADS>();
+    tc_fence_after();
+    tmem = *tmem_slot;
   }
-  Item next{};
-  Walk walk;
-  if (warp == 0) walk.next(p.src, next);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   WaitBound wb{p.status, p.limit_ns, abort_flag};
   auto tiles_of = [&](const Item& it) { return (min(it.len, it.q0 + p.TPT) - 1) / TILE + 1; };
+  // The stages are one ring of uses x = 0, 1, ...: an item's own rows, then its key tiles.
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
+    Item next{};
+    Walk walk;
+    walk.next(p.src, next);
     const uint32_t box_rows = (uint32_t)(Geo::BOXES * 128) * (uint32_t)p.RU;
     bool ok = true;
-    uint32_t n_items = 0, c = 0, n_tail = 0;  // items, key tiles and ragged items so far
+    uint32_t n_items = 0, x = 0, n_tail = 0;  // items, stage uses and ragged items so far
     while (ok) {
       const Item it = next;
       const int slot = (int)(n_items % ITEMS);
@@ -737,51 +743,39 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
           items[slot] = it;
           mbar_arrive(&item_full[slot]);
         }
-        if (ok && it.head >= 0) {
-          ok = mbar_wait(own_empty, (n_items & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
-          if (ok) {
-            mbar_arrive_expect_tx(own_full, 2 * box_rows);
+        for (int j = -1; ok && it.head >= 0 && j < n; ++j, ++x) {
+          const uint32_t st = x % NS;
+          ok = mbar_wait(&empty[st], ((x / NS) & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+          if (!ok) break;
+          uint8_t* a = sStage + st * Geo::STAGE;
+          mbar_arrive_expect_tx(&full[st], j < 0 ? 2 * box_rows : 2 * Geo::TILE_B);
 #pragma unroll
-            for (int b = 0; b < Geo::BOXES; ++b) {
-              tma_load_3d(sQ + b * BOX_BYTES, &tmQ, own_full, 64 * b, it.head * p.G, it.start + it.q0);
-              tma_load_3d(sDO + b * BOX_BYTES, &tmDO, own_full, 64 * b, it.head * p.G, it.start + it.q0);
+          for (int b = 0; b < Geo::BOXES; ++b) {
+            if (j < 0) {
+              tma_load_3d(a + b * BOX_BYTES, &tmQ, &full[st], 64 * b, it.head * p.G, it.start + it.q0);
+              tma_load_3d(a + Geo::TILE_B + b * BOX_BYTES, &tmDO, &full[st], 64 * b, it.head * p.G,
+                          it.start + it.q0);
+            } else {
+              tma_load_2d(a + b * BOX_BYTES, &tmK, &full[st], it.head * HD + 64 * b, it.start + j * TILE);
+              tma_load_2d(a + Geo::TILE_B + b * BOX_BYTES, &tmV, &full[st], it.head * HD + 64 * b,
+                          it.start + j * TILE);
             }
-          }
-          for (int j = 0; ok && j < n; ++j, ++c) {
-            const uint32_t ks = c % KS, vs = c % VS;
-            ok = mbar_wait(&k_empty[ks], ((c / KS) & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&k_full[ks], Geo::TILE_B);
-#pragma unroll
-            for (int b = 0; b < Geo::BOXES; ++b)
-              tma_load_2d(sK + ks * Geo::TILE_B + b * BOX_BYTES, &tmK, &k_full[ks],
-                          it.head * HD + 64 * b, it.start + j * TILE);
-            ok = mbar_wait(&v_empty[vs], ((c / VS) & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&v_full[vs], Geo::TILE_B);
-#pragma unroll
-            for (int b = 0; b < Geo::BOXES; ++b)
-              tma_load_2d(sV + vs * Geo::TILE_B + b * BOX_BYTES, &tmV, &v_full[vs],
-                          it.head * HD + 64 * b, it.start + j * TILE);
           }
         }
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      c = __shfl_sync(0xffffffffu, c, 0);
+      x = __shfl_sync(0xffffffffu, x, 0);
       if (!ok || it.head < 0) break;
       ++n_items;
       walk.next(p.src, next);
       if (n * TILE > it.len) {
-        const uint32_t last = c - 1;
-        const uint32_t ks = last % KS, vs = last % VS;
-        // every lane reads the phases itself: the tiles are then visible to its writes
-        ok = mbar_wait(&k_full[ks], (last / KS) & 1u, wb, SITE_PACKED_PRODUCER) &&
-             mbar_wait(&v_full[vs], (last / VS) & 1u, wb, SITE_PACKED_PRODUCER);
-        ok = __all_sync(0xffffffffu, ok) != 0;
+        const uint32_t last = x - 1;
+        // every lane reads the phase itself: the tiles are then visible to its writes
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[last % NS], (last / NS) & 1u, wb,
+                                               SITE_PACKED_PRODUCER)) != 0;
         if (!ok) break;
-        const int keep = it.len - (n - 1) * TILE;
-        clear_rows(sK + ks * Geo::TILE_B, Geo::BOXES, keep, lane, 32);
-        clear_rows(sV + vs * Geo::TILE_B, Geo::BOXES, keep, lane, 32);
+        // K, then V
+        clear_rows(sStage + (last % NS) * Geo::STAGE, 2 * Geo::BOXES, it.len - (n - 1) * TILE, lane, 32);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tail_ok[n_tail & 1u]);
@@ -792,11 +786,8 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
       walk.end(p.src);
       // copies in flight land before the CTA ends
       WaitBound wd{p.status, p.limit_ns, nullptr};
-      if (n_items > 0) mbar_wait(own_full, (n_items - 1) & 1u, wd, SITE_DRAIN);
-      for (uint32_t b = c > KS ? c - KS : 0; b < c; ++b)
-        mbar_wait(&k_full[b % KS], (b / KS) & 1u, wd, SITE_DRAIN);
-      for (uint32_t b = c > VS ? c - VS : 0; b < c; ++b)
-        mbar_wait(&v_full[b % VS], (b / VS) & 1u, wd, SITE_DRAIN);
+      for (uint32_t b = x > NS ? x - NS : 0; b < x; ++b)
+        mbar_wait(&full[b % NS], (b / NS) & 1u, wd, SITE_DRAIN);
       if (!ok) let_copies_land();
     }
   } else if (warp == 1) {
@@ -804,41 +795,39 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
       // ------------------------------------------------------------ MMA issuer
       const uint32_t idesc_s = make_idesc_bf16(TILE, TILE, false);
       const uint32_t idesc_acc = make_idesc_bf16(TILE, HD, true);
-      const uint64_t dk = make_sdesc_sw128(smem_addr(sK), 16, 1024);
-      const uint64_t dk_mn = make_sdesc_sw128(smem_addr(sK), BOX_BYTES, 1024);
-      const uint64_t dv = make_sdesc_sw128(smem_addr(sV), 16, 1024);
-      const uint32_t k_hi = (uint32_t)(dk >> 32), mn_hi = (uint32_t)(dk_mn >> 32);
-      // c: key tiles so far, over all items
-      auto issue_s = [&](uint32_t c) {
-        const uint32_t lo = (uint32_t)dk + (c % KS) * (Geo::TILE_B / 16);
+      const uint64_t dst0 = make_sdesc_sw128(smem_addr(sStage), 16, 1024);
+      const uint64_t dst0_mn = make_sdesc_sw128(smem_addr(sStage), BOX_BYTES, 1024);
+      const uint32_t st_lo = (uint32_t)dst0, st_hi = (uint32_t)(dst0 >> 32);
+      const uint32_t mn_lo = (uint32_t)dst0_mn, mn_hi = (uint32_t)(dst0_mn >> 32);
+      auto issue_s = [&](uint32_t st) {
+        const uint32_t k_lo = st_lo + st * (Geo::STAGE / 16);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ts_w(tmem + TM_SC, tmem + Geo::TM_Q + (uint32_t)(kk * 8), lo + kmajor_step(kk), k_hi,
+          mma_ts_w(tmem + TM_SC, tmem + Geo::TM_Q + (uint32_t)(kk * 8), k_lo + kmajor_step(kk), st_hi,
                    idesc_s, kk > 0 ? 1u : 0u);
         mma_commit(s_full);
       };
-      auto issue_dp = [&](uint32_t c) {
-        const uint32_t lo = (uint32_t)dv + (c % VS) * (Geo::TILE_B / 16);
+      auto issue_dp = [&](uint32_t st) {
+        const uint32_t v_lo = st_lo + st * (Geo::STAGE / 16) + Geo::TILE_B / 16;
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ts_w(tmem + TM_DP, tmem + Geo::TM_DO + (uint32_t)(kk * 8), lo + kmajor_step(kk), k_hi,
+          mma_ts_w(tmem + TM_DP, tmem + Geo::TM_DO + (uint32_t)(kk * 8), v_lo + kmajor_step(kk), st_hi,
                    idesc_s, kk > 0 ? 1u : 0u);
         mma_commit(dp_full);
-        mma_commit(&v_empty[c % VS]);
       };
-      auto issue_dq = [&](uint32_t c, bool first) {
-        const uint32_t lo = (uint32_t)dk_mn + (c % KS) * (Geo::TILE_B / 16);
+      auto issue_dq = [&](uint32_t st, bool first) {
+        const uint32_t k_lo = mn_lo + st * (Geo::STAGE / 16);
 #pragma unroll
         for (int kk = 0; kk < TILE / 16; ++kk)
-          mma_ts_w(tmem + 0, packed_step(tmem + TM_DP, kk), lo + (uint32_t)(kk * 128), mn_hi, idesc_acc,
+          mma_ts_w(tmem + 0, packed_step(tmem + TM_DP, kk), k_lo + (uint32_t)(kk * 128), mn_hi, idesc_acc,
                    (first && kk == 0) ? 0u : 1u);
-        mma_commit(&k_empty[c % KS]);
+        mma_commit(&empty[st]);
       };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         return mbar_wait_poll(bar, parity & 1u, wb, SITE_PACKED_MMA);
       };
       bool ok = true;
-      uint32_t n_items = 0, c = 0, n_tail = 0;
+      uint32_t n_items = 0, c = 0, x = 0, n_tail = 0;  // items, key tiles, stage uses, ragged items
       while (ok) {
         const int slot = (int)(n_items % ITEMS);
         ok = wait(&item_full[slot], n_items / ITEMS);
@@ -848,39 +837,39 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
         if (it.head < 0) break;
         const int n = tiles_of(it);
         const bool ragged = n * TILE > it.len;
-        // K (and with the ragged last tile also V) of the item's tile j, at c, is in place
-        auto wait_k = [&](int j, uint32_t at) {
-          if (!wait(&k_full[at % KS], at / KS)) return false;
-          if (!ragged || j != n - 1) return true;
+        // the key tile of use x is in place (cleared behind the sequence, if it is the last)
+        auto wait_kv = [&](bool last, uint32_t at) {
+          if (!wait(&full[at % NS], at / NS)) return false;
+          if (!ragged || !last) return true;
           const uint32_t turn = n_tail++;
           return wait(&tail_ok[turn & 1u], turn >> 1);
         };
+        // the own rows are in TMEM: their stage is free
+        ok = wait(a_full, n_items);
+        if (!ok) break;
+        mbar_arrive(&empty[x % NS]);
+        ++x;
         // S over the last tile's S of the item before, once that is in registers
-        ok = wait(a_full, n_items) && wait_k(0, c) && (c == 0 || wait(s_free, c - 1));
+        ok = wait_kv(n == 1, x) && (c == 0 || wait(s_free, c - 1));
         if (!ok) break;
         tc_fence_after();
-        issue_s(c);
-        ok = wait(&v_full[c % VS], c / VS);
-        if (!ok) break;
-        issue_dp(c);
-        for (int j = 0; j < n; ++j, ++c) {
+        issue_s(x % NS);
+        issue_dp(x % NS);
+        for (int j = 0; j < n; ++j, ++c, ++x) {
           const bool more = j + 1 < n;
+          const uint32_t then = (x + 1) % NS;
           if (more) {
             // next scores as soon as the element-wise warps hold this tile's
-            ok = wait_k(j + 1, c + 1) && wait(s_free, c);
+            ok = wait_kv(j + 2 == n, x + 1) && wait(s_free, c);
             if (!ok) break;
             tc_fence_after();
-            issue_s(c + 1);
+            issue_s(then);
           }
           ok = wait(ds_full, c);
           if (!ok) break;
           tc_fence_after();
-          issue_dq(c, j == 0);
-          if (more) {
-            ok = wait(&v_full[(c + 1) % VS], (c + 1) / VS);
-            if (!ok) break;
-            issue_dp(c + 1);
-          }
+          issue_dq(x % NS, j == 0);
+          if (more) issue_dp(then);
         }
         if (ok) mma_commit(acc_done);
         ++n_items;
@@ -914,13 +903,14 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
     // the pieces 4 s + lane % 4, so that four lanes read 64 contiguous bytes
     constexpr int OW = HD / 16;
     const int quad = (lane & ~3) + qq * 32;  // the group's first row in the tile
-    uint32_t n_items = 0, c = 0;
+    uint32_t n_items = 0, c = 0, x = 0;  // items, key tiles, stage uses
     // Takes the next item: its Q (warpgroup 0) or dO (warpgroup 1) row into TMEM, two bf16
     // values per column, as A operands; and this thread's pieces of o on the way to registers
-    // (o[4 s + k]: piece 4 s + lane % 4 of the half row g of row quad + k). The item's Q and dO columns are free: the products of the item before that
+    // (o[4 s + k]: piece 4 s + lane % 4 of the half row g of row quad + k), the same pieces of
+    // dO in registers. The item's Q and dO columns are free: the products of the item before that
     // read them are complete (dP of its last tile was). Chunk w of row r lies at chunk
     // w ^ (r % 8) of its 128 bytes in shared memory (the 128-byte swizzle).
-    auto take = [&](Row& r, uint4 (&o)[OW]) {
+    auto take = [&](Row& r, uint4 (&o)[OW], uint4 (&d)[OW]) {
       r.n = 0;
       const int slot = (int)(n_items % ITEMS);
       if (!warp_wait(&item_full[slot], n_items / ITEMS)) return false;
@@ -944,7 +934,10 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
           o[w] = rows[w & 3] != nullptr ? __ldg(from) : make_uint4(0u, 0u, 0u, 0u);
         }
       }
-      if (!warp_wait(own_full, n_items)) return false;
+      if (!warp_wait(&full[x % NS], x / NS)) return false;
+      const uint8_t* sQ = sStage + (x % NS) * Geo::STAGE;
+      const uint8_t* sDO = sQ + Geo::TILE_B;
+      x += 1 + r.n;
       const uint32_t dst = lane_base + (g == 0 ? Geo::TM_Q : Geo::TM_DO);
       const uint4* src = reinterpret_cast<const uint4*>((g == 0 ? sQ : sDO) + r_local * 128);
 #pragma unroll
@@ -960,52 +953,51 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
         }
         tmem_st32(dst + (uint32_t)(32 * b), u);
       }
+      if (r.n > 1) {
+#pragma unroll
+        for (int w = 0; w < OW; ++w) {
+          const int row = quad + (w & 3);
+          const int piece = g * OW + (w & ~3) + (lane & 3);  // of the row's HD / 8
+          d[w] = *reinterpret_cast<const uint4*>(sDO + (piece >> 3) * BOX_BYTES + row * 128 +
+                                                 16 * ((piece & 7) ^ (row & 7)));
+        }
+      }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(a_full);
       return true;
     };
-    // This thread's half of Delta from o and dO (more than one key tile), and the release of
-    // the item's tiles in shared memory.
-    auto half_delta = [&](const Row& r, const uint4 (&o)[OW]) {
-      if (r.n == 0) return;
-      if (r.n > 1) {
-        float part[4] = {0.f, 0.f, 0.f, 0.f};  // of rows quad + k
+    // This thread's half of Delta from o and dO, where there is more than one key tile.
+    auto half_delta = [&](const Row& r, const uint4 (&o)[OW], const uint4 (&d)[OW]) {
+      if (r.n <= 1) return;
+      float part[4] = {0.f, 0.f, 0.f, 0.f};  // of rows quad + k
 #pragma unroll
-        for (int w = 0; w < OW; ++w) {
-          const int row = quad + (w & 3);
-          const int piece = g * OW + (w & ~3) + (lane & 3);  // of the row's HD / 8
-          const uint4 d = *reinterpret_cast<const uint4*>(sDO + (piece >> 3) * BOX_BYTES + row * 128 +
-                                                          16 * ((piece & 7) ^ (row & 7)));
-          const uint32_t a[4] = {o[w].x, o[w].y, o[w].z, o[w].w}, b[4] = {d.x, d.y, d.z, d.w};
+      for (int w = 0; w < OW; ++w) {
+        const uint32_t a[4] = {o[w].x, o[w].y, o[w].z, o[w].w}, b[4] = {d[w].x, d[w].y, d[w].z, d[w].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            part[w & 3] = fmaf(bf16_lo(a[e]), bf16_lo(b[e]), part[w & 3]);
-            part[w & 3] = fmaf(bf16_hi(a[e]), bf16_hi(b[e]), part[w & 3]);
-          }
+        for (int e = 0; e < 4; ++e) {
+          part[w & 3] = fmaf(bf16_lo(a[e]), bf16_lo(b[e]), part[w & 3]);
+          part[w & 3] = fmaf(bf16_hi(a[e]), bf16_hi(b[e]), part[w & 3]);
         }
-        float del = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          part[k] += __shfl_xor_sync(0xffffffffu, part[k], 1);
-          part[k] += __shfl_xor_sync(0xffffffffu, part[k], 2);
-          if ((lane & 3) == k) del = part[k];
-        }
-        sDel[g * 128 + r_local] = r.pos < 0 ? 0.f : del;
       }
+      float del = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        part[k] += __shfl_xor_sync(0xffffffffu, part[k], 1);
+        part[k] += __shfl_xor_sync(0xffffffffu, part[k], 2);
+        if ((lane & 3) == k) del = part[k];
+      }
+      sDel[g * 128 + r_local] = r.pos < 0 ? 0.f : del;
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(own_empty);
-        if (r.n > 1) mbar_arrive(del_full);
-      }
+      if (lane == 0) mbar_arrive(del_full);
     };
     Row cur;
     bool ok;
     {
-      uint4 o[OW];
-      ok = take(cur, o);
-      if (ok) half_delta(cur, o);
+      uint4 o[OW], d[OW];
+      ok = take(cur, o, d);
+      if (ok) half_delta(cur, o, d);
     }
     while (ok && cur.n > 0) {
       float del = 0.f;
@@ -1103,8 +1095,8 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
       // products run under it; its first dQ waits for the dS that comes after the epilogue
       const uint32_t done = n_items++;
       Row nxt;
-      uint4 o[OW];
-      ok = take(nxt, o);
+      uint4 o[OW], d[OW];
+      ok = take(nxt, o, d);
       if (!ok || !warp_wait(acc_done, done)) break;
       // ---------------------------------------------------------- epilogue
       tc_fence_after();
@@ -1124,7 +1116,7 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
           if (dst[k] != nullptr) dst[k] += 32;
       }
       tc_fence_before();
-      half_delta(nxt, o);
+      half_delta(nxt, o, d);
       cur = nxt;
     }
   }
