@@ -11,11 +11,15 @@
 // rstd is taken again from h: the row is in registers for sum(g h) in any case, so a
 // saved rstd would only add traffic.
 //
-// Bound: HBM. A row is read once, stays in registers between its reduction and its
-// outputs, and is written once. Layout of the work: a row of up to 1024 elements per
-// warp (no block barrier), a longer one per CTA; each thread owns the same columns of
-// every row it meets, so the weight is loaded once and dw is summed in registers.
-// CTAs are persistent.
+// Bound: HBM. A row is read once, stays on chip between its reduction and its outputs, and
+// is written once. Layout of the work: a row of up to 1024 elements per warp (no block
+// barrier), a longer one per CTA; each thread owns the same columns of every row it meets,
+// so the weight is loaded once and dw is summed in registers. CTAs are persistent and copy
+// their next rows into shared memory (cp.async) while they work on the current one. A
+// thread's columns come in pieces of 16 bytes of the widest operand (8 columns of bf16, 4
+// of fp32), so that every access of a warp is contiguous: 8 columns of an fp32 stream
+// per thread read and wrote each 32-byte sector twice (157 us against SPEED_F32).
+// Rows that are not made of whole pieces take single elements, unstaged.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -34,30 +38,35 @@ constexpr int kMaxWidth = 32768;
 // of dw's sum is the same on every device
 constexpr int kBwdCtas = 456;
 
-// VEC consecutive elements as fp32. VEC is 8 (16-byte loads) or 1.
+// VEC consecutive elements as fp32: 8 or 4 (one 16- or 8-byte access of bf16) or 1.
 template <int VEC>
-__device__ __forceinline__ void load_bf16(const __nv_bfloat16* p, float (&v)[VEC]) {
+__device__ __forceinline__ void load_bf16(const void* p, float (&v)[VEC]) {
   if constexpr (VEC == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint4 u = *static_cast<const uint4*>(p);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = bf16_lo(w[i]);
       v[2 * i + 1] = bf16_hi(w[i]);
     }
+  } else if constexpr (VEC == 4) {
+    const uint2 u = *static_cast<const uint2*>(p);
+    v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
   } else {
-    v[0] = __bfloat162float(*p);
+    v[0] = __bfloat162float(*static_cast<const __nv_bfloat16*>(p));
   }
 }
 
 template <int VEC>
-__device__ __forceinline__ void load_f32(const float* p, float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+__device__ __forceinline__ void load_f32(const void* p, float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    v[0] = *static_cast<const float*>(p);
   } else {
-    v[0] = *p;
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      const float4 a = static_cast<const float4*>(p)[i];
+      v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
+    }
   }
 }
 
@@ -70,6 +79,8 @@ __device__ __forceinline__ void store_bf16(__nv_bfloat16* p, const float (&v)[VE
     u.z = pack_bf16x2(v[4], v[5]);
     u.w = pack_bf16x2(v[6], v[7]);
     *reinterpret_cast<uint4*>(p) = u;
+  } else if constexpr (VEC == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
   } else {
     *p = __float2bfloat16_rn(v[0]);
   }
@@ -77,11 +88,12 @@ __device__ __forceinline__ void store_bf16(__nv_bfloat16* p, const float (&v)[VE
 
 template <int VEC>
 __device__ __forceinline__ void store_f32(float* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 8) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
+  if constexpr (VEC == 1) {
     *p = v[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
   }
 }
 
@@ -95,6 +107,24 @@ template <int VEC, int RES>
 __device__ __forceinline__ void store_stream(void* p, long long i, const float (&v)[VEC]) {
   if constexpr (RES == RES_F32) store_f32<VEC>(static_cast<float*>(p) + i, v);
   else store_bf16<VEC>(static_cast<__nv_bfloat16*>(p) + i, v);
+}
+
+// Columns per piece of the staged kernels.
+template <int RES>
+constexpr int piece_of = RES == RES_F32 ? 4 : 8;
+
+// A piece of BYTES from global to shared memory, asynchronously.
+template <int BYTES>
+__device__ __forceinline__ void copy_ahead(void* smem, const void* global) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem)), "l"(global) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(smem)), "l"(global) : "memory");
+}
+__device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait_all_but() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Sum over the row's threads, the same bits in every thread. WARP: the row's threads are
@@ -135,7 +165,7 @@ __device__ __forceinline__ float e4m3_scale(uint32_t top) {
   const float t = __uint_as_float(top);
   if (top == 0u) return 1.f;
   if (top > 0x7f800000u) return t;
-  return fmaxf(t / kE4m3Max, 1.17549435e-38f);
+  return fmaxf(t * (1.f / kE4m3Max), 1.17549435e-38f);
 }
 
 __device__ __forceinline__ uint8_t to_e4m3(float v) {
@@ -161,66 +191,50 @@ struct NormParams {
   float eps;
 };
 
-// One row per warp (WARP) or per CTA; NV times VEC elements per thread.
-// MAXT: the largest block, which bounds the registers of a thread.
-template <int VEC, int NV, bool WARP, int RES, bool E4M3, int MAXT>
-__global__ void __launch_bounds__(MAXT) rmsnorm_fwd_kernel(const NormParams p) {
+// One row per CTA straight from global memory, NV times VEC elements per thread: rows of
+// single elements (VEC 1), and rows too wide to stage.
+template <int VEC, int NV, int RES, bool E4M3>
+__global__ void __launch_bounds__(1024) rmsnorm_fwd_kernel(const NormParams p) {
   __shared__ float part[2][32];
-  __shared__ uint32_t tops[2][VEC == 1 && E4M3 ? kMaxWidth / 128 : 32];
-  const int lanes = WARP ? 32 : blockDim.x;
-  const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const long long row0 = WARP ? (long long)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
-  const long long step = (long long)gridDim.x * (WARP ? 4 : 1);
+  __shared__ uint32_t tops[2][E4M3 ? kMaxWidth / 128 : 32];
+  const int tid = threadIdx.x, lanes = blockDim.x;
   const float inv_n = 1.f / (float)p.width;
   float w[NV][VEC], v[NV][VEC];
   auto col = [&](int i) { return (i * lanes + tid) * VEC; };
-  auto load = [&](long long row) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = col(i);
-      if (c < p.width) {
-        load_bf16<VEC>(p.x + row * p.width + c, v[i]);
-        if constexpr (RES != RES_NONE) {
-          float r[VEC];
-          load_stream<VEC, RES>(p.r, row * p.width + c, r);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) v[i][e] += r[e];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-      }
-    }
-  };
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     if (col(i) < p.width) load_bf16<VEC>(p.w + col(i), w[i]);
   int odd = 0;
-  for (long long row = row0; row < p.rows; row += step, odd ^= 1) {
-    load(row);
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, odd ^= 1) {
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      const long long at = row * p.width + col(i);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
+      if (col(i) < p.width) {
+        load_bf16<VEC>(p.x + at, v[i]);
+        if constexpr (RES != RES_NONE) {
+          float r[VEC];
+          load_stream<VEC, RES>(p.r, at, r);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) v[i][e] += r[e];
+        }
+      }
 #pragma unroll
       for (int e = 0; e < VEC; ++e) ss = fmaf(v[i][e], v[i][e], ss);
     }
-    const float rstd = 1.f / sqrtf(row_sum<WARP>(ss, part[odd]) * inv_n + p.eps);
-    if constexpr (RES != RES_NONE) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (col(i) < p.width) store_stream<VEC, RES>(p.h, row * p.width + col(i), v[i]);
-    }
+    const float rstd = 1.f / sqrtf(row_sum<false>(ss, part[odd]) * inv_n + p.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      if (col(i) >= p.width) continue;
+      if constexpr (RES != RES_NONE) store_stream<VEC, RES>(p.h, row * p.width + col(i), v[i]);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[i][e] = col(i) < p.width ? v[i][e] * rstd * w[i][e] : 0.f;
+      for (int e = 0; e < VEC; ++e) v[i][e] *= rstd * w[i][e];
+      if constexpr (!E4M3)
+        store_bf16<VEC>(static_cast<__nv_bfloat16*>(p.y) + row * p.width + col(i), v[i]);
     }
-    if constexpr (!E4M3) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (col(i) < p.width)
-          store_bf16<VEC>(static_cast<__nv_bfloat16*>(p.y) + row * p.width + col(i), v[i]);
-    } else {
+    if constexpr (E4M3) {
       uint8_t* y8 = static_cast<uint8_t*>(p.y) + row * p.width;
       auto top_of = [&](int i) {
         uint32_t t = 0;
@@ -230,40 +244,21 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_fwd_kernel(const NormParams p) {
       };
       auto store8 = [&](int i, float scale) {
         const float inv = 1.f / scale;
-        if constexpr (VEC == 8) {
-          *reinterpret_cast<uint2*>(y8 + col(i)) =
-              make_uint2(to_e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv),
-                         to_e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv));
-        } else {
-          y8[col(i)] = to_e4m3(v[i][0] * inv);
-        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) y8[col(i) + e] = to_e4m3(v[i][e] * inv);
       };
       if (p.group == 0) {
         uint32_t t = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) t = max(t, top_of(i));
-        const float scale = e4m3_scale(row_max<WARP>(t, tops[odd]));
+        const float scale = e4m3_scale(row_max<false>(t, tops[odd]));
         if (tid == 0) p.scales[row] = scale;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
           if (col(i) < p.width) store8(i, scale);
-      } else if constexpr (VEC == 8) {
-        // 16 consecutive threads hold 128 consecutive columns
-        const int groups = (p.width + 127) / 128;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          uint32_t t = top_of(i);
-#pragma unroll
-          for (int o = 8; o; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
-          const float scale = e4m3_scale(t);
-          if (col(i) < p.width) {
-            if ((tid & 15) == 0) p.scales[row * groups + col(i) / 128] = scale;
-            store8(i, scale);
-          }
-        }
       } else {
-        // 128 consecutive threads hold a group: the largest through shared memory (a
-        // maximum does not depend on the order of the atomics)
+        // the threads of a group meet in shared memory (a maximum does not depend on the
+        // order of the atomics)
         const int groups = (p.width + 127) / 128;
         __syncthreads();
         for (int g = threadIdx.x; g < groups; g += blockDim.x) tops[0][g] = 0u;
@@ -282,129 +277,124 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_fwd_kernel(const NormParams p) {
   }
 }
 
-// Longer rows, staged in shared memory: each thread copies its own 16-byte pieces of the
-// rows ahead (cp.async) and later reads only those, so a wait for its own copies is all the
-// ordering that is needed, and STAGES - 1 rows of every CTA are in flight under the
-// arithmetic and the barriers of the current one.
-__device__ __forceinline__ void copy_ahead(void* smem, const void* global) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem)), "l"(global) : "memory");
-}
-
-template <int RES, bool E4M3, int STAGES, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 4 : 1) rmsnorm_fwd_ring_kernel(const NormParams p) {
-  constexpr int NV = 2;
-  constexpr int SP = RES == RES_NONE ? 0 : RES == RES_F32 ? 2 : 1;  // 16-byte pieces of 8 stream elements
-  constexpr int PIECES = NV * (1 + SP);
-  extern __shared__ uint4 ring[];  // [STAGES][PIECES][threads]
+// Rows staged in shared memory: each thread copies its own pieces of the rows ahead and
+// later reads only those, so a wait for its own copies is all the ordering that is needed,
+// and STAGES - 1 rows are in flight under the arithmetic and the barriers of the current
+// one. One row per warp (WARP) or per CTA.
+template <int NV, bool WARP, int RES, bool E4M3, int STAGES, int MAXT>
+__global__ void __launch_bounds__(MAXT, NV * piece_of<RES> > 16 ? 2 : 1024 / MAXT)
+    rmsnorm_fwd_staged_kernel(const NormParams p) {
+  constexpr int VEC = piece_of<RES>;
+  constexpr int XB = 2 * VEC;                       // bytes of a piece of x
+  constexpr int RB = RES == RES_NONE ? 0 : 16;      // and of the residual
+  extern __shared__ __align__(16) uint8_t ring[];   // [STAGES][NV][threads] pieces of r, then of x
   __shared__ float part[2][32];
   __shared__ uint32_t tops[2][32];
-  const int tid = threadIdx.x, lanes = blockDim.x;
+  const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x, lanes = WARP ? 32 : blockDim.x;
+  const long long row0 = WARP ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  const long long step = WARP ? (long long)gridDim.x * (blockDim.x >> 5) : gridDim.x;
   const float inv_n = 1.f / (float)p.width;
-  auto col = [&](int i) { return (i * lanes + tid) * 8; };
-  auto slot = [&](int stage, int piece) { return ring + (stage * PIECES + piece) * lanes + tid; };
+  auto col = [&](int i) { return (i * lanes + tid) * VEC; };
+  auto r_at = [&](int stage, int i) { return ring + ((stage * NV + i) * blockDim.x + threadIdx.x) * RB; };
+  uint8_t* x_ring = ring + STAGES * NV * blockDim.x * RB;
+  auto x_at = [&](int stage, int i) { return x_ring + ((stage * NV + i) * blockDim.x + threadIdx.x) * XB; };
   auto fetch = [&](long long row, int stage) {
     if (row < p.rows) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (col(i) >= p.width) continue;
         const long long at = row * p.width + col(i);
-        copy_ahead(slot(stage, i), p.x + at);
-#pragma unroll
-        for (int u = 0; u < SP; ++u)
-          copy_ahead(slot(stage, NV + i * SP + u),
-                     static_cast<const char*>(p.r) + at * (RES == RES_F32 ? 4 : 2) + 16 * u);
+        copy_ahead<XB>(x_at(stage, i), p.x + at);
+        if constexpr (RES != RES_NONE)
+          copy_ahead<16>(r_at(stage, i), static_cast<const uint8_t*>(p.r) + at * (16 / VEC));
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    copies_end_group();
   };
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) fetch(blockIdx.x + (long long)s * gridDim.x, s);
-  uint4 w[NV];  // bf16: unpacked where it is used
+  for (int s = 0; s < STAGES - 1; ++s) fetch(row0 + s * step, s);
+  float w[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    w[i] = col(i) < p.width ? *reinterpret_cast<const uint4*>(p.w + col(i)) : make_uint4(0u, 0u, 0u, 0u);
+    if (col(i) < p.width) load_bf16<VEC>(p.w + col(i), w[i]);
   int odd = 0, stage = 0;
-  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, odd ^= 1) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-    float v[NV][8];
+  for (long long row = row0; row < p.rows; row += step, odd ^= 1) {
+    copies_wait_all_but<STAGES - 2>();
+    float v[NV][VEC];
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (col(i) < p.width) {
-        load_bf16<8>(reinterpret_cast<const __nv_bfloat16*>(slot(stage, i)), v[i]);
+        load_bf16<VEC>(x_at(stage, i), v[i]);
         if constexpr (RES != RES_NONE) {
-          float r[8];
-          if constexpr (RES == RES_F32) {
-            const float4 a = *reinterpret_cast<const float4*>(slot(stage, NV + i * SP));
-            const float4 b = *reinterpret_cast<const float4*>(slot(stage, NV + i * SP + 1));
-            r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w;
-            r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
-          } else {
-            load_bf16<8>(reinterpret_cast<const __nv_bfloat16*>(slot(stage, NV + i * SP)), r);
-          }
+          float r[VEC];
+          load_stream<VEC, RES>(r_at(stage, i), 0, r);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[i][e] += r[e];
+          for (int e = 0; e < VEC; ++e) v[i][e] += r[e];
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+        for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+      for (int e = 0; e < VEC; ++e) ss = fmaf(v[i][e], v[i][e], ss);
     }
     // this stage is read; the one before it takes the row furthest ahead
-    fetch(row + (long long)(STAGES - 1) * gridDim.x, stage == 0 ? STAGES - 1 : stage - 1);
+    fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
     stage = stage + 1 == STAGES ? 0 : stage + 1;
-    const float rstd = 1.f / sqrtf(row_sum<false>(ss, part[odd]) * inv_n + p.eps);
-    if constexpr (RES != RES_NONE) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (col(i) < p.width) store_stream<8, RES>(p.h, row * p.width + col(i), v[i]);
-    }
+    const float rstd = 1.f / sqrtf(row_sum<WARP>(ss, part[odd]) * inv_n + p.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      if (col(i) >= p.width) continue;
+      if constexpr (RES != RES_NONE) store_stream<VEC, RES>(p.h, row * p.width + col(i), v[i]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[i][2 * e] *= rstd * bf16_lo(u[e]);
-        v[i][2 * e + 1] *= rstd * bf16_hi(u[e]);
-      }
+      for (int e = 0; e < VEC; ++e) v[i][e] *= rstd * w[i][e];
+      if constexpr (!E4M3)
+        store_bf16<VEC>(static_cast<__nv_bfloat16*>(p.y) + row * p.width + col(i), v[i]);
     }
-    if constexpr (!E4M3) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (col(i) < p.width)
-          store_bf16<8>(static_cast<__nv_bfloat16*>(p.y) + row * p.width + col(i), v[i]);
-    } else {
+    if constexpr (E4M3) {
       uint8_t* y8 = static_cast<uint8_t*>(p.y) + row * p.width;
       uint32_t top[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         top[i] = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top[i] = max(top[i], __float_as_uint(fabsf(v[i][e])));
+        for (int e = 0; e < VEC; ++e) top[i] = max(top[i], __float_as_uint(fabsf(v[i][e])));
       }
       if (p.group == 0) {
-        const uint32_t t = row_max<false>(max(top[0], top[1]), tops[odd]);
-        top[0] = top[1] = t;
+        uint32_t t = top[0];
+#pragma unroll
+        for (int i = 1; i < NV; ++i) t = max(t, top[i]);
+        t = row_max<WARP>(t, tops[odd]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) top[i] = t;
         if (tid == 0) p.scales[row] = e4m3_scale(t);
       } else {
-        // 16 consecutive threads hold 128 consecutive columns
-        const int groups = (p.width + 127) / 128;
+        // 128 / VEC consecutive threads hold 128 consecutive columns
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+          if constexpr (VEC == 4) {
+            top[i] = __reduce_max_sync(0xffffffffu, top[i]);
+          } else {
 #pragma unroll
-          for (int o = 8; o; o >>= 1) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
-          if (col(i) < p.width && (tid & 15) == 0) p.scales[row * groups + col(i) / 128] = e4m3_scale(top[i]);
+            for (int o = 8; o; o >>= 1) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+          }
         }
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const float inv = 1.f / e4m3_scale(top[i]);
-        if (col(i) < p.width)
-          *reinterpret_cast<uint2*>(y8 + col(i)) =
-              make_uint2(to_e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv),
-                         to_e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv));
+        const float scale = e4m3_scale(top[i]);
+        const float inv = __frcp_rn(scale);
+        if (col(i) >= p.width) continue;
+        if (p.group != 0 && tid % (128 / VEC) == 0)
+          p.scales[row * ((p.width + 127) / 128) + col(i) / 128] = scale;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[i][e] *= inv;
+        const uint32_t lo = to_e4m3x4(v[i][0], v[i][1], v[i][2], v[i][3]);
+        if constexpr (VEC == 8)
+          *reinterpret_cast<uint2*>(y8 + col(i)) = make_uint2(lo, to_e4m3x4(v[i][4], v[i][5], v[i][6], v[i][7]));
+        else
+          *reinterpret_cast<uint32_t*>(y8 + col(i)) = lo;
       }
     }
   }
@@ -418,6 +408,7 @@ struct NormBwdParams {
   void* dx;        // h's type
   __nv_bfloat16* dx16;  // optional
   float* partial;  // [CTAs][width]
+  int stage_dh;    // dh is staged too (where it fits shared memory)
   long long rows;
   int width;
   float eps;
@@ -502,98 +493,104 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormBwdParams p
     if (col(i) < p.width) store_f32<VEC>(p.partial + (long long)blockIdx.x * p.width + col(i), dw[i]);
 }
 
-// The same with the rows staged in shared memory, as in the forward's ring kernel.
-template <int NV, int RES, int STAGES, int MAXT>
-__global__ void __launch_bounds__(MAXT) rmsnorm_bwd_ring_kernel(const NormBwdParams p) {
-  constexpr int SP = RES == RES_F32 ? 2 : 1;  // 16-byte pieces of 8 stream elements
-  extern __shared__ uint4 ring[];             // [STAGES][pieces][threads]
+// The same with the rows staged in shared memory, as in the forward: one row per warp (WARP)
+// or per CTA. Operands in bf16 stay packed until they are used, so that 1024 threads fit.
+template <int NV, bool WARP, int RES, int STAGES, int MAXT>
+__global__ void __launch_bounds__(MAXT, WARP ? 2 : MAXT <= 256 ? 3 : 1)
+    rmsnorm_bwd_staged_kernel(const NormBwdParams p) {
+  constexpr int VEC = piece_of<RES>;
+  constexpr int YB = 2 * VEC;                      // bytes of a piece of dy
+  extern __shared__ __align__(16) uint8_t ring[];  // [STAGES][NV][threads] pieces of h, dh, dy
   __shared__ float part[2][2][32];
-  const int tid = threadIdx.x, lanes = blockDim.x;
-  const bool has_dh = p.dh != nullptr;
-  const int pieces = NV * (SP + 1 + (has_dh ? SP : 0));
+  const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x, lanes = WARP ? 32 : blockDim.x;
+  const long long row0 = WARP ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  const long long step = WARP ? (long long)gridDim.x * (blockDim.x >> 5) : gridDim.x;
+  const bool has_dh = p.dh != nullptr, stage_dh = p.stage_dh != 0;
   const float inv_n = 1.f / (float)p.width;
-  auto col = [&](int i) { return (i * lanes + tid) * 8; };
-  auto slot = [&](int stage, int piece) { return ring + ((long long)stage * pieces + piece) * lanes + tid; };
-  const size_t es = RES == RES_F32 ? 4 : 2;
+  const int each = STAGES * NV * blockDim.x * 16;
+  auto col = [&](int i) { return (i * lanes + tid) * VEC; };
+  auto slot = [&](int stage, int i) { return (stage * NV + i) * (int)blockDim.x + (int)threadIdx.x; };
+  auto h_at = [&](int stage, int i) { return ring + slot(stage, i) * 16; };
+  auto d_at = [&](int stage, int i) { return ring + each + slot(stage, i) * 16; };
+  uint8_t* y_ring = ring + (stage_dh ? 2 : 1) * each;
+  auto y_at = [&](int stage, int i) { return y_ring + slot(stage, i) * YB; };
   auto fetch = [&](long long row, int stage) {
     if (row < p.rows) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (col(i) >= p.width) continue;
         const long long at = row * p.width + col(i);
-        const char* h = static_cast<const char*>(p.h) + at * es;
-        const char* d = static_cast<const char*>(p.dh) + at * es;
-#pragma unroll
-        for (int u = 0; u < SP; ++u) {
-          copy_ahead(slot(stage, i * SP + u), h + 16 * u);
-          if (has_dh) copy_ahead(slot(stage, NV * (SP + 1) + i * SP + u), d + 16 * u);
-        }
-        copy_ahead(slot(stage, NV * SP + i), p.dy + at);
+        copy_ahead<16>(h_at(stage, i), static_cast<const uint8_t*>(p.h) + at * (16 / VEC));
+        if (stage_dh) copy_ahead<16>(d_at(stage, i), static_cast<const uint8_t*>(p.dh) + at * (16 / VEC));
+        copy_ahead<YB>(y_at(stage, i), p.dy + at);
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  auto stream_of = [&](int stage, int piece, float (&v)[8]) {
-    if constexpr (RES == RES_F32) {
-      const float4 a = *reinterpret_cast<const float4*>(slot(stage, piece));
-      const float4 b = *reinterpret_cast<const float4*>(slot(stage, piece + 1));
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-      load_bf16<8>(reinterpret_cast<const __nv_bfloat16*>(slot(stage, piece)), v);
-    }
+    copies_end_group();
   };
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) fetch(blockIdx.x + (long long)s * gridDim.x, s);
-  float w[NV][8], dw[NV][8];
+  for (int s = 0; s < STAGES - 1; ++s) fetch(row0 + s * step, s);
+  uint32_t w[NV][VEC / 2], g[NV][VEC / 2];  // bf16 pairs
+  float dw[NV][VEC];
+  auto pieces = [](const void* from, uint32_t (&to)[VEC / 2]) {
+    if constexpr (VEC == 8) {
+      const uint4 u = *static_cast<const uint4*>(from);
+      to[0] = u.x, to[1] = u.y, to[2] = u.z, to[3] = u.w;
+    } else {
+      const uint2 u = *static_cast<const uint2*>(from);
+      to[0] = u.x, to[1] = u.y;
+    }
+  };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[i][e] = dw[i][e] = 0.f;
-    if (col(i) < p.width) load_bf16<8>(p.w + col(i), w[i]);
+    for (int e = 0; e < VEC; ++e) dw[i][e] = 0.f;
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) w[i][e] = g[i][e] = 0u;
+    if (col(i) < p.width) pieces(p.w + col(i), w[i]);
   }
   int odd = 0, stage = 0;
-  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, odd ^= 1) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-    float h[NV][8], g[NV][8];
+  for (long long row = row0; row < p.rows; row += step, odd ^= 1) {
+    copies_wait_all_but<STAGES - 2>();
+    float h[NV][VEC];
     float ss = 0.f, sg = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (col(i) < p.width) {
-        stream_of(stage, i * SP, h[i]);
-        load_bf16<8>(reinterpret_cast<const __nv_bfloat16*>(slot(stage, NV * SP + i)), g[i]);
-      } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] = g[i][e] = 0.f;
+      for (int e = 0; e < VEC; ++e) h[i][e] = 0.f;
+      if (col(i) < p.width) {
+        load_stream<VEC, RES>(h_at(stage, i), 0, h[i]);
+        pieces(y_at(stage, i), g[i]);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < VEC; ++e) {
+        const float wy = e & 1 ? bf16_hi(g[i][e / 2]) * bf16_hi(w[i][e / 2])
+                               : bf16_lo(g[i][e / 2]) * bf16_lo(w[i][e / 2]);
         ss = fmaf(h[i][e], h[i][e], ss);
-        sg = fmaf(g[i][e] * w[i][e], h[i][e], sg);
+        sg = fmaf(wy, h[i][e], sg);
       }
     }
     // the stage of the row before is read to its end: the row furthest ahead goes there
-    {
-      const int into = stage == 0 ? STAGES - 1 : stage - 1;
-      fetch(row + (long long)(STAGES - 1) * gridDim.x, into);
-    }
+    fetch(row + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+    // both sums behind one barrier
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
       ss += __shfl_xor_sync(0xffffffffu, ss, o);
       sg += __shfl_xor_sync(0xffffffffu, sg, o);
     }
-    if ((tid & 31) == 0) {
-      part[odd][0][tid >> 5] = ss;
-      part[odd][1][tid >> 5] = sg;
-    }
-    __syncthreads();
-    const bool in = (tid & 31) < (lanes >> 5);
-    ss = in ? part[odd][0][tid & 31] : 0.f;
-    sg = in ? part[odd][1][tid & 31] : 0.f;
+    if constexpr (!WARP) {
+      if ((tid & 31) == 0) {
+        part[odd][0][tid >> 5] = ss;
+        part[odd][1][tid >> 5] = sg;
+      }
+      __syncthreads();
+      const bool in = (tid & 31) < (lanes >> 5);
+      ss = in ? part[odd][0][tid & 31] : 0.f;
+      sg = in ? part[odd][1][tid & 31] : 0.f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      sg += __shfl_xor_sync(0xffffffffu, sg, o);
+      for (int o = 16; o; o >>= 1) {
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        sg += __shfl_xor_sync(0xffffffffu, sg, o);
+      }
     }
     const float rstd = 1.f / sqrtf(ss * inv_n + p.eps);
     const float coef = rstd * rstd * (sg * inv_n);  // dx = rstd (g - h coef)
@@ -601,22 +598,48 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_bwd_ring_kernel(const NormBwdPar
     for (int i = 0; i < NV; ++i) {
       const int c = col(i);
       if (c >= p.width) continue;
-      float d[8];
-      if (has_dh) stream_of(stage, NV * (SP + 1) + i * SP, d);
+      float d[VEC];
+      if (stage_dh) load_stream<VEC, RES>(d_at(stage, i), 0, d);
+      else if (has_dh) load_stream<VEC, RES>(p.dh, row * p.width + c, d);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float t = rstd * (g[i][e] * w[i][e] - h[i][e] * coef);
-        dw[i][e] = fmaf(g[i][e], h[i][e] * rstd, dw[i][e]);
+      for (int e = 0; e < VEC; ++e) {
+        const float y = e & 1 ? bf16_hi(g[i][e / 2]) : bf16_lo(g[i][e / 2]);
+        const float wt = e & 1 ? bf16_hi(w[i][e / 2]) : bf16_lo(w[i][e / 2]);
+        const float t = rstd * (y * wt - h[i][e] * coef);
+        dw[i][e] = fmaf(y, h[i][e] * rstd, dw[i][e]);
         d[e] = has_dh ? d[e] + t : t;
       }
-      store_stream<8, RES>(p.dx, row * p.width + c, d);
-      if (p.dx16 != nullptr) store_bf16<8>(p.dx16 + row * p.width + c, d);
+      store_stream<VEC, RES>(p.dx, row * p.width + c, d);
+      if (p.dx16 != nullptr) store_bf16<VEC>(p.dx16 + row * p.width + c, d);
     }
     stage = stage + 1 == STAGES ? 0 : stage + 1;
   }
+  float* out = p.partial + (long long)blockIdx.x * p.width;
+  if constexpr (WARP) {
+    // the warps' sums one after the other, in the ring's memory (every warp is done with it)
+    float* sum = reinterpret_cast<float*>(ring);
+    copies_wait_all_but<0>();
+    __syncthreads();
+    for (int k = 0; k < (int)(blockDim.x >> 5); ++k) {
+      if ((int)(threadIdx.x >> 5) == k) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (col(i) < p.width) store_f32<8>(p.partial + (long long)blockIdx.x * p.width + col(i), dw[i]);
+        for (int i = 0; i < NV; ++i) {
+          if (col(i) >= p.width) continue;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            if (k > 0) dw[i][e] += sum[col(i) + e];
+            sum[col(i) + e] = dw[i][e];
+          }
+          if (k == (int)(blockDim.x >> 5) - 1) store_f32<VEC>(out + col(i), dw[i]);
+        }
+      }
+      __syncthreads();
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (col(i) < p.width) store_f32<VEC>(out + col(i), dw[i]);
+  }
 }
 
 // dw[c] = sum of the partial rows, in a fixed order: 32 row groups per column, then their
@@ -644,49 +667,49 @@ bool aligned16(std::initializer_list<const void*> ptrs) {
   return true;
 }
 
-// Threads of a CTA that holds a row of `items` (vectors or elements), NV per thread.
+// Threads of a CTA that holds a row of `items` (pieces or elements), nv per thread.
 int row_threads(int items, int nv) { return ((items + nv - 1) / nv + 31) / 32 * 32; }
 
-template <int VEC, int NV, bool WARP, int RES, bool E4M3>
-void launch_fwd_variant(const NormParams& p, cudaStream_t s) {
-  constexpr int MAXT = WARP ? 128 : 1024;
-  const int threads = WARP ? 128 : row_threads((p.width + VEC - 1) / VEC, NV);
-  const long long blocks = WARP ? (p.rows + 3) / 4 : p.rows;
-  // resident CTAs: 2048 threads per SM
-  const long long cap = (long long)sm_count() * std::max(1, 2048 / threads);
-  rmsnorm_fwd_kernel<VEC, NV, WARP, RES, E4M3, MAXT>
-      <<<(unsigned)std::min(blocks, cap), threads, 0, s>>>(p);
+template <int VEC, int NV, int RES, bool E4M3>
+tsp_status launch_fwd_direct(const NormParams& p, cudaStream_t s) {
+  const int threads = row_threads((p.width + VEC - 1) / VEC, NV);
+  const long long cap = (long long)sm_count() * std::max(1, 1024 / threads);
+  rmsnorm_fwd_kernel<VEC, NV, RES, E4M3><<<(unsigned)std::min<long long>(p.rows, cap), threads, 0, s>>>(p);
+  return TSP_OK;
 }
 
-template <int RES, bool E4M3, int STAGES, int MAXT>
-tsp_status launch_fwd_ring(const NormParams& p, int threads, cudaStream_t s) {
-  auto kernel = rmsnorm_fwd_ring_kernel<RES, E4M3, STAGES, MAXT>;
-  const size_t smem = (size_t)STAGES * 2 * (1 + (RES == RES_NONE ? 0 : RES == RES_F32 ? 2 : 1)) * 16 * threads;
+template <int NV, bool WARP, int RES, bool E4M3, int STAGES, int MAXT>
+tsp_status launch_fwd_staged(const NormParams& p, int threads, cudaStream_t s) {
+  auto kernel = rmsnorm_fwd_staged_kernel<NV, WARP, RES, E4M3, STAGES, MAXT>;
+  const size_t smem = (size_t)STAGES * NV * threads * (2 * piece_of<RES> + (RES == RES_NONE ? 0 : 16));
   TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem,
                             "rmsnorm: cudaFuncSetAttribute"));
-  // resident CTAs: by registers (four of 256 threads, one of 1024) and by shared memory
-  const long long per_sm = std::min<long long>(std::max(1, 1024 / threads), (220 * 1024) / (long long)smem);
+  // resident CTAs: by registers (1024 threads, half of them with 32 columns each) and by
+  // shared memory
+  const int by_regs = NV * piece_of<RES> > 16 ? 2 : std::max(1, 1024 / threads);
+  const long long per_sm = std::min<long long>(by_regs, (220 * 1024) / (long long)smem);
   const long long cap = (long long)sm_count() * std::max<long long>(1, per_sm);
-  kernel<<<(unsigned)std::min<long long>(p.rows, cap), threads, smem, s>>>(p);
+  const long long blocks = WARP ? (p.rows + threads / 32 - 1) / (threads / 32) : p.rows;
+  kernel<<<(unsigned)std::min(blocks, cap), threads, smem, s>>>(p);
   return TSP_OK;
 }
 
+// vec: rows are whole pieces. A warp takes a row of up to 32 columns per lane; a CTA 16 per
+// thread. The fewer bytes a warp has per row, the more rows are staged ahead.
 template <int RES, bool E4M3>
 tsp_status launch_fwd_res(const NormParams& p, bool vec, cudaStream_t s) {
-  if (vec) {
-    const int vecs = p.width / 8;
-    const int threads = row_threads(vecs, 2);
-    if (vecs <= 32) launch_fwd_variant<8, 1, true, RES, E4M3>(p, s);
-    else if (vecs <= 64) launch_fwd_variant<8, 2, true, RES, E4M3>(p, s);
-    else if (vecs <= 128) launch_fwd_variant<8, 4, true, RES, E4M3>(p, s);
-    else if (threads <= 256) return launch_fwd_ring<RES, E4M3, 3, 256>(p, threads, s);
-    else if (threads <= 1024) return launch_fwd_ring<RES, E4M3, 2, 1024>(p, threads, s);
-    else launch_fwd_variant<8, 4, false, RES, E4M3>(p, s);
-  } else {
-    if (p.width <= 4096) launch_fwd_variant<1, 8, false, RES, E4M3>(p, s);
-    else launch_fwd_variant<1, 32, false, RES, E4M3>(p, s);
+  constexpr int P = 8 / piece_of<RES>;  // pieces per 8 columns
+  if (!vec) {
+    if (p.width <= 4096) return launch_fwd_direct<1, 8, RES, E4M3>(p, s);
+    return launch_fwd_direct<1, 32, RES, E4M3>(p, s);
   }
-  return TSP_OK;
+  if (p.width <= 256) return launch_fwd_staged<P, true, RES, E4M3, 4, 256>(p, 256, s);
+  if (p.width <= 512) return launch_fwd_staged<2 * P, true, RES, E4M3, 3, 256>(p, 256, s);
+  if (p.width <= 1024) return launch_fwd_staged<4 * P, true, RES, E4M3, 2, 256>(p, 256, s);
+  const int threads = row_threads(p.width / 8, 2);
+  if (threads <= 256) return launch_fwd_staged<2 * P, false, RES, E4M3, 2, 256>(p, threads, s);
+  if (threads <= 1024) return launch_fwd_staged<2 * P, false, RES, E4M3, 2, 1024>(p, threads, s);
+  return launch_fwd_direct<8, 4, RES, E4M3>(p, s);
 }
 
 tsp_status launch_fwd(const NormParams& p, int res, bool e4m3, bool vec, cudaStream_t s) {
@@ -707,46 +730,50 @@ tsp_status launch_fwd(const NormParams& p, int res, bool e4m3, bool vec, cudaStr
 }
 
 template <int VEC, int NV, int RES>
-void launch_bwd_variant(const NormBwdParams& p, int ctas, cudaStream_t s) {
+tsp_status launch_bwd_direct(const NormBwdParams& p, int ctas, cudaStream_t s) {
   rmsnorm_bwd_kernel<VEC, NV, RES>
       <<<ctas, row_threads((p.width + VEC - 1) / VEC, NV), 0, s>>>(p);
+  return TSP_OK;
 }
 
-template <int NV, int RES, int STAGES, int MAXT>
-tsp_status launch_bwd_ring(const NormBwdParams& p, int ctas, int threads, size_t smem, cudaStream_t s) {
-  auto kernel = rmsnorm_bwd_ring_kernel<NV, RES, STAGES, MAXT>;
+template <int NV, bool WARP, int RES, int STAGES, int MAXT>
+tsp_status launch_bwd_staged(NormBwdParams p, int ctas, int threads, cudaStream_t s) {
+  auto kernel = rmsnorm_bwd_staged_kernel<NV, WARP, RES, STAGES, MAXT>;
+  const size_t piece = (size_t)STAGES * NV * threads;
+  const size_t lean = piece * (2 * piece_of<RES> + 16), most = lean + piece * 16;
+  p.stage_dh = p.dh != nullptr && most <= 220 * 1024;
+  const size_t smem = p.stage_dh ? most : lean;
   TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem,
                             "rmsnorm backward: cudaFuncSetAttribute"));
   kernel<<<ctas, threads, smem, s>>>(p);
   return TSP_OK;
 }
 
+// How the backward covers a row of whole pieces, and with how many CTAs (those that fit the
+// GPU at a time: three per SM of up to 256 threads, two where a warp takes a row, one of
+// more threads).
+int bwd_ctas(int64_t rows, int width, bool vec) {
+  const int threads = row_threads(width / 8, 2);
+  const int most = !vec ? kBwdCtas : width <= 1024 ? kBwdCtas / 3 * 2 : threads <= 256 ? kBwdCtas : kBwdCtas / 3;
+  return (int)std::min<int64_t>(rows, most);
+}
+
 template <int RES>
 tsp_status launch_bwd_res(const NormBwdParams& p, bool vec, int ctas, cudaStream_t s) {
+  constexpr int P = 8 / piece_of<RES>;
   if (!vec) {
-    if (p.width <= 4096) launch_bwd_variant<1, 8, RES>(p, ctas, s);
-    else launch_bwd_variant<1, 32, RES>(p, ctas, s);
-    return TSP_OK;
+    if (p.width <= 4096) return launch_bwd_direct<1, 8, RES>(p, ctas, s);
+    return launch_bwd_direct<1, 32, RES>(p, ctas, s);
   }
-  const int vecs = p.width / 8;
-  const int nv = vecs <= 128 ? 1 : 2;
-  const int threads = row_threads(vecs, nv);
-  // shared memory of a staged row: whole 16-byte pieces of every thread
-  const size_t row = (size_t)threads * nv * 16 * ((RES == RES_F32 ? 2 : 1) * (p.dh ? 2 : 1) + 1);
-  // three stages where three CTAs fit an SM with them, else two; a row too wide for two
-  // stages is loaded straight into registers
-  const bool three = 3 * row <= 74 * 1024;
-  const size_t smem = (three ? 3 : 2) * row;
-  if (threads <= 1024 && smem <= 220 * 1024) {
-    if (nv == 1) return launch_bwd_ring<1, RES, 3, 256>(p, ctas, threads, 3 * row, s);
-    if (threads <= 256) {
-      if (three) return launch_bwd_ring<2, RES, 3, 256>(p, ctas, threads, smem, s);
-      return launch_bwd_ring<2, RES, 2, 256>(p, ctas, threads, smem, s);
-    }
-    return launch_bwd_ring<2, RES, 2, 1024>(p, ctas, threads, 2 * row, s);
-  }
-  launch_bwd_variant<8, 4, RES>(p, ctas, s);
-  return TSP_OK;
+  if (p.width <= 256) return launch_bwd_staged<P, true, RES, 4, 256>(p, ctas, 256, s);
+  if (p.width <= 512) return launch_bwd_staged<2 * P, true, RES, 3, 256>(p, ctas, 256, s);
+  if (p.width <= 1024) return launch_bwd_staged<4 * P, true, RES, 2, 256>(p, ctas, 256, s);
+  const int threads = row_threads(p.width / 8, 2);
+  if (threads <= 128) return launch_bwd_staged<2 * P, false, RES, 4, 128>(p, ctas, threads, s);
+  if (threads <= 256) return launch_bwd_staged<2 * P, false, RES, 2, 256>(p, ctas, threads, s);
+  if (threads <= 512) return launch_bwd_staged<2 * P, false, RES, P == 1 ? 3 : 2, 512>(p, ctas, threads, s);
+  if (threads <= 1024) return launch_bwd_staged<2 * P, false, RES, 2, 1024>(p, ctas, threads, s);
+  return launch_bwd_direct<8, 4, RES>(p, ctas, s);
 }
 
 // Checks shared by the three calls.
@@ -863,8 +890,8 @@ tsp_status tsp_rmsnorm_bwd(int64_t rows, int width, const void* h, int h_f32, co
   p.rows = rows;
   p.width = width;
   p.eps = eps;
-  const int ctas = (int)std::min<int64_t>(rows, kBwdCtas);
   const bool vec = width % 8 == 0 && aligned16({h, weight, dy, dh, dx, dx16});
+  const int ctas = bwd_ctas(rows, width, vec);
   TSP_TRY(h_f32 ? launch_bwd_res<RES_F32>(p, vec, ctas, s) : launch_bwd_res<RES_BF16>(p, vec, ctas, s));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "rmsnorm backward: launch");

@@ -146,8 +146,9 @@ def test_norm_backward(rows, width):
     w = (1 + 0.3 * n(width)).bfloat16()
     dy = n(rows, width).bfloat16()
     op = tsp.TSPRMSNorm(rows, width, eps=EPS)
-    # rows of a CTA one after the other, then up to 456 partial rows in 32 chains and a tree
-    dw_steps = 64 + math.ceil(rows / 456) + 456 / 32 + 5
+    # rows of a CTA (of 152 at least) and of its eight warps one after the other, then up to 456
+    # partial rows in 32 chains and a tree
+    dw_steps = 64 + math.ceil(rows / 152) + 8 + 456 / 32 + 5
     for kind in (torch.bfloat16, torch.float32):
         h = (3 * n(rows, width) * torch.exp(n(width))).to(kind)
         for dh in (None, n(rows, width).to(kind)):
