@@ -8,6 +8,7 @@ the library is not built, loading fails loudly.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import re
@@ -763,42 +764,50 @@ def tsp_grad_workspace_bytes(n: int) -> int:
 _GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
+def _grad_list(grads, name):
+    """(pointers, element counts, types) of the tensors as host arrays."""
+    if not all([t.is_contiguous() for t in grads]):
+        raise ValueError(f"{name} must be contiguous")
+    types = [_GRAD_TYPES.get(t.dtype, -1) for t in grads]
+    if -1 in types:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    return (array.array("q", [t.data_ptr() for t in grads]), array.array("q", [t.numel() for t in grads]),
+            array.array("i", types))
+
+
 def _grad_args(grads, norm, ws):
-    device = _same_device((*grads, norm, ws))
+    devices = {t.get_device() for t in grads}
+    devices.add(_same_device((norm, ws)))
+    if len(devices) != 1:
+        raise ValueError("gradients, norm and ws must be on one CUDA device")
     if norm.dtype != torch.float32 or norm.numel() != 1:
         raise ValueError("norm must be one float32 value")
-    n = len(grads)
-    types = [_GRAD_TYPES.get(t.dtype) for t in grads]
-    if None in types:
-        raise ValueError("gradients must be float32 or bfloat16")
-    if not all([t.is_contiguous() for t in grads]):
-        raise ValueError("gradients must be contiguous")
-    return (device, n, (_L * n)(*[t.data_ptr() for t in grads]), [t.numel() for t in grads], types,
-            _dev(ws, "ws", tsp_grad_workspace_bytes(n), torch.uint8))
+    return (devices.pop(), len(grads), *_grad_list(grads, "gradients"),
+            _dev(ws, "ws", tsp_grad_workspace_bytes(len(grads)), torch.uint8))
+
+
+def _at(values):
+    """Address of a host array (the caller keeps it alive over the call)."""
+    return values.buffer_info()[0] if values else None
 
 
 def tsp_grad_norm(grads, norm, ws, stream=None):
     """norm (one float32 on the device) = the 2-norm over all elements of the tensors."""
     device, n, ptrs, sizes, types, wp = _grad_args(grads, norm, ws)
-    _launch("tsp_grad_norm", device, stream, n, ptrs, (_L * n)(*sizes), (_I * n)(*types),
-            norm.data_ptr(), wp)
+    _launch("tsp_grad_norm", device, stream, n, _at(ptrs), _at(sizes), _at(types), norm.data_ptr(), wp)
 
 
 def tsp_grad_clip(grads, outs, max_norm, norm, ws, stream=None):
     """The norm, and outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6)); outs[i] may be
     grads[i]."""
     device, n, ptrs, sizes, types, wp = _grad_args(grads, norm, ws)
-    if outs is grads:
-        out_ptrs = ptrs
-    else:
-        if n and _same_device(outs) != device:
-            raise ValueError("outs on another device than the gradients")
-        if ([t.numel() for t in outs] != sizes or [_GRAD_TYPES.get(t.dtype) for t in outs] != types
-                or not all([t.is_contiguous() for t in outs])):
-            raise ValueError("outs must be contiguous and match the gradients in number, size and type")
-        out_ptrs = (_L * n)(*[t.data_ptr() for t in outs])
-    _launch("tsp_grad_clip", device, stream, n, ptrs, out_ptrs, (_L * n)(*sizes), (_I * n)(*types),
-            max_norm, norm.data_ptr(), wp)
+    out_ptrs = ptrs
+    if outs is not grads:
+        out_ptrs, out_sizes, out_types = _grad_list(outs, "outs")
+        if out_sizes != sizes or out_types != types or any([t.get_device() != device for t in outs]):
+            raise ValueError("outs must match the gradients in number, size, type and device")
+    _launch("tsp_grad_clip", device, stream, n, _at(ptrs), _at(out_ptrs), _at(sizes), _at(types), max_norm,
+            norm.data_ptr(), wp)
 
 
 # ------------------------------------------------------------------ packed attention

@@ -16,11 +16,11 @@
 
 #include <cstdio>
 #include <cstdlib>
+#include <map>
 #include <mutex>
 #include <new>
-#include <set>
 #include <string>
-#include <tuple>
+#include <utility>
 
 #include "tsp_device.cuh"
 #include "tsp_internal.h"
@@ -60,20 +60,19 @@ tsp_status fail(tsp_status code, const std::string& msg) {
 }
 
 tsp_status ensure_smem_limit(const void* kernel, int bytes, const char* what) {
+  // the limit in force per kernel and device: a kernel launched with several sizes keeps the
+  // largest, because setting a smaller one would lower it
   static std::mutex mu;
-  static std::set<std::tuple<const void*, int, int>> done;
+  static std::map<std::pair<const void*, int>, int> limits;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, what);
-  const auto key = std::make_tuple(kernel, dev, bytes);
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (done.count(key)) return TSP_OK;
-  }
+  std::lock_guard<std::mutex> lock(mu);
+  int& limit = limits[std::make_pair(kernel, dev)];
+  if (limit >= bytes) return TSP_OK;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return cuda_fail(e, what);
-  std::lock_guard<std::mutex> lock(mu);
-  done.insert(key);
+  limit = bytes;
   return TSP_OK;
 }
 

@@ -190,6 +190,21 @@ def test_norm_backward_matches_differences():
         assert abs(dw[j].item() - want.item()) < 1e-5
 
 
+@pytest.mark.parametrize("width", [1024, 4096, 8192])
+def test_norm_backward_with_and_without_dh_in_turn(width):
+    """The two take different amounts of shared memory in one kernel."""
+    n = gen(width)
+    rows = 40
+    h, dh = n(rows, width).bfloat16(), n(rows, width).bfloat16()
+    w, dy = (1 + 0.3 * n(width)).bfloat16(), n(rows, width).bfloat16()
+    op = tsp.TSPRMSNorm(rows, width, eps=EPS)
+    first = [op.backward(h, w, dy, dh=d) for d in (dh, None)]
+    for _ in range(2):
+        for d, (dx, dw) in zip((dh, None), first):
+            dx2, dw2 = op.backward(h, w, dy, dh=d)
+            assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
 def test_norm_no_rows():
     op = tsp.TSPRMSNorm(4, 64)
     x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
