@@ -540,16 +540,6 @@ const void* mapped_host_alias(const void* host) {
 
 using namespace tsp;
 
-#define TSP_GUARD_BEGIN try {
-#define TSP_GUARD_END                                                   \
-  }                                                                     \
-  catch (const std::bad_alloc&) {                                       \
-    return fail(TSP_ERR_INVALID_ARG, "host allocation failed");         \
-  }                                                                     \
-  catch (...) {                                                         \
-    return fail(TSP_ERR_INVALID_ARG, "unexpected host exception");      \
-  }
-
 extern "C" {
 
 tsp_status tsp_plan(int D, int64_t S, int hidden, int heads, int ffn, tsp_plan_t* out) {

@@ -355,25 +355,25 @@ size_t tsp_grad_workspace_bytes(int n) {
 
 tsp_status tsp_grad_norm(int n, const void* const* grads, const int64_t* sizes, const int* types,
                          float* norm, void* ws, void* stream) {
+  TSP_GUARD_BEGIN
   const List l{n, grads, nullptr, sizes, types};
   TSP_TRY(check_list("tsp_grad_norm", l, norm, ws));
   return norm_and_scale(l, 0.f, norm, ws, static_cast<cudaStream_t>(stream));
+  TSP_GUARD_END
 }
 
 tsp_status tsp_grad_clip(int n, const void* const* grads, void* const* outs, const int64_t* sizes,
                          const int* types, float max_norm, float* norm, void* ws, void* stream) {
-  try {
-    if (n > 0 && !outs) return fail(TSP_ERR_INVALID_ARG, "tsp_grad_clip: null list");
-    if (!(max_norm >= 0.f)) return fail(TSP_ERR_INVALID_ARG, "tsp_grad_clip: max_norm must not be negative");
-    const void* none = nullptr;
-    void* none_out = nullptr;
-    const List l{n, n > 0 ? grads : &none, n > 0 ? outs : &none_out, sizes, types};
-    TSP_TRY(check_list("tsp_grad_clip", l, norm, ws));
-    TSP_TRY(check_overlap("tsp_grad_clip", l));
-    return norm_and_scale(l, max_norm, norm, ws, static_cast<cudaStream_t>(stream));
-  } catch (...) {
-    return fail(TSP_ERR_INVALID_ARG, "tsp_grad_clip: host allocation failed");
-  }
+  TSP_GUARD_BEGIN
+  if (n > 0 && !outs) return fail(TSP_ERR_INVALID_ARG, "tsp_grad_clip: null list");
+  if (!(max_norm >= 0.f)) return fail(TSP_ERR_INVALID_ARG, "tsp_grad_clip: max_norm must not be negative");
+  const void* none = nullptr;
+  void* none_out = nullptr;
+  const List l{n, n > 0 ? grads : &none, n > 0 ? outs : &none_out, sizes, types};
+  TSP_TRY(check_list("tsp_grad_clip", l, norm, ws));
+  TSP_TRY(check_overlap("tsp_grad_clip", l));
+  return norm_and_scale(l, max_norm, norm, ws, static_cast<cudaStream_t>(stream));
+  TSP_GUARD_END
 }
 
 }  // extern "C"

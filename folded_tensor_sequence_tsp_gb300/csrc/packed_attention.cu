@@ -711,6 +711,7 @@ tsp_status tsp_packed_attention_fwd(int64_t tokens, int n_seqs, const int32_t* s
                                     int64_t ld_q, const tsp_bf16* k, int64_t ld_k, const tsp_bf16* v,
                                     int64_t ld_v, tsp_bf16* o, int64_t ld_o, float* lse,
                                     int64_t ld_lse, void* ws, void* stream) {
+  TSP_GUARD_BEGIN
   const char* what = "tsp_packed_attention_fwd";
   Shape s;
   TSP_TRY(make_shape(what, tokens, n_seqs, heads, kv_heads, head_dim, &s));
@@ -751,6 +752,7 @@ tsp_status tsp_packed_attention_fwd(int64_t tokens, int n_seqs, const int32_t* s
   }
   if (head_dim == 64) return launch_fwd<64>(s, p, q, ld_q, k, ld_k, v, ld_v, st);
   return launch_fwd<128>(s, p, q, ld_q, k, ld_k, v, ld_v, st);
+  TSP_GUARD_END
 }
 
 }  // extern "C"

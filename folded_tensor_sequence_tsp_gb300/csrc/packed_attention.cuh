@@ -73,80 +73,89 @@ struct Source {
 };
 
 #ifdef __CUDACC__
-// The idx-th item of the packed batch, costliest first, by every warp for itself. Items of
-// equal distance b from the cheap end of their sequence cost the same; Sum max(0, nb - b)
-// items lie at b or further, so b comes from a binary search over warp sums, and the
-// sequence from a rank among those with more than b items. About 0.3 us, against 4 us for a
-// kernel that writes the list.
-static __device__ __forceinline__ bool search_item(const Source& src, int idx, Item& it) {
+// Work w of a launch as an item and its key head, by a whole warp; false if there are no more
+// than w works, or if the starts are not in order. The works of a group of key heads come
+// item by item, the costliest first, every head of the group at each item.
+//
+// Up to SEARCH_SEQS sequences the item comes from the starts themselves: items of equal
+// distance b from the cheap end of their sequence cost the same, and sum max(0, nb - b) items
+// lie at b or further, so b comes from a binary search over warp sums and the sequence from a
+// rank among those with more than b items. About a microsecond, which the persistent kernels
+// spend beside their products, against 5 for a kernel that writes the list.
+static __device__ __forceinline__ bool find_item(const Source& src, unsigned w, Item& it) {
   constexpr int K = SEARCH_SEQS / 32;
   const int lane = threadIdx.x & 31;
   int nb[K], st[K], ln[K];
-  bool bad = false;
-  int total = 0, most = 0;
-#pragma unroll
-  for (int u = 0; u < K; ++u) {
-    const int s = u * 32 + lane;
-    st[u] = ln[u] = nb[u] = 0;
-    if (s < src.n_seqs) {
-      const int a = src.starts[s], b = src.starts[s + 1];
-      bad = bad || a < 0 || b < a || b > src.tokens;
-      st[u] = a;
-      ln[u] = b - a;
-      nb[u] = (int)(((long long)ln[u] + src.tile - 1) / src.tile);
-    }
-    total += nb[u];
-    most = max(most, nb[u]);
-  }
-  if (__any_sync(0xffffffffu, bad)) {
-    if (threadIdx.x == 0) record_error(src.status, kStatusInvalid, SITE_PACKED_STARTS);
-    return false;
-  }
-  total = __reduce_add_sync(0xffffffffu, total);
-  if (idx >= total) return false;
-  auto from = [&](int b) {
-    int c = 0;
-#pragma unroll
-    for (int u = 0; u < K; ++u) c += max(0, nb[u] - b);
-    return __reduce_add_sync(0xffffffffu, c);
-  };
-  int lo = 0, hi = __reduce_max_sync(0xffffffffu, most) - 1;  // the largest b with from(b) > idx
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (from(mid) > idx) lo = mid;
-    else hi = mid - 1;
-  }
-  int r = idx - from(lo + 1);
-#pragma unroll
-  for (int u = 0; u < K; ++u) {
-    const unsigned mask = __ballot_sync(0xffffffffu, nb[u] > lo);
-    const int here = __popc(mask);
-    if (r >= 0 && r < here) {
-      const bool mine = ((mask >> lane) & 1u) && __popc(mask & ((1u << lane) - 1u)) == r;
-      const int from_lane = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-      it.start = __shfl_sync(0xffffffffu, st[u], from_lane);
-      it.len = __shfl_sync(0xffffffffu, ln[u], from_lane);
-      const int n = __shfl_sync(0xffffffffu, nb[u], from_lane);
-      it.q0 = (src.from_end ? n - 1 - lo : lo) * src.tile;
-    }
-    r -= here;
-  }
-  return true;
-}
-
-// Work `rem` of head group `grp` as an item and its key head, by a whole warp; false if there
-// is none (the number of works is an upper bound), or if the item does not lie in this call's
-// buffers.
-static __device__ __forceinline__ bool find_item(const Source& src, int grp, int rem, Item& it) {
-  const int in_g = min(src.group, src.kv_heads - grp * src.group);
-  const int at = rem / in_g;
+  int total;
   if (src.items == nullptr) {
-    if (!search_item(src, at, it)) return false;
+    bool bad = false;
+    total = 0;
+#pragma unroll
+    for (int u = 0; u < K; ++u) {
+      const int s = u * 32 + lane;
+      st[u] = ln[u] = nb[u] = 0;
+      if (s < src.n_seqs) {
+        const int a = src.starts[s], b = src.starts[s + 1];
+        bad = bad || a < 0 || b < a || b > src.tokens;
+        st[u] = a;
+        ln[u] = b - a;
+        nb[u] = (int)(((long long)ln[u] + src.tile - 1) / src.tile);
+      }
+      total += nb[u];
+    }
+    if (__any_sync(0xffffffffu, bad)) {
+      if (threadIdx.x == 0) record_error(src.status, kStatusInvalid, SITE_PACKED_STARTS);
+      return false;
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
   } else {
-    if (at >= *src.count) return false;
-    it = src.items[at];
+    total = *src.count;
   }
-  it.head = grp * src.group + (rem - at * in_g);
+  if (total <= 0 || w >= (unsigned long long)total * (unsigned)src.kv_heads) return false;
+  const unsigned per_group = (unsigned)total * (unsigned)src.group;
+  const int grp = (int)(w / per_group);
+  const int in_g = min(src.group, src.kv_heads - grp * src.group);
+  const int rem = (int)(w - grp * per_group);
+  const int idx = rem / in_g;
+  it.head = grp * src.group + (rem - idx * in_g);
+  if (src.items != nullptr) {
+    const Item listed = src.items[idx];
+    it.start = listed.start;
+    it.len = listed.len;
+    it.q0 = listed.q0;
+  } else {
+    auto from = [&](int b) {
+      int c = 0;
+#pragma unroll
+      for (int u = 0; u < K; ++u) c += max(0, nb[u] - b);
+      return __reduce_add_sync(0xffffffffu, c);
+    };
+    int most = 0;
+#pragma unroll
+    for (int u = 0; u < K; ++u) most = max(most, nb[u]);
+    int lo = 0, hi = __reduce_max_sync(0xffffffffu, most) - 1;  // the largest b with from(b) > idx
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (from(mid) > idx) lo = mid;
+      else hi = mid - 1;
+    }
+    int r = idx - from(lo + 1);
+#pragma unroll
+    for (int u = 0; u < K; ++u) {
+      const unsigned mask = __ballot_sync(0xffffffffu, nb[u] > lo);
+      const int here = __popc(mask);
+      if (r >= 0 && r < here) {
+        const bool mine = ((mask >> lane) & 1u) && __popc(mask & ((1u << lane) - 1u)) == r;
+        const int from_lane = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+        it.start = __shfl_sync(0xffffffffu, st[u], from_lane);
+        it.len = __shfl_sync(0xffffffffu, ln[u], from_lane);
+        const int n = __shfl_sync(0xffffffffu, nb[u], from_lane);
+        it.q0 = (src.from_end ? n - 1 - lo : lo) * src.tile;
+      }
+      r -= here;
+    }
+  }
+  // the list may only be trusted as far as this call's own buffers
   return it.start >= 0 && it.q0 >= 0 && it.len > it.q0 &&
          (long long)it.start + it.len <= src.tokens;
 }
@@ -158,20 +167,13 @@ struct Walk {
   bool begun = false;
   // Moves on to the next item (the first call: to the first); head -1 at the end.
   __device__ __forceinline__ void next(const Source& src, Item& it) {
-    const long long works = (long long)src.max_items * src.kv_heads;
-    const int per_group = src.max_items * src.group;
-    while (true) {
-      unsigned w = blockIdx.x;
-      if (begun) {
-        if ((threadIdx.x & 31) == 0) w = gridDim.x + atomicAdd(src.next, 1u);
-        w = __shfl_sync(0xffffffffu, w, 0);
-      }
-      begun = true;
-      if (w >= works) break;
-      const int grp = (int)(w / (unsigned)per_group);
-      if (find_item(src, grp, (int)w - grp * per_group, it)) return;
+    unsigned w = blockIdx.x;
+    if (begun) {
+      if ((threadIdx.x & 31) == 0) w = gridDim.x + atomicAdd(src.next, 1u);
+      w = __shfl_sync(0xffffffffu, w, 0);
     }
-    it.head = -1;
+    begun = true;
+    if (!find_item(src, w, it)) it.head = -1;
   }
   // Once per CTA, after its last next(), by one thread: the last CTA leaves the counters at 0.
   __device__ __forceinline__ void end(const Source& src) {

@@ -150,11 +150,7 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
                           const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
   using Geo = KeyGeom<HD>;
   Item it;
-  {
-    const int per_group = p.src.max_items * p.src.group;
-    const int grp = (int)blockIdx.x / per_group;
-    if (!find_item(p.src, grp, (int)blockIdx.x - grp * per_group, it)) return;
-  }
+  if (!find_item(p.src, blockIdx.x, it)) return;  // the grid is an upper bound
   const int head = it.head;
   extern __shared__ uint8_t smem_raw[];
   float* sLse = reinterpret_cast<float*>(smem_raw);  // [QS][128]
@@ -1116,6 +1112,7 @@ extern "C" tsp_status tsp_packed_attention_bwd(
     int64_t ld_v, const tsp_bf16* o, int64_t ld_o, const float* lse, int64_t ld_lse,
     const tsp_bf16* dout, int64_t ld_do, tsp_bf16* dq, int64_t ld_dq, tsp_bf16* dk, int64_t ld_dk,
     tsp_bf16* dv, int64_t ld_dv, void* ws, void* stream) {
+  TSP_GUARD_BEGIN
   const char* what = "tsp_packed_attention_bwd";
   Shape s;
   TSP_TRY(make_shape(what, tokens, n_seqs, heads, kv_heads, head_dim, &s));
@@ -1183,4 +1180,5 @@ extern "C" tsp_status tsp_packed_attention_bwd(
   }
   if (head_dim == 64) return launch_bwd<64>(s, queries, keys, p, q, ld_q, dout, ld_do, k, ld_k, v, ld_v, st);
   return launch_bwd<128>(s, queries, keys, p, q, ld_q, dout, ld_do, k, ld_k, v, ld_v, st);
+  TSP_GUARD_END
 }

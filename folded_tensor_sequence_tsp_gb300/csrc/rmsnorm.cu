@@ -838,17 +838,21 @@ extern "C" {
 tsp_status tsp_rmsnorm_fwd(int64_t rows, int width, const tsp_bf16* x, const void* residual,
                            int residual_f32, const tsp_bf16* weight, float eps, void* h, tsp_bf16* y,
                            void* stream) {
+  TSP_GUARD_BEGIN
   return rmsnorm_fwd("tsp_rmsnorm_fwd", rows, width, x, residual, residual_f32, weight, eps, h, y,
                      false, 0, nullptr, static_cast<cudaStream_t>(stream));
+  TSP_GUARD_END
 }
 
 tsp_status tsp_rmsnorm_fwd_e4m3(int64_t rows, int width, const tsp_bf16* x, const void* residual,
                                 int residual_f32, const tsp_bf16* weight, float eps, int group,
                                 void* h, uint8_t* y, float* scales, void* stream) {
+  TSP_GUARD_BEGIN
   if (group != 0 && group != 128)
     return fail(TSP_ERR_UNSUPPORTED, "tsp_rmsnorm_fwd_e4m3: group 0 (a row) or 128 columns");
   return rmsnorm_fwd("tsp_rmsnorm_fwd_e4m3", rows, width, x, residual, residual_f32, weight, eps, h,
                      y, true, group, scales, static_cast<cudaStream_t>(stream));
+  TSP_GUARD_END
 }
 
 size_t tsp_rmsnorm_workspace_bytes(int64_t rows, int width) {
@@ -860,6 +864,7 @@ size_t tsp_rmsnorm_workspace_bytes(int64_t rows, int width) {
 tsp_status tsp_rmsnorm_bwd(int64_t rows, int width, const void* h, int h_f32, const tsp_bf16* weight,
                            float eps, const tsp_bf16* dy, const void* dh, void* dx, tsp_bf16* dx16,
                            float* dw, void* ws, void* stream) {
+  TSP_GUARD_BEGIN
   const char* what = "tsp_rmsnorm_bwd";
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TSP_TRY(check_shape(what, rows, width, eps));
@@ -898,6 +903,7 @@ tsp_status tsp_rmsnorm_bwd(int64_t rows, int width, const void* h, int h_f32, co
   rmsnorm_dw_kernel<<<(width + 31) / 32, 1024, 0, s>>>(p.partial, ctas, width, dw);
   e = cudaGetLastError();
   return e == cudaSuccess ? TSP_OK : cuda_fail(e, "rmsnorm backward: dw launch");
+  TSP_GUARD_END
 }
 
 }  // extern "C"

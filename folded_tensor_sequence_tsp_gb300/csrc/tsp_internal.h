@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include <initializer_list>
+#include <new>
 #include <string>
 
 #include "../../include/tsp.h"
@@ -86,6 +87,17 @@ template <class T>
 T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
 }
+
+// Around the body of a C entry point: no C++ exception crosses the ABI.
+#define TSP_GUARD_BEGIN try {
+#define TSP_GUARD_END                                           \
+  }                                                             \
+  catch (const std::bad_alloc&) {                               \
+    return fail(TSP_ERR_INVALID_ARG, "host allocation failed");  \
+  }                                                             \
+  catch (...) {                                                 \
+    return fail(TSP_ERR_INVALID_ARG, "unexpected host exception"); \
+  }
 
 // Argument checks of the C entry points (they set the error message).
 inline tsp_status check_ptrs(std::initializer_list<const void*> ptrs, const char* what) {
