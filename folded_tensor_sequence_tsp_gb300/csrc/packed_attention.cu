@@ -62,22 +62,39 @@ __device__ __forceinline__ uint32_t tm_o(int t) { return t ? 384u : 128u; }
 // ------------------------------------------------------------------ work lists
 constexpr int LIST_THREADS = 1024;
 
-// f(start, len, first token) for every item: a thread fetches one sequence, then each warp
-// walks its 32 sequences, lane by lane over the items of one.
+// f(any, start, len, first token) for every item, by whole warps (lanes with `any` false have
+// none): a thread fetches one sequence and takes it if it is a single item; of the others, a
+// warp walks one sequence after the other, lane by lane over its items.
 template <class F>
 __device__ __forceinline__ void each_item(const int32_t* starts, int n, int tile, F f) {
   const int lane = threadIdx.x & 31;
   for (int base = 0; base < n; base += LIST_THREADS) {
     const int i = base + threadIdx.x;
-    const int start = i < n ? starts[i] : 0, end = i < n ? starts[i + 1] : 0;
-    const unsigned some = __ballot_sync(0xffffffffu, end > start);
-    for (unsigned left = some; left; left &= left - 1) {
+    const int start = i < n ? starts[i] : 0, len = i < n ? starts[i + 1] - start : 0;
+    f(len > 0 && len <= tile, start, len, 0);
+    for (unsigned left = __ballot_sync(0xffffffffu, len > tile); left; left &= left - 1) {
       const int from = __ffs(left) - 1;
       const int s = __shfl_sync(0xffffffffu, start, from);
-      const int len = __shfl_sync(0xffffffffu, end, from) - s;
-      for (long long q0 = (long long)lane * tile; q0 < len; q0 += 32ll * tile) f(s, len, (int)q0);
+      const int m = __shfl_sync(0xffffffffu, len, from);
+      for (long long q0 = 0; q0 < m; q0 += 32ll * tile) {
+        const long long mine = q0 + (long long)lane * tile;
+        f(mine < m, s, m, (int)mine);
+      }
     }
   }
+}
+
+// Adds one to counter[b] for every lane with `any` and returns the lane's own number, with one
+// atomic per distinct b of the warp: most items of a batch of short sequences cost the same.
+__device__ __forceinline__ int claim(int* counter, int b, bool any) {
+  const unsigned active = __ballot_sync(0xffffffffu, any);
+  if (!any) return -1;
+  const int lane = threadIdx.x & 31;
+  const unsigned peers = __match_any_sync(active, b);
+  const int leader = __ffs(peers) - 1;
+  int first = 0;
+  if (lane == leader) first = atomicAdd(&counter[b], __popc(peers));
+  return __shfl_sync(peers, first, leader) + __popc(peers & ((1u << lane) - 1u));
 }
 
 __global__ void __launch_bounds__(LIST_THREADS)
@@ -103,7 +120,9 @@ __global__ void __launch_bounds__(LIST_THREADS)
                                 : (min((long long)len, (long long)q0 + l.tile) - 1) / TILE;
     return min(cost >> l.shift, 1023);
   };
-  each_item(starts, n, l.tile, [&](int, int len, int q0) { atomicAdd(&hist[bucket(len, q0)], 1); });
+  each_item(starts, n, l.tile, [&](bool any, int, int len, int q0) {
+    claim(hist, any ? bucket(len, q0) : 0, any);
+  });
   __syncthreads();
   // first slot of each bucket, the costliest bucket first
   const int mine = hist[1023 - tid];
@@ -130,9 +149,9 @@ __global__ void __launch_bounds__(LIST_THREADS)
   if (tid == LIST_THREADS - 1) *l.count = min(incl, l.max_items);
   __syncthreads();
   // the order inside a bucket may change from run to run: every item is its own CTA's work
-  each_item(starts, n, l.tile, [&](int s, int len, int q0) {
-    const int slot = atomicAdd(&hist[bucket(len, q0)], 1);
-    if (slot < l.max_items) l.items[slot] = Item{s, len, q0, 0};
+  each_item(starts, n, l.tile, [&](bool any, int s, int len, int q0) {
+    const int slot = claim(hist, any ? bucket(len, q0) : 0, any);
+    if (any && slot < l.max_items) l.items[slot] = Item{s, len, q0, 0};
   });
 }
 

@@ -13,11 +13,7 @@
 //             dO in TMEM as A operands. It also forms Delta, from its rows of o and dO, or
 //             from P and dP where one key tile holds all keys of its rows, and leaves it for
 //             the key side.
-//   key side  a CTA per item (a persistent one that walks the items, as the query side's, was
-//             slower from a few tiles per item on: 3.47 against 3.27 ms at 16381 tokens, 20
-//             against 17 us at 1000; faster only for sequences of up to 64 tokens, by a tenth)
-//             owns 128 keys of one key head and streams every query tile that sees
-//             them: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q. A tile's rows
+//   key side  a CTA owns 128 keys of one key head and streams every query tile that sees them: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q. A tile's rows
 //             are all heads of the group, so the group's sum needs nothing more: it happens
 //             in the fp32 accumulators, in a fixed order.
 // P and dS are rounded to bf16 as operands of the tensor core, 2^-9 relative per term; dS is
@@ -27,7 +23,8 @@
 // those past TPT x G when G does not divide 128) enter the key side's sums with P = 0: their
 // lse is +infinity and their Q and dO rows are zeros in shared memory, so nothing that lies
 // behind the sequence can reach a sum. The query side clears its last K and V tile the same
-// way. Pairs above the diagonal are set to 0 by selection, in P and in dS.
+// way. Pairs above the diagonal are set to 0 by selection in P, and on the query side, where
+// dP may hold a later key's infinity, in dS as well.
 //
 // Schedules (per streamed tile j; products of one issuing lane execute in order): query side
 // S(j+1), dQ(j), dP(j+1); key side dV(j), S^T(j+1), dK(j), dP^T(j+1) with two 128-column
@@ -75,13 +72,14 @@ constexpr int ITEMS = 4;  // items between the producer and the slowest reader
 template <int HD>
 struct KeyGeom {
   static constexpr int THREADS = 352;  // TMA, MMA, 2 x 4 element-wise warps, statistics
+  static constexpr int READERS = 10;   // of an item: MMA lane, statistics, 8 warps
   static constexpr int BOXES = HD / 64;
   static constexpr uint32_t TILE_B = 128 * HD * 2;
   // Q tiles (with lse) and dO tiles (with Delta) in separate rings: a Q tile is read last
   // by dK, a full tile after its scores, so it gets the deeper ring
   static constexpr int QS = 3;
   static constexpr int OS = 2;
-  static constexpr uint32_t SMALL = (QS + OS) * 512 + 256;
+  static constexpr uint32_t SMALL = (QS + OS) * 512 + ITEMS * 16 + 384;
   static constexpr uint32_t TILES_OFF = (SMALL + 1023) / 1024 * 1024;
   static constexpr size_t USED = TILES_OFF + (size_t)(2 + QS + OS) * TILE_B;
   static constexpr size_t SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
@@ -149,27 +147,28 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
                           const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
   using Geo = KeyGeom<HD>;
-  Item it;
-  if (!find_item(p.src, blockIdx.x, it)) return;  // the grid is an upper bound
-  const int head = it.head;
+  constexpr uint32_t QS = Geo::QS, OS = Geo::OS;
   extern __shared__ uint8_t smem_raw[];
   float* sLse = reinterpret_cast<float*>(smem_raw);  // [QS][128]
-  float* sDel = sLse + Geo::QS * 128;                // [OS][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sDel + Geo::OS * 128);
-  uint64_t* kv_full = bars;                // [1]
-  uint64_t* q_full = kv_full + 1;          // [QS] Q tile (TMA) and its lse (statistics warp)
-  uint64_t* q_empty = q_full + Geo::QS;    // [QS]
-  uint64_t* o_full = q_empty + Geo::QS;    // [OS] dO tile and its Delta
-  uint64_t* o_empty = o_full + Geo::OS;    // [OS]
-  uint64_t* s_full = o_empty + Geo::OS;    // scores of the current tile written
-  uint64_t* g_full = s_full + 1;           // dP^T of the current tile written
-  uint64_t* p_ready = g_full + 1;          // packed P^T stored (8 warps)
-  uint64_t* g_taken = p_ready + 1;         // dP^T loaded into registers (8 warps)
-  uint64_t* ds_ready = g_taken + 1;        // packed dS^T stored (8 warps)
-  uint64_t* acc_done = ds_ready + 1;
-  uint64_t* tail_q = acc_done + 1;         // the last Q tile is cleared behind the sequence
-  uint64_t* tail_o = tail_q + 1;           // and the last dO tile
-  uint64_t* drain = tail_o + 1;
+  float* sDel = sLse + QS * 128;                     // [OS][128]
+  Item* items = reinterpret_cast<Item*>(sDel + OS * 128);           // [ITEMS]
+  uint64_t* item_full = reinterpret_cast<uint64_t*>(items + ITEMS); // [ITEMS]
+  uint64_t* item_empty = item_full + ITEMS;  // [ITEMS]
+  uint64_t* kv_full = item_empty + ITEMS;    // the item's K and V
+  uint64_t* kv_empty = kv_full + 1;          // its S^T and dP^T are all computed
+  uint64_t* q_full = kv_empty + 1;           // [QS] Q tile (TMA) and its lse (statistics warp)
+  uint64_t* q_empty = q_full + QS;           // [QS]
+  uint64_t* q_tail = q_empty + QS;           // [QS] a ragged Q tile is cleared behind the sequence
+  uint64_t* o_full = q_tail + QS;            // [OS] dO tile and its Delta
+  uint64_t* o_empty = o_full + OS;           // [OS]
+  uint64_t* o_tail = o_empty + OS;           // [OS]
+  uint64_t* s_full = o_tail + OS;            // scores of the current tile written
+  uint64_t* g_full = s_full + 1;             // dP^T of the current tile written
+  uint64_t* p_ready = g_full + 1;            // packed P^T stored (8 warps)
+  uint64_t* g_taken = p_ready + 1;           // dP^T loaded into registers (8 warps)
+  uint64_t* ds_ready = g_taken + 1;          // packed dS^T stored (8 warps)
+  uint64_t* acc_done = ds_ready + 1;         // the item's dK and dV complete
+  uint64_t* drain = acc_done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t tiles_off = tiles_offset(smem_raw, Geo::SMALL, Geo::TILES_OFF);
@@ -179,24 +178,26 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
   }
   uint8_t* sK = smem_raw + tiles_off;
   uint8_t* sV = sK + Geo::TILE_B;
-  uint8_t* sQ0 = sV + Geo::TILE_B;               // [QS]
-  uint8_t* sO0 = sQ0 + Geo::QS * Geo::TILE_B;    // [OS]
+  uint8_t* sQ0 = sV + Geo::TILE_B;        // [QS]
+  uint8_t* sO0 = sQ0 + QS * Geo::TILE_B;  // [OS]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int k0 = it.q0;              // first key
-  const int first = k0 / p.TPT;      // the first query tile that sees a key
-  const int n_inner = (it.len - 1) / p.TPT + 1 - first;
-  const bool ragged = (first + n_inner) * p.TPT > it.len;
-
   if (threadIdx.x == 0) {
+    for (int s = 0; s < ITEMS; ++s) {
+      mbar_init(&item_full[s], 1);
+      mbar_init(&item_empty[s], Geo::READERS);
+    }
     mbar_init(kv_full, 1);
-    for (int s = 0; s < Geo::QS; ++s) {
+    mbar_init(kv_empty, 1);
+    for (uint32_t s = 0; s < QS; ++s) {
       mbar_init(&q_full[s], 2);
       mbar_init(&q_empty[s], 1);
+      mbar_init(&q_tail[s], 1);
     }
-    for (int s = 0; s < Geo::OS; ++s) {
+    for (uint32_t s = 0; s < OS; ++s) {
       mbar_init(&o_full[s], 2);
       mbar_init(&o_empty[s], 1);
+      mbar_init(&o_tail[s], 1);
     }
     mbar_init(s_full, 1);
     mbar_init(g_full, 1);
@@ -204,126 +205,168 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
     mbar_init(g_taken, 8);
     mbar_init(ds_ready, 8);
     mbar_init(acc_done, 1);
-    mbar_init(tail_q, 1);
-    mbar_init(tail_o, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    // K and V are under way while the CTA sets itself up
-    mbar_arrive_expect_tx(kv_full, 2 * Geo::TILE_B);
-#pragma unroll
-    for (int b = 0; b < Geo::BOXES; ++b) {
-      tma_load_2d(sK + b * BOX_BYTES, &tmK, kv_full, head * HD + 64 * b, it.start + k0);
-      tma_load_2d(sV + b * BOX_BYTES, &tmV, kv_full, head * HD + 64 * b, it.start + k0);
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmDO);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  uint32_t tmem = 0;
+  if (warp == 0) {
+    __syncwarp();
+    start_arrive<Geo::THREADS>();
+  } else {
+    if (warp == 1) {
+      tmem_alloc(tmem_slot, TMEM_COLS);
+      tmem_relinquish();
     }
+    if (p.RU < 128) {
+      // rows that no TMA box writes: zeros for the whole run
+      for (uint32_t s = 0; s < QS + OS; ++s)
+        clear_rows(sQ0 + s * Geo::TILE_B, Geo::BOXES, p.RU, threadIdx.x - 32, Geo::THREADS - 32);
+      fence_proxy_async();
+    }
+    tc_fence_before();
+    start_sync<Geo::THREADS>();
+    tc_fence_after();
+    tmem = *tmem_slot;
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, TMEM_COLS);
-    tmem_relinquish();
-  }
-  if (p.RU < 128) {
-    // rows that no TMA box writes: zeros for the whole run
-    for (int s = 0; s < Geo::QS + Geo::OS; ++s)
-      clear_rows(sQ0 + s * Geo::TILE_B, Geo::BOXES, p.RU, threadIdx.x, Geo::THREADS);
-    fence_proxy_async();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   WaitBound wb{p.status, p.limit_ns, abort_flag};
-  const uint32_t box_rows = (uint32_t)(Geo::BOXES * 128) * (uint32_t)p.RU;
+  // streamed query tiles of an item: from the first that sees one of its keys
+  auto first_of = [&](const Item& it) { return it.q0 / p.TPT; };
+  auto inner_of = [&](const Item& it) { return (it.len - 1) / p.TPT + 1 - it.q0 / p.TPT; };
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ producer
-      int q_last[Geo::QS], o_last[Geo::OS];
-      for (int s = 0; s < Geo::QS; ++s) q_last[s] = -1;
-      for (int s = 0; s < Geo::OS; ++s) o_last[s] = -1;
-      bool ok = true;
-      for (int idx = 0; idx < n_inner; ++idx) {
-        const int r0 = it.start + (first + idx) * p.TPT;
-        const int qs = idx % Geo::QS, os = idx % Geo::OS;
-        const uint32_t qph = (uint32_t)((idx / Geo::QS) & 1), oph = (uint32_t)((idx / Geo::OS) & 1);
-        ok = mbar_wait(&q_empty[qs], qph ^ 1u, wb, SITE_PACKED_PRODUCER);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&q_full[qs], box_rows);
+    // -------------------------------------------------------------- producer
+    const uint32_t box_rows = (uint32_t)(Geo::BOXES * 128) * (uint32_t)p.RU;
+    Item next{};
+    Walk walk;
+    walk.next(p.src, next);
+    bool ok = true;
+    uint32_t n_items = 0, c = 0;  // items and streamed tiles so far
+    while (ok) {
+      const Item it = next;
+      const int slot = (int)(n_items % ITEMS);
+      if (lane == 0) {
+        ok = mbar_wait(&item_empty[slot], ((n_items / ITEMS) & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+        if (ok) {
+          items[slot] = it;
+          mbar_arrive(&item_full[slot]);
+        }
+        if (ok && it.head >= 0) {
+          ok = mbar_wait(kv_empty, (n_items & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+          if (ok) {
+            mbar_arrive_expect_tx(kv_full, 2 * Geo::TILE_B);
 #pragma unroll
-        for (int b = 0; b < Geo::BOXES; ++b)
-          tma_load_3d(sQ0 + qs * Geo::TILE_B + b * BOX_BYTES, &tmQ, &q_full[qs], 64 * b, head * p.G, r0);
-        q_last[qs] = (int)qph;
-        ok = mbar_wait(&o_empty[os], oph ^ 1u, wb, SITE_PACKED_PRODUCER);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&o_full[os], box_rows);
+            for (int b = 0; b < Geo::BOXES; ++b) {
+              tma_load_2d(sK + b * BOX_BYTES, &tmK, kv_full, it.head * HD + 64 * b, it.start + it.q0);
+              tma_load_2d(sV + b * BOX_BYTES, &tmV, kv_full, it.head * HD + 64 * b, it.start + it.q0);
+            }
+          }
+          const int n = inner_of(it);
+          int r0 = it.start + first_of(it) * p.TPT;
+          for (int j = 0; ok && j < n; ++j, ++c, r0 += p.TPT) {
+            const uint32_t qs = c % QS, os = c % OS;
+            ok = mbar_wait(&q_empty[qs], ((c / QS) & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&q_full[qs], box_rows);
 #pragma unroll
-        for (int b = 0; b < Geo::BOXES; ++b)
-          tma_load_3d(sO0 + os * Geo::TILE_B + b * BOX_BYTES, &tmDO, &o_full[os], 64 * b, head * p.G, r0);
-        o_last[os] = (int)oph;
+            for (int b = 0; b < Geo::BOXES; ++b)
+              tma_load_3d(sQ0 + qs * Geo::TILE_B + b * BOX_BYTES, &tmQ, &q_full[qs], 64 * b,
+                          it.head * p.G, r0);
+            ok = mbar_wait(&o_empty[os], ((c / OS) & 1u) ^ 1u, wb, SITE_PACKED_PRODUCER);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&o_full[os], box_rows);
+#pragma unroll
+            for (int b = 0; b < Geo::BOXES; ++b)
+              tma_load_3d(sO0 + os * Geo::TILE_B + b * BOX_BYTES, &tmDO, &o_full[os], 64 * b,
+                          it.head * p.G, r0);
+          }
+        }
       }
-      // copies in flight land before the CTA ends. After a wait that gave up, the
-      // statistics warp may have left a phase without its arrival: these waits then end
-      // at their bound.
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok || it.head < 0) break;
+      ++n_items;
+      walk.next(p.src, next);
+    }
+    if (lane == 0) {
+      walk.end(p.src);
+      // copies in flight land before the CTA ends
       WaitBound wd{p.status, p.limit_ns, nullptr};
-      mbar_wait(kv_full, 0, wd, SITE_DRAIN);
-      for (int s = 0; s < Geo::QS; ++s)
-        if (q_last[s] >= 0) mbar_wait(&q_full[s], (uint32_t)q_last[s], wd, SITE_DRAIN);
-      for (int s = 0; s < Geo::OS; ++s)
-        if (o_last[s] >= 0) mbar_wait(&o_full[s], (uint32_t)o_last[s], wd, SITE_DRAIN);
+      if (n_items > 0) mbar_wait(kv_full, (n_items - 1) & 1u, wd, SITE_DRAIN);
+      for (uint32_t b = c > QS ? c - QS : 0; b < c; ++b)
+        mbar_wait(&q_full[b % QS], (b / QS) & 1u, wd, SITE_DRAIN);
+      for (uint32_t b = c > OS ? c - OS : 0; b < c; ++b)
+        mbar_wait(&o_full[b % OS], (b / OS) & 1u, wd, SITE_DRAIN);
+      if (!ok) let_copies_land();
     }
   } else if (warp == 10) {
     // -------------------------------------------------------------- statistics
-    // lse and Delta of each streamed tile: row r = token * G + head; four rows per lane,
-    // fetched a tile ahead
-    const float* lse_h = p.lse + (long long)head * p.G * p.ld_lse + it.start;
-    const float* del_h = p.delta + (long long)head * p.G * p.ld_delta + it.start;
-    float ls[4], de[4];
-    auto fetch = [&](int idx) {
-      const int t0 = (first + idx) * p.TPT;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int r = u * 32 + lane, tok = r / p.G, g = r - tok * p.G;
-        const bool is = r < p.RU && t0 + tok < it.len;
-        ls[u] = is ? lse_h[(long long)g * p.ld_lse + t0 + tok] : INFINITY;
-        de[u] = is ? del_h[(long long)g * p.ld_delta + t0 + tok] : 0.f;
-      }
-    };
-    fetch(0);
+    // lse and Delta of each streamed tile, row r = token * G + head, four rows per lane,
+    // fetched a tile ahead; then zeros behind the sequence in its last Q and dO tiles
     bool ok = true;
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, wb, SITE_PACKED_PRODUCER)) != 0;
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, wb, SITE_PACKED_PRODUCER)) != 0;
     };
-    for (int idx = 0; ok && idx < n_inner; ++idx) {
-      const int qs = idx % Geo::QS, os = idx % Geo::OS;
-      const uint32_t qph = (uint32_t)((idx / Geo::QS) & 1), oph = (uint32_t)((idx / Geo::OS) & 1);
-      ok = warp_wait(&q_empty[qs], qph ^ 1u);
-      if (!ok) break;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) sLse[qs * 128 + u * 32 + lane] = ls[u];
+    uint32_t n_items = 0, c = 0;
+    while (ok) {
+      const int slot = (int)(n_items % ITEMS);
+      if (!warp_wait(&item_full[slot], n_items / ITEMS)) break;
+      ++n_items;
+      const Item it = items[slot];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[qs]);
-      ok = warp_wait(&o_empty[os], oph ^ 1u);
-      if (!ok) break;
+      if (lane == 0) mbar_arrive(&item_empty[slot]);
+      if (it.head < 0) break;
+      const int n = inner_of(it);
+      const float* lse_h = p.lse + (long long)it.head * p.G * p.ld_lse + it.start;
+      const float* del_h = p.delta + (long long)it.head * p.G * p.ld_delta + it.start;
+      float ls[4], de[4];
+      auto fetch = [&](int t0) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) sDel[os * 128 + u * 32 + lane] = de[u];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&o_full[os]);
-      if (idx + 1 < n_inner) fetch(idx + 1);
-    }
-    if (ok && ragged) {
-      const int last = n_inner - 1;
-      const int keep = (it.len - (first + last) * p.TPT) * p.G;  // rows of the sequence
-      const int qs = last % Geo::QS, os = last % Geo::OS;
-      if (warp_wait(&q_full[qs], (uint32_t)((last / Geo::QS) & 1))) {
+        for (int u = 0; u < 4; ++u) {
+          const int r = u * 32 + lane, tok = r / p.G, g = r - tok * p.G;
+          const bool is = r < p.RU && t0 + tok < it.len;
+          ls[u] = is ? lse_h[(long long)g * p.ld_lse + t0 + tok] : INFINITY;
+          de[u] = is ? del_h[(long long)g * p.ld_delta + t0 + tok] : 0.f;
+        }
+      };
+      int t0 = first_of(it) * p.TPT;
+      fetch(t0);
+      for (int j = 0; ok && j < n; ++j, ++c, t0 += p.TPT) {
+        const uint32_t qs = c % QS, os = c % OS;
+        ok = warp_wait(&q_empty[qs], (c / QS) ^ 1u);
+        if (!ok) break;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sLse[qs * 128 + u * 32 + lane] = ls[u];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[qs]);
+        ok = warp_wait(&o_empty[os], (c / OS) ^ 1u);
+        if (!ok) break;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sDel[os * 128 + u * 32 + lane] = de[u];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_full[os]);
+        if (j + 1 < n) fetch(t0 + p.TPT);
+      }
+      // rows of the sequence in the item's last tile
+      const int keep = (it.len - (t0 - p.TPT)) * p.G;
+      if (ok && keep < p.RU) {
+        const uint32_t last = c - 1;
+        const uint32_t qs = last % QS, os = last % OS;
+        ok = warp_wait(&q_full[qs], last / QS);
+        if (!ok) break;
         clear_rows(sQ0 + qs * Geo::TILE_B, Geo::BOXES, keep, lane, 32);
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(tail_q);
-        if (warp_wait(&o_full[os], (uint32_t)((last / Geo::OS) & 1))) {
-          clear_rows(sO0 + os * Geo::TILE_B, Geo::BOXES, keep, lane, 32);
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(tail_o);
-        }
+        if (lane == 0) mbar_arrive(&q_tail[qs]);
+        ok = warp_wait(&o_full[os], last / OS);
+        if (!ok) break;
+        clear_rows(sO0 + os * Geo::TILE_B, Geo::BOXES, keep, lane, 32);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_tail[os]);
       }
     }
   } else if (warp == 1) {
@@ -340,88 +383,108 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
       const uint32_t k_lo = (uint32_t)dk0, k_hi = (uint32_t)(dk0 >> 32);
       const uint32_t v_lo = (uint32_t)dv0, v_hi = (uint32_t)(dv0 >> 32);
       const uint32_t kq_hi = (uint32_t)(dq0 >> 32), mn_hi = (uint32_t)(dq0_mn >> 32);
-      auto issue_s = [&](int j) {
-        const uint32_t q_lo = (uint32_t)dq0 + (uint32_t)(j % Geo::QS) * (Geo::TILE_B / 16);
+      // c: streamed tiles so far, over all items; qs, os: their stages
+      auto issue_s = [&](uint32_t c, uint32_t qs) {
+        const uint32_t q_lo = (uint32_t)dq0 + qs * (Geo::TILE_B / 16);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ss_w(tmem + tm_s(j), k_lo + kmajor_step(kk), k_hi, q_lo + kmajor_step(kk), kq_hi,
+          mma_ss_w(tmem + tm_s((int)c), k_lo + kmajor_step(kk), k_hi, q_lo + kmajor_step(kk), kq_hi,
                    idesc_s, kk > 0 ? 1u : 0u);
         mma_commit(s_full);
       };
-      auto issue_g = [&](int j) {
-        const uint32_t o_lo = (uint32_t)do0 + (uint32_t)(j % Geo::OS) * (Geo::TILE_B / 16);
+      auto issue_g = [&](uint32_t c, uint32_t os) {
+        const uint32_t o_lo = (uint32_t)do0 + os * (Geo::TILE_B / 16);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
-          mma_ss_w(tmem + tm_g(j), v_lo + kmajor_step(kk), v_hi, o_lo + kmajor_step(kk), kq_hi,
+          mma_ss_w(tmem + tm_g((int)c), v_lo + kmajor_step(kk), v_hi, o_lo + kmajor_step(kk), kq_hi,
                    idesc_s, kk > 0 ? 1u : 0u);
         mma_commit(g_full);
       };
-      auto issue_dv = [&](int j) {
-        const uint32_t o_lo = (uint32_t)do0_mn + (uint32_t)(j % Geo::OS) * (Geo::TILE_B / 16);
+      auto issue_dv = [&](uint32_t c, uint32_t os, bool first) {
+        const uint32_t o_lo = (uint32_t)do0_mn + os * (Geo::TILE_B / 16);
 #pragma unroll
         for (int kk = 0; kk < TILE / 16; ++kk)
-          mma_ts_w(tmem + 0, tmem + packed_step(tm_s(j), kk), o_lo + (uint32_t)(kk * 128), mn_hi,
-                   idesc_acc, (j == 0 && kk == 0) ? 0u : 1u);
+          mma_ts_w(tmem + 0, tmem + packed_step(tm_s((int)c), kk), o_lo + (uint32_t)(kk * 128), mn_hi,
+                   idesc_acc, (first && kk == 0) ? 0u : 1u);
       };
-      auto issue_dk = [&](int j) {
-        const uint32_t q_lo = (uint32_t)dq0_mn + (uint32_t)(j % Geo::QS) * (Geo::TILE_B / 16);
+      auto issue_dk = [&](uint32_t c, uint32_t qs, bool first) {
+        const uint32_t q_lo = (uint32_t)dq0_mn + qs * (Geo::TILE_B / 16);
 #pragma unroll
         for (int kk = 0; kk < TILE / 16; ++kk)
-          mma_ts_w(tmem + HD, tmem + packed_step(tm_s(j) + 32, kk), q_lo + (uint32_t)(kk * 128),
-                   mn_hi, idesc_acc, (j == 0 && kk == 0) ? 0u : 1u);
+          mma_ts_w(tmem + HD, tmem + packed_step(tm_s((int)c) + 32, kk), q_lo + (uint32_t)(kk * 128),
+                   mn_hi, idesc_acc, (first && kk == 0) ? 0u : 1u);
       };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return mbar_wait_poll(bar, parity, wb, SITE_PACKED_MMA);
+        return mbar_wait_poll(bar, parity & 1u, wb, SITE_PACKED_MMA);
       };
-      // tile j's Q (dO) is in shared memory, and cleared where it is the ragged last one
-      auto wait_q = [&](int j) {
-        return wait(&q_full[j % Geo::QS], (uint32_t)((j / Geo::QS) & 1)) &&
-               (!ragged || j != n_inner - 1 || wait(tail_q, 0));
+      // The Q (dO) tile of a stage is in place, and cleared if it is its sequence's ragged last
+      // one. Bit st of ph_q, ph_o, turn_q and turn_o is the phase of the stage's barrier.
+      uint32_t ph_q = 0, ph_o = 0, turn_q = 0, turn_o = 0;
+      auto landed = [&](uint64_t* full, uint64_t* tail, uint32_t st, uint32_t& ph, uint32_t& turn, bool ragged) {
+        if (!wait(&full[st], ph >> st)) return false;
+        ph ^= 1u << st;
+        if (!ragged) return true;
+        const bool ok = wait(&tail[st], turn >> st);
+        turn ^= 1u << st;
+        return ok;
       };
-      auto wait_o = [&](int j) {
-        return wait(&o_full[j % Geo::OS], (uint32_t)((j / Geo::OS) & 1)) &&
-               (!ragged || j != n_inner - 1 || wait(tail_o, 0));
-      };
-      bool ok = wait(kv_full, 0) && wait_q(0);
-      if (ok) {
-        tc_fence_after();
-        issue_s(0);
-      }
-      ok = ok && wait_o(0);
-      if (ok) {
-        tc_fence_after();
-        issue_g(0);
-      }
-      // per tile j: dV(j) once P^T(j) is stored; S^T(j+1) into the dP^T(j) region once the
-      // element-wise warps hold dP^T(j); dK(j) once dS^T(j) is stored; dP^T(j+1) into the
-      // region of tile j, after dV(j) and dK(j) have read it (in issue order)
-      for (int j = 0; ok && j < n_inner; ++j) {
-        const uint32_t ph = (uint32_t)(j & 1);
-        const bool more = j + 1 < n_inner;
-        ok = wait(p_ready, ph);
+      auto wait_q = [&](uint32_t st, bool ragged) { return landed(q_full, q_tail, st, ph_q, turn_q, ragged); };
+      auto wait_o = [&](uint32_t st, bool ragged) { return landed(o_full, o_tail, st, ph_o, turn_o, ragged); };
+      bool ok = true;
+      uint32_t n_items = 0, c = 0, qs = 0;
+      while (ok) {
+        const int slot = (int)(n_items % ITEMS);
+        ok = wait(&item_full[slot], n_items / ITEMS);
+        if (!ok) break;
+        const Item it = items[slot];
+        mbar_arrive(&item_empty[slot]);
+        if (it.head < 0) break;
+        const int n = inner_of(it);
+        const bool ragged = (first_of(it) + n) * p.TPT > it.len;
+        // S^T(c) goes over the dP^T(c - 1) of the item before, once that is in registers
+        ok = wait(kv_full, n_items) && wait_q(qs, ragged && n == 1) && (c == 0 || wait(g_taken, c - 1));
         if (!ok) break;
         tc_fence_after();
-        issue_dv(j);
-        if (more) {
-          ok = wait(g_taken, ph) && wait_q(j + 1);
-          if (!ok) break;
-          tc_fence_after();
-          issue_s(j + 1);
-        }
-        ok = wait(ds_ready, ph);
+        issue_s(c, qs);
+        ok = wait_o(c % OS, ragged && n == 1);
         if (!ok) break;
         tc_fence_after();
-        issue_dk(j);
-        mma_commit(&q_empty[j % Geo::QS]);
-        mma_commit(&o_empty[j % Geo::OS]);
-        if (more) {
-          ok = wait_o(j + 1);
+        issue_g(c, c % OS);
+        if (n == 1) mma_commit(kv_empty);
+        // per tile: dV once P^T is stored; the next S^T into the dP^T region once the
+        // element-wise warps hold dP^T; dK once dS^T is stored; the next dP^T into the
+        // region of this tile, after dV and dK have read it (in issue order)
+        for (int j = 0; j < n; ++j, ++c) {
+          const bool more = j + 1 < n, last_next = ragged && j + 2 == n;
+          const uint32_t os = c % OS, qn = qs + 1 == QS ? 0 : qs + 1;
+          ok = wait(p_ready, c);
           if (!ok) break;
           tc_fence_after();
-          issue_g(j + 1);
+          issue_dv(c, os, j == 0);
+          if (more) {
+            ok = wait(g_taken, c) && wait_q(qn, last_next);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(c + 1, qn);
+          }
+          ok = wait(ds_ready, c);
+          if (!ok) break;
+          tc_fence_after();
+          issue_dk(c, qs, j == 0);
+          mma_commit(&q_empty[qs]);
+          mma_commit(&o_empty[os]);
+          qs = qn;
+          if (more) {
+            ok = wait_o(os ^ 1u, last_next);
+            if (!ok) break;
+            tc_fence_after();
+            issue_g(c + 1, os ^ 1u);
+            if (j + 2 == n) mma_commit(kv_empty);
+          }
         }
+        if (ok) mma_commit(acc_done);
+        ++n_items;
       }
-      if (ok) mma_commit(acc_done);
       mma_commit(drain);
       WaitBound wd{p.status, p.limit_ns, nullptr};
       mbar_wait(drain, 0, wd, SITE_DRAIN);
@@ -430,130 +493,147 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
     // -------------------------------------------------------------- element-wise
     const int g = (warp - 2) >> 2;  // query rows [64g, 64g + 64) of every tile
     const int qq = warp & 3;        // TMEM lane quarter
-    const int kp = k0 + qq * 32 + lane;  // this thread's key, as a position of the sequence
     const uint32_t lane_base = tmem + ((uint32_t)(qq * 32) << 16);
     const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
-    bool ok = true;
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool mine = mbar_wait(bar, parity, wb, SITE_PACKED_SOFTMAX);
+      const bool mine = mbar_wait(bar, parity & 1u, wb, SITE_PACKED_SOFTMAX);
       return __all_sync(0xffffffffu, mine) != 0;
     };
-    for (int j = 0; j < n_inner; ++j) {
-      const uint32_t ph = (uint32_t)(j & 1);
-      const int qs = j % Geo::QS, os = j % Geo::OS;
-      if (!warp_wait(s_full, ph) || !warp_wait(&q_full[qs], (uint32_t)((j / Geo::QS) & 1))) {
-        ok = false;
-        break;
+    // The loop below is short of issue slots: stages, phases and addresses step along instead
+    // of being computed from the tile's number (remainders by 3 alone cost 0.1 of 1.8 us a tile).
+    uint32_t n_items = 0, c = 0;              // items and streamed tiles so far
+    uint32_t qs = 0, qph = 0;                 // stage and phase of the Q ring
+    uint32_t s_t = lane_base + tm_s(0) + (uint32_t)(GCOLS * g);  // this tile's scores
+    uint32_t g_t = lane_base + tm_g(0) + (uint32_t)(GCOLS * g);  // and its dP^T
+    while (true) {
+      const int slot = (int)(n_items % ITEMS);
+      if (!warp_wait(&item_full[slot], n_items / ITEMS)) break;
+      // what the epilogue needs of the item is read again there, and only then is the slot
+      // released: the loop below has no registers to spare
+      int n, t0, kp;
+      {
+        const Item it = items[slot];
+        if (it.head < 0) break;
+        n = inner_of(it);
+        t0 = first_of(it) * p.TPT;
+        kp = it.q0 + qq * 32 + lane;  // this thread's key, as a position of the sequence
       }
-      tc_fence_after();
-      const uint32_t s_t = lane_base + tm_s(j) + (uint32_t)(GCOLS * g);
-      const uint32_t g_t = lane_base + tm_g(j) + (uint32_t)(GCOLS * g);
-      uint32_t sv[2][32];
-      tmem_ld32(s_t, sv[0]);
-      tmem_ld32(s_t + 32, sv[1]);
-      const float4* sl4 = reinterpret_cast<const float4*>(sLse + qs * 128 + g * GCOLS);
-      // row c of the tile is the query at token t0 + c / G: it sees this key iff
-      // c >= (kp - t0) G
-      const int t0 = (first + j) * p.TPT;
-      const bool masked = t0 < k0 + TILE - 1;
-      const int c_min = max(kp - t0, 0) * p.G - g * GCOLS;
-      tmem_ld_wait();
-      // P^T = exp2(s * scale_log2 - lse[q]), kept in fp32 for dS^T and stored as bf16
-      float pf[64];
-      uint32_t pp[32];
-      auto p_chunk = [&](const uint32_t (&s)[32], int c0, auto mask_tag) {
-        constexpr bool MASK = decltype(mask_tag)::value;
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 l4 = sl4[(c0 + e) >> 2];
-          const uint64_t nl[2] = {f2_pack(-l4.x, -l4.y), f2_pack(-l4.z, -l4.w)};
-#pragma unroll
-          for (int u = 0; u < 4; u += 2) {
-            float x0, x1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e + u]), __uint_as_float(s[e + u + 1])),
-                             scale2, nl[u >> 1]),
-                      x0, x1);
-            float p0 = ex2(x0), p1 = ex2(x1);
-            if constexpr (MASK) {
-              p0 = c0 + e + u >= c_min ? p0 : 0.f;
-              p1 = c0 + e + u + 1 >= c_min ? p1 : 0.f;
-            }
-            pf[c0 + e + u] = p0;
-            pf[c0 + e + u + 1] = p1;
-            pp[(c0 + e + u) >> 1] = pack_bf16x2(p0, p1);
-          }
+      bool ok = true;
+      for (int j = 0; j < n; ++j, ++c, t0 += p.TPT) {
+        const uint32_t os = c & 1u;
+        if (!warp_wait(s_full, c) || !warp_wait(&q_full[qs], qph)) {
+          ok = false;
+          break;
         }
-      };
-      if (masked) {
-        p_chunk(sv[0], 0, std::true_type{});
-        p_chunk(sv[1], 32, std::true_type{});
-      } else {
-        p_chunk(sv[0], 0, std::false_type{});
-        p_chunk(sv[1], 32, std::false_type{});
-      }
-      tmem_st32(s_t, pp);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_ready);
-      if (!warp_wait(g_full, ph) || !warp_wait(&o_full[os], (uint32_t)((j / Geo::OS) & 1))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      uint32_t gv[2][32];
-      tmem_ld32(g_t, gv[0]);
-      tmem_ld32(g_t + 32, gv[1]);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(g_taken);
-      // dS^T = P^T (dP^T - Delta[q])
-      const float4* sd4 = reinterpret_cast<const float4*>(sDel + os * 128 + g * GCOLS);
-      auto ds_chunk = [&](int c, auto mask_tag) {
-        constexpr bool MASK = decltype(mask_tag)::value;
-        uint32_t dd[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 d4 = sd4[(32 * c + e) >> 2];
-          const uint64_t dl[2] = {f2_pack(d4.x, d4.y), f2_pack(d4.z, d4.w)};
-#pragma unroll
-          for (int u = 0; u < 4; u += 2) {
-            float d0, d1;
-            f2_unpack(f2_mul(f2_pack(pf[32 * c + e + u], pf[32 * c + e + u + 1]),
-                             f2_sub(f2_pack(__uint_as_float(gv[c][e + u]),
-                                            __uint_as_float(gv[c][e + u + 1])),
-                                    dl[u >> 1])),
-                      d0, d1);
-            if constexpr (MASK) {  // 0 times a dP that is not finite is not 0
-              d0 = 32 * c + e + u >= c_min ? d0 : 0.f;
-              d1 = 32 * c + e + u + 1 >= c_min ? d1 : 0.f;
+        tc_fence_after();
+        uint32_t sv[2][32];
+        tmem_ld32(s_t, sv[0]);
+        tmem_ld32(s_t + 32, sv[1]);
+        const float4* sl4 = reinterpret_cast<const float4*>(sLse + qs * 128 + g * GCOLS);
+        // row e of the tile is the query at token t0 + e / G: it sees this key iff
+        // e >= (kp - t0) G
+        const bool masked = t0 < kp - (qq * 32 + lane) + TILE - 1;
+        const int c_min = max(kp - t0, 0) * p.G - g * GCOLS;
+        tmem_ld_wait();
+        // P^T = exp2(s * scale_log2 - lse[q]), kept in fp32 for dS^T and stored as bf16
+        float pf[64];
+        uint32_t pp[32];
+        auto p_chunk = [&](const uint32_t (&s)[32], int c0, auto mask_tag) {
+          constexpr bool MASK = decltype(mask_tag)::value;
+  #pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 l4 = sl4[(c0 + e) >> 2];
+            const uint64_t nl[2] = {f2_pack(-l4.x, -l4.y), f2_pack(-l4.z, -l4.w)};
+  #pragma unroll
+            for (int u = 0; u < 4; u += 2) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e + u]), __uint_as_float(s[e + u + 1])),
+                               scale2, nl[u >> 1]),
+                        x0, x1);
+              float p0 = ex2(x0), p1 = ex2(x1);
+              if constexpr (MASK) {
+                p0 = c0 + e + u >= c_min ? p0 : 0.f;
+                p1 = c0 + e + u + 1 >= c_min ? p1 : 0.f;
+              }
+              pf[c0 + e + u] = p0;
+              pf[c0 + e + u + 1] = p1;
+              pp[(c0 + e + u) >> 1] = pack_bf16x2(p0, p1);
             }
-            dd[(e + u) >> 1] = pack_bf16x2(d0, d1);
           }
+        };
+        if (masked) {
+          p_chunk(sv[0], 0, std::true_type{});
+          p_chunk(sv[1], 32, std::true_type{});
+        } else {
+          p_chunk(sv[0], 0, std::false_type{});
+          p_chunk(sv[1], 32, std::false_type{});
         }
-        tmem_st16(s_t + 32 + 16 * c, dd);
-      };
-      if (masked) {
-        ds_chunk(0, std::true_type{});
-        ds_chunk(1, std::true_type{});
-      } else {
-        ds_chunk(0, std::false_type{});
-        ds_chunk(1, std::false_type{});
+        tmem_st32(s_t, pp);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready);
+        if (!warp_wait(g_full, c) || !warp_wait(&o_full[os], c >> 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t gv[2][32];
+        tmem_ld32(g_t, gv[0]);
+        tmem_ld32(g_t + 32, gv[1]);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(g_taken);
+        // dS^T = P^T (dP^T - Delta[q]), 0 where P^T was set to 0
+        const float4* sd4 = reinterpret_cast<const float4*>(sDel + os * 128 + g * GCOLS);
+        auto ds_chunk = [&](int h) {
+          uint32_t dd[16];
+  #pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 d4 = sd4[(32 * h + e) >> 2];
+            const uint64_t dl[2] = {f2_pack(d4.x, d4.y), f2_pack(d4.z, d4.w)};
+  #pragma unroll
+            for (int u = 0; u < 4; u += 2) {
+              float d0, d1;
+              f2_unpack(f2_mul(f2_pack(pf[32 * h + e + u], pf[32 * h + e + u + 1]),
+                               f2_sub(f2_pack(__uint_as_float(gv[h][e + u]),
+                                              __uint_as_float(gv[h][e + u + 1])),
+                                      dl[u >> 1])),
+                        d0, d1);
+              dd[(e + u) >> 1] = pack_bf16x2(d0, d1);
+            }
+          }
+          tmem_st16(s_t + 32 + 16 * h, dd);
+        };
+        ds_chunk(0);
+        ds_chunk(1);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_ready);
+        if (++qs == QS) {
+          qs = 0;
+          qph ^= 1u;
+        }
+        const uint32_t swap = s_t;
+        s_t = g_t;
+        g_t = swap;
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ds_ready);
-    }
-    // ------------------------------------------------------------ epilogue
-    if (ok && warp_wait(acc_done, 0u)) {
+      if (!ok || !warp_wait(acc_done, n_items)) break;
+      ++n_items;
+      // ---------------------------------------------------------- epilogue
+      // P^T of the next item is handed over after these loads, and only then may its first
+      // products overwrite dV and dK
       tc_fence_after();
+      const Item it = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[slot]);
       const bool row_ok = kp < it.len;
       const long long row = (long long)it.start + (row_ok ? kp : 0);
       auto store = [&](__nv_bfloat16* base, long long ld, uint32_t column, float f) {
         __nv_bfloat16* dst[4];
-        group_rows(row_ok ? base + row * ld + head * HD + g * (HD / 2) : nullptr, dst);
+        group_rows(row_ok ? base + row * ld + it.head * HD + g * (HD / 2) : nullptr, dst);
 #pragma unroll
         for (int e0 = 0; e0 < HD / 2; e0 += 32) {
           uint32_t r[32], w[16];
@@ -570,6 +650,7 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
       };
       store(p.dv, p.ld_dv, 0u, 1.f);
       store(p.dk, p.ld_dk, (uint32_t)HD, p.scale);
+      tc_fence_before();
     }
   }
 
@@ -763,7 +844,8 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
         return mbar_wait_poll(bar, parity & 1u, wb, SITE_PACKED_MMA);
       };
       bool ok = true;
-      uint32_t n_items = 0, c = 0, x = 0, n_tail = 0;  // items, key tiles, stage uses, ragged items
+      uint32_t n_items = 0, c = 0, n_tail = 0;  // items, key tiles, ragged items
+      uint32_t st = 0, ph = 0;                  // the ring's next stage, and bit st: its phase
       while (ok) {
         const int slot = (int)(n_items % ITEMS);
         ok = wait(&item_full[slot], n_items / ITEMS);
@@ -773,30 +855,33 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
         if (it.head < 0) break;
         const int n = tiles_of(it);
         const bool ragged = n * TILE > it.len;
-        // the key tile of use x is in place (cleared behind the sequence, if it is the last)
-        auto wait_kv = [&](bool last, uint32_t at) {
-          if (!wait(&full[at % NS], at / NS)) return false;
+        // the key tile of a stage is in place (cleared behind the sequence, if it is the last)
+        auto wait_kv = [&](uint32_t at, bool last) {
+          if (!wait(&full[at], ph >> at)) return false;
+          ph ^= 1u << at;
           if (!ragged || !last) return true;
           const uint32_t turn = n_tail++;
           return wait(&tail_ok[turn & 1u], turn >> 1);
         };
+        auto after = [](uint32_t at) { return at + 1 == NS ? 0u : at + 1; };
         // the own rows are in TMEM: their stage is free
         ok = wait(a_full, n_items);
         if (!ok) break;
-        mbar_arrive(&empty[x % NS]);
-        ++x;
+        mbar_arrive(&empty[st]);
+        ph ^= 1u << st;
+        st = after(st);
         // S over the last tile's S of the item before, once that is in registers
-        ok = wait_kv(n == 1, x) && (c == 0 || wait(s_free, c - 1));
+        ok = wait_kv(st, n == 1) && (c == 0 || wait(s_free, c - 1));
         if (!ok) break;
         tc_fence_after();
-        issue_s(x % NS);
-        issue_dp(x % NS);
-        for (int j = 0; j < n; ++j, ++c, ++x) {
+        issue_s(st);
+        issue_dp(st);
+        for (int j = 0; j < n; ++j, ++c) {
           const bool more = j + 1 < n;
-          const uint32_t then = (x + 1) % NS;
+          const uint32_t then = after(st);
           if (more) {
             // next scores as soon as the element-wise warps hold this tile's
-            ok = wait_kv(j + 2 == n, x + 1) && wait(s_free, c);
+            ok = wait_kv(then, j + 2 == n) && wait(s_free, c);
             if (!ok) break;
             tc_fence_after();
             issue_s(then);
@@ -804,8 +889,9 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
           ok = wait(ds_full, c);
           if (!ok) break;
           tc_fence_after();
-          issue_dq(x % NS, j == 0);
+          issue_dq(st, j == 0);
           if (more) issue_dp(then);
+          st = then;
         }
         if (ok) mma_commit(acc_done);
         ++n_items;
@@ -1092,7 +1178,8 @@ tsp_status launch_bwd(const Shape& s, const Source& queries, const Source& keys,
     TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem,
                               "packed attention backward: cudaFuncSetAttribute"));
     p.src = keys;
-    kernel<<<(unsigned)keys.max_items * (unsigned)s.kv_heads, KeyGeom<HD>::THREADS, smem, stream>>>(tq, tdo, tk, tv, p);
+    const unsigned grid = (unsigned)std::min<long long>((long long)keys.max_items * s.kv_heads, sm_count());
+    kernel<<<grid, KeyGeom<HD>::THREADS, smem, stream>>>(tq, tdo, tk, tv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "packed attention backward (key side): launch");
   }
