@@ -130,6 +130,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, 4)
     grad_norm_kernel(const __grid_constant__ Table<N> t, double* partial) {
   double sum = 0.;
+  dependents_may_start();
   const unsigned int chunks = t.first[t.count];
   for (unsigned int c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int i = tensor_of(t, c);
@@ -157,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 // The norm from the partial sums, the same bits in every block.
 __device__ __forceinline__ double norm_of(const double* partial, int n) {
   double s = 0.;
+  prior_kernel_done();
   for (int i = threadIdx.x; i < n; i += kThreads) s += partial[i];
   return sqrt(block_sum(s));
 }
@@ -266,17 +268,24 @@ tsp_status run(const List& l, double* partial, float max_norm, float* norm, cuda
     fill(t, l, k * N, std::min(N, l.n - k * N));
     grad_norm_kernel<N><<<kCtas, kThreads, 0, s>>>(t, partial + (size_t)k * kCtas);
   }
-  if (!l.out) {
-    grad_norm_join_kernel<<<1, kThreads, 0, s>>>(partial, n_partial, norm);
-  } else {
-    for (int k = launches - 1; k >= 0; --k) {
-      if (launches > 1) fill(t, l, k * N, std::min(N, l.n - k * N));
-      const unsigned int ctas = std::max(1u, std::min((unsigned)kCtas, t.first[t.count]));
-      grad_scale_kernel<N><<<ctas, kThreads, 0, s>>>(t, partial, n_partial, max_norm, norm);
-    }
-  }
   cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? TSP_OK : cuda_fail(e, "gradient clip: launch");
+  if (e != cudaSuccess) return cuda_fail(e, "gradient clip: launch");
+  if (!l.out) {
+    e = launch_early(grad_norm_join_kernel, 1, kThreads, 0, s, partial, n_partial, norm);
+    return e == cudaSuccess ? TSP_OK : cuda_fail(e, "gradient norm: launch");
+  }
+  for (int k = launches - 1; k >= 0; --k) {
+    if (launches > 1) fill(t, l, k * N, std::min(N, l.n - k * N));
+    const unsigned int ctas = std::max(1u, std::min((unsigned)kCtas, t.first[t.count]));
+    if (k == launches - 1) {
+      e = launch_early(grad_scale_kernel<N>, ctas, kThreads, 0, s, t, partial, n_partial, max_norm, norm);
+    } else {
+      grad_scale_kernel<N><<<ctas, kThreads, 0, s>>>(t, partial, n_partial, max_norm, norm);
+      e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "gradient clip: launch");
+  }
+  return TSP_OK;
 }
 
 tsp_status check_list(const char* what, const List& l, const float* norm, void* ws) {

@@ -100,6 +100,7 @@ __device__ __forceinline__ int claim(int* counter, int b, bool any) {
 __global__ void __launch_bounds__(LIST_THREADS)
     packed_lists_kernel(const int32_t* __restrict__ starts, int n, long long tokens, ListArgs a,
                         ListArgs b, DevStatus* status) {
+  dependents_may_start();
   const ListArgs l = blockIdx.x == 0 ? a : b;
   __shared__ int hist[1024];
   __shared__ int sums[32];
@@ -270,6 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     WaitBound wd{p.status, p.limit_ns, nullptr};
     Item next{};
     Walk walk;
+    prior_kernel_done();  // the list, where there is one
     walk.next(p.src, next);
     bool ok = true;
     uint32_t n_items = 0, c = 0, n_tail = 0;  // items, key tiles and ragged items so far
@@ -598,8 +600,13 @@ tsp_status launch_fwd(const Shape& s, const FwdParams& p, const void* q, int64_t
   TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem,
                             "packed attention: cudaFuncSetAttribute"));
   const unsigned grid = (unsigned)std::min<long long>((long long)p.src.max_items * s.kv_heads, sm_count());
-  kernel<<<grid, THREADS, smem, stream>>>(tq, tk, tv, p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (p.src.items != nullptr) {  // behind the kernel that writes the list
+    e = launch_early(kernel, grid, THREADS, smem, stream, tq, tk, tv, p);
+  } else {
+    kernel<<<grid, THREADS, smem, stream>>>(tq, tk, tv, p);
+    e = cudaGetLastError();
+  }
   return e == cudaSuccess ? TSP_OK : cuda_fail(e, "packed attention: launch");
 }
 

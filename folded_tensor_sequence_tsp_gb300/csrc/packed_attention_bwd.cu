@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
     }
     if (lane == 0) {
       walk.end(p.src);
+      prior_kernel_done();  // this kernel ends after the query side, items or none
       // copies in flight land before the CTA ends
       WaitBound wd{p.status, p.limit_ns, nullptr};
       if (n_items > 0) mbar_wait(kv_full, (n_items - 1) & 1u, wd, SITE_DRAIN);
@@ -310,6 +311,7 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, wb, SITE_PACKED_PRODUCER)) != 0;
     };
+    prior_kernel_done();  // the query side has left Delta
     uint32_t n_items = 0, c = 0;
     while (ok) {
       const int slot = (int)(n_items % ITEMS);
@@ -746,6 +748,9 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
     // -------------------------------------------------------------- producer
     Item next{};
     Walk walk;
+    prior_kernel_done();  // the lists, where there are any
+    // the key side may begin: its list is there, and all that it reads but Delta
+    dependents_may_start();
     walk.next(p.src, next);
     const uint32_t box_rows = (uint32_t)(Geo::BOXES * 128) * (uint32_t)p.RU;
     bool ok = true;
@@ -1168,8 +1173,13 @@ tsp_status launch_bwd(const Shape& s, const Source& queries, const Source& keys,
                               "packed attention backward: cudaFuncSetAttribute"));
     p.src = queries;
     const unsigned grid = (unsigned)std::min<long long>((long long)queries.max_items * s.kv_heads, sm_count());
-    kernel<<<grid, QueryGeom<HD>::THREADS, smem, stream>>>(tq, tdo, tk, tv, p);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e;
+    if (p.src.items != nullptr) {  // behind the kernel that writes the lists
+      e = launch_early(kernel, grid, QueryGeom<HD>::THREADS, smem, stream, tq, tdo, tk, tv, p);
+    } else {
+      kernel<<<grid, QueryGeom<HD>::THREADS, smem, stream>>>(tq, tdo, tk, tv, p);
+      e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return cuda_fail(e, "packed attention backward (query side): launch");
   }
   {
@@ -1179,8 +1189,7 @@ tsp_status launch_bwd(const Shape& s, const Source& queries, const Source& keys,
                               "packed attention backward: cudaFuncSetAttribute"));
     p.src = keys;
     const unsigned grid = (unsigned)std::min<long long>((long long)keys.max_items * s.kv_heads, sm_count());
-    kernel<<<grid, KeyGeom<HD>::THREADS, smem, stream>>>(tq, tdo, tk, tv, p);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_early(kernel, grid, KeyGeom<HD>::THREADS, smem, stream, tq, tdo, tk, tv, p);
     if (e != cudaSuccess) return cuda_fail(e, "packed attention backward (key side): launch");
   }
   return TSP_OK;

@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormBwdParams p
   __shared__ float part[2][2][32];
   const int tid = threadIdx.x, lanes = blockDim.x;
   const float inv_n = 1.f / (float)p.width;
+  dependents_may_start();
   auto col = [&](int i) { return (i * lanes + tid) * VEC; };
   float w[NV][VEC], dw[NV][VEC];
 #pragma unroll
@@ -508,6 +509,7 @@ __global__ void __launch_bounds__(MAXT, WARP ? 2 : MAXT <= 256 ? 3 : 1)
   const bool has_dh = p.dh != nullptr, stage_dh = p.stage_dh != 0;
   const float inv_n = 1.f / (float)p.width;
   const int each = STAGES * NV * blockDim.x * 16;
+  dependents_may_start();
   auto col = [&](int i) { return (i * lanes + tid) * VEC; };
   auto slot = [&](int stage, int i) { return (stage * NV + i) * (int)blockDim.x + (int)threadIdx.x; };
   auto h_at = [&](int stage, int i) { return ring + slot(stage, i) * 16; };
@@ -650,6 +652,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* __restric
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + cx;
   float s = 0.f;
+  prior_kernel_done();
   if (c < width)
     for (int r = ry; r < n; r += 32) s += partial[(long long)r * width + c];
   part[ry][cx] = s;
@@ -900,8 +903,7 @@ tsp_status tsp_rmsnorm_bwd(int64_t rows, int width, const void* h, int h_f32, co
   TSP_TRY(h_f32 ? launch_bwd_res<RES_F32>(p, vec, ctas, s) : launch_bwd_res<RES_BF16>(p, vec, ctas, s));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "rmsnorm backward: launch");
-  rmsnorm_dw_kernel<<<(width + 31) / 32, 1024, 0, s>>>(p.partial, ctas, width, dw);
-  e = cudaGetLastError();
+  e = launch_early(rmsnorm_dw_kernel, (width + 31) / 32, 1024, 0, s, p.partial, ctas, width, dw);
   return e == cudaSuccess ? TSP_OK : cuda_fail(e, "rmsnorm backward: dw launch");
   TSP_GUARD_END
 }

@@ -230,6 +230,17 @@ __device__ __forceinline__ uint64_t l2_policy_evict_first() {
 }
 
 // ----------------------------------------------------------------------------
+// Two kernels of a stream overlapping (launch_early)
+// ----------------------------------------------------------------------------
+// The kernel before this one on the stream is complete and its writes are visible. Returns at
+// once in a kernel that was not launched early.
+__device__ __forceinline__ void prior_kernel_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel may start once every CTA has called this (or ended).
+__device__ __forceinline__ void dependents_may_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ----------------------------------------------------------------------------
 // tcgen05: tensor memory and the 5th-generation tensor-core MMA
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_slot, uint32_t ncols) {

@@ -243,6 +243,26 @@ tsp_status attention_block(const Plan& p, const void* xs, const void* wpack, con
 tsp_status mlp_block(const Plan& p, const void* hs, const void* wpack, const void* residual,
                      int residual_f32, void* out, void* ws, cudaStream_t s);
 
+// Launches a kernel that may start while the one before it on the stream is still running: on
+// multiprocessors that this has left, once all of its CTAs have called dependents_may_start().
+// What the kernel reads of the earlier one's output comes after prior_kernel_done(). It hides
+// the launch and set-up of the second of two kernels, 2 to 4 us.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                         A&&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // An NVTX range around the host-side enqueue of one step of the schedules (a
 // broadcast iteration's projection and attention, the O projection, the MLP ring),
 // so that a trace tool shows which shard step issued which kernels. NVTX3 is
