@@ -14,9 +14,9 @@
 // of its tile than one head alone would. Tiles never span sequences: a sequence's result
 // has the same bits whatever else is packed beside it.
 //
-// One CTA computes two query tiles (A and B) of one key head:
-//   warp 0      TMA: Q_A, Q_B, K_0, then pairs (V_j, K_{j+1}) into a 2-stage ring; then
-//               clears what follows the sequence in its last V tile (below)
+// A CTA works on two neighbouring query tiles (A and B) of one key head, its item:
+//   warp 0      finds the items, and loads by TMA: Q_A, Q_B, K_0, then pairs (V_j, K_{j+1})
+//               into a 2-stage ring; then clears what follows the sequence in its last V tile
 //   warp 1      TMEM allocation; one lane issues per key tile O_A += P_A V_j,
 //               S_A = Q_A K_{j+1}^T, and the same for B: while one tile's softmax runs,
 //               the tensor core works for the other
@@ -25,20 +25,27 @@
 //               exceeded by more than 8 (P <= 256; O and l are rescaled then), P written
 //               as bf16 over the scores' TMEM columns as the A operand of P V
 // TMEM columns: S_A [0,128) O_A [128,256) S_B [256,384) O_B [384,512).
-// P is rounded to bf16 for the tensor core while l sums the fp32 values: 2^-9 relative per
-// term, below the rounding of o itself.
+// P is rounded to bf16 for the tensor core while l sums the fp32 values: at most 2^-8 of a
+// term, and the terms' errors cancel in the sum where o's own rounding does not.
+//
+// CTAs are persistent, one per multiprocessor, and the roles meet only at barriers whose
+// phases run on across items: the next item's loads and first scores are under way while the
+// last one is stored. Items are (sequence, tile pair) sorted by their number of key tiles,
+// longest first, and drawn from a counter. Up to 128 sequences warp 0 finds an item in
+// `starts` by a search in registers; beyond, a small kernel writes the sorted list first.
+// starts is data, not a launch parameter: a captured graph may be replayed with other
+// lengths. Starts that decrease or leave the buffers give no items and an error in the
+// status word.
 //
 // A key tile at a sequence's end reads on into the next sequence, or into rows that belong
 // to none. Their scores are replaced by -inf, so P is 0 there, but 0 times a NaN or an
 // infinity in V is not 0: warp 0 overwrites those rows of V with zeros in shared memory
 // before the product may start.
 //
-// CTAs take (sequence, tile pair) items sorted by their number of key tiles, longest first,
-// so that the last ones to run are short. Up to 128 sequences every CTA finds its own item
-// in `starts` by a search in registers; beyond, a small kernel writes the sorted list first.
-// starts is data, not a launch parameter: a captured graph may be replayed with other
-// lengths. Starts that decrease or leave the buffers give no items and an error in the
-// status word.
+// Measured, 32 query and 8 key heads of 128: one sequence of 32768 tokens and 1000 others 6.0
+// ms, 1470 TFLOP/s (0.77 of the measured burst rate; the softmax warps' issue slots bind);
+// 16384 tokens in 18 sequences 0.39 ms, 1220 TFLOP/s, against 0.42 with a CTA per item and
+// 0.40 with rows stored lane by lane; 128 sequences of 128 tokens 0.08 ms (0.05 of it HBM).
 #include <algorithm>
 #include <cmath>
 

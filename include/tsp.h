@@ -636,7 +636,8 @@ tsp_status tsp_cost_max_batch(int scheme, int D, int tp, int64_t S, int hidden, 
  * visible keys of exp(scale q.k), as tsp_causal_attention_lse stores it.
  *
  * ws: tsp_packed_attention_workspace_bytes (0 for an unsupported shape), 256-byte aligned,
- * initialised once by tsp_status_init. One workspace serves one call at a time.
+ * initialised once by tsp_status_init. One workspace serves one call at a time; calls that
+ * overlapped on one leave it undefined until the next tsp_status_init.
  * ------------------------------------------------------------------------- */
 size_t tsp_packed_attention_workspace_bytes(int64_t tokens, int n_seqs, int heads, int kv_heads,
                                             int head_dim);
@@ -678,9 +679,10 @@ tsp_status tsp_packed_attention_bwd(int64_t tokens, int n_seqs, const int32_t* s
  * x, y [rows][width]; residual and h [rows][width] in bf16, or in fp32 with residual_f32
  * (a residual stream kept in fp32). residual and h are both NULL (the norm of x alone) or
  * both given; h may be the residual itself (updated in place) and y may be x. Sums in
- * fp32. rows in [0, 2^31) (0: nothing happens), width in [1, 32768], any of them odd; eps
- * positive and finite. Buffers need their element's alignment; with width % 8 == 0 and
- * every buffer 16-byte aligned the loads are 16 bytes wide.
+ * fp32: a row whose sum of squares overflows it gives y = 0. rows in [0, 2^31) (0: nothing
+ * happens), width in [1, 32768], any of them odd; eps positive and finite. Buffers need
+ * their element's alignment; with width % 8 == 0 and every buffer 16-byte aligned the
+ * loads are 16 bytes wide.
  */
 tsp_status tsp_rmsnorm_fwd(int64_t rows, int width, const tsp_bf16* x, const void* residual,
                            int residual_f32, const tsp_bf16* weight, float eps, void* h, tsp_bf16* y,
