@@ -233,6 +233,28 @@ def test_bad_starts_are_reported_and_write_nothing(starts):
     check_forward(c, o, None, "after")
 
 
+@pytest.mark.parametrize("where", [0, 150, 398])
+def test_bad_starts_among_many_sequences(where):
+    """The same where the kernels take their items from a list."""
+    c = Case([5] * 399, 4, 2, 64)
+    op = c.op()
+    o, lse = op.forward_train(c.q, c.k, c.v, c.starts)
+    bad = c.starts.clone()
+    bad[where] = -1 if where == 0 else bad[where + 1] + 3
+    out = torch.full_like(c.do, 3)
+    grads = [torch.full_like(t, 3) for t in (c.do, c.k.contiguous(), c.v.contiguous())]
+    op.forward(c.q, c.k, c.v, bad, out=out)
+    with pytest.raises(tsp.TSPError):
+        op.check()
+    op.backward(c.q, c.k, c.v, bad, o, lse, c.do, *grads)
+    with pytest.raises(tsp.TSPError):
+        op.check()
+    assert (out == 3).all() and all((g == 3).all() for g in grads)
+    again = op.forward(c.q, c.k, c.v, c.starts)
+    op.check()
+    assert torch.equal(again, o)
+
+
 def test_no_tokens_and_no_sequences():
     op = tsp.TSPPackedAttention(16, 4, 4, 2, 64)
     e = lambda n, h: torch.empty(n, h, 64, dtype=torch.bfloat16, device="cuda")  # noqa: E731
