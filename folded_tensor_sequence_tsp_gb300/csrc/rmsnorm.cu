@@ -21,7 +21,6 @@
 // thread made each copy fetch half sectors (16384 x 4096: 157 us against 135).
 // 16384 x 4096, of the measured copy rate: fp32 stream 128 us (0.93), e4m3 beside a bf16
 // stream 78 us (0.90), backward 88 us (0.90).
-// Rows that are not made of whole pieces take single elements, unstaged.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -244,8 +243,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_kernel(const NormParams p) {
         for (int e = 0; e < VEC; ++e) t = max(t, __float_as_uint(fabsf(v[i][e])));
         return t;
       };
-      auto store8 = [&](int i, float scale) {
-        const float inv = 1.f / scale;
+      auto store8 = [&](int i, float inv) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) y8[col(i) + e] = to_e4m3(v[i][e] * inv);
       };
@@ -254,26 +252,36 @@ __global__ void __launch_bounds__(1024) rmsnorm_fwd_kernel(const NormParams p) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) t = max(t, top_of(i));
         const float scale = e4m3_scale(row_max<false>(t, tops[odd]));
+        const float inv = __frcp_rn(scale);
         if (tid == 0) p.scales[row] = scale;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (col(i) < p.width) store8(i, scale);
+          if (col(i) < p.width) store8(i, inv);
       } else {
-        // the threads of a group meet in shared memory (a maximum does not depend on the
-        // order of the atomics)
+        // a warp's columns of one i lie in one group (VEC 1), or a half warp's (VEC 8); the
+        // warps of a group meet in shared memory (a maximum does not depend on the order of
+        // the atomics)
         const int groups = (p.width + 127) / 128;
         __syncthreads();
         for (int g = threadIdx.x; g < groups; g += blockDim.x) tops[0][g] = 0u;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (col(i) < p.width) atomicMax(&tops[0][col(i) / 128], top_of(i));
+        for (int i = 0; i < NV; ++i) {
+          uint32_t t = top_of(i);
+#pragma unroll
+          for (int o = VEC == 8 ? 8 : 16; o; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
+          if (tid % (VEC == 8 ? 16 : 32) == 0 && col(i) < p.width) atomicMax(&tops[0][col(i) / 128], t);
+        }
         __syncthreads();
-        for (int g = threadIdx.x; g < groups; g += blockDim.x)
-          p.scales[row * groups + g] = e4m3_scale(tops[0][g]);
+        for (int g = threadIdx.x; g < groups; g += blockDim.x) {
+          const float scale = e4m3_scale(tops[0][g]);
+          p.scales[row * groups + g] = scale;
+          tops[1][g] = __float_as_uint(__frcp_rn(scale));
+        }
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (col(i) < p.width) store8(i, e4m3_scale(tops[0][col(i) / 128]));
+          if (col(i) < p.width) store8(i, __uint_as_float(tops[1][col(i) / 128]));
       }
     }
   }
@@ -646,6 +654,128 @@ __global__ void __launch_bounds__(MAXT, WARP ? 2 : MAXT <= 256 ? 3 : 1)
   }
 }
 
+// Rows that are not made of whole pieces (odd widths, unaligned buffers). The backward copies
+// the aligned 16-byte spans that cover a row, one row ahead, and works on single elements of
+// the copy. A span's bytes outside the row are ignored; spans that leave the buffer are
+// copied element by element. (16384 x 4095: 228 us, 430 without copies. The forward, with fewer
+// operands, is faster without.)
+template <class E>
+__device__ __forceinline__ const E* copy_row(uint8_t* smem, const E* buffer, long long row, long long rows,
+                                             int width) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(buffer);
+  const uintptr_t hi = lo + (uintptr_t)rows * (uintptr_t)width * sizeof(E);
+  const uintptr_t at = lo + (uintptr_t)row * (uintptr_t)width * sizeof(E);
+  const uintptr_t first = at & ~(uintptr_t)15;
+  if (row < rows) {
+    const int spans = (int)((at - first + (uintptr_t)width * sizeof(E) + 15) >> 4);
+    for (int k = threadIdx.x; k < spans; k += blockDim.x) {
+      const uintptr_t src = first + 16u * (unsigned)k;
+      if (src >= lo && src + 16 <= hi) {
+        copy_ahead<16>(smem + 16 * k, reinterpret_cast<const void*>(src));
+      } else {
+#pragma unroll
+        for (unsigned e = 0; e < 16; e += sizeof(E))
+          if (src + e >= lo && src + e < hi)
+            *reinterpret_cast<E*>(smem + 16 * k + e) = *reinterpret_cast<const E*>(src + e);
+      }
+    }
+  }
+  return reinterpret_cast<const E*>(smem + (at - first));
+}
+// Shared memory of a copied row of `width` elements.
+__host__ __device__ constexpr int row_bytes(int width, int element) {
+  return (width * element + 15 + 15) / 16 * 16;
+}
+template <int RES>
+struct StreamOf {
+  using type = __nv_bfloat16;
+};
+template <>
+struct StreamOf<RES_F32> {
+  using type = float;
+};
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void store_as(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_as(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// dw is summed in shared memory, each column by the thread that owns it.
+template <int RES>
+__global__ void __launch_bounds__(512, 2) rmsnorm_bwd_odd_kernel(const NormBwdParams p) {
+  using R = typename StreamOf<RES>::type;
+  extern __shared__ __align__(16) uint8_t ring[];  // dw, then two copies of h, dy (and dh)
+  __shared__ float part[2][2][32];
+  float* dw = reinterpret_cast<float*>(ring);
+  const bool has_dh = p.dh != nullptr;
+  const int hb = row_bytes(p.width, sizeof(R)), yb = row_bytes(p.width, 2);
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const float inv_n = 1.f / (float)p.width;
+  dependents_may_start();
+  struct Row {
+    const R* h;
+    const R* d;
+    const __nv_bfloat16* y;
+  };
+  auto fetch = [&](long long row, int stage) {
+    uint8_t* to = ring + row_bytes(p.width, 4) + stage * (hb + yb + (has_dh ? hb : 0));
+    Row r;
+    r.h = copy_row(to, static_cast<const R*>(p.h), row, p.rows, p.width);
+    r.y = copy_row(to + hb, p.dy, row, p.rows, p.width);
+    r.d = has_dh ? copy_row(to + hb + yb, static_cast<const R*>(p.dh), row, p.rows, p.width) : nullptr;
+    copies_end_group();
+    return r;
+  };
+  for (int c = tid; c < p.width; c += threads) dw[c] = 0.f;
+  Row now = fetch(blockIdx.x, 0);
+  int odd = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, odd ^= 1) {
+    const Row next = fetch(row + gridDim.x, odd ^ 1);
+    copies_wait_all_but<1>();
+    __syncthreads();
+    float ss = 0.f, sg = 0.f;
+#pragma unroll 4
+    for (int c = tid; c < p.width; c += threads) {
+      const float h = as_float(now.h[c]);
+      ss = fmaf(h, h, ss);
+      sg = fmaf(__bfloat162float(now.y[c]) * __bfloat162float(p.w[c]), h, sg);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      sg += __shfl_xor_sync(0xffffffffu, sg, o);
+    }
+    if ((tid & 31) == 0) {
+      part[odd][0][tid >> 5] = ss;
+      part[odd][1][tid >> 5] = sg;
+    }
+    __syncthreads();
+    const bool in = (tid & 31) < (threads >> 5);
+    ss = in ? part[odd][0][tid & 31] : 0.f;
+    sg = in ? part[odd][1][tid & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      sg += __shfl_xor_sync(0xffffffffu, sg, o);
+    }
+    const float rstd = 1.f / sqrtf(ss * inv_n + p.eps);
+    const float coef = rstd * rstd * (sg * inv_n);  // dx = rstd (g - h coef)
+    R* dx = static_cast<R*>(p.dx) + row * p.width;
+    __nv_bfloat16* dx16 = p.dx16 == nullptr ? nullptr : p.dx16 + row * p.width;
+#pragma unroll 4
+    for (int c = tid; c < p.width; c += threads) {
+      const float h = as_float(now.h[c]), y = __bfloat162float(now.y[c]);
+      float t = rstd * (y * __bfloat162float(p.w[c]) - h * coef);
+      dw[c] = fmaf(y, h * rstd, dw[c]);
+      if (has_dh) t += as_float(now.d[c]);
+      store_as(dx + c, t);
+      if (dx16 != nullptr) dx16[c] = __float2bfloat16_rn(t);
+    }
+    __syncthreads();  // the copies are read: the row after the next goes there
+    now = next;
+  }
+  for (int c = tid; c < p.width; c += threads) p.partial[(long long)blockIdx.x * p.width + c] = dw[c];
+}
+
 // dw[c] = sum of the partial rows, in a fixed order: 32 row groups per column, then their
 // sum.
 __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* __restrict__ partial, int n,
@@ -674,6 +804,9 @@ bool aligned16(std::initializer_list<const void*> ptrs) {
 
 // Threads of a CTA that holds a row of `items` (pieces or elements), nv per thread.
 int row_threads(int items, int nv) { return ((items + nv - 1) / nv + 31) / 32 * 32; }
+
+// Threads of a CTA on a row of single elements: about eight columns each.
+int odd_threads(int width) { return width <= 1024 ? 128 : width <= 2048 ? 256 : 512; }
 
 template <int VEC, int NV, int RES, bool E4M3>
 tsp_status launch_fwd_direct(const NormParams& p, cudaStream_t s) {
@@ -771,8 +904,14 @@ template <int RES>
 tsp_status launch_bwd_res(const NormBwdParams& p, bool vec, int ctas, cudaStream_t s) {
   constexpr int P = 8 / piece_of<RES>;
   if (!vec) {
-    if (p.width <= 4096) return launch_bwd_direct<1, 8, RES>(p, ctas, s);
-    return launch_bwd_direct<1, 32, RES>(p, ctas, s);
+    const int hb = row_bytes(p.width, RES == RES_F32 ? 4 : 2);
+    const size_t smem = row_bytes(p.width, 4) + 2 * (row_bytes(p.width, 2) + (p.dh ? 2 : 1) * hb);
+    if (smem > 220 * 1024) return launch_bwd_direct<1, 32, RES>(p, ctas, s);
+    auto kernel = rmsnorm_bwd_odd_kernel<RES>;
+    TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem,
+                              "rmsnorm backward: cudaFuncSetAttribute"));
+    kernel<<<ctas, odd_threads(p.width), smem, s>>>(p);
+    return TSP_OK;
   }
   if (p.width <= 256) return launch_bwd_staged<P, true, RES, 4, 256>(p, ctas, 256, s);
   if (p.width <= 512) return launch_bwd_staged<2 * P, true, RES, 3, 256>(p, ctas, 256, s);
