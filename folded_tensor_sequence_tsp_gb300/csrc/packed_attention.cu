@@ -12,7 +12,8 @@
 // key head (row = token * G + head; one TMA box of 64 columns x G heads x TPT tokens lays
 // them out), so a K/V tile serves the whole group, and a short sequence fills G times more
 // of its tile than one head alone would. Tiles never span sequences: a sequence's result
-// has the same bits whatever else is packed beside it.
+// has the same bits whatever else is packed beside it. Sequences of a few tokens go to no
+// tile: the softmax warps take them first, on the CUDA cores (packed_short.cuh).
 //
 // A CTA works on two neighbouring query tiles (A and B) of one key head, its item:
 //   warp 0      finds the items, and loads by TMA: Q_A, Q_B, K_0, then pairs (V_j, K_{j+1})
@@ -51,6 +52,7 @@
 
 #include "attention_math.cuh"
 #include "packed_attention.cuh"
+#include "packed_short.cuh"
 
 namespace tsp {
 namespace packed {
@@ -73,13 +75,13 @@ constexpr int LIST_THREADS = 1024;
 // none): a thread fetches one sequence and takes it if it is a single item; of the others, a
 // warp walks one sequence after the other, lane by lane over its items.
 template <class F>
-__device__ __forceinline__ void each_item(const int32_t* starts, int n, int tile, F f) {
+__device__ __forceinline__ void each_item(const int32_t* starts, int n, int tile, int short_len, F f) {
   const int lane = threadIdx.x & 31;
   for (int base = 0; base < n; base += LIST_THREADS) {
     const int i = base + threadIdx.x;
     const int start = i < n ? starts[i] : 0, len = i < n ? starts[i + 1] - start : 0;
-    f(len > 0 && len <= tile, start, len, 0);
-    for (unsigned left = __ballot_sync(0xffffffffu, len > tile); left; left &= left - 1) {
+    f(len > short_len && len <= tile, start, len, 0);
+    for (unsigned left = __ballot_sync(0xffffffffu, len > short_len && len > tile); left; left &= left - 1) {
       const int from = __ffs(left) - 1;
       const int s = __shfl_sync(0xffffffffu, start, from);
       const int m = __shfl_sync(0xffffffffu, len, from);
@@ -111,14 +113,17 @@ __global__ void __launch_bounds__(LIST_THREADS)
   const ListArgs l = blockIdx.x == 0 ? a : b;
   __shared__ int hist[1024];
   __shared__ int sums[32];
+  __shared__ int n_short;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   hist[tid] = 0;
+  if (tid == 0) n_short = 0;
   bool ok = true;
   for (int i = tid; i < n; i += LIST_THREADS)
     ok = ok && starts[i] >= 0 && starts[i + 1] >= starts[i] && starts[i + 1] <= tokens;
   if (__syncthreads_or(!ok)) {
     if (tid == 0) {
       *l.count = 0;
+      if (l.short_len > 0) *l.short_count = 0;
       record_error(status, kStatusInvalid, SITE_PACKED_STARTS);
     }
     return;
@@ -128,7 +133,7 @@ __global__ void __launch_bounds__(LIST_THREADS)
                                 : (min((long long)len, (long long)q0 + l.tile) - 1) / TILE;
     return min(cost >> l.shift, 1023);
   };
-  each_item(starts, n, l.tile, [&](bool any, int, int len, int q0) {
+  each_item(starts, n, l.tile, l.short_len, [&](bool any, int, int len, int q0) {
     claim(hist, any ? bucket(len, q0) : 0, any);
   });
   __syncthreads();
@@ -157,10 +162,21 @@ __global__ void __launch_bounds__(LIST_THREADS)
   if (tid == LIST_THREADS - 1) *l.count = min(incl, l.max_items);
   __syncthreads();
   // the order inside a bucket may change from run to run: every item is its own CTA's work
-  each_item(starts, n, l.tile, [&](bool any, int s, int len, int q0) {
+  each_item(starts, n, l.tile, l.short_len, [&](bool any, int s, int len, int q0) {
     const int slot = claim(hist, any ? bucket(len, q0) : 0, any);
     if (any && slot < l.max_items) l.items[slot] = Item{s, len, q0, 0};
   });
+  if (l.short_len > 0) {
+    for (int base = 0; base < n; base += LIST_THREADS) {
+      const int i = base + tid;
+      const int start = i < n ? starts[i] : 0, len = i < n ? starts[i + 1] - start : 0;
+      const bool is = len > 0 && len <= l.short_len;
+      const int slot = claim(&n_short, 0, is);
+      if (is) l.short_items[slot] = make_int2(start, len);
+    }
+    __syncthreads();
+    if (tid == 0) *l.short_count = n_short;
+  }
 }
 
 // ------------------------------------------------------------------ forward
@@ -175,11 +191,15 @@ struct Geometry {
 };
 
 struct FwdParams {
+  const __nv_bfloat16* q;  // read directly for the short sequences
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  long long ld_q, ld_k, ld_v;
   __nv_bfloat16* o;
   long long ld_o;
   float* lse;  // optional [heads][ld_lse]
   long long ld_lse;
-  Source src;
+  ShortSource src;
   int G, TPT, RU;
   float scale_log2;
   DevStatus* status;
@@ -462,6 +482,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool mine = mbar_wait(bar, parity & 1u, wbs, SITE_PACKED_SOFTMAX);
       return __all_sync(0xffffffffu, mine) != 0;
     };
+    // the short sequences, under the first item's loads; dealt out from the last CTA on, since
+    // the last ones have the cheapest item or none
+    short_forward<HD>(p, (gridDim.x - 1u - blockIdx.x) * 8u + (unsigned)(warp - 2), gridDim.x * 8u);
     uint32_t n_items = 0;
     uint32_t ph = 0;  // phase bits: 1 of s_full, 2 of o_done
     while (true) {
@@ -659,6 +682,7 @@ Workspace make_workspace(const Shape& s) {
   w.counts = take(256);
   w.items = take((size_t)w.max_query * sizeof(Item));
   w.key_items = take((size_t)w.max_key * sizeof(Item));
+  w.short_items = take((size_t)s.n_seqs * sizeof(int2));
   w.delta = take((size_t)s.heads * (size_t)w.ld_stat * sizeof(float));
   w.total = off;
   return w;
@@ -765,13 +789,23 @@ tsp_status tsp_packed_attention_fwd(int64_t tokens, int n_seqs, const int32_t* s
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const Workspace w = make_workspace(s);
   FwdParams p{};
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.k = reinterpret_cast<const __nv_bfloat16*>(k);
+  p.v = reinterpret_cast<const __nv_bfloat16*>(v);
+  p.ld_q = ld_q;
+  p.ld_k = ld_k;
+  p.ld_v = ld_v;
   p.o = reinterpret_cast<__nv_bfloat16*>(o);
   p.ld_o = ld_o;
   p.lse = lse;
   p.ld_lse = ld_lse;
   // 72 MB of K and V in L2 at a time, as for the plan's attention
-  p.src = make_source(s, starts, 2 * s.TPT, false, head_group(s, 72ll << 20), at<Item>(ws, w.items),
-                      at<int>(ws, w.counts), (int)w.max_fwd, ws, 0);
+  static_cast<Source&>(p.src) =
+      make_source(s, starts, 2 * s.TPT, false, head_group(s, 72ll << 20), at<Item>(ws, w.items),
+                  at<int>(ws, w.counts), (int)w.max_fwd, ws, 0);
+  p.src.short_len = short_length(s.G);
+  p.src.short_items = at<int2>(ws, w.short_items);
+  p.src.short_count = at<int>(ws, w.counts) + 2;
   p.G = s.G;
   p.TPT = s.TPT;
   p.RU = s.RU;
@@ -780,7 +814,8 @@ tsp_status tsp_packed_attention_fwd(int64_t tokens, int n_seqs, const int32_t* s
   p.limit_ns = wait_limit_ns();
   if (p.src.items != nullptr) {
     const ListArgs list{2 * s.TPT, 0, list_shift((tokens + TILE - 1) / TILE), at<Item>(ws, w.items),
-                        at<int>(ws, w.counts), (int)w.max_fwd};
+                        at<int>(ws, w.counts), (int)w.max_fwd, p.src.short_len,
+                        at<int2>(ws, w.short_items), at<int>(ws, w.counts) + 2};
     TSP_TRY(launch_lists(s, starts, list, ListArgs{}, p.status, st));
   }
   if (head_dim == 64) return launch_fwd<64>(s, p, q, ld_q, k, ld_k, v, ld_v, st);

@@ -29,12 +29,17 @@ struct Shape {
   int RU;   // rows in use, TPT * G <= 128
 };
 
+// Sequences of up to this many tokens are short: at most 8, and 32 rows of tokens x heads of a
+// group (packed_short.cuh takes them in the forward; tiles take the others).
+inline int short_length(int G) { return 32 / G < 8 ? 32 / G : 8; }
+
 // Workspace (byte offsets from its 256-byte aligned start).
 struct Workspace {
   // the first 256 bytes: the status word, and from COUNTERS on two words per kernel for Walk
-  size_t counts;  // int[2]: items in each list
+  size_t counts;  // int[3]: items in each list
   size_t items;   // forward, or query side of the backward
   size_t key_items;
+  size_t short_items;
   size_t delta;   // [heads][ld_stat] fp32
   size_t total;
   long long max_fwd, max_query, max_key;  // capacity of the lists
@@ -51,6 +56,9 @@ struct ListArgs {
   Item* items;
   int* count;
   int max_items;
+  int short_len;      // sequences of up to so many tokens go to this list (start, tokens)
+  int2* short_items;
+  int* short_count;
 };
 
 // Where a kernel takes its items from: a list made by launch_lists, or, for up to
@@ -70,6 +78,15 @@ struct Source {
   unsigned* next;  // [2] in the workspace: works handed out beyond the first of each CTA, and
                    // CTAs that are done; both 0 before and after a launch
   DevStatus* status;
+  static constexpr bool SHORT = false;
+};
+
+// The same where short sequences are no items.
+struct ShortSource : Source {
+  int short_len;            // the longest of them
+  const int2* short_items;  // with a list
+  const int* short_count;
+  static constexpr bool SHORT = true;
 };
 
 #ifdef __CUDACC__
@@ -82,7 +99,8 @@ struct Source {
 // lie at b or further, so b comes from a binary search over warp sums and the sequence from a
 // rank among those with more than b items. About a microsecond, which the persistent kernels
 // spend beside their products, against 5 for a kernel that writes the list.
-static __device__ __forceinline__ bool find_item(const Source& src, unsigned w, Item& it) {
+template <class Src>
+__device__ __forceinline__ bool find_item(const Src& src, unsigned w, Item& it) {
   constexpr int K = SEARCH_SEQS / 32;
   const int lane = threadIdx.x & 31;
   int nb[K], st[K], ln[K];
@@ -100,6 +118,7 @@ static __device__ __forceinline__ bool find_item(const Source& src, unsigned w, 
         st[u] = a;
         ln[u] = b - a;
         nb[u] = (int)(((long long)ln[u] + src.tile - 1) / src.tile);
+        if constexpr (Src::SHORT) nb[u] = ln[u] <= src.short_len ? 0 : nb[u];
       }
       total += nb[u];
     }
@@ -166,7 +185,8 @@ static __device__ __forceinline__ bool find_item(const Source& src, unsigned w, 
 struct Walk {
   bool begun = false;
   // Moves on to the next item (the first call: to the first); head -1 at the end.
-  __device__ __forceinline__ void next(const Source& src, Item& it) {
+  template <class Src>
+  __device__ __forceinline__ void next(const Src& src, Item& it) {
     unsigned w = blockIdx.x;
     if (begun) {
       if ((threadIdx.x & 31) == 0) w = gridDim.x + atomicAdd(src.next, 1u);

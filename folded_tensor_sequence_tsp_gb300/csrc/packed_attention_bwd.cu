@@ -1277,9 +1277,9 @@ extern "C" tsp_status tsp_packed_attention_bwd(
                                   (int)w.max_key, ws, 2);
   if (queries.items != nullptr) {
     const ListArgs a{s.TPT, 0, list_shift((tokens + TILE - 1) / TILE), at<Item>(ws, w.items), counts,
-                     (int)w.max_query};
+                     (int)w.max_query, 0, nullptr, nullptr};
     const ListArgs b{TILE, s.TPT, list_shift((tokens + s.TPT - 1) / s.TPT), at<Item>(ws, w.key_items),
-                     counts + 1, (int)w.max_key};
+                     counts + 1, (int)w.max_key, 0, nullptr, nullptr};
     TSP_TRY(launch_lists(s, starts, a, b, p.status, st));
   }
   if (head_dim == 64) return launch_bwd<64>(s, queries, keys, p, q, ld_q, dout, ld_do, k, ld_k, v, ld_v, st);
