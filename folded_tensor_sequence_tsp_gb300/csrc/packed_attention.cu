@@ -108,7 +108,8 @@ __device__ __forceinline__ int claim(int* counter, int b, bool any) {
 
 __global__ void __launch_bounds__(LIST_THREADS)
     packed_lists_kernel(const int32_t* __restrict__ starts, int n, long long tokens, ListArgs a,
-                        ListArgs b, DevStatus* status) {
+                        ListArgs b, int short_len, int2* short_items, int* short_count,
+                        DevStatus* status) {
   dependents_may_start();
   const ListArgs l = blockIdx.x == 0 ? a : b;
   __shared__ int hist[1024];
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(LIST_THREADS)
   if (__syncthreads_or(!ok)) {
     if (tid == 0) {
       *l.count = 0;
-      if (l.short_len > 0) *l.short_count = 0;
+      if (blockIdx.x == 0) *short_count = 0;
       record_error(status, kStatusInvalid, SITE_PACKED_STARTS);
     }
     return;
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(LIST_THREADS)
                                 : (min((long long)len, (long long)q0 + l.tile) - 1) / TILE;
     return min(cost >> l.shift, 1023);
   };
-  each_item(starts, n, l.tile, l.short_len, [&](bool any, int, int len, int q0) {
+  each_item(starts, n, l.tile, short_len, [&](bool any, int, int len, int q0) {
     claim(hist, any ? bucket(len, q0) : 0, any);
   });
   __syncthreads();
@@ -162,20 +163,20 @@ __global__ void __launch_bounds__(LIST_THREADS)
   if (tid == LIST_THREADS - 1) *l.count = min(incl, l.max_items);
   __syncthreads();
   // the order inside a bucket may change from run to run: every item is its own CTA's work
-  each_item(starts, n, l.tile, l.short_len, [&](bool any, int s, int len, int q0) {
+  each_item(starts, n, l.tile, short_len, [&](bool any, int s, int len, int q0) {
     const int slot = claim(hist, any ? bucket(len, q0) : 0, any);
     if (any && slot < l.max_items) l.items[slot] = Item{s, len, q0, 0};
   });
-  if (l.short_len > 0) {
+  if (blockIdx.x == 0) {  // the short sequences, for every kernel behind this one
     for (int base = 0; base < n; base += LIST_THREADS) {
       const int i = base + tid;
       const int start = i < n ? starts[i] : 0, len = i < n ? starts[i + 1] - start : 0;
-      const bool is = len > 0 && len <= l.short_len;
+      const bool is = len > 0 && len <= short_len;
       const int slot = claim(&n_short, 0, is);
-      if (is) l.short_items[slot] = make_int2(start, len);
+      if (is) short_items[slot] = make_int2(start, len);
     }
     __syncthreads();
-    if (tid == 0) *l.short_count = n_short;
+    if (tid == 0) *short_count = n_short;
   }
 }
 
@@ -199,7 +200,7 @@ struct FwdParams {
   long long ld_o;
   float* lse;  // optional [heads][ld_lse]
   long long ld_lse;
-  ShortSource src;
+  Source src;
   int G, TPT, RU;
   float scale_log2;
   DevStatus* status;
@@ -484,6 +485,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
     // the short sequences, under the first item's loads; dealt out from the last CTA on, since
     // the last ones have the cheapest item or none
+    prior_kernel_done();  // the list, where there is one
     short_forward<HD>(p, (gridDim.x - 1u - blockIdx.x) * 8u + (unsigned)(warp - 2), gridDim.x * 8u);
     uint32_t n_items = 0;
     uint32_t ph = 0;  // phase bits: 1 of s_full, 2 of o_done
@@ -689,12 +691,16 @@ Workspace make_workspace(const Shape& s) {
 }
 
 Source make_source(const Shape& s, const int32_t* starts, int tile, bool from_end, int group,
-                   const Item* items, const int* count, int max_items, void* ws, int counter) {
+                   const Item* items, const int* count, int max_items, void* ws, const Workspace& w,
+                   int counter) {
   Source src{};
   if (s.n_seqs > SEARCH_SEQS) {
     src.items = items;
     src.count = count;
+    src.short_items = at<int2>(ws, w.short_items);
+    src.short_count = at<int>(ws, w.counts) + 2;
   }
+  src.short_len = short_length(s.G);
   src.starts = starts;
   src.n_seqs = s.n_seqs;
   src.tile = tile;
@@ -715,9 +721,10 @@ int list_shift(long long max_cost) {
 }
 
 tsp_status launch_lists(const Shape& s, const int32_t* starts, const ListArgs& a, const ListArgs& b,
-                        DevStatus* status, cudaStream_t stream) {
-  packed_lists_kernel<<<b.tile ? 2 : 1, LIST_THREADS, 0, stream>>>(starts, s.n_seqs, s.tokens, a, b,
-                                                                   status);
+                        void* ws, const Workspace& w, DevStatus* status, cudaStream_t stream) {
+  packed_lists_kernel<<<b.tile ? 2 : 1, LIST_THREADS, 0, stream>>>(
+      starts, s.n_seqs, s.tokens, a, b, short_length(s.G), at<int2>(ws, w.short_items),
+      at<int>(ws, w.counts) + 2, status);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? TSP_OK : cuda_fail(e, "packed attention: work list launch");
 }
@@ -800,12 +807,8 @@ tsp_status tsp_packed_attention_fwd(int64_t tokens, int n_seqs, const int32_t* s
   p.lse = lse;
   p.ld_lse = ld_lse;
   // 72 MB of K and V in L2 at a time, as for the plan's attention
-  static_cast<Source&>(p.src) =
-      make_source(s, starts, 2 * s.TPT, false, head_group(s, 72ll << 20), at<Item>(ws, w.items),
-                  at<int>(ws, w.counts), (int)w.max_fwd, ws, 0);
-  p.src.short_len = short_length(s.G);
-  p.src.short_items = at<int2>(ws, w.short_items);
-  p.src.short_count = at<int>(ws, w.counts) + 2;
+  p.src = make_source(s, starts, 2 * s.TPT, false, head_group(s, 72ll << 20), at<Item>(ws, w.items),
+                      at<int>(ws, w.counts), (int)w.max_fwd, ws, w, 0);
   p.G = s.G;
   p.TPT = s.TPT;
   p.RU = s.RU;
@@ -814,9 +817,8 @@ tsp_status tsp_packed_attention_fwd(int64_t tokens, int n_seqs, const int32_t* s
   p.limit_ns = wait_limit_ns();
   if (p.src.items != nullptr) {
     const ListArgs list{2 * s.TPT, 0, list_shift((tokens + TILE - 1) / TILE), at<Item>(ws, w.items),
-                        at<int>(ws, w.counts), (int)w.max_fwd, p.src.short_len,
-                        at<int2>(ws, w.short_items), at<int>(ws, w.counts) + 2};
-    TSP_TRY(launch_lists(s, starts, list, ListArgs{}, p.status, st));
+                        at<int>(ws, w.counts), (int)w.max_fwd};
+    TSP_TRY(launch_lists(s, starts, list, ListArgs{}, ws, w, p.status, st));
   }
   if (head_dim == 64) return launch_fwd<64>(s, p, q, ld_q, k, ld_k, v, ld_v, st);
   return launch_fwd<128>(s, p, q, ld_q, k, ld_k, v, ld_v, st);

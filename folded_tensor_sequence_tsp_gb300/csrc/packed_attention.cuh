@@ -30,7 +30,7 @@ struct Shape {
 };
 
 // Sequences of up to this many tokens are short: at most 8, and 32 rows of tokens x heads of a
-// group (packed_short.cuh takes them in the forward; tiles take the others).
+// group (packed_short.cuh takes them, tiles the others).
 inline int short_length(int G) { return 32 / G < 8 ? 32 / G : 8; }
 
 // Workspace (byte offsets from its 256-byte aligned start).
@@ -56,9 +56,6 @@ struct ListArgs {
   Item* items;
   int* count;
   int max_items;
-  int short_len;      // sequences of up to so many tokens go to this list (start, tokens)
-  int2* short_items;
-  int* short_count;
 };
 
 // Where a kernel takes its items from: a list made by launch_lists, or, for up to
@@ -78,15 +75,9 @@ struct Source {
   unsigned* next;  // [2] in the workspace: works handed out beyond the first of each CTA, and
                    // CTAs that are done; both 0 before and after a launch
   DevStatus* status;
-  static constexpr bool SHORT = false;
-};
-
-// The same where short sequences are no items.
-struct ShortSource : Source {
-  int short_len;            // the longest of them
-  const int2* short_items;  // with a list
+  int short_len;            // sequences of up to so many tokens are no items
+  const int2* short_items;  // with a list: those sequences (start, tokens)
   const int* short_count;
-  static constexpr bool SHORT = true;
 };
 
 #ifdef __CUDACC__
@@ -99,8 +90,7 @@ struct ShortSource : Source {
 // lie at b or further, so b comes from a binary search over warp sums and the sequence from a
 // rank among those with more than b items. About a microsecond, which the persistent kernels
 // spend beside their products, against 5 for a kernel that writes the list.
-template <class Src>
-__device__ __forceinline__ bool find_item(const Src& src, unsigned w, Item& it) {
+static __device__ __forceinline__ bool find_item(const Source& src, unsigned w, Item& it) {
   constexpr int K = SEARCH_SEQS / 32;
   const int lane = threadIdx.x & 31;
   int nb[K], st[K], ln[K];
@@ -117,8 +107,7 @@ __device__ __forceinline__ bool find_item(const Src& src, unsigned w, Item& it) 
         bad = bad || a < 0 || b < a || b > src.tokens;
         st[u] = a;
         ln[u] = b - a;
-        nb[u] = (int)(((long long)ln[u] + src.tile - 1) / src.tile);
-        if constexpr (Src::SHORT) nb[u] = ln[u] <= src.short_len ? 0 : nb[u];
+        nb[u] = ln[u] <= src.short_len ? 0 : (int)(((long long)ln[u] + src.tile - 1) / src.tile);
       }
       total += nb[u];
     }
@@ -185,8 +174,7 @@ __device__ __forceinline__ bool find_item(const Src& src, unsigned w, Item& it) 
 struct Walk {
   bool begun = false;
   // Moves on to the next item (the first call: to the first); head -1 at the end.
-  template <class Src>
-  __device__ __forceinline__ void next(const Src& src, Item& it) {
+  __device__ __forceinline__ void next(const Source& src, Item& it) {
     unsigned w = blockIdx.x;
     if (begun) {
       if ((threadIdx.x & 31) == 0) w = gridDim.x + atomicAdd(src.next, 1u);
@@ -260,9 +248,10 @@ tsp_status make_shape(const char* what, int64_t tokens, int n_seqs, int heads, i
 Workspace make_workspace(const Shape& s);
 // Fills one or two lists (b.tile == 0: one) from the sequence starts, on the device.
 tsp_status launch_lists(const Shape& s, const int32_t* starts, const ListArgs& a, const ListArgs& b,
-                        DevStatus* status, cudaStream_t stream);
+                        void* ws, const Workspace& w, DevStatus* status, cudaStream_t stream);
 Source make_source(const Shape& s, const int32_t* starts, int tile, bool from_end, int group,
-                   const Item* items, const int* count, int max_items, void* ws, int counter);
+                   const Item* items, const int* count, int max_items, void* ws, const Workspace& w,
+                   int counter);
 int list_shift(long long max_cost);
 // Query heads grouped by key head: box of 64 columns x G heads x TPT tokens.
 tsp_status make_query_map(CUtensorMap* map, const Shape& s, const void* base, int64_t ld);

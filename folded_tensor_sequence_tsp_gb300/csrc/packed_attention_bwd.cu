@@ -13,13 +13,15 @@
 //             dO in TMEM as A operands. It also forms Delta, from its rows of o and dO, or
 //             from P and dP where one key tile holds all keys of its rows, and leaves it for
 //             the key side.
-//   key side  a CTA owns 128 keys of one key head and streams every query tile that sees them: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q. A tile's rows
+//   key side  a CTA owns 128 keys of one key head and streams every query tile that sees
+//             them: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q. A tile's rows
 //             are all heads of the group, so the group's sum needs nothing more: it happens
 //             in the fp32 accumulators, in a fixed order.
 // P and dS are rounded to bf16 as operands of the tensor core, at most 2^-8 of a term; dS is
 // formed from the unrounded P. Accumulators and statistics are fp32.
 // Both kernels are persistent as the forward is. The key side may start on multiprocessors
-// that the query side has left; only its Delta waits for the end of that.
+// that the query side has left; only its Delta waits for the end of that. Sequences of a few
+// tokens go to no tile (packed_short.cuh).
 //
 // Rows that are no query of the sequence (the rows of a tile behind the sequence's end, and
 // those past TPT x G when G does not divide 128) enter the key side's sums with P = 0: their
@@ -45,6 +47,7 @@
 
 #include "attention_math.cuh"
 #include "packed_attention.cuh"
+#include "packed_short.cuh"
 
 namespace tsp {
 namespace packed {
@@ -63,6 +66,11 @@ struct BwdParams {
   long long ld_dq, ld_dk, ld_dv;
   const __nv_bfloat16* o;
   long long ld_o;
+  const __nv_bfloat16* q;  // read directly for the short sequences
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const __nv_bfloat16* dout;
+  long long ld_q, ld_k, ld_v, ld_do;
   const float* lse;
   long long ld_lse;
   float* delta;
@@ -152,7 +160,7 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
     packed_bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmDO,
                           const __grid_constant__ CUtensorMap tmK,
-                          const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
+                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ BwdParams p) {
   using Geo = KeyGeom<HD>;
   constexpr uint32_t QS = Geo::QS, OS = Geo::OS;
   extern __shared__ uint8_t smem_raw[];
@@ -508,6 +516,8 @@ __global__ void __launch_bounds__(KeyGeom<HD>::THREADS, 1)
       const bool mine = mbar_wait(bar, parity & 1u, wb, SITE_PACKED_SOFTMAX);
       return __all_sync(0xffffffffu, mine) != 0;
     };
+    // the short sequences, under the first item's loads
+    short_key_side<HD>(p, (gridDim.x - 1u - blockIdx.x) * 8u + (unsigned)(warp - 2), gridDim.x * 8u);
     // The loop below is short of issue slots: stages, phases and addresses step along instead
     // of being computed from the tile's number (remainders by 3 alone cost 0.1 of 1.8 us a tile).
     uint32_t n_items = 0, c = 0;              // items and streamed tiles so far
@@ -677,7 +687,7 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
     packed_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmDO,
                          const __grid_constant__ CUtensorMap tmK,
-                         const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
+                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ BwdParams p) {
   using Geo = QueryGeom<HD>;
   constexpr uint32_t NS = Geo::NS;
   extern __shared__ uint8_t smem_raw[];
@@ -1027,6 +1037,9 @@ __global__ void __launch_bounds__(QueryGeom<HD>::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(del_full);
     };
+    // the short sequences, under the first item's loads
+    prior_kernel_done();  // the lists, where there are any
+    short_query_side<HD>(p, (gridDim.x - 1u - blockIdx.x) * 8u + (unsigned)(warp - 2), gridDim.x * 8u);
     Row cur;
     bool ok;
     {
@@ -1257,6 +1270,14 @@ extern "C" tsp_status tsp_packed_attention_bwd(
   p.ld_dv = ld_dv;
   p.o = in(o);
   p.ld_o = ld_o;
+  p.q = in(q);
+  p.k = in(k);
+  p.v = in(v);
+  p.dout = in(dout);
+  p.ld_q = ld_q;
+  p.ld_k = ld_k;
+  p.ld_v = ld_v;
+  p.ld_do = ld_do;
   p.lse = lse;
   p.ld_lse = ld_lse;
   p.delta = at<float>(ws, w.delta);
@@ -1272,15 +1293,15 @@ extern "C" tsp_status tsp_packed_attention_bwd(
   // 48 MB of K and V in L2 at a time, as for the plan's backward
   const int group = head_group(s, 48ll << 20);
   const Source queries = make_source(s, starts, s.TPT, false, group, at<Item>(ws, w.items), counts,
-                                     (int)w.max_query, ws, 1);
+                                     (int)w.max_query, ws, w, 1);
   const Source keys = make_source(s, starts, TILE, true, group, at<Item>(ws, w.key_items), counts + 1,
-                                  (int)w.max_key, ws, 2);
+                                  (int)w.max_key, ws, w, 2);
   if (queries.items != nullptr) {
     const ListArgs a{s.TPT, 0, list_shift((tokens + TILE - 1) / TILE), at<Item>(ws, w.items), counts,
-                     (int)w.max_query, 0, nullptr, nullptr};
+                     (int)w.max_query};
     const ListArgs b{TILE, s.TPT, list_shift((tokens + s.TPT - 1) / s.TPT), at<Item>(ws, w.key_items),
-                     counts + 1, (int)w.max_key, 0, nullptr, nullptr};
-    TSP_TRY(launch_lists(s, starts, a, b, p.status, st));
+                     counts + 1, (int)w.max_key};
+    TSP_TRY(launch_lists(s, starts, a, b, ws, w, p.status, st));
   }
   if (head_dim == 64) return launch_bwd<64>(s, queries, keys, p, q, ld_q, dout, ld_do, k, ld_k, v, ld_v, st);
   return launch_bwd<128>(s, queries, keys, p, q, ld_q, dout, ld_do, k, ld_k, v, ld_v, st);

@@ -1,7 +1,7 @@
-"""Packed attention over sequences of a few tokens, which warps take on the CUDA cores, beside
-ones that tiles take: against the formula in float64 with the bounds of the packed attention's
-own tests (products here keep P and dS in fp32, so they hold with room), found in registers and
-from the list, and with values that are not finite in masked places."""
+"""Packed attention over sequences of a few tokens, which single warps take, beside ones that
+tiles take: against the formula in float64 with the bounds of the packed attention's own tests
+(the same roundings, but that the forward keeps P in fp32), found in registers and from the
+list, and with values that are not finite in masked places."""
 import pytest
 import torch
 
