@@ -108,8 +108,7 @@ __device__ __forceinline__ int claim(int* counter, int b, bool any) {
 
 __global__ void __launch_bounds__(LIST_THREADS)
     packed_lists_kernel(const int32_t* __restrict__ starts, int n, long long tokens, ListArgs a,
-                        ListArgs b, int short_len, int2* short_items, int* short_count,
-                        DevStatus* status) {
+                        ListArgs b, int short_len, int* short_count, DevStatus* status) {
   dependents_may_start();
   const ListArgs l = blockIdx.x == 0 ? a : b;
   __shared__ int hist[1024];
@@ -167,13 +166,15 @@ __global__ void __launch_bounds__(LIST_THREADS)
     const int slot = claim(hist, any ? bucket(len, q0) : 0, any);
     if (any && slot < l.max_items) l.items[slot] = Item{s, len, q0, 0};
   });
-  if (blockIdx.x == 0) {  // the short sequences, for every kernel behind this one
+  if (blockIdx.x == 0) {
+    // the short sequences, for every kernel behind this one: from the other end of the list,
+    // which has a place for each, since a sequence that is short has no item
     for (int base = 0; base < n; base += LIST_THREADS) {
       const int i = base + tid;
       const int start = i < n ? starts[i] : 0, len = i < n ? starts[i + 1] - start : 0;
       const bool is = len > 0 && len <= short_len;
       const int slot = claim(&n_short, 0, is);
-      if (is) short_items[slot] = make_int2(start, len);
+      if (is) l.items[l.max_items - 1 - slot] = Item{start, len, 0, 0};
     }
     __syncthreads();
     if (tid == 0) *short_count = n_short;
@@ -684,21 +685,17 @@ Workspace make_workspace(const Shape& s) {
   w.counts = take(256);
   w.items = take((size_t)w.max_query * sizeof(Item));
   w.key_items = take((size_t)w.max_key * sizeof(Item));
-  w.short_items = take((size_t)s.n_seqs * sizeof(int2));
   w.delta = take((size_t)s.heads * (size_t)w.ld_stat * sizeof(float));
   w.total = off;
   return w;
 }
 
 Source make_source(const Shape& s, const int32_t* starts, int tile, bool from_end, int group,
-                   const Item* items, const int* count, int max_items, void* ws, const Workspace& w,
-                   int counter) {
+                   const Item* items, const int* count, int max_items, void* ws, int counter) {
   Source src{};
   if (s.n_seqs > SEARCH_SEQS) {
     src.items = items;
     src.count = count;
-    src.short_items = at<int2>(ws, w.short_items);
-    src.short_count = at<int>(ws, w.counts) + 2;
   }
   src.short_len = short_length(s.G);
   src.starts = starts;
@@ -721,10 +718,9 @@ int list_shift(long long max_cost) {
 }
 
 tsp_status launch_lists(const Shape& s, const int32_t* starts, const ListArgs& a, const ListArgs& b,
-                        void* ws, const Workspace& w, DevStatus* status, cudaStream_t stream) {
+                        int* short_count, DevStatus* status, cudaStream_t stream) {
   packed_lists_kernel<<<b.tile ? 2 : 1, LIST_THREADS, 0, stream>>>(
-      starts, s.n_seqs, s.tokens, a, b, short_length(s.G), at<int2>(ws, w.short_items),
-      at<int>(ws, w.counts) + 2, status);
+      starts, s.n_seqs, s.tokens, a, b, short_length(s.G), short_count, status);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? TSP_OK : cuda_fail(e, "packed attention: work list launch");
 }
@@ -808,7 +804,7 @@ tsp_status tsp_packed_attention_fwd(int64_t tokens, int n_seqs, const int32_t* s
   p.ld_lse = ld_lse;
   // 72 MB of K and V in L2 at a time, as for the plan's attention
   p.src = make_source(s, starts, 2 * s.TPT, false, head_group(s, 72ll << 20), at<Item>(ws, w.items),
-                      at<int>(ws, w.counts), (int)w.max_fwd, ws, w, 0);
+                      at<int>(ws, w.counts), (int)w.max_fwd, ws, 0);
   p.G = s.G;
   p.TPT = s.TPT;
   p.RU = s.RU;
@@ -816,9 +812,11 @@ tsp_status tsp_packed_attention_fwd(int64_t tokens, int n_seqs, const int32_t* s
   p.status = status_of(ws);
   p.limit_ns = wait_limit_ns();
   if (p.src.items != nullptr) {
+    p.src.short_last = p.src.items + w.max_fwd - 1;
+    p.src.short_count = at<int>(ws, w.counts) + 2;
     const ListArgs list{2 * s.TPT, 0, list_shift((tokens + TILE - 1) / TILE), at<Item>(ws, w.items),
                         at<int>(ws, w.counts), (int)w.max_fwd};
-    TSP_TRY(launch_lists(s, starts, list, ListArgs{}, ws, w, p.status, st));
+    TSP_TRY(launch_lists(s, starts, list, ListArgs{}, at<int>(ws, w.counts) + 2, p.status, st));
   }
   if (head_dim == 64) return launch_fwd<64>(s, p, q, ld_q, k, ld_k, v, ld_v, st);
   return launch_fwd<128>(s, p, q, ld_q, k, ld_k, v, ld_v, st);

@@ -39,7 +39,6 @@ struct Workspace {
   size_t counts;  // int[3]: items in each list
   size_t items;   // forward, or query side of the backward
   size_t key_items;
-  size_t short_items;
   size_t delta;   // [heads][ld_stat] fp32
   size_t total;
   long long max_fwd, max_query, max_key;  // capacity of the lists
@@ -76,7 +75,7 @@ struct Source {
                    // CTAs that are done; both 0 before and after a launch
   DevStatus* status;
   int short_len;            // sequences of up to so many tokens are no items
-  const int2* short_items;  // with a list: those sequences (start, tokens)
+  const Item* short_last;   // with a list: those sequences, backwards from here
   const int* short_count;
 };
 
@@ -117,7 +116,7 @@ static __device__ __forceinline__ bool find_item(const Source& src, unsigned w, 
     }
     total = __reduce_add_sync(0xffffffffu, total);
   } else {
-    total = *src.count;
+    total = min(*src.count, src.max_items);
   }
   if (total <= 0 || w >= (unsigned long long)total * (unsigned)src.kv_heads) return false;
   const unsigned per_group = (unsigned)total * (unsigned)src.group;
@@ -248,10 +247,9 @@ tsp_status make_shape(const char* what, int64_t tokens, int n_seqs, int heads, i
 Workspace make_workspace(const Shape& s);
 // Fills one or two lists (b.tile == 0: one) from the sequence starts, on the device.
 tsp_status launch_lists(const Shape& s, const int32_t* starts, const ListArgs& a, const ListArgs& b,
-                        void* ws, const Workspace& w, DevStatus* status, cudaStream_t stream);
+                        int* short_count, DevStatus* status, cudaStream_t stream);
 Source make_source(const Shape& s, const int32_t* starts, int tile, bool from_end, int group,
-                   const Item* items, const int* count, int max_items, void* ws, const Workspace& w,
-                   int counter);
+                   const Item* items, const int* count, int max_items, void* ws, int counter);
 int list_shift(long long max_cost);
 // Query heads grouped by key head: box of 64 columns x G heads x TPT tokens.
 tsp_status make_query_map(CUtensorMap* map, const Shape& s, const void* base, int64_t ld);

@@ -1292,16 +1292,18 @@ extern "C" tsp_status tsp_packed_attention_bwd(
   int* counts = at<int>(ws, w.counts);
   // 48 MB of K and V in L2 at a time, as for the plan's backward
   const int group = head_group(s, 48ll << 20);
-  const Source queries = make_source(s, starts, s.TPT, false, group, at<Item>(ws, w.items), counts,
-                                     (int)w.max_query, ws, w, 1);
-  const Source keys = make_source(s, starts, TILE, true, group, at<Item>(ws, w.key_items), counts + 1,
-                                  (int)w.max_key, ws, w, 2);
+  Source queries = make_source(s, starts, s.TPT, false, group, at<Item>(ws, w.items), counts,
+                               (int)w.max_query, ws, 1);
+  Source keys = make_source(s, starts, TILE, true, group, at<Item>(ws, w.key_items), counts + 1,
+                            (int)w.max_key, ws, 2);
   if (queries.items != nullptr) {
+    queries.short_last = keys.short_last = queries.items + w.max_query - 1;
+    queries.short_count = keys.short_count = counts + 2;
     const ListArgs a{s.TPT, 0, list_shift((tokens + TILE - 1) / TILE), at<Item>(ws, w.items), counts,
                      (int)w.max_query};
     const ListArgs b{TILE, s.TPT, list_shift((tokens + s.TPT - 1) / s.TPT), at<Item>(ws, w.key_items),
                      counts + 1, (int)w.max_key};
-    TSP_TRY(launch_lists(s, starts, a, b, ws, w, p.status, st));
+    TSP_TRY(launch_lists(s, starts, a, b, counts + 2, p.status, st));
   }
   if (head_dim == 64) return launch_bwd<64>(s, queries, keys, p, q, ld_q, dout, ld_do, k, ld_k, v, ld_v, st);
   return launch_bwd<128>(s, queries, keys, p, q, ld_q, dout, ld_do, k, ld_k, v, ld_v, st);
