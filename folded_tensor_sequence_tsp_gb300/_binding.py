@@ -856,7 +856,9 @@ def _stat(t, name, heads, tokens):
         raise ValueError(f"{name} must be float32 [{heads}, {tokens}]")
     if tokens > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: the values of a head must be contiguous")
-    return t.data_ptr(), max(t.stride(0), tokens) if heads > 1 else tokens
+    if heads > 1 and t.stride(0) < tokens:
+        raise ValueError(f"{name}: the rows of two heads overlap")
+    return t.data_ptr(), t.stride(0) if heads > 1 else tokens
 
 
 def _ws_packed(ws, sizes):

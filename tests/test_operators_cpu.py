@@ -167,3 +167,12 @@ def test_packed_attention_workspace(lib):
 def test_status_init_needs_a_workspace(lib):
     expect(lib, lib.tsp_status_init(None, None), B.TSP_ERR_INVALID_ARG, "workspace")
     expect(lib, lib.tsp_status_init(P(0) + 8, None), B.TSP_ERR_INVALID_ARG, "256-byte")
+
+
+def test_row_statistics_whose_rows_overlap():
+    one = torch.empty(1, 5)
+    assert B._stat(one, "lse", 1, 5) == (one.data_ptr(), 5)
+    assert B._stat(torch.empty(3, 8)[:, :5], "lse", 3, 5)[1] == 8
+    for t in (one.expand(3, 5), torch.empty(9).as_strided((3, 5), (2, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            B._stat(t, "lse", 3, 5)
