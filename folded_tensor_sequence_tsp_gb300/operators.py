@@ -5,7 +5,8 @@ does not bring.
 One object serves one stream at a time: its calls share its workspace, so calls that may
 overlap (two streams, two captured graphs that replay at the same time) need an object
 each. The workspace is never replaced, so a captured graph stays valid as long as its
-object lives.
+object lives. An object may serve another stream than the one it was made on; like any
+tensor, it is deleted once the streams it served are done with it.
 """
 from __future__ import annotations
 
@@ -55,6 +56,9 @@ class TSPPackedAttention:
             raise TSPError(2, tsp_last_error())
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         tsp_status_init(self.ws)
+        if not torch.cuda.is_current_stream_capturing():
+            # the first call may come on another stream
+            torch.cuda.current_stream(self.device).synchronize()
 
     def _check(self, q, k, starts):
         if q.shape[1:] != (self.heads, self.head_dim) or k.shape[1:] != (self.kv_heads, self.head_dim):

@@ -228,3 +228,19 @@ def test_two_streams_at_once_with_an_object_each():
     assert all(torch.equal(x, y) for x, y in zip(got, want[0]))
     for op in ops:
         op.check()
+
+
+def test_object_made_behind_queued_work_serves_another_stream():
+    """The workspace is ready when the constructor returns, whatever its stream still has to do."""
+    g = gen(3)
+    q, k, v = (g(300, h, 64).bfloat16() for h in (4, 2, 2))
+    starts = torch.tensor([0] + list(range(2, 301, 2)), dtype=torch.int32, device="cuda")
+    want = tsp.TSPPackedAttention(300, 150, 4, 2, 64).forward(q, k, v, starts)
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)  # about 10 ms, bounded
+    op = tsp.TSPPackedAttention(300, 150, 4, 2, 64)
+    op.forward(q, k, v, starts, out=out, stream=side)
+    op.check(side)
+    assert torch.equal(out, want)
