@@ -175,7 +175,8 @@ __global__ void __launch_bounds__(kThreads, 4)
                       float max_norm, float* norm) {
   const double v = norm_of(partial, n_partial);
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
-  const double want = (double)max_norm / (v + 1e-6);
+  // an infinite max_norm clips nothing, not even an infinite norm; a NaN norm stays one
+  const double want = isinf(max_norm) && !isnan(v) ? 1. : (double)max_norm / (v + 1e-6);
   // a NaN norm gives a NaN factor; one below 2^-100, which fp32 would round to few bits,
   // is applied as factor * 2^64 and then 2^-64, which is exact
   const bool tiny = want < 7.9e-31;

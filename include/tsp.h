@@ -732,7 +732,8 @@ typedef enum tsp_dtype { TSP_F32 = 0, TSP_BF16 = 1 } tsp_dtype;
  * 1e-6)), rounded once to the tensor's type. outs[i] may be grads[i] (in place; then
  * nothing is written when the factor is 1); it may not overlap anything else of the list
  * (TSP_ERR_INVALID_ARG). max_norm >= 0, infinity for no clipping. A NaN norm makes every
- * output NaN, an infinite norm 0 (NaN where the gradient is infinite).
+ * output NaN; an infinite norm above a finite max_norm makes it 0 (NaN where the gradient
+ * is infinite).
  *
  * ws: tsp_grad_workspace_bytes(n) bytes, 256-byte aligned, scratch of the call. n from 0
  * (norm 0) to TSP_GRAD_MAX_TENSORS. Both calls only launch kernels: they can be captured,

@@ -353,3 +353,16 @@ def test_norm_and_clip_replay_from_a_graph_on_another_stream():
     y, _ = norm_op.forward(x, w, residual=r, stream=side)
     side.synchronize()
     assert torch.equal(y, eager[0])
+
+
+def test_no_clipping_of_an_infinite_norm():
+    """max_norm infinite: the gradients stay as they are, whatever the norm but NaN."""
+    op = tsp.TSPGradClip(2)
+    a = torch.tensor([1.0, math.inf, -3.0], device="cuda")
+    b = torch.tensor([2.0, -4.0], device="cuda", dtype=torch.bfloat16)
+    outs = [torch.zeros_like(a), torch.zeros_like(b)]
+    assert math.isinf(op.clip([a, b], math.inf, outs=outs).item())
+    assert torch.equal(outs[0], a) and torch.equal(outs[1], b)
+    a[1] = math.nan
+    assert math.isnan(op.clip([a, b], math.inf, outs=outs).item())
+    assert torch.isnan(outs[0]).all() and torch.isnan(outs[1]).all()
