@@ -116,7 +116,9 @@ static __device__ __forceinline__ bool find_item(const Source& src, unsigned w, 
     }
     total = __reduce_add_sync(0xffffffffu, total);
   } else {
-    total = min(*src.count, src.max_items);
+    // past L1: the key side reads the list without having waited for the kernel that wrote it
+    // (the query side has, before it let the key side start)
+    total = min(__ldcg(src.count), src.max_items);
   }
   if (total <= 0 || w >= (unsigned long long)total * (unsigned)src.kv_heads) return false;
   const unsigned per_group = (unsigned)total * (unsigned)src.group;
@@ -126,10 +128,10 @@ static __device__ __forceinline__ bool find_item(const Source& src, unsigned w, 
   const int idx = rem / in_g;
   it.head = grp * src.group + (rem - idx * in_g);
   if (src.items != nullptr) {
-    const Item listed = src.items[idx];
-    it.start = listed.start;
-    it.len = listed.len;
-    it.q0 = listed.q0;
+    const int4 listed = __ldcg(reinterpret_cast<const int4*>(src.items + idx));  // an Item
+    it.start = listed.x;
+    it.len = listed.y;
+    it.q0 = listed.z;
   } else {
     auto from = [&](int b) {
       int c = 0;

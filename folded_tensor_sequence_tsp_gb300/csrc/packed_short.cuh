@@ -41,7 +41,7 @@ struct ShortFinder {
   int st[K], ln[K];
   // Their number (0 where the starts are not in order).
   __device__ __forceinline__ int load(const Source& src) {
-    if (src.items != nullptr) return min(*src.short_count, src.n_seqs);
+    if (src.items != nullptr) return min(__ldcg(src.short_count), src.n_seqs);
     bool bad = false;
     int n = 0;
 #pragma unroll
@@ -61,9 +61,9 @@ struct ShortFinder {
   // Sequence `rank` of the short ones (rank below their number).
   __device__ __forceinline__ void get(const Source& src, int rank, int& start, int& len) const {
     if (src.items != nullptr) {
-      const Item it = *(src.short_last - rank);
-      start = it.start;
-      len = it.len;
+      const int2 it = __ldcg(reinterpret_cast<const int2*>(src.short_last - rank));  // an Item's
+      start = it.x;
+      len = it.y;
       return;
     }
     const int lane = threadIdx.x & 31;
