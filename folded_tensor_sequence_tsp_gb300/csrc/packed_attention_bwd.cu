@@ -28,7 +28,10 @@
 // lse is +infinity and their Q and dO rows are zeros in shared memory, so nothing that lies
 // behind the sequence can reach a sum. The query side clears its last K and V tile the same
 // way. Pairs above the diagonal are set to 0 by selection in P, and on the query side, where
-// dP may hold a later key's infinity, in dS as well.
+// dP may hold a later key's infinity, in dS as well. On the key side selection in dS would not
+// keep an earlier query's infinity out: 0 times its rows of Q and dO enters dK and dV all the
+// same. So it reaches the later keys that share a tile with it: those below k0 + 128 for a key
+// tile from k0 on, whose first query tile begins at floor(k0 / TPT) TPT.
 //
 // Measured, heads of 128: 16381 tokens, 32/4 heads 2.3 ms and 3.4 ms (1430 and 1300 TFLOP/s of
 // the products that run); 8192 tokens in 27 sequences, 32/8 heads 0.15 and 0.16 ms (the 128 x

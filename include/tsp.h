@@ -628,9 +628,12 @@ tsp_status tsp_cost_max_batch(int scheme, int D, int tp, int64_t S, int hidden, 
  * starts on the device a captured call can be replayed with other lengths. Starts that
  * decrease or leave [0, tokens] write nothing and set TSP_ERR_INVALID_ARG in the status
  * word (tsp_device_status).
- * A sequence's results have the same bits whatever is packed beside it. Inside a sequence
- * a NaN or an infinity in the row of one token may reach the results of tokens up to 127
- * positions before it (they share a tile, where its weight of 0 multiplies it).
+ * A sequence's results have the same bits whatever is packed beside it. Inside a sequence a
+ * pair above the diagonal has the weight 0 in a tile's product, and 0 times a NaN or an
+ * infinity is not 0: beyond what causality has it reach, one in the k or v row of a token may
+ * reach o and dq of tokens up to R positions before it, and one in its q, o or dout row dk
+ * and dv of tokens up to R positions after it. R is 127 where floor(128 / G) divides 128, as
+ * for every power of two, and 126 + floor(128 / G) otherwise. lse is not reached.
  * scale multiplies the scores (1/sqrt(d) is customary); positive and finite.
  * lse (fp32 [heads][ld_lse], one value per head and token): log2 of the sum over the
  * visible keys of exp(scale q.k), as tsp_causal_attention_lse stores it.
