@@ -778,15 +778,14 @@ __global__ void __launch_bounds__(512, 2) rmsnorm_bwd_odd_kernel(const NormBwdPa
 
 // dw[c] = sum of the partial rows, in a fixed order: 32 row groups per column, then their
 // sum.
-__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* __restrict__ partial, int n,
-                                                          int width, float* __restrict__ dw) {
+__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* partial, int n, int width, float* dw) {
   __shared__ float part[32][33];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + cx;
   float s = 0.f;
   prior_kernel_done();
   if (c < width)
-    for (int r = ry; r < n; r += 32) s += partial[(long long)r * width + c];
+    for (int r = ry; r < n; r += 32) s += __ldcg(partial + (long long)r * width + c);
   part[ry][cx] = s;
   __syncthreads();
   // column ry's 32 sums, one per lane

@@ -245,8 +245,10 @@ tsp_status mlp_block(const Plan& p, const void* hs, const void* wpack, const voi
 
 // Launches a kernel that may start while the one before it on the stream is still running: on
 // multiprocessors that this has left, once all of its CTAs have called dependents_may_start().
-// What the kernel reads of the earlier one's output comes after prior_kernel_done(). It hides
-// the launch and set-up of the second of two kernels, 2 to 4 us.
+// What the kernel reads of the earlier one's output comes after prior_kernel_done(), and through
+// plain or __ldcg loads: the earlier kernel still writes it while this one is alive, so it is not
+// read-only for the kernel's lifetime, as __ldg and a pointer to const __restrict__ would promise.
+// It hides the launch and set-up of the second of two kernels, 2 to 4 us.
 template <class... P, class... A>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                          A&&... args) {
