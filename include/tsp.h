@@ -695,9 +695,10 @@ tsp_status tsp_rmsnorm_fwd(int64_t rows, int width, const tsp_bf16* x, const voi
  * tsp_rmsnorm_fwd_e4m3 - the same with an 8-bit output: y holds e4m3 values (4 exponent
  * and 3 mantissa bits, largest 448) and scales fp32 factors, so that y * scale stands for
  * the normed row. group 0: one scale per row, scales [rows]; group 128: one per 128
- * columns, scales [rows][ceil(width / 128)], the last group may be short. scale = max|y| /
- * 448 over the group (not below 2^-126; 1 for a group of zeros), y rounded to nearest
- * even from the fp32 value. A group with a NaN or an infinity has a NaN or infinite scale.
+ * columns, scales [rows][ceil(width / 128)], the last group may be short. From the normed
+ * row in fp32: scale = max|y| / 448 over the group (not below 2^-126; 1 for a group of zeros)
+ * and y = the quotient by it, both fp32 divisions rounded to nearest, the quotient then to
+ * e4m3, to even at a tie. A group with a NaN or an infinity has a NaN or infinite scale.
  * y must not be x; other groups are TSP_ERR_UNSUPPORTED.
  */
 tsp_status tsp_rmsnorm_fwd_e4m3(int64_t rows, int width, const tsp_bf16* x, const void* residual,
