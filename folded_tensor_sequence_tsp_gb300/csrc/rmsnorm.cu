@@ -880,10 +880,14 @@ tsp_status launch_fwd_res(const NormParams& p, bool vec, cudaStream_t s) {
   if (p.width <= 512) return launch_fwd_staged<2 * P, true, RES, E4M3, 3, 256>(p, 256, s);
   if (p.width <= 1024) return launch_fwd_staged<4 * P, true, RES, E4M3, 2, 256>(p, 256, s);
   const int threads = row_threads(p.width / 8, 2);
-  // an fp32 stream beside a bf16 output moves the most bytes per column: four CTAs' loads in
-  // flight keep up without staging (16384 x 4096: 128 us against 135; every other kind gains
-  // from staging, e4m3 78 us against 97)
-  if (RES == RES_F32 && !E4M3 && threads <= 256) return launch_fwd_direct<8, 2, RES, E4M3>(p, s);
+  // an fp32 stream beside a bf16 output moves the most bytes per column: with at least four CTAs to
+  // a multiprocessor, their loads in flight keep up without staging (67M elements, direct against
+  // staged: 138 us against 143 at 1032 columns, 123 against 135 at 2048, 128 against 135 at 4096;
+  // with fewer CTAs 136 and 136 at 4608 and 8192, 132 against 136 at 5120, but 147 against 136 at
+  // 6144 and 175 against 136 at 12288). Every other kind gains from staging (e4m3 beside bf16 at
+  // 4096: 78 us against 97).
+  if constexpr (RES == RES_F32 && !E4M3)
+    if (threads <= 256) return launch_fwd_direct<8, 2, RES, E4M3>(p, s);
   if (threads <= 256) return launch_fwd_staged<2 * P, false, RES, E4M3, 2, 256>(p, threads, s);
   if (threads <= 1024) return launch_fwd_staged<2 * P, false, RES, E4M3, 2, 1024>(p, threads, s);
   return launch_fwd_direct<8, 4, RES, E4M3>(p, s);
