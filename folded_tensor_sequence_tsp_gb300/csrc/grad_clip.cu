@@ -30,7 +30,7 @@ namespace {
 constexpr int kChunk = 16384;
 constexpr int kThreads = 256;
 constexpr int kCtas = 608;   // partial sums per launch: a constant, so that their order is
-constexpr int kSmall = 64;   // tensors per launch in the small table (2.4 KB of parameters)
+constexpr int kSmall = 64;   // tensors per launch in the small table (1.9 KB of parameters)
 constexpr int kLarge = 1024; // and in the large one
 
 template <int N>
@@ -317,7 +317,8 @@ tsp_status check_list(const char* what, const List& l, const float* norm, void* 
     if (reinterpret_cast<uintptr_t>(l.in[i]) % a || (l.out && reinterpret_cast<uintptr_t>(l.out[i]) % a))
       return fail(TSP_ERR_INVALID_ARG, w + ": tensor not aligned to its element");
   }
-  // 2^32 chunks: 2^46 elements per launch
+  // at most 2^31 chunks (2^45 elements) over the list, so that a launch's chunk numbers and its
+  // stride of CTAs fit 32 bits
   int64_t total = 0;
   for (int i = 0; i < l.n; ++i) total += (l.sizes[i] + kChunk - 1) / kChunk;
   if (total > (1ll << 31)) return fail(TSP_ERR_UNSUPPORTED, w + ": too many elements");
