@@ -24,7 +24,12 @@ __all__ = ["TSPPackedAttention", "TSPRMSNorm", "TSPGradClip"]
 
 
 def _device(device):
-    device = torch.device(device or "cuda")
+    """The CUDA device of an object: the given one, by default the current one."""
+    if isinstance(device, int):
+        return torch.device("cuda", device)
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError(f"expected a CUDA device, got {device}")
     return device if device.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
