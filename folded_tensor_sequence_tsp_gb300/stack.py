@@ -6,9 +6,12 @@ Per layer, on the sharded activations ([D, S/D, H], or [D, batch, S/D, H]):
 and a last norm behind the last layer. The blocks are tsp_attention_fwd / tsp_mlp_fwd,
 which return without a residual; the residual's addition, the rounding of the stream and
 the next norm are one pass (tsp_rmsnorm_fwd). The stream h is kept in fp32 by default. All
-layers share one plan and one workspace.
+layers share one plan and one workspace. Calls run on the stack's device, on the stream that is
+current there.
 """
 from __future__ import annotations
+
+import functools
 
 import torch
 
@@ -16,36 +19,56 @@ from ._binding import (TSP_OK, TSPError, tsp_attention_bwd, tsp_attention_fwd, t
                        tsp_device_status, tsp_last_error, tsp_mlp_bwd, tsp_mlp_fwd, tsp_pack_weights,
                        tsp_packed_weight_bytes, tsp_plan, tsp_plan_batched, tsp_workspace_bytes,
                        tsp_workspace_init)
-from .operators import TSPGradClip, TSPRMSNorm
+from .operators import TSPGradClip, TSPRMSNorm, _device
 
 __all__ = ["TSPStack"]
+
+_MATRICES = ("Wq", "Wk", "Wv", "Wo", "W1", "W3", "W2")
+_NORMS = ("attn_norm", "mlp_norm")
+
+
+def _on_its_device(method):
+    """The layer's calls launch on the current device, whatever device their tensors are on."""
+    @functools.wraps(method)
+    def call(self, *args, **kwargs):
+        with torch.cuda.device(self.device):
+            return method(self, *args, **kwargs)
+    return call
 
 
 class TSPStack:
     """weights: one dict per layer with Wq, Wk, Wv, Wo, W1, W3, W2 (bfloat16 CUDA tensors,
-    nn.Linear layout) and the norm weights attn_norm and mlp_norm [hidden]; last_norm [hidden]."""
+    nn.Linear layout) and the norm weights attn_norm and mlp_norm [hidden]; last_norm [hidden]; all
+    on `device` (by default the current one)."""
 
     def __init__(self, D, S, hidden, heads, ffn, weights, last_norm, eps=1e-5, batch=1,
                  stream_dtype=torch.float32, device=None):
         if stream_dtype not in (torch.float32, torch.bfloat16):
             raise ValueError("stream_dtype must be float32 or bfloat16")
-        self.device = torch.device(device or "cuda")
+        self.device = _device(device)
+        if any(t.device != self.device for t in [last_norm, *(w[k] for w in weights for k in _MATRICES + _NORMS)]):
+            raise ValueError(f"the weights must be on {self.device}")
         self.plan = (tsp_plan(D, S, hidden, heads, ffn) if batch == 1
                      else tsp_plan_batched(D, S, batch, hidden, heads, ffn))
         self.stream_dtype = stream_dtype
         self.wpack = []
+        self._pack(weights)
+        # the norm in front of each block, and the last one
+        self.norms = [w[k] for w in weights for k in _NORMS] + [last_norm]
+        self.norm = TSPRMSNorm(self.plan.info.tokens, hidden, eps, device=self.device)
+        self.clipper = TSPGradClip(len(self.wpack) + len(self.norms), device=self.device)
+
+    @_on_its_device
+    def _pack(self, weights):
         for w in weights:
             packed = torch.empty(tsp_packed_weight_bytes(self.plan) // 2, dtype=torch.bfloat16,
                                  device=self.device)
-            tsp_pack_weights(self.plan, *(w[k] for k in ("Wq", "Wk", "Wv", "Wo", "W1", "W3", "W2")), packed)
+            tsp_pack_weights(self.plan, *(w[k] for k in _MATRICES), packed)
             self.wpack.append(packed)
-        # the norm in front of each block, and the last one
-        self.norms = [w[k] for w in weights for k in ("attn_norm", "mlp_norm")] + [last_norm]
-        self.norm = TSPRMSNorm(self.plan.info.tokens, hidden, eps, device=self.device)
-        self.clipper = TSPGradClip(len(self.wpack) + len(self.norms), device=self.device)
         self.ws = torch.empty(tsp_workspace_bytes(self.plan), dtype=torch.uint8, device=self.device)
         tsp_workspace_init(self.plan, self.ws)
 
+    @_on_its_device
     def enable_backward(self):
         """Grow the workspace to the backward's size (it serves the forward too). Call it before
         capturing a graph of the forward: growing replaces the workspace."""
@@ -83,16 +106,19 @@ class TSPStack:
             keep.append((y, h))
         return y
 
+    @_on_its_device
     def forward(self, xs):
         """The normed output of the stack for the sharded bfloat16 input xs."""
         return self._run(xs.view(self.shape), None)
 
+    @_on_its_device
     def forward_train(self, xs):
         """(output, saved): forward() that keeps each block's input and the stream."""
         self.enable_backward()
         saved = []
         return self._run(xs.view(self.shape), saved), saved
 
+    @_on_its_device
     def backward(self, saved, dout):
         """(dxs, grads) of the output gradient dout: dxs in the stream's type; grads is one
         packed fp32 weight gradient per layer (see tsp_unpack_weight_grads), then one fp32
@@ -118,11 +144,13 @@ class TSPStack:
             dh, dblock = through_norm(i, dy, dh)
         return dh, dpacked + dnorms
 
+    @_on_its_device
     def clip(self, grads, max_norm):
         """Scale backward()'s grads in place to a global norm of at most max_norm; returns the
         norm as one float32 on the device. The packed layout's padding holds zeros."""
         return self.clipper.clip(grads, max_norm)
 
+    @_on_its_device
     def check(self):
         """Synchronise and raise TSPError if a bounded device wait gave up."""
         st = tsp_device_status(self.ws)

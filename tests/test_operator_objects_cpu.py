@@ -1,8 +1,9 @@
 """The objects around the operators on the host: which device they take, which one they launch
 on, and what their workspaces do when they grow. No GPU: what allocates or launches is replaced."""
-import torch
+from types import SimpleNamespace
 
 import pytest
+import torch
 
 tsp = pytest.importorskip("folded_tensor_sequence_tsp_gb300")
 operators = tsp.operators
@@ -23,3 +24,94 @@ def test_the_device_asked_for(second_device, device, want):
 def test_only_cuda_devices(second_device, device):
     with pytest.raises(ValueError, match="CUDA device"):
         operators._device(device)
+
+
+# ------------------------------------------------------------------ TSPStack
+stack_module = tsp.stack
+
+
+class Fakes:
+    """The calls of a TSPStack as records of (name, device current at the call)."""
+
+    def __init__(self, monkeypatch):
+        self.calls, self.current = [], None
+        fakes = self
+
+        class Device:
+            def __init__(self, device):
+                self.device = device
+
+            def __enter__(self):
+                self.before, fakes.current = fakes.current, self.device
+
+            def __exit__(self, *exc):
+                fakes.current = self.before
+
+        def record(name, result=None):
+            def call(*args, **kwargs):
+                fakes.calls.append((name, fakes.current))
+                return result
+            return call
+
+        info = SimpleNamespace(D=2, T=4, batch=1, hidden=8, tokens=8, wpack_elems=16)
+        monkeypatch.setattr(torch.cuda, "device", Device)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+        monkeypatch.setattr(stack_module, "_device", lambda device: torch.device("cpu"))
+        for name, result in (("tsp_plan", SimpleNamespace(info=info)), ("tsp_packed_weight_bytes", 32),
+                             ("tsp_workspace_bytes", 256), ("tsp_bwd_workspace_bytes", 512),
+                             ("tsp_workspace_init", None), ("tsp_pack_weights", None),
+                             ("tsp_attention_fwd", None), ("tsp_mlp_fwd", None), ("tsp_attention_bwd", None),
+                             ("tsp_mlp_bwd", None), ("tsp_device_status", 0)):
+            monkeypatch.setattr(stack_module, name, record(name, result))
+
+        class Norm:
+            def __init__(self, *args, **kwargs):
+                pass
+
+            def forward(self, x, w, residual=None, y=None, h=None):
+                return x.clone(), residual
+
+            def backward(self, h, w, dy, dh=None, dx=None, dx16=None):
+                return h.clone(), torch.zeros(8)
+
+        class Clip:
+            def __init__(self, *args, **kwargs):
+                pass
+
+            def clip(self, grads, max_norm):
+                return record("clip")()
+
+        monkeypatch.setattr(stack_module, "TSPRMSNorm", Norm)
+        monkeypatch.setattr(stack_module, "TSPGradClip", Clip)
+
+    def stack(self, weights=None):
+        if weights is None:
+            weights = [{k: torch.zeros(8) for k in ("Wq", "Wk", "Wv", "Wo", "W1", "W3", "W2", "attn_norm",
+                                                     "mlp_norm")} for _ in range(2)]
+        return tsp.TSPStack(2, 8, 8, 2, 16, weights, torch.zeros(8))
+
+
+def test_a_stack_launches_on_its_own_device(monkeypatch):
+    fakes = Fakes(monkeypatch)
+    s = fakes.stack()
+    x = torch.zeros(2, 4, 8, dtype=torch.bfloat16)
+    s.forward(x)
+    out, saved = s.forward_train(x)
+    _, grads = s.backward(saved, out)
+    s.clip(grads, 1.0)
+    s.check()
+    launched = {name for name, _ in fakes.calls}
+    assert {"tsp_pack_weights", "tsp_workspace_init", "tsp_attention_fwd", "tsp_mlp_fwd", "tsp_attention_bwd",
+            "tsp_mlp_bwd", "tsp_device_status", "clip"} <= launched
+    for name, device in fakes.calls:
+        if name not in ("tsp_plan", "tsp_packed_weight_bytes", "tsp_workspace_bytes", "tsp_bwd_workspace_bytes"):
+            assert device == s.device, name
+    assert fakes.current is None
+
+
+def test_a_stack_refuses_weights_of_another_device(monkeypatch):
+    fakes = Fakes(monkeypatch)
+    w = {k: torch.zeros(8) for k in ("Wq", "Wk", "Wv", "Wo", "W1", "W3", "W2", "attn_norm", "mlp_norm")}
+    w["mlp_norm"] = torch.zeros(8, device="meta")
+    with pytest.raises(ValueError, match="must be on"):
+        fakes.stack([w])
