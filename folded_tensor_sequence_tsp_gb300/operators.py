@@ -5,8 +5,9 @@ does not bring.
 One object serves one stream at a time: its calls share its workspace, so calls that may
 overlap (two streams, two captured graphs that replay at the same time) need an object
 each. The workspace is never replaced, so a captured graph stays valid as long as its
-object lives. An object may serve another stream than the one it was made on; like any
-tensor, it is deleted once the streams it served are done with it.
+object lives. An object may serve another stream than the one it was made on: its workspace is
+ready when the constructor returns. Like any tensor, it is deleted once the streams it served
+are done with it.
 """
 from __future__ import annotations
 
@@ -42,6 +43,14 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
+def _ready(device):
+    """Wait for what a constructor has queued, and for what its stream still has to do on memory
+    that the constructor took over: the first call may come on another stream."""
+    with torch.cuda.device(device):
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(device).synchronize()
+
+
 class TSPPackedAttention:
     """Causal attention over packed sequences with grouped heads: up to `tokens` rows in up to
     `n_seqs` sequences.
@@ -61,9 +70,7 @@ class TSPPackedAttention:
             raise TSPError(2, tsp_last_error())
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         tsp_status_init(self.ws)
-        if not torch.cuda.is_current_stream_capturing():
-            # the first call may come on another stream
-            torch.cuda.current_stream(self.device).synchronize()
+        _ready(self.device)
 
     def _check(self, q, k, starts):
         if q.shape[1:] != (self.heads, self.head_dim) or k.shape[1:] != (self.kv_heads, self.head_dim):
@@ -125,6 +132,7 @@ class TSPRMSNorm:
         if nbytes == 0:
             raise ValueError(f"TSPRMSNorm: unsupported size {rows} x {width}")
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        _ready(self.device)
 
     def _rows(self, t):
         """t as a [rows, width] matrix (None stays None)."""
@@ -189,6 +197,7 @@ class TSPGradClip:
         self.tensors = tensors
         self.device = _device(device)
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        _ready(self.device)
 
     def _norm(self, norm, stream):
         if norm is None:

@@ -19,7 +19,7 @@ from ._binding import (TSP_OK, TSPError, tsp_attention_bwd, tsp_attention_fwd, t
                        tsp_device_status, tsp_last_error, tsp_mlp_bwd, tsp_mlp_fwd, tsp_pack_weights,
                        tsp_packed_weight_bytes, tsp_plan, tsp_plan_batched, tsp_workspace_bytes,
                        tsp_workspace_init)
-from .operators import TSPGradClip, TSPRMSNorm, _device
+from .operators import TSPGradClip, TSPRMSNorm, _device, _ready
 
 __all__ = ["TSPStack"]
 
@@ -65,8 +65,12 @@ class TSPStack:
                                  device=self.device)
             tsp_pack_weights(self.plan, *(w[k] for k in _MATRICES), packed)
             self.wpack.append(packed)
-        self.ws = torch.empty(tsp_workspace_bytes(self.plan), dtype=torch.uint8, device=self.device)
+        self._workspace(tsp_workspace_bytes(self.plan))
+
+    def _workspace(self, nbytes):
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         tsp_workspace_init(self.plan, self.ws)
+        _ready(self.device)
 
     @_on_its_device
     def enable_backward(self):
@@ -74,8 +78,7 @@ class TSPStack:
         capturing a graph of the forward: growing replaces the workspace."""
         need = tsp_bwd_workspace_bytes(self.plan)
         if self.ws.numel() < need:
-            self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            tsp_workspace_init(self.plan, self.ws)
+            self._workspace(need)
 
     @property
     def shape(self):

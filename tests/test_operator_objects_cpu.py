@@ -55,7 +55,10 @@ class Fakes:
 
         info = SimpleNamespace(D=2, T=4, batch=1, hidden=8, tokens=8, wpack_elems=16)
         monkeypatch.setattr(torch.cuda, "device", Device)
-        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.capturing)
+        monkeypatch.setattr(torch.cuda, "current_stream",
+                            lambda device=None: SimpleNamespace(cuda_stream=0, synchronize=record("synchronize")))
+        self.capturing = False
         monkeypatch.setattr(stack_module, "_device", lambda device: torch.device("cpu"))
         for name, result in (("tsp_plan", SimpleNamespace(info=info)), ("tsp_packed_weight_bytes", 32),
                              ("tsp_workspace_bytes", 256), ("tsp_bwd_workspace_bytes", 512),
@@ -115,3 +118,31 @@ def test_a_stack_refuses_weights_of_another_device(monkeypatch):
     w["mlp_norm"] = torch.zeros(8, device="meta")
     with pytest.raises(ValueError, match="must be on"):
         fakes.stack([w])
+
+
+def waits_last(fakes):
+    """The last thing that was queued has been waited for, on the right device."""
+    name, device = fakes.calls[-1]
+    return name == "synchronize" and device == torch.device("cpu")
+
+
+def test_a_workspace_is_ready_when_the_constructor_returns(monkeypatch):
+    """Memory that the constructor took over may still be written by what its stream has queued,
+    and the first call may come on another stream."""
+    fakes = Fakes(monkeypatch)
+    monkeypatch.setattr(operators, "_device", lambda device: torch.device("cpu"))
+    for name in ("tsp_packed_attention_workspace_bytes", "tsp_rmsnorm_workspace_bytes", "tsp_grad_workspace_bytes"):
+        monkeypatch.setattr(operators, name, lambda *args: 256)
+    monkeypatch.setattr(operators, "tsp_status_init", lambda ws: fakes.calls.append(("init", fakes.current)))
+    for make in (lambda: tsp.TSPPackedAttention(8, 1, 2, 1, 64), lambda: tsp.TSPRMSNorm(8, 64),
+                 lambda: tsp.TSPGradClip(3), fakes.stack):
+        fakes.calls.clear()
+        make()
+        assert waits_last(fakes)
+    stack = fakes.stack()
+    fakes.calls.clear()
+    stack.enable_backward()
+    assert waits_last(fakes) and ("tsp_workspace_init", stack.device) in fakes.calls
+    fakes.calls.clear()
+    stack.enable_backward()  # nothing to grow
+    assert all(name == "tsp_bwd_workspace_bytes" for name, _ in fakes.calls)
