@@ -43,6 +43,14 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
+def _not_in_a_capture(device, what):
+    """What a constructor launches would become part of the graph instead of running now: an object
+    with a status word and counters to zero is made before the capture."""
+    with torch.cuda.device(device):
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError(f"{what} cannot be captured: call it before the capture begins")
+
+
 def _ready(device):
     """Wait for what a constructor has queued, and for what its stream still has to do on memory
     that the constructor took over: the first call may come on another stream."""
@@ -65,6 +73,7 @@ class TSPPackedAttention:
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self.scale = head_dim ** -0.5 if scale is None else float(scale)
         self.device = _device(device)
+        _not_in_a_capture(self.device, "TSPPackedAttention()")
         nbytes = tsp_packed_attention_workspace_bytes(tokens, n_seqs, heads, kv_heads, head_dim)
         if nbytes == 0:
             raise TSPError(2, tsp_last_error())

@@ -19,7 +19,7 @@ from ._binding import (TSP_OK, TSPError, tsp_attention_bwd, tsp_attention_fwd, t
                        tsp_device_status, tsp_last_error, tsp_mlp_bwd, tsp_mlp_fwd, tsp_pack_weights,
                        tsp_packed_weight_bytes, tsp_plan, tsp_plan_batched, tsp_workspace_bytes,
                        tsp_workspace_init)
-from .operators import TSPGradClip, TSPRMSNorm, _device, _ready
+from .operators import TSPGradClip, TSPRMSNorm, _device, _not_in_a_capture, _ready
 
 __all__ = ["TSPStack"]
 
@@ -46,6 +46,7 @@ class TSPStack:
         if stream_dtype not in (torch.float32, torch.bfloat16):
             raise ValueError("stream_dtype must be float32 or bfloat16")
         self.device = _device(device)
+        _not_in_a_capture(self.device, "TSPStack()")
         if any(t.device != self.device for t in [last_norm, *(w[k] for w in weights for k in _MATRICES + _NORMS)]):
             raise ValueError(f"the weights must be on {self.device}")
         self.plan = (tsp_plan(D, S, hidden, heads, ffn) if batch == 1
@@ -75,9 +76,10 @@ class TSPStack:
     @_on_its_device
     def enable_backward(self):
         """Grow the workspace to the backward's size (it serves the forward too). Call it before
-        capturing a graph of the forward: growing replaces the workspace."""
+        capturing a graph: growing replaces the workspace."""
         need = tsp_bwd_workspace_bytes(self.plan)
         if self.ws.numel() < need:
+            _not_in_a_capture(self.device, "TSPStack.enable_backward()")
             self._workspace(need)
 
     @property

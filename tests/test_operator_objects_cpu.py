@@ -146,3 +146,25 @@ def test_a_workspace_is_ready_when_the_constructor_returns(monkeypatch):
     fakes.calls.clear()
     stack.enable_backward()  # nothing to grow
     assert all(name == "tsp_bwd_workspace_bytes" for name, _ in fakes.calls)
+
+
+def test_what_zeroes_a_status_word_is_not_captured(monkeypatch):
+    """Inside a capture the zeroing would wait for a replay, and a call outside it would find
+    counters of any value."""
+    fakes = Fakes(monkeypatch)
+    monkeypatch.setattr(operators, "_device", lambda device: torch.device("cpu"))
+    stack = fakes.stack()
+    fakes.capturing = True
+    before = stack.ws
+    fakes.calls.clear()
+    x = torch.zeros(2, 4, 8, dtype=torch.bfloat16)
+    for call in (lambda: tsp.TSPPackedAttention(8, 1, 2, 1, 64), fakes.stack, stack.enable_backward,
+                 lambda: stack.forward_train(x)):
+        with pytest.raises(RuntimeError, match="before the capture"):
+            call()
+    assert stack.ws is before and all(name == "tsp_bwd_workspace_bytes" for name, _ in fakes.calls)
+    stack.forward(x)  # needs nothing of the kind
+    fakes.capturing = False
+    stack.enable_backward()
+    fakes.capturing = True
+    stack.forward_train(x)
