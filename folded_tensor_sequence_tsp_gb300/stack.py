@@ -6,8 +6,8 @@ Per layer, on the sharded activations ([D, S/D, H], or [D, batch, S/D, H]):
 and a last norm behind the last layer. The blocks are tsp_attention_fwd / tsp_mlp_fwd,
 which return without a residual; the residual's addition, the rounding of the stream and
 the next norm are one pass (tsp_rmsnorm_fwd). The stream h is kept in fp32 by default. All
-layers share one plan and one workspace. Calls run on the stack's device, on the stream that is
-current there.
+layers share one plan and one workspace. Like the operators' objects, a stack serves one stream
+at a time. Calls run on the stack's device, on the stream that is current there.
 """
 from __future__ import annotations
 
@@ -53,6 +53,7 @@ class TSPStack:
                      else tsp_plan_batched(D, S, batch, hidden, heads, ffn))
         self.stream_dtype = stream_dtype
         self.wpack = []
+        self._kept = []  # a workspace that growing replaced
         self._pack(weights)
         # the norm in front of each block, and the last one
         self.norms = [w[k] for w in weights for k in _NORMS] + [last_norm]
@@ -76,10 +77,12 @@ class TSPStack:
     @_on_its_device
     def enable_backward(self):
         """Grow the workspace to the backward's size (it serves the forward too). Call it before
-        capturing a graph: growing replaces the workspace."""
+        capturing a training step. Graphs of the forward captured before it go on in the workspace
+        that they were captured with, which is kept for them."""
         need = tsp_bwd_workspace_bytes(self.plan)
         if self.ws.numel() < need:
             _not_in_a_capture(self.device, "TSPStack.enable_backward()")
+            self._kept.append(self.ws)
             self._workspace(need)
 
     @property
@@ -158,6 +161,7 @@ class TSPStack:
     @_on_its_device
     def check(self):
         """Synchronise and raise TSPError if a bounded device wait gave up."""
-        st = tsp_device_status(self.ws)
-        if st != TSP_OK:
-            raise TSPError(st, tsp_last_error())
+        for ws in (self.ws, *self._kept):
+            st = tsp_device_status(ws)
+            if st != TSP_OK:
+                raise TSPError(st, tsp_last_error())

@@ -1,5 +1,7 @@
 """The objects around the operators on the host: which device they take, which one they launch
 on, and what their workspaces do when they grow. No GPU: what allocates or launches is replaced."""
+import gc
+import weakref
 from types import SimpleNamespace
 
 import pytest
@@ -168,3 +170,20 @@ def test_what_zeroes_a_status_word_is_not_captured(monkeypatch):
     stack.enable_backward()
     fakes.capturing = True
     stack.forward_train(x)
+
+
+def test_a_graph_keeps_the_workspace_it_was_captured_with(monkeypatch):
+    """forward_train grows the workspace; a graph of the forward, captured earlier, writes to the
+    one before it when it is replayed."""
+    stack = Fakes(monkeypatch).stack()
+    captured = weakref.ref(stack.ws)
+    stack.forward_train(torch.zeros(2, 4, 8, dtype=torch.bfloat16))
+    gc.collect()
+    assert stack.ws.numel() == 512 and captured() is not None
+    looked_at = []
+    monkeypatch.setattr(stack_module, "tsp_device_status", lambda ws: looked_at.append(ws.numel()) or 0)
+    stack.check()
+    assert sorted(looked_at) == [256, 512]
+    del stack
+    gc.collect()
+    assert captured() is None
