@@ -740,6 +740,12 @@ int head_group(const Shape& s, long long l2_bytes) {
   return (int)((s.kv_heads + groups - 1) / groups);
 }
 
+tsp_status check_scale(const char* what, float scale) {
+  if (!(scale > 0.f) || !std::isfinite(LOG2E * scale))
+    return fail(TSP_ERR_INVALID_ARG, std::string(what) + ": scale must be positive, and finite in base 2 as well");
+  return TSP_OK;
+}
+
 tsp_status check_matrix(const char* what, const char* name, const void* p, int64_t ld, int64_t cols) {
   const std::string w = std::string(what) + ": " + name;
   if (!p) return fail(TSP_ERR_INVALID_ARG, w + " is a null pointer");
@@ -775,8 +781,7 @@ tsp_status tsp_packed_attention_fwd(int64_t tokens, int n_seqs, const int32_t* s
   const char* what = "tsp_packed_attention_fwd";
   Shape s;
   TSP_TRY(make_shape(what, tokens, n_seqs, heads, kv_heads, head_dim, &s));
-  if (!(scale > 0.f) || !std::isfinite(scale))
-    return fail(TSP_ERR_INVALID_ARG, std::string(what) + ": scale must be positive and finite");
+  TSP_TRY(check_scale(what, scale));
   if (tokens == 0 || n_seqs == 0) return TSP_OK;
   if (!starts || (reinterpret_cast<uintptr_t>(starts) & 3u))
     return fail(TSP_ERR_INVALID_ARG, std::string(what) + ": starts is null or misaligned");
@@ -808,7 +813,7 @@ tsp_status tsp_packed_attention_fwd(int64_t tokens, int n_seqs, const int32_t* s
   p.G = s.G;
   p.TPT = s.TPT;
   p.RU = s.RU;
-  p.scale_log2 = 1.4426950408889634f * scale;
+  p.scale_log2 = LOG2E * scale;
   p.status = status_of(ws);
   p.limit_ns = wait_limit_ns();
   if (p.src.items != nullptr) {

@@ -10,6 +10,7 @@ namespace packed {
 
 constexpr int TILE = 128;                  // rows of a tensor-core tile, and keys per key tile
 constexpr uint32_t BOX_BYTES = 128 * 128;  // 128 rows x 64 bf16 in shared memory
+constexpr float LOG2E = 1.4426950408889634f;
 constexpr size_t COUNTERS = 128;           // byte offset in the workspace's first 256 bytes
 
 // One CTA's share of a sequence: the tile (or pair of tiles) that begins at token q0.
@@ -257,6 +258,8 @@ int list_shift(long long max_cost);
 tsp_status make_query_map(CUtensorMap* map, const Shape& s, const void* base, int64_t ld);
 // Key heads whose K and V share L2 (CTAs of a group run together).
 int head_group(const Shape& s, long long l2_bytes);
+// The kernels multiply the scores by scale log2(e): it may not overflow, or a score of 0 is NaN.
+tsp_status check_scale(const char* what, float scale);
 tsp_status check_matrix(const char* what, const char* name, const void* p, int64_t ld, int64_t cols);
 
 }  // namespace packed

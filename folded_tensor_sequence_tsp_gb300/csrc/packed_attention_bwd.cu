@@ -1236,8 +1236,7 @@ extern "C" tsp_status tsp_packed_attention_bwd(
   const char* what = "tsp_packed_attention_bwd";
   Shape s;
   TSP_TRY(make_shape(what, tokens, n_seqs, heads, kv_heads, head_dim, &s));
-  if (!(scale > 0.f) || !std::isfinite(scale))
-    return fail(TSP_ERR_INVALID_ARG, std::string(what) + ": scale must be positive and finite");
+  TSP_TRY(check_scale(what, scale));
   if (tokens == 0 || n_seqs == 0) return TSP_OK;
   if (!starts || (reinterpret_cast<uintptr_t>(starts) & 3u))
     return fail(TSP_ERR_INVALID_ARG, std::string(what) + ": starts is null or misaligned");
@@ -1288,7 +1287,7 @@ extern "C" tsp_status tsp_packed_attention_bwd(
   p.G = s.G;
   p.TPT = s.TPT;
   p.RU = s.RU;
-  p.scale_log2 = 1.4426950408889634f * scale;
+  p.scale_log2 = LOG2E * scale;
   p.scale = scale;
   p.status = status_of(ws);
   p.limit_ns = wait_limit_ns();

@@ -634,7 +634,7 @@ tsp_status tsp_cost_max_batch(int scheme, int D, int tp, int64_t S, int hidden, 
  * reach o and dq of tokens up to R positions before it, and one in its q, o or dout row dk
  * and dv of tokens up to R positions after it. R is 127 where floor(128 / G) divides 128, as
  * for every power of two, and 126 + floor(128 / G) otherwise. lse is not reached.
- * scale multiplies the scores (1/sqrt(d) is customary); positive and finite.
+ * scale multiplies the scores (1/sqrt(d) is customary); positive, and finite times log2(e).
  * lse (fp32 [heads][ld_lse], one value per head and token): log2 of the sum over the
  * visible keys of exp(scale q.k), as tsp_causal_attention_lse stores it.
  *
