@@ -713,7 +713,9 @@ tsp_status tsp_rmsnorm_fwd_e4m3(int64_t rows, int width, const tsp_bf16* x, cons
  *     dw = the gradient of the weight, fp32 [width], overwritten
  * h, dh and dx are bf16, or all fp32 with h_f32. dx16 (optional) receives dx in bf16 as
  * well: the gradient of a bf16 block output beside an fp32 stream. dx may be dh, and dx16
- * (or a bf16 dx) may be dy. dw is summed in a fixed order. rows 0: dw is zeroed. ws:
+ * (or a bf16 dx) may be dy. dw is summed in a fixed order. Sums in fp32, as in the forward: a
+ * row whose sum of squares overflows it has dx = dh (0 without) and no share in dw, as y = 0
+ * there, or NaN in dx where the sum of dy weight h overflows too. rows 0: dw is zeroed. ws:
  * tsp_rmsnorm_workspace_bytes(rows, width) bytes, 256-byte aligned, scratch of this call.
  */
 size_t tsp_rmsnorm_workspace_bytes(int64_t rows, int width);
