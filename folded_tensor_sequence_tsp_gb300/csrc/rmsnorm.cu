@@ -886,9 +886,10 @@ tsp_status launch_fwd_res(const NormParams& p, bool vec, cudaStream_t s) {
   // with fewer CTAs 136 and 136 at 4608 and 8192, 132 against 136 at 5120, but 147 against 136 at
   // 6144 and 175 against 136 at 12288). Every other kind gains from staging (e4m3 beside bf16 at
   // 4096: 78 us against 97).
-  if constexpr (RES == RES_F32 && !E4M3)
-    if (threads <= 256) return launch_fwd_direct<8, 2, RES, E4M3>(p, s);
-  if (threads <= 256) return launch_fwd_staged<2 * P, false, RES, E4M3, 2, 256>(p, threads, s);
+  if (threads <= 256) {
+    if constexpr (RES == RES_F32 && !E4M3) return launch_fwd_direct<8, 2, RES, E4M3>(p, s);
+    else return launch_fwd_staged<2 * P, false, RES, E4M3, 2, 256>(p, threads, s);
+  }
   if (threads <= 1024) return launch_fwd_staged<2 * P, false, RES, E4M3, 2, 1024>(p, threads, s);
   return launch_fwd_direct<8, 4, RES, E4M3>(p, s);
 }
