@@ -43,10 +43,13 @@
 // infinity in V is not 0: warp 0 overwrites those rows of V with zeros in shared memory
 // before the product may start.
 //
-// Measured, 32 query and 8 key heads of 128: one sequence of 32768 tokens and 1000 others 6.0
-// ms, 1470 TFLOP/s (0.77 of the measured burst rate; the softmax warps' issue slots bind);
-// 16384 tokens in 18 sequences 0.39 ms, 1220 TFLOP/s, against 0.42 with a CTA per item and
-// 0.40 with rows stored lane by lane; 128 sequences of 128 tokens 0.08 ms (0.05 of it HBM).
+// Measured, 32 query and 8 key heads of 128: one sequence of 32768 tokens and 1000 others 6.0 to
+// 6.2 ms, 1425 to 1460 TFLOP/s (0.75 of the measured burst rate); 16384 tokens in 18 sequences
+// 0.39 ms, 1220 TFLOP/s, against 0.42 with a CTA per item and 0.40 with rows stored lane by lane;
+// 128 sequences of 128 tokens 0.08 ms (0.05 of it HBM). What binds the long sequence is the latency
+// of a tile's chain (scores, their load from tensor memory, softmax, P, product) through two tiles
+// in turn: the schedulers issue 0.36 instructions a cycle, the exponential unit is 32% busy, the
+// tensor pipe 63% (55% in the ragged batch), and 3.5 warps per issue wait for a load.
 #include <algorithm>
 #include <cmath>
 

@@ -28,7 +28,8 @@ def calls(lib, scale):
 
 @pytest.mark.parametrize("scale", [MAX, MAX / 1.4, 2.4e38])
 def test_scales_that_overflow_in_base_2(lib, scale):
-    assert np.isinf(LOG2E * np.float32(scale))
+    with np.errstate(over="ignore"):
+        assert np.isinf(LOG2E * np.float32(scale))
     for status in calls(lib, scale):
         assert status == B.TSP_ERR_INVALID_ARG and "scale" in B.tsp_last_error()
 
