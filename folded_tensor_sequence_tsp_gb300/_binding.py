@@ -33,7 +33,7 @@ __all__ = [
     "tsp_rank_attention", "tsp_rank_o_accumulate", "tsp_rank_mlp_step",
     "tsp_packed_attention_workspace_bytes", "tsp_status_init", "tsp_packed_attention_fwd",
     "tsp_packed_attention_bwd", "tsp_rmsnorm_fwd", "tsp_rmsnorm_fwd_e4m3", "tsp_rmsnorm_workspace_bytes", "tsp_rmsnorm_bwd",
-    "tsp_grad_workspace_bytes", "tsp_grad_norm", "tsp_grad_clip",
+    "tsp_grad_workspace_bytes", "tsp_grad_norm", "tsp_grad_clip", "tsp_quantize_e4m3", "tsp_adamw_step",
 ]
 
 TSP_OK, TSP_ERR_INVALID_ARG, TSP_ERR_UNSUPPORTED, TSP_ERR_CUDA, TSP_ERR_TIMEOUT = range(5)
@@ -65,6 +65,15 @@ class PlanInfo(ctypes.Structure):
 
     def as_dict(self):
         return {k: getattr(self, k) for k, _ in self._fields_}
+
+
+class AdamW(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("max_norm", ctypes.c_double),
+        ("t", ctypes.c_int64), ("seed", ctypes.c_uint32), ("norm", ctypes.c_void_p),
+        ("device_lr", ctypes.c_void_p), ("device_t", ctypes.c_void_p),
+    ]
 
 
 class Cost(ctypes.Structure):
@@ -144,6 +153,8 @@ _SIGS = {
     "tsp_grad_workspace_bytes": (ctypes.c_size_t, [_I]),
     "tsp_grad_norm": (_I, [_I] + [_P] * 6),
     "tsp_grad_clip": (_I, [_I] + [_P] * 4 + [_F] + [_P] * 3),
+    "tsp_quantize_e4m3": (_I, [_L, _L, _P, _I, _L, _I, _P, _L, _P, _P, _L, _P, _P]),
+    "tsp_adamw_step": (_I, [_I] + [_P] * 10 + [_I, ctypes.POINTER(AdamW), _P]),
 }
 
 
@@ -808,6 +819,127 @@ def tsp_grad_clip(grads, outs, max_norm, norm, ws, stream=None):
             raise ValueError("outs must match the gradients in number, size, type and device")
     _launch("tsp_grad_clip", device, stream, n, _at(ptrs), _at(out_ptrs), _at(sizes), _at(types), max_norm,
             norm.data_ptr(), wp)
+
+
+# ------------------------------------------------------------------ 8 bits
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _rows(t, name, shape=None, dtypes=(_E4M3,)):
+    """(pointer, row stride) of a [rows, width] tensor whose rows are contiguous."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    own = t.shape
+    if len(own) != 2 or (shape is not None and own != shape):
+        raise ValueError(f"{name} must have shape {shape or '[rows, width]'}, got {tuple(own)}")
+    row, one = t.stride()
+    if own[1] > 1 and one != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.data_ptr(), row if own[0] > 1 else own[1]
+
+
+def tsp_quantize_e4m3(x, y=None, scales=None, yt=None, scales_t=None, block=1, stream=None):
+    """e4m3 values of x [rows, width] (bfloat16 or float32) with a float32 scale for each block.
+
+    block 1: y [rows, width] and scales [rows, ceil(width / 128)], one for 128 columns of a row; yt
+    [width, rows] and scales_t [width, ceil(rows / 128)] the transpose, one for 128 rows of a column.
+    block 128: scales [ceil(rows / 128), ceil(width / 128)], yt and scales_t the transposes of y and
+    scales. Either pair may be left out. Rows may be strided; products want strides of a multiple of 16."""
+    device = _same_device((x, y, scales, yt, scales_t))
+    xp, ldx = _rows(x, "x", None, _STREAM_DTYPES)
+    r, w = x.shape
+    blocks = lambda n: -(-n // 128)  # noqa: E731
+    yp = sp = tp = stp = None
+    ldy = ldt = 0
+    if (y is None) != (scales is None) or (yt is None) != (scales_t is None):
+        raise ValueError("values and their scales are written together")
+    if y is not None:
+        yp, ldy = _rows(y, "y", (r, w))
+        sp = _matrix(scales, "scales", (r if block == 1 else blocks(r), blocks(w)), (torch.float32,))
+    if yt is not None:
+        tp, ldt = _rows(yt, "yt", (w, r))
+        stp = _matrix(scales_t, "scales_t", (w if block == 1 else blocks(w), blocks(r)), (torch.float32,))
+    _launch("tsp_quantize_e4m3", device, stream, r, w, xp, int(x.dtype == torch.float32), ldx, block, yp, ldy, sp,
+            tp, ldt, stp)
+
+
+class TensorList:
+    """Host arrays of a list of tensors: addresses, element counts and types (None: address 0)."""
+
+    __slots__ = ("n", "device", "given", "pointers", "sizes", "types")
+
+    def __init__(self, tensors, name, dtypes=_GRAD_TYPES):
+        self.n = len(tensors)
+        self.given = [t is not None for t in tensors]
+        some = [t for t in tensors if t is not None]
+        devices = {t.get_device() for t in some}
+        if len(devices) > 1 or min(devices, default=0) < 0:
+            raise ValueError(f"{name} must be on one CUDA device")
+        self.device = devices.pop() if devices else None
+        if not all([t.is_contiguous() for t in some]):
+            raise ValueError(f"{name} must be contiguous")
+        types = [0 if t is None else dtypes.get(t.dtype, -1) for t in tensors]
+        if -1 in types:
+            raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}")
+        self.types = array.array("i", types)
+        self.pointers = array.array("q", [0 if t is None else t.data_ptr() for t in tensors])
+        self.sizes = array.array("q", [0 if t is None else t.numel() for t in tensors])
+
+    def like(self, other, name, blocks=False):
+        """Check that the tensors hold as many elements as the other list's, or one per 128 of them."""
+        want = [-(-n // 128) for n in other.sizes] if blocks else other.sizes
+        if self.n != other.n or any([a != b and given for given, a, b in zip(self.given, self.sizes, want)]):
+            raise ValueError(f"{name} must match the weights in number and size")
+        if self.device is not None and other.device is not None and self.device != other.device:
+            raise ValueError(f"{name} must be on the weights' device")
+        return self
+
+
+def _scalar(t, name, dtype, device):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != 1 or t.get_device() != device:
+        raise ValueError(f"{name} must be one {dtype} value on cuda:{device}")
+    return t.data_ptr()
+
+
+def _adamw_lists(params, masters, m, v, m_scales, v_scales):
+    """The TensorLists of a step but for the gradients, checked against one another."""
+    p = TensorList(params, "params")
+    dtypes = {torch.float32: 0} if m_scales is None else {_E4M3: 0}
+    lists = [p, None if masters is None else TensorList(masters, "masters", {torch.float32: 0}).like(p, "masters")]
+    lists += [TensorList(x, n, dtypes).like(p, n) for x, n in ((m, "m"), (v, "v"))]
+    if (m_scales is None) != (v_scales is None):
+        raise ValueError("m_scales and v_scales belong together")
+    lists += [None if x is None else TensorList(x, n, {torch.float32: 0}).like(p, n, blocks=True)
+              for x, n in ((m_scales, "m_scales"), (v_scales, "v_scales"))]
+    return lists
+
+
+def _adamw_launch(lists, grads, step, stream):
+    p, masters, m, v, ms, vs = lists
+    g = TensorList(grads, "gradients").like(p, "gradients")
+    at = lambda x: None if x is None else _at(x.pointers)  # noqa: E731
+    if p.device is None:
+        return
+    _launch("tsp_adamw_step", p.device, stream, p.n, at(p), _at(p.types), at(masters), at(g), _at(g.types), at(m),
+            at(v), at(ms), at(vs), _at(p.sizes), 32 if ms is None else 8, ctypes.byref(step))
+
+
+def tsp_adamw_step(params, grads, m, v, lr, t, masters=None, m_scales=None, v_scales=None, betas=(0.9, 0.999),
+                   eps=1e-8, weight_decay=0.0, norm=None, max_norm=float("inf"), seed=0, stream=None):
+    """One AdamW step over lists of tensors, in place; see TSPAdamW, which keeps the states. m and v
+    are float32, or float8_e4m3fn with m_scales and v_scales. grads and masters may hold None. lr and t
+    are numbers, or one float32 and one int64 value on the device, read when the kernel runs."""
+    lists = _adamw_lists(params, masters, m, v, m_scales, v_scales)
+    device = lists[0].device
+    dev = lambda x: isinstance(x, torch.Tensor)  # noqa: E731
+    step = AdamW(0.0 if dev(lr) else lr, betas[0], betas[1], eps, weight_decay, max_norm, 1 if dev(t) else t,
+                 seed & 0xFFFFFFFF, _scalar(norm, "norm", torch.float32, device),
+                 _scalar(lr, "lr", torch.float32, device) if dev(lr) else None,
+                 _scalar(t, "t", torch.int64, device) if dev(t) else None)
+    _adamw_launch(lists, grads, step, stream)
 
 
 # ------------------------------------------------------------------ packed attention

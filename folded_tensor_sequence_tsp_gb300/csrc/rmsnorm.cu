@@ -23,11 +23,11 @@
 // 16384 x 4096, of the measured copy rate: fp32 stream 128 us (0.93), e4m3 beside a bf16
 // stream 78 us (0.90), backward 88 us (0.90); backward of an fp32 stream 170 us (0.81), with dx
 // over dh and a bf16 copy of dx 184 us (0.86).
-#include <cuda_fp8.h>
 
 #include <algorithm>
 #include <cmath>
 
+#include "e4m3.cuh"
 #include "tsp_device.cuh"
 #include "tsp_internal.h"
 
@@ -35,7 +35,6 @@ namespace tsp {
 namespace {
 
 enum { RES_NONE = 0, RES_BF16 = 1, RES_F32 = 2 };
-constexpr float kE4m3Max = 448.0f;
 constexpr int kMaxWidth = 32768;
 // CTAs of the backward at most: three per SM of this part, a constant so that the order
 // of dw's sum is the same on every device
@@ -159,55 +158,6 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* part) {
     v = __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < warps ? part[threadIdx.x & 31] : 0u);
   }
   return v;
-}
-
-// The scale of a group whose largest |y| has the bits `top`: top / 448, rounded to nearest (the
-// product with the reciprocal, and its remainder, exact in an fma, times the reciprocal; a
-// quotient by 448 = 7 x 64 is never near halfway between two numbers). A group of zeros takes 1;
-// the smallest scale is the smallest normal number, so that its reciprocal is finite.
-// NaN or infinity in the group gives a NaN or infinite scale.
-__device__ __forceinline__ float e4m3_scale(uint32_t top) {
-  const float t = __uint_as_float(top);
-  if (top == 0u) return 1.f;
-  if (top >= 0x7f800000u) return t;
-  constexpr float r = 1.f / kE4m3Max;
-  const float q = t * r;
-  return fmaxf(fmaf(fmaf(-q, kE4m3Max, t), r, q), 1.17549435e-38f);
-}
-
-// y / scale, rounded to nearest as the fp32 division is, without a division per element: with
-// the correctly rounded reciprocal, each step q - (q scale - y) / scale takes an exact remainder,
-// the first leaves less than one unit in the last place and the second none (P. Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990). A product
-// with the reciprocal alone is off by a unit, which at a tie between two e4m3 values picks the
-// wrong one. Small scales are raised by 2^64, so that the remainders do not underflow. 16384 x 4096
-// with groups of 128: 78 us beside a bf16 stream and 120 beside fp32, as without the steps; 66
-// instead of 54 without a residual (93, 126 and 75 with the division itself, which the kernel of
-// single elements uses: 260 us for 4095 columns beside a bf16 stream, 240 without).
-struct Quotient {
-  float up, inv, sc;
-  __device__ __forceinline__ explicit Quotient(float scale) {
-    up = scale < 1e-18f ? 18446744073709551616.f : 1.f;
-    inv = __frcp_rn(scale * up);
-    sc = isinf(scale) ? 0.f : scale * up;  // no remainders: finite / infinity is 0
-  }
-  // of two values, in place; from -y, so that a zero keeps its sign
-  __device__ __forceinline__ void pair(float& a, float& b) const {
-    const uint64_t n = f2_mul(f2_pack(-a, -b), f2_pack(up, up)), ni = f2_pack(-inv, -inv), s = f2_pack(sc, sc);
-    uint64_t q = f2_mul(n, ni);
-    q = f2_fma(f2_fma(q, s, n), ni, q);
-    f2_unpack(f2_fma(f2_fma(q, s, n), ni, q), a, b);
-  }
-};
-
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
-  return static_cast<uint8_t>(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3));
-}
-// four values, the first in the low byte: one conversion instruction per pair
-__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
 }
 
 struct NormParams {

@@ -15,13 +15,13 @@ import contextlib
 
 import torch
 
-from ._binding import (TSP_OK, TSPError, tsp_device_status, tsp_grad_clip, tsp_grad_norm,
+from ._binding import (AdamW, TSP_OK, TSPError, _adamw_launch, _adamw_lists, _scalar, tsp_device_status, tsp_grad_clip, tsp_grad_norm,
                        tsp_grad_workspace_bytes, tsp_last_error, tsp_packed_attention_bwd,
                        tsp_packed_attention_fwd,
                        tsp_packed_attention_workspace_bytes, tsp_rmsnorm_bwd, tsp_rmsnorm_fwd,
                        tsp_rmsnorm_fwd_e4m3, tsp_rmsnorm_workspace_bytes, tsp_status_init)
 
-__all__ = ["TSPPackedAttention", "TSPRMSNorm", "TSPGradClip"]
+__all__ = ["TSPPackedAttention", "TSPRMSNorm", "TSPGradClip", "TSPAdamW"]
 
 
 def _device(device):
@@ -226,3 +226,62 @@ class TSPGradClip:
         norm = self._norm(norm, stream)
         tsp_grad_clip(grads, grads if outs is None else outs, float(max_norm), norm, self.ws, stream)
         return norm
+
+
+class TSPAdamW:
+    """AdamW over a list of float32 and bfloat16 weights, updated in place.
+
+    masters: for each bfloat16 weight a float32 tensor that holds it exactly, or None (the weight is
+    then rounded stochastically). The states are made here, as zeros: float32, or with state_bits 8
+    float8_e4m3fn with a float32 scale for each 128 elements. The object keeps the addresses of weights,
+    masters and states: they are updated where they are, and may not be replaced."""
+
+    def __init__(self, params, masters=None, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, state_bits=32, seed=0,
+                 device=None):
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits must be 32 or 8")
+        self.params, self.masters = list(params), None if masters is None else list(masters)
+        self.betas, self.eps, self.weight_decay, self.seed = betas, eps, weight_decay, seed
+        self.state_bits = state_bits
+        self.device = _device(self.params[0].device if self.params and device is None else device)
+        if any(p.device != self.device for p in self.params):
+            raise ValueError(f"the weights must be on {self.device}")
+        if self.masters is not None and any(m is not None and p.dtype != torch.bfloat16
+                                            for m, p in zip(self.masters, self.params)):
+            raise ValueError("a master belongs beside a bfloat16 weight")
+        _not_in_a_capture(self.device, "TSPAdamW()")
+        kind = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+        new = lambda n, dtype: torch.zeros(n, dtype=dtype, device=self.device)  # noqa: E731
+        sizes = [p.numel() for p in self.params]
+        scales = [[new(-(-n // 128), torch.float32) for n in sizes] if state_bits == 8 else None for _ in range(2)]
+        self.resume(0, [new(n, kind) for n in sizes], [new(n, kind) for n in sizes], *scales)
+        _ready(self.device)
+
+    def resume(self, t, m, v, m_scales=None, v_scales=None):
+        """Go on after t steps with these states (of the types and sizes that the constructor makes),
+        which are taken over, not copied."""
+        if (m_scales is not None) != (self.state_bits == 8):
+            raise ValueError("scales belong to states of 8 bits")
+        lists = _adamw_lists(self.params, self.masters, m, v, m_scales, v_scales)
+        self.t, self.m, self.v, self.m_scales, self.v_scales = t, m, v, m_scales, v_scales
+        self._lists = lists
+
+    def step(self, grads, lr, norm=None, max_norm=float("inf"), t=None, stream=None):
+        """One step with the gradients of all weights (None: that weight is left as it is).
+
+        norm: the gradients' global norm, one float32 on the device (TSPGradClip.norm); they are
+        then scaled to a norm of at most max_norm on the way. lr may be one float32 on the device,
+        and t one int64, this step's number from 1, in place of the object's own count: a captured
+        step is then replayed with their values of that moment."""
+        device = self.device.index
+        step = AdamW(0.0, *self.betas, self.eps, self.weight_decay, max_norm, self.t + 1, self.seed & 0xFFFFFFFF,
+                     _scalar(norm, "norm", torch.float32, device), None, None)
+        if isinstance(lr, torch.Tensor):
+            step.device_lr = _scalar(lr, "lr", torch.float32, device)
+        else:
+            step.lr = lr
+        if t is not None:
+            step.device_t = _scalar(t, "t", torch.int64, device)
+        _adamw_launch(self._lists, grads, step, stream)
+        if t is None:
+            self.t += 1

@@ -751,6 +751,68 @@ tsp_status tsp_grad_norm(int n, const void* const* grads, const int64_t* sizes, 
 tsp_status tsp_grad_clip(int n, const void* const* grads, void* const* outs, const int64_t* sizes,
                          const int* types, float max_norm, float* norm, void* ws, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A training step in 8 bits: values of e4m3 with an fp32 scale for each block of 128, the products
+ * of a linear layer on them, and the AdamW step. These calls take sizes instead of a plan.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * tsp_quantize_e4m3 - e4m3 values of x [rows][width] (bf16, or fp32 with x_f32; rows ld_x elements
+ * apart), so that value * scale stands for x: scale = max|x| / 448 over the block (not below
+ * 2^-126; 1 for a block of zeros) and value = the quotient by it, both fp32 divisions rounded to
+ * nearest, the quotient then to e4m3, to even at a tie. A block with a NaN or an infinity has a NaN or
+ * infinite scale.
+ *   block 1:   y [rows][ld_y] with a scale for 128 columns of one row, scales
+ *              [rows][ceil(width/128)]; yt [width][ld_yt] is the transpose with a scale for 128
+ *              rows of one column, scales_t [width][ceil(rows/128)].
+ *   block 128: one scale for 128 x 128 values, scales [ceil(rows/128)][ceil(width/128)]; yt is the
+ *              transpose of the same values, scales_t that of the same scales.
+ * Either of y (with scales) and yt (with scales_t) may be NULL. Short blocks at the edges are
+ * blocks like the others; bytes behind a row's end are left as they were. Row strides are in elements;
+ * products want those of y and yt to be multiples of 16. Outputs may not overlap x or one another.
+ */
+tsp_status tsp_quantize_e4m3(int64_t rows, int64_t width, const void* x, int x_f32, int64_t ld_x, int block,
+                             uint8_t* y, int64_t ld_y, float* scales, uint8_t* yt, int64_t ld_yt, float* scales_t,
+                             void* stream);
+
+/*
+ * tsp_adamw_step - one step over n tensors, in place:
+ *     g' = g * min(1, max_norm / (norm + 1e-6)) where norm is given (tsp_grad_norm's), else g
+ *     m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *     p = p - lr (weight_decay p + (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps))
+ * in fp32: the clipping factor is one fp32 quotient, and each product and sum of m and v is rounded.
+ * params[i] is fp32 or bf16 (types[i]); a bf16 weight may have an fp32 master (masters[i], else
+ * NULL; masters itself may be NULL): the master is updated and the weight is the master rounded to nearest.
+ * grads[i] is fp32 or bf16 (grad_types[i]); a tensor whose grads[i] is NULL or whose size is 0 is left
+ * as it is. m and v are fp32 with state_bits 32; with 8 they are e4m3, one fp32 scale for each 128
+ * elements of a tensor (m_scales[i] and v_scales[i] [ceil(size/128)], the last block may be short),
+ * the scale formed as tsp_quantize_e4m3 forms it. Zeros are states to begin with.
+ *
+ * 8-bit states, and bf16 weights without a master, are rounded stochastically: to the upper
+ * neighbour with the probability of the distance from the lower one, by random bits that are a
+ * function of seed, t, the tensor's place in the list and the element. A v above zero is not
+ * rounded to zero. A block of a state that holds a NaN or an infinity is NaN from then on.
+ *
+ * The lists are HOST arrays, read during the call; norm, device_lr and device_t are on the device.
+ * device_lr and device_t, where given, are read instead of lr and t when the kernel runs: a captured step
+ * goes on counting. No weight, master or state may overlap another tensor of the call. n from 0 to
+ * TSP_GRAD_MAX_TENSORS. Only launches kernels.
+ */
+typedef struct tsp_adamw {
+  double lr, beta1, beta2, eps, weight_decay;
+  double max_norm;          /* read with norm only; infinity for no clipping */
+  int64_t t;                /* the step's number, from 1                     */
+  uint32_t seed;
+  const float* norm;        /* device, may be NULL */
+  const float* device_lr;   /* device, may be NULL */
+  const int64_t* device_t;  /* device, may be NULL */
+} tsp_adamw;
+
+tsp_status tsp_adamw_step(int n, void* const* params, const int* types, void* const* masters,
+                          const void* const* grads, const int* grad_types, void* const* m, void* const* v,
+                          float* const* m_scales, float* const* v_scales, const int64_t* sizes, int state_bits,
+                          const tsp_adamw* step, void* stream);
+
 /*
  * tsp_device_status - synchronise `stream`, then read and clear the workspace
  * status word. Returns TSP_OK, TSP_ERR_TIMEOUT (a bounded device wait gave up; the
