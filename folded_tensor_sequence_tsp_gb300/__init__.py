@@ -18,11 +18,12 @@ from ._binding import (tsp_layer_fwd, tsp_layer_fwd_host, tsp_pack_weights, tsp_
                        tsp_bwd_workspace_bytes, tsp_layer_bwd, tsp_unpack_weight_grads,
                        tsp_saved_bytes, tsp_layer_fwd_train, tsp_layer_bwd_saved)
 
-from .operators import TSPAdamW, TSPGradClip, TSPPackedAttention, TSPRMSNorm
+from .operators import (TSPAdamW, TSPGradClip, TSPLinearE4M3, TSPPackedAttention, TSPRMSNorm,
+                        TSPWeightE4M3)
 from .stack import TSPStack
 
 __all__ = list(_binding_all) + ["TSPLayer", "TSPPackedAttention", "TSPRMSNorm", "TSPGradClip",
-                                 "TSPAdamW", "TSPStack"]
+                                 "TSPLinearE4M3", "TSPWeightE4M3", "TSPAdamW", "TSPStack"]
 
 
 class TSPLayer:

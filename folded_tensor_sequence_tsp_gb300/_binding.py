@@ -33,7 +33,8 @@ __all__ = [
     "tsp_rank_attention", "tsp_rank_o_accumulate", "tsp_rank_mlp_step",
     "tsp_packed_attention_workspace_bytes", "tsp_status_init", "tsp_packed_attention_fwd",
     "tsp_packed_attention_bwd", "tsp_rmsnorm_fwd", "tsp_rmsnorm_fwd_e4m3", "tsp_rmsnorm_workspace_bytes", "tsp_rmsnorm_bwd",
-    "tsp_grad_workspace_bytes", "tsp_grad_norm", "tsp_grad_clip", "tsp_quantize_e4m3", "tsp_adamw_step",
+    "tsp_grad_workspace_bytes", "tsp_grad_norm", "tsp_grad_clip", "tsp_quantize_e4m3",
+    "tsp_matmul_e4m3_workspace_bytes", "tsp_matmul_e4m3", "tsp_adamw_step",
 ]
 
 TSP_OK, TSP_ERR_INVALID_ARG, TSP_ERR_UNSUPPORTED, TSP_ERR_CUDA, TSP_ERR_TIMEOUT = range(5)
@@ -154,6 +155,8 @@ _SIGS = {
     "tsp_grad_norm": (_I, [_I] + [_P] * 6),
     "tsp_grad_clip": (_I, [_I] + [_P] * 4 + [_F] + [_P] * 3),
     "tsp_quantize_e4m3": (_I, [_L, _L, _P, _I, _L, _I, _P, _L, _P, _P, _L, _P, _P]),
+    "tsp_matmul_e4m3_workspace_bytes": (ctypes.c_size_t, []),
+    "tsp_matmul_e4m3": (_I, [_L, _L, _L, _P, _L, _P, _P, _L, _P, _I, _P, _L, _I, _I, _P, _P]),
     "tsp_adamw_step": (_I, [_I] + [_P] * 10 + [_I, ctypes.POINTER(AdamW), _P]),
 }
 
@@ -862,6 +865,31 @@ def tsp_quantize_e4m3(x, y=None, scales=None, yt=None, scales_t=None, block=1, s
         stp = _matrix(scales_t, "scales_t", (w if block == 1 else blocks(w), blocks(r)), (torch.float32,))
     _launch("tsp_quantize_e4m3", device, stream, r, w, xp, int(x.dtype == torch.float32), ldx, block, yp, ldy, sp,
             tp, ldt, stp)
+
+
+def tsp_matmul_e4m3_workspace_bytes() -> int:
+    return load_library().tsp_matmul_e4m3_workspace_bytes()
+
+
+def tsp_matmul_e4m3(a, a_scales, b, b_scales, c, ws, b_block=128, accumulate=False, stream=None):
+    """c [m, n] = a b^T (plus c with accumulate) of e4m3 matrices a [m, k] and b [n, k] with block scales.
+
+    a_scales [m, ceil(k / 128)]; b_scales [n, ceil(k / 128)] with b_block 1, [ceil(n / 128), ceil(k / 128)] with
+    128. c is bfloat16 or float32 (accumulate: float32). The rows of a and b start on 16 bytes."""
+    device = _same_device((a, a_scales, b, b_scales, c, ws))
+    ap, lda = _rows(a, "a")
+    bp, ldb = _rows(b, "b")
+    (m, k), n = a.shape, b.shape[0]
+    if b.shape[1] != k:
+        raise ValueError(f"b has shape {tuple(b.shape)} beside a {(m, k)}")
+    cp, ldc = _rows(c, "c", (m, n), _STREAM_DTYPES)
+    blocks = -(-k // 128)
+    asp = _matrix(a_scales, "a_scales", (m, blocks), (torch.float32,))
+    bsp = _matrix(b_scales, "b_scales", (n if b_block == 1 else -(-n // 128), blocks), (torch.float32,))
+    # one row needs no stride of its own
+    _launch("tsp_matmul_e4m3", device, stream, m, n, k, ap, lda if m > 1 else -(-k // 16) * 16, asp, bp,
+            ldb if n > 1 else -(-k // 16) * 16, bsp, b_block, cp, ldc, int(c.dtype == torch.float32), int(accumulate),
+            _ws_status(ws))
 
 
 class TensorList:

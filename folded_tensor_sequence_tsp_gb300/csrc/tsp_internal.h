@@ -120,6 +120,10 @@ inline tsp_status check_ws(void* ws, const char* what) {
 tsp_status make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                              uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
 
+// The same of single bytes.
+tsp_status make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                           uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
+
 // 3D bf16 map of dims {inner (contiguous), middle, outer} with the same swizzle and fill.
 tsp_status make_tmap_3d_bf16(CUtensorMap* map, const void* base, const uint64_t (&dims)[3],
                              const uint64_t (&strides_bytes)[2], const uint32_t (&box)[3]);
@@ -249,20 +253,29 @@ tsp_status mlp_block(const Plan& p, const void* hs, const void* wpack, const voi
 // plain or __ldcg loads: the earlier kernel still writes it while this one is alive, so it is not
 // read-only for the kernel's lifetime, as __ldg and a pointer to const __restrict__ would promise.
 // It hides the launch and set-up of the second of two kernels, 2 to 4 us.
+// launch_early_cluster: in clusters of `cluster` CTAs, which divides the grid.
 template <class... P, class... A>
-cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                         A&&... args) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+cudaError_t launch_early_cluster(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                 int cluster, A&&... args) {
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                         A&&... args) {
+  return launch_early_cluster(kernel, grid, block, smem, stream, 1, static_cast<P>(args)...);
 }
 
 // An NVTX range around the host-side enqueue of one step of the schedules (a

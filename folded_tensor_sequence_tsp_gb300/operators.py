@@ -12,16 +12,19 @@ are done with it.
 from __future__ import annotations
 
 import contextlib
+from typing import NamedTuple
 
 import torch
 
-from ._binding import (AdamW, TSP_OK, TSPError, _adamw_launch, _adamw_lists, _scalar, tsp_device_status, tsp_grad_clip, tsp_grad_norm,
-                       tsp_grad_workspace_bytes, tsp_last_error, tsp_packed_attention_bwd,
+from ._binding import (AdamW, TSP_OK, TSPError, _adamw_launch, _adamw_lists, _launch, _matrix, _rows, _same_device,
+                       _scalar, tsp_device_status, tsp_grad_clip, tsp_grad_norm,
+                       tsp_grad_workspace_bytes, tsp_last_error, tsp_matmul_e4m3_workspace_bytes, tsp_packed_attention_bwd,
                        tsp_packed_attention_fwd,
-                       tsp_packed_attention_workspace_bytes, tsp_rmsnorm_bwd, tsp_rmsnorm_fwd,
+                       tsp_packed_attention_workspace_bytes, tsp_quantize_e4m3, tsp_rmsnorm_bwd, tsp_rmsnorm_fwd,
                        tsp_rmsnorm_fwd_e4m3, tsp_rmsnorm_workspace_bytes, tsp_status_init)
 
-__all__ = ["TSPPackedAttention", "TSPRMSNorm", "TSPGradClip", "TSPAdamW"]
+__all__ = ["TSPPackedAttention", "TSPRMSNorm", "TSPGradClip", "TSPWeightE4M3", "TSPLinearE4M3",
+           "TSPAdamW"]
 
 
 def _device(device):
@@ -226,6 +229,169 @@ class TSPGradClip:
         norm = self._norm(norm, stream)
         tsp_grad_clip(grads, grads if outs is None else outs, float(max_norm), norm, self.ws, stream)
         return norm
+
+
+class TSPWeightE4M3(NamedTuple):
+    """A linear layer's weight [out, in] in 8 bits: values with a scale for 128 x 128 of them, and
+    for the backward their transposes."""
+
+    values: torch.Tensor
+    scales: torch.Tensor
+    values_t: torch.Tensor | None = None
+    scales_t: torch.Tensor | None = None
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def _up16(n):
+    return -(-n // 16) * 16
+
+
+class TSPLinearE4M3:
+    """y = x w^T with products in e4m3: x and the gradients quantised per row and 128 columns (for dw
+    along the tokens, per column and 128 tokens), w per 128 x 128 tile, sums in fp32. Up to `tokens`
+    rows; the weight is an argument of each call."""
+
+    def __init__(self, tokens, out_features, in_features, device=None):
+        if tokens < 0 or out_features < 1 or in_features < 1:
+            raise ValueError(f"TSPLinearE4M3: unsupported size {tokens} x {out_features} x {in_features}")
+        self.tokens, self.out_features, self.in_features = tokens, out_features, in_features
+        self.device = _device(device)
+        _not_in_a_capture(self.device, "TSPLinearE4M3()")
+        self._kept = []  # a workspace that growing replaced
+        # byte offsets: status, then values and scales of x; of dy; of the transpose of dy
+        self._at, at = [], tsp_matmul_e4m3_workspace_bytes()
+        for rows, width in ((tokens, in_features), (tokens, out_features), (out_features, tokens)):
+            self._at.append((at, at + _up16(width) * rows))
+            at += _up16(width) * rows + -(-4 * rows * _blocks(width) // 256) * 256
+            at = -(-at // 256) * 256
+        self._sizes = (self._at[1][0], at)
+        self._workspace(self._sizes[0])
+
+    def _workspace(self, nbytes):
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        tsp_status_init(self.ws)
+        _ready(self.device)
+
+    def enable_backward(self):
+        """Grow the workspace to the backward's size. Call it before capturing a training step; graphs
+        captured before go on in the workspace that they were captured with, which is kept for them."""
+        if self.ws.numel() < self._sizes[1]:
+            _not_in_a_capture(self.device, "TSPLinearE4M3.enable_backward()")
+            self._kept.append(self.ws)
+            self._workspace(self._sizes[1])
+
+    def quantize_weight(self, w, training=True, stream=None):
+        """The TSPWeightE4M3 of w [out, in] (bfloat16 or float32), with its transpose for training."""
+        n, k = self.out_features, self.in_features
+        if w.shape != (n, k):
+            raise ValueError(f"expected a weight [{n}, {k}], got {tuple(w.shape)}")
+        with _on(stream, self.device):
+            new = lambda r, c: torch.empty(r, _up16(c), dtype=torch.float8_e4m3fn, device=self.device)[:, :c]  # noqa: E731
+            scale = lambda r, c: torch.empty(_blocks(r), _blocks(c), device=self.device)  # noqa: E731
+            out = TSPWeightE4M3(new(n, k), scale(n, k), *((new(k, n), scale(k, n)) if training else ()))
+        tsp_quantize_e4m3(w, *out, block=128, stream=stream)
+        return out
+
+    def _input(self, x, width, name):
+        """(rows, address, row stride) of a bfloat16 [..., width] tensor."""
+        if x.dim() != 2:
+            if x.dim() < 1 or x.shape[-1] != width:
+                raise ValueError(f"{name}: expected rows of {width}, got shape {tuple(x.shape)}")
+            x = x.view(-1, width)
+        if x.shape[0] > self.tokens:
+            raise ValueError(f"{x.shape[0]} rows; the object was made for {self.tokens}")
+        return x.shape[0], *_rows(x, name, (x.shape[0], width), (torch.bfloat16,))
+
+    def _weight(self, values, scales, rows, width):
+        if values is None:
+            raise ValueError("the backward needs the weight's transpose: quantize_weight(w, training=True)")
+        p, ld = _rows(values, "weight", (rows, width))
+        return p, ld if rows > 1 else _up16(width), _matrix(scales, "weight scales", (_blocks(rows), _blocks(width)),
+                                                            (torch.float32,))
+
+    def _out(self, out, shape, dtype, stream, name):
+        if out is None:
+            with _on(stream, self.device):
+                out = torch.empty(shape, dtype=dtype, device=self.device)
+        elif out.dtype != dtype or out.shape != shape or not out.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+        return out
+
+    def forward(self, x, weight, scales=None, out=None, stream=None):
+        """y [..., out] in bfloat16. x [..., in]: bfloat16, or e4m3 [rows, in] with scales [rows, ceil(in / 128)]
+        as TSPRMSNorm.forward_e4m3 (group 128) and tsp_quantize_e4m3 leave them."""
+        n, k = self.out_features, self.in_features
+        device = _same_device((x, scales, *weight[:2], out, self.ws))
+        out = self._out(out, (*x.shape[:-1], n), torch.bfloat16, stream, "out")
+        w = self._weight(*weight[:2], n, k)
+        ws = self.ws.data_ptr()
+        if scales is None:
+            m, xp, ldx = self._input(x, k, "x")
+            if m:
+                a, ld_a, sa = ws + self._at[0][0], _up16(k), ws + self._at[0][1]
+                _launch("tsp_quantize_e4m3", device, stream, m, k, xp, 0, ldx, 1, a, ld_a, sa, None, 0, None)
+        else:
+            m = x.numel() // k if x.dim() else 0
+            a, ld_a = _rows(x if x.dim() == 2 else x.view(-1, k), "x", (m, k))
+            ld_a = ld_a if m > 1 else _up16(k)
+            sa = _matrix(scales, "scales", (m, _blocks(k)), (torch.float32,))
+        if m:
+            _launch("tsp_matmul_e4m3", device, stream, m, n, k, a, ld_a, sa, *w, 128, out.data_ptr(), n, 0, 0, ws)
+        return out
+
+    def forward_train(self, x, weight, out=None, stream=None):
+        """(y, saved): forward() of a bfloat16 x that also keeps what backward() needs of it, the transpose of
+        x in 8 bits."""
+        self.enable_backward()
+        n, k = self.out_features, self.in_features
+        device = _same_device((x, *weight[:2], out, self.ws))
+        out = self._out(out, (*x.shape[:-1], n), torch.bfloat16, stream, "out")
+        w = self._weight(*weight[:2], n, k)
+        m, xp, ldx = self._input(x, k, "x")
+        with _on(stream, self.device):
+            saved = (torch.empty(k, _up16(m), dtype=torch.float8_e4m3fn, device=self.device)[:, :m],
+                     torch.empty(k, _blocks(m), device=self.device))
+        if m:
+            ws = self.ws.data_ptr()
+            a, ld_a, sa = ws + self._at[0][0], _up16(k), ws + self._at[0][1]
+            _launch("tsp_quantize_e4m3", device, stream, m, k, xp, 0, ldx, 1, a, ld_a, sa, saved[0].data_ptr(),
+                    _up16(m), saved[1].data_ptr())
+            _launch("tsp_matmul_e4m3", device, stream, m, n, k, a, ld_a, sa, *w, 128, out.data_ptr(), n, 0, 0, ws)
+        return out, saved
+
+    def backward(self, saved, dy, weight, dx=None, dw=None, accumulate=False, stream=None):
+        """(dx, dw) of forward_train's saved and the gradient dy [..., out] of y (bfloat16): dx in bfloat16, dw
+        in float32, added to the given dw with accumulate."""
+        self.enable_backward()
+        n, k = self.out_features, self.in_features
+        device = _same_device((dy, *saved, *weight[2:], dx, dw, self.ws))
+        m, gp, ldg = self._input(dy, n, "dy")
+        if saved[0].shape != (k, m):
+            raise ValueError(f"saved belongs to {saved[0].shape[1]} rows, dy has {m}")
+        wt = self._weight(*(weight[2:] or (None, None)), k, n)
+        if accumulate and dw is None:
+            raise ValueError("accumulate needs a dw to add to")
+        dx = self._out(dx, (*dy.shape[:-1], k), torch.bfloat16, stream, "dx")
+        dw = self._out(dw, (n, k), torch.float32, stream, "dw")
+        ws = self.ws.data_ptr()
+        g, sg, gt, sgt = (ws + at for pair in self._at[1:] for at in pair)
+        if m:
+            _launch("tsp_quantize_e4m3", device, stream, m, n, gp, 0, ldg, 1, g, _up16(n), sg, gt, _up16(m), sgt)
+            _launch("tsp_matmul_e4m3", device, stream, m, k, n, g, _up16(n), sg, *wt, 128, dx.data_ptr(), k, 0, 0, ws)
+        _launch("tsp_matmul_e4m3", device, stream, n, k, m, gt, _up16(m), sgt, saved[0].data_ptr(), _up16(m),
+                saved[1].data_ptr(), 1, dw.data_ptr(), k, 1, int(accumulate), ws)
+        return dx, dw
+
+    def check(self, stream=None):
+        """Synchronise and raise TSPError if a bounded device wait gave up."""
+        with torch.cuda.device(self.device):
+            for ws in (self.ws, *self._kept):
+                st = tsp_device_status(ws, stream)
+                if st != TSP_OK:
+                    raise TSPError(st, tsp_last_error())
 
 
 class TSPAdamW:

@@ -776,6 +776,28 @@ tsp_status tsp_quantize_e4m3(int64_t rows, int64_t width, const void* x, int x_f
                              void* stream);
 
 /*
+ * tsp_matmul_e4m3 - C [m][n] = A B^T of e4m3 matrices a [m][k] and b [n][k] with their block scales:
+ *     C[i][j] = sum over blocks kb of 128 of k:  s  sum over the block of a[i][.] b[j][.]
+ *     s = a_scales[i][kb] * b_scales[j][kb]          (b_block 1:   b_scales [n][ceil(k/128)])
+ *     s = a_scales[i][kb] * b_scales[j / 128][kb]    (b_block 128: b_scales [ceil(n/128)][ceil(k/128)])
+ * in fp32 (s too), the result rounded once to bf16, or fp32 with c_f32, then added to c with accumulate.
+ * These are a linear layer's products on what tsp_quantize_e4m3 writes: y = x w^T with b = w in tiles;
+ * dx = dy w with b = the transpose of w in tiles; dw = dy^T x with a and b the transposes (columns
+ * form) of dy and x, b_block 1. A block's sum is formed before its scales are applied: with an
+ * infinite or NaN scale every element that it enters is infinite or NaN, but NaN where the block's sum is 0.
+ *
+ * Rows of a and b start on 16 bytes (base and ld_a, ld_b multiples of 16), those of c anywhere on its
+ * element; what lies behind a row's end is neither read into the result nor written. m, n, k in
+ * [0, 2^30]; k 0 gives zeros. c may not overlap an input. Sums are in a fixed order that goes by m, n and
+ * k alone. ws: tsp_matmul_e4m3_workspace_bytes() bytes, 256-byte aligned, initialised once by
+ * tsp_status_init; calls may share it.
+ */
+size_t tsp_matmul_e4m3_workspace_bytes(void);
+tsp_status tsp_matmul_e4m3(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t ld_a, const float* a_scales,
+                           const uint8_t* b, int64_t ld_b, const float* b_scales, int b_block, void* c, int64_t ld_c,
+                           int c_f32, int accumulate, void* ws, void* stream);
+
+/*
  * tsp_adamw_step - one step over n tensors, in place:
  *     g' = g * min(1, max_norm / (norm + 1e-6)) where norm is given (tsp_grad_norm's), else g
  *     m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
