@@ -28,18 +28,22 @@ constexpr int BM = 128;
 constexpr int BK = 128;
 constexpr int THREADS = 384;
 constexpr int EPI_WARPS = 8;
-constexpr int EPI_THREADS = 32 * EPI_WARPS;
 constexpr uint32_t P_BYTES = BM * BK;
 
-template <int BN>
+// PAIR: two CTAs on a tile of 256 x BN, each with 128 rows of P, half of Q's in its shared memory, and
+// BN columns of sums.
+template <int BN, bool PAIR>
 struct Config {
-  static constexpr uint32_t Q_BYTES = BN * BK;
+  static constexpr uint32_t Q_BYTES = (PAIR ? BN / 2 : BN) * BK;
   static constexpr uint32_t STAGE_BYTES = P_BYTES + Q_BYTES;
-  static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-  static constexpr uint32_t TMEM_COLS = BN < 16 ? 32 : 2 * BN;
-  static constexpr int CH = BN >= 64 ? 32 : BN / 2;  // columns per tensor memory load
-  static constexpr size_t SCALE_BYTES = 2 * BN * 4;
-  static constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * STAGE_BYTES + SCALE_BYTES + 256;
+  static constexpr int STAGES = PAIR ? 4 : BN == 128 ? 6 : 8;
+  static constexpr uint32_t TMEM_COLS = 2 * BN;
+  static constexpr int CH = BN >= 32 ? 16 : 8;  // columns per tensor memory load
+  // scales of four blocks of K: of P's rows, and of Q's rows or of its (one or two) blocks of 128
+  static constexpr int SCALES = 4 * (BM + BN);
+  static constexpr size_t SCALE_BYTES = 2 * SCALES * 4;
+  static constexpr size_t OUT_BYTES = PAIR ? 65536 : 0;  // a pair's sums on their way out: 32 KB for each warpgroup
+  static constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + 256;
 };
 
 struct Params {
@@ -52,7 +56,7 @@ struct Params {
   void* c;
   long long ldc;
   int c_f32, accumulate;
-  int wide;     // C's rows start on 32 bytes
+  int tma_out;  // pairs: C is written by TMA (rows start on 16 bytes, nothing is added)
   int group_p;  // tile order of the persistent walk
   DevStatus* status;
   unsigned long long limit_ns;
@@ -69,12 +73,14 @@ __device__ __forceinline__ void tile_coords(int tile, int num_p, int num_q, int 
 
 template <int CH>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[CH]) {
-  if constexpr (CH == 32) tmem_ld32(addr, r);
-  else if constexpr (CH == 16) tmem_ld16(addr, r);
+  if constexpr (CH == 16) tmem_ld16(addr, r);
   else tmem_ld8(addr, r);
 }
-
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(EPI_THREADS) : "memory"); }
+template <int CH>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[CH]) {
+  if constexpr (CH == 16) tmem_ld_wait16(r);
+  else tmem_ld_wait8(r);
+}
 
 __device__ __forceinline__ void put(const Params& p, long long at, float v) {
   if (p.c_f32) {
@@ -85,46 +91,46 @@ __device__ __forceinline__ void put(const Params& p, long long at, float v) {
   }
 }
 
-__device__ __forceinline__ void st_v8(void* ptr, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
 // COLS: Q has a scale for every row (a column of the tile), else one for 128 rows.
 // TURNED: P = B and Q = A, C[q][p]; else C[p][q].
-template <int BN, bool COLS, bool TURNED>
+template <int BN, bool COLS, bool TURNED, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1)
     matmul_e4m3_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
-                       const Params p) {
-  using cfg = Config<BN>;
+                       const __grid_constant__ CUtensorMap tm_c, const Params p) {
+  using cfg = Config<BN, PAIR>;
   constexpr int STAGES = cfg::STAGES, CH = cfg::CH, HALF = BN / 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* s_p = smem;
   uint8_t* s_q = smem + STAGES * P_BYTES;
-  float* s_scale = reinterpret_cast<float*>(smem + STAGES * cfg::STAGE_BYTES);  // [2][BN]
+  uint8_t* s_out = smem + STAGES * cfg::STAGE_BYTES;
+  float* s_scale = reinterpret_cast<float*>(s_out + cfg::OUT_BYTES);  // [2][4][BM + BN]
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_scale) + cfg::SCALE_BYTES);
   uint64_t* full = bars;                   // [STAGES] TMA landed
   uint64_t* empty = bars + STAGES;         // [STAGES] MMAs reading the stage are done
   uint64_t* acc_full = bars + 2 * STAGES;  // [2] a block's product is complete
   uint64_t* acc_empty = acc_full + 2;      // [2] it has been taken
-  uint64_t* drain = acc_empty + 2;         // [1] every MMA issued has completed
+  uint64_t* scale_full = acc_empty + 2;    // [2] the scales of four blocks are there
+  uint64_t* scale_empty = scale_full + 2;  // [2] they have been read
+  uint64_t* drain = scale_empty + 2;       // [1] every MMA issued has completed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   namespace cg = cooperative_groups;
   const cg::cluster_group cluster = cg::this_cluster();
-  const int split = (int)cluster.num_blocks();
-  const int rank = (int)cluster.block_rank();
+  const int rank = (int)cluster.block_rank();  // of the CTAs on one tile
+  const int ranks = (int)cluster.num_blocks();
+  const int split = PAIR ? 1 : ranks;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int num_p = (p.rows_p + BM - 1) / BM;
+  constexpr int TILE_P = PAIR ? 2 * BM : BM;
+  const int num_p = (p.rows_p + TILE_P - 1) / TILE_P;
   const int num_q = (p.rows_q + BN - 1) / BN;
   const int num_tiles = num_p * num_q;
-  const int first_tile = blockIdx.x / split, tile_step = gridDim.x / split;
-  const int kb0 = (int)((long long)p.nkb * rank / split), kb1 = (int)((long long)p.nkb * (rank + 1) / split);
+  const int first_tile = blockIdx.x / ranks, tile_step = gridDim.x / ranks;
+  const int kb0 = PAIR ? 0 : (int)((long long)p.nkb * rank / split);
+  const int kb1 = PAIR ? p.nkb : (int)((long long)p.nkb * (rank + 1) / split);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -133,7 +139,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], EPI_WARPS);
+      mbar_init(&acc_empty[a], PAIR ? 2 * EPI_WARPS : EPI_WARPS);
+      mbar_init(&scale_full[a], 2);
+      mbar_init(&scale_empty[a], EPI_WARPS);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -142,11 +150,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     tma_prefetch_desc(&tm_q);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, cfg::TMEM_COLS);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, cfg::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, cfg::TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster.sync();  // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   dependents_may_start();
@@ -170,13 +184,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         int tp, tq;
         tile_coords(tile, num_p, num_q, p.group_p, tp, tq);
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, wb, SITE_E4M3_PRODUCER)) {
+          if (!mbar_wait_short(&empty[stage], phase ^ 1u, wb, SITE_E4M3_PRODUCER)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[stage], cfg::STAGE_BYTES);
-          tma_load_2d(s_p + stage * P_BYTES, &tm_p, &full[stage], kb * BK, tp * BM);
-          tma_load_2d(s_q + stage * cfg::Q_BYTES, &tm_q, &full[stage], kb * BK, tq * BN);
+          if constexpr (PAIR) {
+            // both CTAs' bytes count on the first one's barrier, whose MMA warp reads them
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * cfg::STAGE_BYTES);
+            const uint32_t bar = cluster_addr(&full[stage], 0);
+            tma_load_2d_pair(s_p + stage * P_BYTES, &tm_p, bar, kb * BK, tp * TILE_P + rank * BM);
+            tma_load_2d_pair(s_q + stage * cfg::Q_BYTES, &tm_q, bar, kb * BK, tq * BN + rank * (BN / 2));
+          } else {
+            mbar_arrive_expect_tx(&full[stage], cfg::STAGE_BYTES);
+            tma_load_2d(s_p + stage * P_BYTES, &tm_p, &full[stage], kb * BK, tp * BM);
+            tma_load_2d(s_q + stage * cfg::Q_BYTES, &tm_q, &full[stage], kb * BK, tq * BN);
+          }
 #pragma unroll
           for (int s = 0; s < STAGES; ++s)
             if (s == stage) last_parity[s] = (int)phase;
@@ -186,15 +208,24 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
-      // Do not leave while a TMA copy into this CTA's shared memory is in flight.
+      // Do not leave while a TMA copy into this CTA's shared memory is in flight. Those of a pair's
+      // second CTA count on the first one's barriers: its sums have waited for MMAs on all of them,
+      // or, when a wait gave up, it gives them a millisecond.
       WaitBound wd{p.status, p.limit_ns, nullptr};
+      if (PAIR && rank != 0) {
+        if (!ok) {
+          const unsigned long long t0 = global_ns();
+          while (global_ns() - t0 < 1000000ull) __nanosleep(1000);
+        }
+      } else {
 #pragma unroll
-      for (int s = 0; s < STAGES; ++s)
-        if (last_parity[s] >= 0) mbar_wait(&full[s], (uint32_t)last_parity[s], wd, SITE_DRAIN);
+        for (int s = 0; s < STAGES; ++s)
+          if (last_parity[s] >= 0) mbar_wait(&full[s], (uint32_t)last_parity[s], wd, SITE_DRAIN);
+      }
     }
-    if (warp == 1 && lane == 0) {
+    if (warp == 1 && (!PAIR || rank == 0)) {
       // ------------------------------------------------------------ MMA issuer
-      constexpr uint32_t idesc = make_idesc_e4m3(BM, BN);
+      constexpr uint32_t idesc = make_idesc_e4m3(TILE_P, BN);
       const uint64_t dp0 = make_sdesc_sw128(smem_addr(s_p), 16, 1024);
       const uint64_t dq0 = make_sdesc_sw128(smem_addr(s_q), 16, 1024);
       const uint32_t dp_lo = (uint32_t)dp0, dp_hi = (uint32_t)(dp0 >> 32);
@@ -203,21 +234,32 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int tile = first_tile; ok && tile < num_tiles; tile += tile_step) {
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u, wb, SITE_E4M3_MMA) ||
-              !mbar_wait(&full[stage], phase, wb, SITE_E4M3_MMA)) {
-            ok = false;
-            break;
-          }
+        for (int kb = kb0; ok && kb < kb1; ++kb) {
+          ok = mbar_wait_short(&acc_empty[acc], acc_phase ^ 1u, wb, SITE_E4M3_MMA) &&
+               mbar_wait_short(&full[stage], phase, wb, SITE_E4M3_MMA);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem_base + (uint32_t)(acc * BN);
           const uint32_t p_lo = dp_lo + (uint32_t)stage * (P_BYTES >> 4);
           const uint32_t q_lo = dq_lo + (uint32_t)stage * (cfg::Q_BYTES >> 4);
+          if (elect_lane()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            mma_ss_f8_w(d, p_lo + 2 * kk, dp_hi, q_lo + 2 * kk, dq_hi, idesc, kk != 0 ? 1u : 0u);
-          mma_commit(&empty[stage]);
-          mma_commit(&acc_full[acc]);
+            for (int kk = 0; kk < BK / 32; ++kk) {
+              if constexpr (PAIR)
+                mma_ss_f8_pair_w(d, p_lo + 2 * kk, dp_hi, q_lo + 2 * kk, dq_hi, idesc, kk != 0 ? 1u : 0u);
+              else
+                mma_ss_f8_w(d, p_lo + 2 * kk, dp_hi, q_lo + 2 * kk, dq_hi, idesc, kk != 0 ? 1u : 0u);
+            }
+            if constexpr (PAIR) {
+              mma_commit_pair(&acc_full[acc]);
+              mma_commit_pair(&empty[stage]);
+            } else {
+              mma_commit(&acc_full[acc]);
+              mma_commit(&empty[stage]);
+            }
+          }
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -227,9 +269,59 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       // Every MMA issued above completes before TMEM is released.
-      mma_commit(drain);
+      if (elect_lane()) {
+        if constexpr (PAIR) mma_commit_pair(drain);
+        else mma_commit(drain);
+      }
+      __syncwarp();
       WaitBound wd{p.status, p.limit_ns, nullptr};
       mbar_wait(drain, 0, wd, SITE_DRAIN);
+    }
+    if (warp >= 2) {
+      // ------------------------------------------------------------ scales: P's by warp 2, Q's by warp 3
+      const bool of_p = warp == 2;
+      const int rows = of_p ? p.rows_p : p.rows_q;
+      const long long ld = of_p ? p.ld_sp : p.ld_sq;
+      const float* base = of_p ? p.sp : p.sq;
+      const int shift = of_p ? p.p_shift : COLS ? 0 : 7;
+      const int count = of_p ? BM : COLS ? BN : (BN + BM - 1) / BM;  // values of a block of K
+      // four blocks by one load where they start on 16 bytes
+      const bool vec = (reinterpret_cast<uintptr_t>(base) & 15u) == 0 && (ld & 3) == 0 && (kb0 & 3) == 0;
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = first_tile; ok && tile < num_tiles; tile += tile_step) {
+        int tp, tq;
+        tile_coords(tile, num_p, num_q, p.group_p, tp, tq);
+        const long long row0 = of_p ? (long long)tp * TILE_P + (PAIR ? rank * BM : 0) : (long long)tq * BN;
+        for (int kb = kb0; kb < kb1; kb += 4) {
+          ok = __all_sync(0xffffffffu, mbar_wait_short(&scale_empty[slot], phase ^ 1u, wb, SITE_E4M3_PRODUCER));
+          if (!ok) break;
+          float* to = s_scale + slot * cfg::SCALES + (of_p ? 0 : BM);
+#pragma unroll 4
+          for (int i = lane; i < count; i += 32) {
+            const long long r = row0 + (of_p || COLS ? i : i * BM);
+            const float* from = base + (min(r, (long long)rows - 1) >> shift) * ld + kb;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (vec && kb + 4 <= kb1) {
+              v = *reinterpret_cast<const float4*>(from);
+            } else {
+              v.x = from[0];
+              if (kb + 1 < kb1) v.y = from[1];
+              if (kb + 2 < kb1) v.z = from[2];
+              if (kb + 3 < kb1) v.w = from[3];
+            }
+            to[i] = v.x;
+            to[(BM + BN) + i] = v.y;
+            to[2 * (BM + BN) + i] = v.z;
+            to[3 * (BM + BN) + i] = v.w;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&scale_full[slot]);
+          slot ^= 1;
+          if (slot == 0) phase ^= 1u;
+        }
+      }
     }
   } else {
     // -------------------------------------------------------------- sums
@@ -237,154 +329,173 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int quarter = warp & 3;         // TMEM lanes this warp may access
     const int half = (warp - 4) >> 2;     // of the tile's columns
     const int r_in_tile = quarter * 32 + lane;
-    const int tid = threadIdx.x - 128;
     const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * HALF);
-    int acc = 0;
-    uint32_t acc_phase = 0;
+    int acc = 0, slot = 0;
+    uint32_t acc_phase = 0, slot_phase = 0;
     bool ok = true;
+    // Every warp goes through every tile, also after a wait gave up: they meet at barriers below.
     for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
       int tp, tq;
       tile_coords(tile, num_p, num_q, p.group_p, tp, tq);
       uint64_t sum[HALF / 2];
 #pragma unroll
       for (int j = 0; j < HALF / 2; ++j) sum[j] = 0ull;
-      const long long row = (long long)tp * BM + r_in_tile;
-      const float* row_scale = p.sp + (min(row, (long long)p.rows_p - 1) >> p.p_shift) * p.ld_sp;
-      // the scale of a column per thread, or that of this half's block
-      const long long col = (long long)tq * BN + (COLS ? tid : half * HALF);
-      const float* col_scale = p.sq + (min(col, (long long)p.rows_q - 1) >> (COLS ? 0 : 7)) * p.ld_sq;
-      const bool loads = !COLS || tid < BN;
-      // one block ahead (two for what goes through shared memory)
-      float rs = kb0 < kb1 ? row_scale[kb0] : 0.f;
-      float cs = 0.f;
-      if (loads && kb0 < kb1) cs = col_scale[kb0];
-      if constexpr (COLS) {
-        epilogue_sync();  // the last tile's scales have been read
-        if (loads) {
-          s_scale[(kb0 & 1) * BN + tid] = cs;
-          if (kb0 + 1 < kb1) cs = col_scale[kb0 + 1];
+      for (int kb = kb0; ok && kb < kb1; ++kb) {
+        const int k4 = (kb - kb0) & 3;
+        if (k4 == 0) {
+          ok = mbar_wait_short(&scale_full[slot], slot_phase, wb, SITE_E4M3_EPILOGUE);
+          if (!ok) break;
         }
-      }
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const float rs_now = rs, cs_now = cs;
-        if (kb + 1 < kb1) rs = row_scale[kb + 1];
-        if constexpr (COLS) {
-          epilogue_sync();
-          if (loads && kb + 1 < kb1) {
-            s_scale[((kb + 1) & 1) * BN + tid] = cs;
-            if (kb + 2 < kb1) cs = col_scale[kb + 2];
-          }
-        } else {
-          if (kb + 1 < kb1) cs = col_scale[kb + 1];
-        }
-        ok = ok && mbar_wait(&acc_full[acc], acc_phase, wb, SITE_E4M3_EPILOGUE);
-        if (ok) {
-          tc_fence_after();
-          const uint32_t from = lanes + (uint32_t)(acc * BN);
-          const float f = COLS ? rs_now : rs_now * cs_now;
-          const uint64_t f2 = f2_pack(f, f);
+        const float* scales = s_scale + slot * cfg::SCALES + k4 * (BM + BN);
+        float f = scales[r_in_tile];
+        const float* col_scales = scales + BM + (COLS ? half * HALF : BN == 256 ? half : 0);
+        if constexpr (!COLS) f *= col_scales[0];
+        ok = mbar_wait_short(&acc_full[acc], acc_phase, wb, SITE_E4M3_EPILOGUE);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t from = lanes + (uint32_t)(acc * BN);
+        const uint64_t f2 = f2_pack(f, f);
+        // a load is under way while the columns of the one before it are added
+        uint32_t v[2][CH];
+        tmem_ld<CH>(from, v[0]);
 #pragma unroll
-          for (int c = 0; c < HALF; c += CH) {
-            uint32_t v[CH];
-            tmem_ld<CH>(from + c, v);
-            tmem_ld_wait();
-            if constexpr (COLS) {
-              const float4* s4 = reinterpret_cast<const float4*>(s_scale + (kb & 1) * BN + half * HALF + c);
-#pragma unroll
-              for (int j = 0; j < CH; j += 4) {
-                const float4 s = s4[j >> 2];
-                uint64_t& a = sum[(c + j) >> 1];
-                uint64_t& b = sum[((c + j) >> 1) + 1];
-                a = f2_fma(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f2_mul(f2, f2_pack(s.x, s.y)), a);
-                b = f2_fma(f2_pack(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), f2_mul(f2, f2_pack(s.z, s.w)), b);
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < CH; j += 2) {
-                uint64_t& a = sum[(c + j) >> 1];
-                a = f2_fma(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f2, a);
-              }
+        for (int c = 0; c < HALF; c += CH) {
+          uint32_t(&now)[CH] = v[(c / CH) & 1];
+          tmem_wait<CH>(now);
+          if (c + CH < HALF) {
+            tmem_ld<CH>(from + c + CH, v[(c / CH + 1) & 1]);
+          } else {
+            // all of it is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(&acc_empty[acc], 0));
+              else mbar_arrive(&acc_empty[acc]);
             }
           }
-          tc_fence_before();
+#pragma unroll
+          for (int j = 0; j < CH; j += 2) {
+            uint64_t scale = f2;
+            if constexpr (COLS) {
+              const float2 s = *reinterpret_cast<const float2*>(col_scales + c + j);
+              scale = f2_mul(f2, f2_pack(s.x, s.y));
+            }
+            uint64_t& a = sum[(c + j) >> 1];
+            a = f2_fma(f2_pack(__uint_as_float(now[j]), __uint_as_float(now[j + 1])), scale, a);
+          }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[acc]);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
+        if (k4 == 3 || kb + 1 == kb1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&scale_empty[slot]);
+          slot ^= 1;
+          if (slot == 0) slot_phase ^= 1u;
+        }
       }
 
-      if (split > 1) {
-        // this CTA's share of the sum, [column][row]; the ring is idle: every block has been taken
-        float* part = reinterpret_cast<float*>(smem);
-#pragma unroll
-        for (int j = 0; j < HALF; j += 2) {
-          float a, b;
-          f2_unpack(sum[j >> 1], a, b);
-          part[(half * HALF + j) * BM + r_in_tile] = a;
-          part[(half * HALF + j + 1) * BM + r_in_tile] = b;
-        }
-        continue;  // one tile per cluster
-      }
-      const bool row_ok = row < p.rows_p;
+      const long long row = (long long)tp * TILE_P + (PAIR ? rank * BM : 0) + r_in_tile;
       const long long q0 = (long long)tq * BN + half * HALF;
-      if (!row_ok) continue;
       if constexpr (TURNED) {
+        if (split > 1) {
+          // this CTA's share of the sum, [column][row]; the ring is idle: every block has been taken
+          float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int j = 0; j < HALF; j += 2) {
-          float a, b;
-          f2_unpack(sum[j >> 1], a, b);
-          if (q0 + j < p.rows_q) put(p, (q0 + j) * p.ldc + row, a);
-          if (q0 + j + 1 < p.rows_q) put(p, (q0 + j + 1) * p.ldc + row, b);
-        }
-      } else if (p.wide && q0 + HALF <= p.rows_q) {
-        if (p.c_f32) {
-          float* c = static_cast<float*>(p.c) + row * p.ldc + q0;
-#pragma unroll
-          for (int j = 0; j < HALF; j += 8) {
-            float f[8];
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) f2_unpack(sum[(j + e) >> 1], f[e], f[e + 1]);
-            if (p.accumulate) {
-              const float4 x = *reinterpret_cast<const float4*>(c + j), y = *reinterpret_cast<const float4*>(c + j + 4);
-              f[0] += x.x, f[1] += x.y, f[2] += x.z, f[3] += x.w, f[4] += y.x, f[5] += y.y, f[6] += y.z, f[7] += y.w;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(f[e]);
-            st_v8(c + j, w);
+          for (int j = 0; j < HALF; j += 2) {
+            float a, b;
+            f2_unpack(sum[j >> 1], a, b);
+            part[(half * HALF + j) * BM + r_in_tile] = a;
+            part[(half * HALF + j + 1) * BM + r_in_tile] = b;
           }
-        } else {
-          __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.c) + row * p.ldc + q0;
+        } else if (row < p.rows_p) {
 #pragma unroll
-          for (int j = 0; j < HALF; j += 16) {
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float a, b;
-              f2_unpack(sum[(j >> 1) + e], a, b);
-              w[e] = pack_bf16x2(a, b);
-            }
-            st_v8(c + j, w);
+          for (int j = 0; j < HALF; j += 2) {
+            float a, b;
+            f2_unpack(sum[j >> 1], a, b);
+            if (q0 + j < p.rows_q) put(p, (q0 + j) * p.ldc + row, a);
+            if (q0 + j + 1 < p.rows_q) put(p, (q0 + j + 1) * p.ldc + row, b);
           }
         }
       } else {
+        // through 32 KB of shared memory per warpgroup, as boxes of 128 rows x 128 bytes with their
+        // 16-byte chunks swizzled by the row: two boxes of 64 bf16 columns, or in two rounds of 32 fp32
+        uint8_t* out = s_out + half * 32768;
+        const int warp_in = warp & 3;
+        const bool leader = warp_in == 0 && lane == 0;
 #pragma unroll
-        for (int j = 0; j < HALF; j += 2) {
-          float a, b;
-          f2_unpack(sum[j >> 1], a, b);
-          if (q0 + j < p.rows_q) put(p, row * p.ldc + q0 + j, a);
-          if (q0 + j + 1 < p.rows_q) put(p, row * p.ldc + q0 + j + 1, b);
+        for (int round = 0; round < 2; ++round) {
+          if (round == 1 && !p.c_f32) break;
+          if (leader) bulk_wait_read();  // the boxes are free
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+          if (p.c_f32) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {  // 16 chunks of 4 columns
+              float a, b, c, d;
+              f2_unpack(sum[32 * round + 2 * j], a, b);
+              f2_unpack(sum[32 * round + 2 * j + 1], c, d);
+              *reinterpret_cast<float4*>(out + (j >> 3) * 16384 + r_in_tile * 128 + (((j & 7) ^ (r_in_tile & 7)) << 4)) =
+                  make_float4(a, b, c, d);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {  // 16 chunks of 8 columns
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float a, b;
+                f2_unpack(sum[4 * j + e], a, b);
+                w[e] = pack_bf16x2(a, b);
+              }
+              *reinterpret_cast<uint4*>(out + (j >> 3) * 16384 + r_in_tile * 128 + (((j & 7) ^ (r_in_tile & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          fence_proxy_async();
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+          const int first_col = tq * BN + half * HALF + round * 64;
+          const int first_row = tp * TILE_P + (PAIR ? rank * BM : 0);
+          if (p.tma_out) {
+            if (leader) {
+              const int per = p.c_f32 ? 32 : 64;
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                if (first_col + b * per < p.rows_q && first_row < p.rows_p)
+                  tma_store_2d(&tm_c, out + b * 16384, first_col + b * per, first_row);
+              bulk_commit();
+            }
+          } else {
+            // row by row, a column per lane
+            for (int i = 0; i < 32; ++i) {
+              const int r = warp_in * 32 + i;
+              if (first_row + r >= p.rows_p) break;
+              const long long at = (long long)(first_row + r) * p.ldc;
+              for (int c = lane; c < (p.c_f32 ? 64 : 128); c += 32) {
+                if (first_col + c >= p.rows_q) break;
+                if (p.c_f32) {
+                  const float x = *reinterpret_cast<const float*>(out + (c >> 5) * 16384 + r * 128 +
+                                                                  ((((c & 31) >> 2) ^ (r & 7)) << 4) + (c & 3) * 4);
+                  put(p, at + first_col + c, x);
+                } else {
+                  const __nv_bfloat16 x = *reinterpret_cast<const __nv_bfloat16*>(
+                      out + (c >> 6) * 16384 + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 7) * 2);
+                  static_cast<__nv_bfloat16*>(p.c)[at + first_col + c] = x;
+                }
+              }
+            }
+          }
         }
       }
     }
+    if constexpr (!TURNED) bulk_wait();
   }
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster.sync();  // neither leaves while the other may reach its memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, cfg::TMEM_COLS);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, cfg::TMEM_COLS);
+    else tmem_dealloc(tmem_base, cfg::TMEM_COLS);
   }
   if constexpr (TURNED) {
     if (split > 1) {
@@ -404,12 +515,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-template <int BN, bool COLS, bool TURNED>
-tsp_status launch(const CUtensorMap& tp, const CUtensorMap& tq, const Params& p, int ctas, int split, cudaStream_t s) {
-  auto kernel = matmul_e4m3_kernel<BN, COLS, TURNED>;
-  TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)Config<BN>::SMEM_BYTES,
-                            "matmul_e4m3: cudaFuncSetAttribute"));
-  const cudaError_t e = launch_early_cluster(kernel, ctas, THREADS, Config<BN>::SMEM_BYTES, s, split, tp, tq, p);
+template <int BN, bool COLS, bool TURNED, bool PAIR>
+tsp_status launch(const CUtensorMap& tp, const CUtensorMap& tq, const CUtensorMap& tc, const Params& p, int ctas, int cluster, cudaStream_t s) {
+  auto kernel = matmul_e4m3_kernel<BN, COLS, TURNED, PAIR>;
+  constexpr size_t smem = Config<BN, PAIR>::SMEM_BYTES;
+  TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem, "matmul_e4m3: cudaFuncSetAttribute"));
+  const cudaError_t e = launch_early_cluster(kernel, ctas, THREADS, smem, s, cluster, tp, tq, tc, p);
   return e == cudaSuccess ? TSP_OK : cuda_fail(e, "matmul_e4m3: launch");
 }
 
@@ -421,11 +532,18 @@ struct Operand {
   int shift;  // 0: a scale for every row, 7: one for 128 rows
 };
 
-template <int BN, bool COLS, bool TURNED>
+// split: CTAs on the blocks of K of one tile; a pair takes the whole of K.
+template <int BN, bool COLS, bool TURNED, bool PAIR>
 tsp_status run(const Operand& op, const Operand& oq, int64_t k, Params p, int split, cudaStream_t s) {
-  CUtensorMap tp, tq;
+  CUtensorMap tp, tq, tc{};
   TSP_TRY(make_tmap_2d_u8(&tp, op.x, (uint64_t)k, (uint64_t)op.rows, (uint64_t)op.ld, BK, BM));
-  TSP_TRY(make_tmap_2d_u8(&tq, oq.x, (uint64_t)k, (uint64_t)oq.rows, (uint64_t)oq.ld, BK, BN));
+  TSP_TRY(make_tmap_2d_u8(&tq, oq.x, (uint64_t)k, (uint64_t)oq.rows, (uint64_t)oq.ld, BK, PAIR ? BN / 2 : BN));
+  if (!TURNED && p.tma_out) {
+    if (p.c_f32)
+      TSP_TRY(make_tmap_2d_f32(&tc, p.c, (uint64_t)oq.rows, (uint64_t)op.rows, (uint64_t)p.ldc * 4, 32, BM));
+    else
+      TSP_TRY(make_tmap_2d_bf16(&tc, p.c, (uint64_t)oq.rows, (uint64_t)op.rows, (uint64_t)p.ldc * 2, 64, BM));
+  }
   p.rows_p = (int)op.rows;
   p.rows_q = (int)oq.rows;
   p.sp = op.scales;
@@ -433,10 +551,12 @@ tsp_status run(const Operand& op, const Operand& oq, int64_t k, Params p, int sp
   p.p_shift = op.shift;
   p.sq = oq.scales;
   p.ld_sq = oq.ld_scales;
-  const int64_t tiles = ((op.rows + BM - 1) / BM) * ((oq.rows + BN - 1) / BN);
-  if (tiles * split > (1ll << 30)) return fail(TSP_ERR_UNSUPPORTED, "tsp_matmul_e4m3: too many tiles");
-  const int64_t ctas = split > 1 ? tiles * split : std::min<int64_t>(tiles, sm_count());
-  return launch<BN, COLS, TURNED>(tp, tq, p, (int)ctas, split, s);
+  constexpr int tile_p = PAIR ? 2 * BM : BM;
+  const int cluster = PAIR ? 2 : split;
+  const int64_t tiles = ((op.rows + tile_p - 1) / tile_p) * ((oq.rows + BN - 1) / BN);
+  if (tiles * cluster > (1ll << 30)) return fail(TSP_ERR_UNSUPPORTED, "tsp_matmul_e4m3: too many tiles");
+  const int64_t clusters = split > 1 ? tiles : std::min<int64_t>(tiles, std::max(1, sm_count() / cluster));
+  return launch<BN, COLS, TURNED, PAIR>(tp, tq, tc, p, (int)(clusters * cluster), cluster, s);
 }
 
 }  // namespace
@@ -489,7 +609,7 @@ tsp_status tsp_matmul_e4m3(int64_t m, int64_t n, int64_t k, const uint8_t* a, in
   p.ldc = ld_c;
   p.c_f32 = c_f32;
   p.accumulate = accumulate;
-  p.wide = (reinterpret_cast<uintptr_t>(c) & 31u) == 0 && (ld_c * es) % 32 == 0;
+  p.tma_out = !accumulate && al16(c) && (ld_c * es) % 16 == 0;
   p.group_p = 1;
   p.status = status_of(ws);
   p.limit_ns = wait_limit_ns();
@@ -499,17 +619,17 @@ tsp_status tsp_matmul_e4m3(int64_t m, int64_t n, int64_t k, const uint8_t* a, in
     // about 32 MB of A's row blocks walk down each column block of B together where B does not fit the L2 well
     const int64_t g = n * k <= (48ll << 20) ? 1 : (32ll << 20) / (BM * k);
     p.group_p = (int)std::max<int64_t>(1, g);
-    return b_block == 1 ? run<256, true, false>(oa, ob, k, p, 1, s) : run<256, false, false>(oa, ob, k, p, 1, s);
+    return b_block == 1 ? run<256, true, false, true>(oa, ob, k, p, 1, s) : run<256, false, false, true>(oa, ob, k, p, 1, s);
   }
   const int bn = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
   const int64_t tiles = ((n + BM - 1) / BM) * ((m + bn - 1) / bn);
   int split = 1;
   while (split < 8 && tiles * split * 2 <= 2 * sm_count() && nkb >= split * 4) split *= 2;
   switch (bn) {
-    case 16: return run<16, true, true>(ob, oa, k, p, split, s);
-    case 32: return run<32, true, true>(ob, oa, k, p, split, s);
-    case 64: return run<64, true, true>(ob, oa, k, p, split, s);
-    default: return run<128, true, true>(ob, oa, k, p, split, s);
+    case 16: return run<16, true, true, false>(ob, oa, k, p, split, s);
+    case 32: return run<32, true, true, false>(ob, oa, k, p, split, s);
+    case 64: return run<64, true, true, false>(ob, oa, k, p, split, s);
+    default: return run<128, true, true, false>(ob, oa, k, p, split, s);
   }
   TSP_GUARD_END
 }
