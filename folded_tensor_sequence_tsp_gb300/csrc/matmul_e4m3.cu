@@ -29,6 +29,7 @@ constexpr int BK = 128;
 constexpr int THREADS = 384;
 constexpr int EPI_WARPS = 8;
 constexpr uint32_t P_BYTES = BM * BK;
+constexpr int KS = 8;  // blocks of K whose scales are fetched together
 
 // PAIR: two CTAs on a tile of 256 x BN, each with 128 rows of P, half of Q's in its shared memory, and
 // BN columns of sums.
@@ -38,9 +39,8 @@ struct Config {
   static constexpr uint32_t STAGE_BYTES = P_BYTES + Q_BYTES;
   static constexpr int STAGES = PAIR ? 4 : BN == 128 ? 6 : 8;
   static constexpr uint32_t TMEM_COLS = 2 * BN;
-  static constexpr int CH = BN >= 32 ? 16 : 8;  // columns per tensor memory load
-  // scales of four blocks of K: of P's rows, and of Q's rows or of its (one or two) blocks of 128
-  static constexpr int SCALES = 4 * (BM + BN);
+  // scales of some blocks of K: of P's rows, and of Q's rows or of its (one or two) blocks of 128
+  static constexpr int SCALES = KS * (BM + BN);
   static constexpr size_t SCALE_BYTES = 2 * SCALES * 4;
   static constexpr size_t OUT_BYTES = PAIR ? 65536 : 0;  // a pair's sums on their way out: 32 KB for each warpgroup
   static constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + 256;
@@ -73,12 +73,14 @@ __device__ __forceinline__ void tile_coords(int tile, int num_p, int num_q, int 
 
 template <int CH>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[CH]) {
-  if constexpr (CH == 16) tmem_ld16(addr, r);
+  if constexpr (CH == 32) tmem_ld32(addr, r);
+  else if constexpr (CH == 16) tmem_ld16(addr, r);
   else tmem_ld8(addr, r);
 }
 template <int CH>
 __device__ __forceinline__ void tmem_wait(uint32_t (&r)[CH]) {
-  if constexpr (CH == 16) tmem_ld_wait16(r);
+  if constexpr (CH == 32) tmem_ld_wait32(r);
+  else if constexpr (CH == 16) tmem_ld_wait16(r);
   else tmem_ld_wait8(r);
 }
 
@@ -98,19 +100,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     matmul_e4m3_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_c, const Params p) {
   using cfg = Config<BN, PAIR>;
-  constexpr int STAGES = cfg::STAGES, CH = cfg::CH, HALF = BN / 2;
+  constexpr int STAGES = cfg::STAGES, HALF = BN / 2;
+  constexpr int CH = BN == 16 ? 8 : 16;  // columns per tensor memory load
+  // Pairs with a scale per column: a thread holds four rows of every fourth pair of columns, so that it
+  // needs 32 columns' scales from shared memory for a block and not 128.
+  constexpr bool QUAD = COLS && PAIR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* s_p = smem;
   uint8_t* s_q = smem + STAGES * P_BYTES;
   uint8_t* s_out = smem + STAGES * cfg::STAGE_BYTES;
-  float* s_scale = reinterpret_cast<float*>(s_out + cfg::OUT_BYTES);  // [2][4][BM + BN]
+  float* s_scale = reinterpret_cast<float*>(s_out + cfg::OUT_BYTES);  // [2][KS][BM + BN]
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_scale) + cfg::SCALE_BYTES);
   uint64_t* full = bars;                   // [STAGES] TMA landed
   uint64_t* empty = bars + STAGES;         // [STAGES] MMAs reading the stage are done
   uint64_t* acc_full = bars + 2 * STAGES;  // [2] a block's product is complete
   uint64_t* acc_empty = acc_full + 2;      // [2] it has been taken
-  uint64_t* scale_full = acc_empty + 2;    // [2] the scales of four blocks are there
+  uint64_t* scale_full = acc_empty + 2;    // [2] the scales of KS blocks are there
   uint64_t* scale_empty = scale_full + 2;  // [2] they have been read
   uint64_t* drain = scale_empty + 2;       // [1] every MMA issued has completed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -169,9 +175,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   WaitBound wb{p.status, p.limit_ns, abort_flag};
 
   // Registers: 384 threads start with 168 each, the most that three warps per scheduler leave; the
-  // sums of a wide tile (128 of them per thread) need more. 4 x 72 + 8 x 216 = 12 x 168.
+  // sums of a wide tile (128 of them per thread) need more. 4 x 56 + 8 x 224 = 12 x 168.
   if (warp < 4) {
-    if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && lane == 0) {
       // ------------------------------------------------------------ producer
       int stage = 0;
@@ -235,31 +241,32 @@ __global__ void __launch_bounds__(THREADS, 1)
       bool ok = true;
       for (int tile = first_tile; ok && tile < num_tiles; tile += tile_step) {
         for (int kb = kb0; ok && kb < kb1; ++kb) {
-          ok = mbar_wait_short(&acc_empty[acc], acc_phase ^ 1u, wb, SITE_E4M3_MMA) &&
-               mbar_wait_short(&full[stage], phase, wb, SITE_E4M3_MMA);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
           const uint32_t d = tmem_base + (uint32_t)(acc * BN);
           const uint32_t p_lo = dp_lo + (uint32_t)stage * (P_BYTES >> 4);
           const uint32_t q_lo = dq_lo + (uint32_t)stage * (cfg::Q_BYTES >> 4);
           if (elect_lane()) {
+            // the accumulator is what is waited for: nothing but the MMAs comes after it
+            ok = mbar_wait_short(&full[stage], phase, wb, SITE_E4M3_MMA) &&
+                 mbar_wait_short(&acc_empty[acc], acc_phase ^ 1u, wb, SITE_E4M3_MMA);
+            if (ok) {
+              tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk) {
-              if constexpr (PAIR)
-                mma_ss_f8_pair_w(d, p_lo + 2 * kk, dp_hi, q_lo + 2 * kk, dq_hi, idesc, kk != 0 ? 1u : 0u);
-              else
-                mma_ss_f8_w(d, p_lo + 2 * kk, dp_hi, q_lo + 2 * kk, dq_hi, idesc, kk != 0 ? 1u : 0u);
-            }
-            if constexpr (PAIR) {
-              mma_commit_pair(&acc_full[acc]);
-              mma_commit_pair(&empty[stage]);
-            } else {
-              mma_commit(&acc_full[acc]);
-              mma_commit(&empty[stage]);
+              for (int kk = 0; kk < BK / 32; ++kk) {
+                if constexpr (PAIR)
+                  mma_ss_f8_pair_w(d, p_lo + 2 * kk, dp_hi, q_lo + 2 * kk, dq_hi, idesc, kk != 0 ? 1u : 0u);
+                else
+                  mma_ss_f8_w(d, p_lo + 2 * kk, dp_hi, q_lo + 2 * kk, dq_hi, idesc, kk != 0 ? 1u : 0u);
+              }
+              if constexpr (PAIR) {
+                mma_commit_pair(&acc_full[acc]);
+                mma_commit_pair(&empty[stage]);
+              } else {
+                mma_commit(&acc_full[acc]);
+                mma_commit(&empty[stage]);
+              }
             }
           }
-          __syncwarp();
+          ok = __all_sync(0xffffffffu, ok);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -294,27 +301,29 @@ __global__ void __launch_bounds__(THREADS, 1)
         int tp, tq;
         tile_coords(tile, num_p, num_q, p.group_p, tp, tq);
         const long long row0 = of_p ? (long long)tp * TILE_P + (PAIR ? rank * BM : 0) : (long long)tq * BN;
-        for (int kb = kb0; kb < kb1; kb += 4) {
+        for (int kb = kb0; kb < kb1; kb += KS) {
           ok = __all_sync(0xffffffffu, mbar_wait_short(&scale_empty[slot], phase ^ 1u, wb, SITE_E4M3_PRODUCER));
           if (!ok) break;
           float* to = s_scale + slot * cfg::SCALES + (of_p ? 0 : BM);
-#pragma unroll 4
           for (int i = lane; i < count; i += 32) {
             const long long r = row0 + (of_p || COLS ? i : i * BM);
             const float* from = base + (min(r, (long long)rows - 1) >> shift) * ld + kb;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (vec && kb + 4 <= kb1) {
-              v = *reinterpret_cast<const float4*>(from);
-            } else {
-              v.x = from[0];
-              if (kb + 1 < kb1) v.y = from[1];
-              if (kb + 2 < kb1) v.z = from[2];
-              if (kb + 3 < kb1) v.w = from[3];
+#pragma unroll
+            for (int k = 0; k < KS; k += 4) {
+              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (vec && kb + k + 4 <= kb1) {
+                v = *reinterpret_cast<const float4*>(from + k);
+              } else {
+                if (kb + k < kb1) v.x = from[k];
+                if (kb + k + 1 < kb1) v.y = from[k + 1];
+                if (kb + k + 2 < kb1) v.z = from[k + 2];
+                if (kb + k + 3 < kb1) v.w = from[k + 3];
+              }
+              to[k * (BM + BN) + i] = v.x;
+              to[(k + 1) * (BM + BN) + i] = v.y;
+              to[(k + 2) * (BM + BN) + i] = v.z;
+              to[(k + 3) * (BM + BN) + i] = v.w;
             }
-            to[i] = v.x;
-            to[(BM + BN) + i] = v.y;
-            to[2 * (BM + BN) + i] = v.z;
-            to[3 * (BM + BN) + i] = v.w;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&scale_full[slot]);
@@ -325,11 +334,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else {
     // -------------------------------------------------------------- sums
-    if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int quarter = warp & 3;         // TMEM lanes this warp may access
     const int half = (warp - 4) >> 2;     // of the tile's columns
     const int r_in_tile = quarter * 32 + lane;
     const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * HALF);
+    const uint32_t taken0 = cluster_addr(&acc_empty[0], 0), taken1 = cluster_addr(&acc_empty[1], 0);  // pairs
     int acc = 0, slot = 0;
     uint32_t acc_phase = 0, slot_phase = 0;
     bool ok = true;
@@ -340,57 +350,127 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint64_t sum[HALF / 2];
 #pragma unroll
       for (int j = 0; j < HALF / 2; ++j) sum[j] = 0ull;
-      for (int kb = kb0; ok && kb < kb1; ++kb) {
-        const int k4 = (kb - kb0) & 3;
-        if (k4 == 0) {
-          ok = mbar_wait_short(&scale_full[slot], slot_phase, wb, SITE_E4M3_EPILOGUE);
-          if (!ok) break;
+      // Shared memory is busy with the operands, and an access to it takes some 150 cycles: the scales of
+      // a block's rows are read, and its product is first asked for, while the block before it is added.
+      const float* scales = s_scale + slot * cfg::SCALES;
+      bool ready = false;
+      float f[QUAD ? 4 : 1];
+      auto row_scales = [&]() {
+        if constexpr (QUAD) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = scales[quarter * 32 + (lane >> 2) + 8 * e];
+        } else {
+          f[0] = scales[r_in_tile];
+          if constexpr (!COLS) f[0] *= scales[BM + half];
         }
-        const float* scales = s_scale + slot * cfg::SCALES + k4 * (BM + BN);
-        float f = scales[r_in_tile];
-        const float* col_scales = scales + BM + (COLS ? half * HALF : BN == 256 ? half : 0);
-        if constexpr (!COLS) f *= col_scales[0];
-        ok = mbar_wait_short(&acc_full[acc], acc_phase, wb, SITE_E4M3_EPILOGUE);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t from = lanes + (uint32_t)(acc * BN);
-        const uint64_t f2 = f2_pack(f, f);
-        // a load is under way while the columns of the one before it are added
-        uint32_t v[2][CH];
-        tmem_ld<CH>(from, v[0]);
-#pragma unroll
-        for (int c = 0; c < HALF; c += CH) {
-          uint32_t(&now)[CH] = v[(c / CH) & 1];
-          tmem_wait<CH>(now);
-          if (c + CH < HALF) {
-            tmem_ld<CH>(from + c + CH, v[(c / CH + 1) & 1]);
-          } else {
-            // all of it is in registers
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(&acc_empty[acc], 0));
-              else mbar_arrive(&acc_empty[acc]);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < CH; j += 2) {
-            uint64_t scale = f2;
-            if constexpr (COLS) {
-              const float2 s = *reinterpret_cast<const float2*>(col_scales + c + j);
-              scale = f2_mul(f2, f2_pack(s.x, s.y));
-            }
-            uint64_t& a = sum[(c + j) >> 1];
-            a = f2_fma(f2_pack(__uint_as_float(now[j]), __uint_as_float(now[j + 1])), scale, a);
-          }
+      };
+      // the block is in registers, its scales too: on to the next
+      auto taken = [&](int kb) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR) mbar_arrive_cluster(acc ? taken1 : taken0);
+          else mbar_arrive(&acc_empty[acc]);
         }
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
-        if (k4 == 3 || kb + 1 == kb1) {
-          __syncwarp();
+        const int done = kb + 1 - kb0;
+        if (kb + 1 == kb1 || (done & (KS - 1)) == 0) {
           if (lane == 0) mbar_arrive(&scale_empty[slot]);
           slot ^= 1;
           if (slot == 0) slot_phase ^= 1u;
+          scales = s_scale + slot * cfg::SCALES;
+          if (kb + 1 < kb1) ok = mbar_wait_short(&scale_full[slot], slot_phase, wb, SITE_E4M3_EPILOGUE);
+        } else {
+          scales += BM + BN;
+        }
+        if (kb + 1 < kb1) {
+          ready = mbar_try_wait(&acc_full[acc], acc_phase);
+          row_scales();
+        }
+      };
+      if (ok && kb0 < kb1) {
+        ok = mbar_wait_short(&scale_full[slot], slot_phase, wb, SITE_E4M3_EPILOGUE);
+        row_scales();
+      }
+      for (int kb = kb0; ok && kb < kb1; ++kb) {
+        if (!ready) ok = mbar_wait_short(&acc_full[acc], acc_phase, wb, SITE_E4M3_EPILOGUE);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t from = lanes + (uint32_t)(acc * BN);
+        const float* col_scales = scales + BM + half * HALF;
+        // a load is under way while the columns of the one before it are added
+        if constexpr (QUAD) {
+          uint64_t rows[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) rows[e] = f2_pack(f[e], f[e]);
+          uint32_t v[2][16];
+          uint64_t cs[4];
+          auto load = [&](int c, int hh) {
+            tmem_ld_16x256(from + ((uint32_t)(16 * hh) << 16) + (uint32_t)c, v[hh]);
+            if (hh == 0) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 s = *reinterpret_cast<const float2*>(col_scales + c + 8 * i + 2 * (lane & 3));
+                cs[i] = f2_pack(s.x, s.y);
+              }
+            }
+          };
+          load(0, 0);
+#pragma unroll
+          for (int c = 0; c < HALF; c += 32) {
+            uint64_t now[4];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              tmem_ld_wait16(v[hh]);
+              if (hh == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) now[i] = cs[i];
+                load(c, 1);
+              } else if (c + 32 < HALF) {
+                load(c + 32, 0);
+              } else {
+                taken(kb);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  uint64_t& a = sum[((c >> 5) * 4 + 2 * hh + e) * 4 + i];
+                  a = f2_fma(f2_pack(__uint_as_float(v[hh][4 * i + 2 * e]), __uint_as_float(v[hh][4 * i + 2 * e + 1])),
+                             f2_mul(rows[2 * hh + e], now[i]), a);
+                }
+            }
+          }
+        } else {
+          const uint64_t f2 = f2_pack(f[0], f[0]);
+          uint32_t v[2][CH];
+          float4 cs[2][COLS ? CH / 4 : 1];
+          auto load = [&](int c) {
+            tmem_ld<CH>(from + c, v[(c / CH) & 1]);
+            if constexpr (COLS) {
+#pragma unroll
+              for (int j = 0; j < CH / 4; ++j) cs[(c / CH) & 1][j] = *reinterpret_cast<const float4*>(col_scales + c + 4 * j);
+            }
+          };
+          load(0);
+#pragma unroll
+          for (int c = 0; c < HALF; c += CH) {
+            uint32_t(&now)[CH] = v[(c / CH) & 1];
+            tmem_wait<CH>(now);
+            if (c + CH < HALF) load(c + CH);
+            else taken(kb);
+#pragma unroll
+            for (int j = 0; j < CH; j += 2) {
+              uint64_t scale = f2;
+              if constexpr (COLS) {
+                const float4& s = cs[(c / CH) & 1][j >> 2];
+                scale = f2_mul(f2, (j & 2) ? f2_pack(s.z, s.w) : f2_pack(s.x, s.y));
+              }
+              uint64_t& a = sum[(c + j) >> 1];
+              a = f2_fma(f2_pack(__uint_as_float(now[j]), __uint_as_float(now[j + 1])), scale, a);
+            }
+          }
         }
       }
 
@@ -427,7 +507,28 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (round == 1 && !p.c_f32) break;
           if (leader) bulk_wait_read();  // the boxes are free
           asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-          if (p.c_f32) {
+          if constexpr (QUAD) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {  // 32 columns
+              if (p.c_f32 && c >> 1 != round) continue;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int r = quarter * 32 + 8 * e + (lane >> 2);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  float a, b;
+                  f2_unpack(sum[(c * 4 + e) * 4 + i], a, b);
+                  if (p.c_f32)
+                    *reinterpret_cast<float2*>(out + (c & 1) * 16384 + r * 128 +
+                                               (((2 * i + ((lane & 3) >> 1)) ^ (r & 7)) << 4) + (lane & 1) * 8) =
+                        make_float2(a, b);
+                  else
+                    *reinterpret_cast<uint32_t*>(out + (c >> 1) * 16384 + r * 128 +
+                                                 ((((c & 1) * 4 + i) ^ (r & 7)) << 4) + (lane & 3) * 4) = pack_bf16x2(a, b);
+                }
+              }
+            }
+          } else if (p.c_f32) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {  // 16 chunks of 4 columns
               float a, b, c, d;
