@@ -11,9 +11,9 @@
 //               accumulators in tensor memory, each block from zero
 //   warps 4..11 take a finished accumulator (a row and BN / 2 columns per thread), scale it and add
 //               it to the tile's sum in registers, while the next block's MMAs run
-// Large products: P = A, Q = B with BN = 256, persistent CTAs. Few rows or few tiles: P = B, Q = A
-// with BN >= the rows of A, and the blocks of K split over a cluster of CTAs, which join their sums through
-// distributed shared memory in a fixed order.
+// Large products: P = A, Q = B with BN = 256, persistent CTAs. Few rows or few tiles: P = B, Q = A, a tile
+// per CTA or, with the blocks of K split, per cluster of CTAs, which join their sums through distributed
+// shared memory in a fixed order.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -30,6 +30,8 @@ constexpr int THREADS = 384;
 constexpr int EPI_WARPS = 8;
 constexpr uint32_t P_BYTES = BM * BK;
 constexpr int KS = 8;  // blocks of K whose scales are fetched together
+// Row stride of the sums in shared memory: a quarter warp's accesses to two columns' rows hit all banks
+constexpr int PART = BM + 4;
 
 // PAIR: two CTAs on a tile of 256 x BN, each with 128 rows of P, half of Q's in its shared memory, and
 // BN columns of sums.
@@ -37,7 +39,9 @@ template <int BN, bool PAIR>
 struct Config {
   static constexpr uint32_t Q_BYTES = (PAIR ? BN / 2 : BN) * BK;
   static constexpr uint32_t STAGE_BYTES = P_BYTES + Q_BYTES;
-  static constexpr int STAGES = PAIR ? 4 : BN == 128 ? 6 : 8;
+  // small tiles leave room for two CTAs on an SM
+  static constexpr int CTAS = BN <= 32 ? 2 : 1;
+  static constexpr int STAGES = PAIR ? 4 : BN == 128 ? 5 : BN == 64 ? 8 : 5;
   static constexpr uint32_t TMEM_COLS = 2 * BN;
   // scales of some blocks of K: of P's rows, and of Q's rows or of its (one or two) blocks of 128
   static constexpr int SCALES = KS * (BM + BN);
@@ -96,15 +100,15 @@ __device__ __forceinline__ void put(const Params& p, long long at, float v) {
 // COLS: Q has a scale for every row (a column of the tile), else one for 128 rows.
 // TURNED: P = B and Q = A, C[q][p]; else C[p][q].
 template <int BN, bool COLS, bool TURNED, bool PAIR>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(THREADS, Config<BN, PAIR>::CTAS)
     matmul_e4m3_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_c, const Params p) {
   using cfg = Config<BN, PAIR>;
   constexpr int STAGES = cfg::STAGES, HALF = BN / 2;
   constexpr int CH = BN == 16 ? 8 : 16;  // columns per tensor memory load
-  // Pairs with a scale per column: a thread holds four rows of every fourth pair of columns, so that it
-  // needs 32 columns' scales from shared memory for a block and not 128.
-  constexpr bool QUAD = COLS && PAIR;
+  // Where columns have a scale each, and there are enough: a thread holds four rows of every fourth pair of columns, so that it
+  // needs a fourth of them from shared memory.
+  constexpr bool QUAD = COLS && BN >= 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* s_p = smem;
@@ -474,26 +478,29 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
 
-      const long long row = (long long)tp * TILE_P + (PAIR ? rank * BM : 0) + r_in_tile;
-      const long long q0 = (long long)tq * BN + half * HALF;
       if constexpr (TURNED) {
-        if (split > 1) {
-          // this CTA's share of the sum, [column][row]; the ring is idle: every block has been taken
-          float* part = reinterpret_cast<float*>(smem);
+        // this CTA's share of the sum, [column][row], where the ring was: every block has been taken
+        float* part = reinterpret_cast<float*>(smem) + half * HALF * PART;
+        if constexpr (QUAD) {
+#pragma unroll
+          for (int c = 0; c < HALF / 32; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float a, b;
+                f2_unpack(sum[(c * 4 + e) * 4 + i], a, b);
+                float* at = part + (32 * c + 8 * i + 2 * (lane & 3)) * PART + quarter * 32 + 8 * e + (lane >> 2);
+                at[0] = a;
+                at[PART] = b;
+              }
+        } else {
 #pragma unroll
           for (int j = 0; j < HALF; j += 2) {
             float a, b;
             f2_unpack(sum[j >> 1], a, b);
-            part[(half * HALF + j) * BM + r_in_tile] = a;
-            part[(half * HALF + j + 1) * BM + r_in_tile] = b;
-          }
-        } else if (row < p.rows_p) {
-#pragma unroll
-          for (int j = 0; j < HALF; j += 2) {
-            float a, b;
-            f2_unpack(sum[j >> 1], a, b);
-            if (q0 + j < p.rows_q) put(p, (q0 + j) * p.ldc + row, a);
-            if (q0 + j + 1 < p.rows_q) put(p, (q0 + j + 1) * p.ldc + row, b);
+            part[j * PART + r_in_tile] = a;
+            part[(j + 1) * PART + r_in_tile] = b;
           }
         }
       } else {
@@ -599,20 +606,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     else tmem_dealloc(tmem_base, cfg::TMEM_COLS);
   }
   if constexpr (TURNED) {
-    if (split > 1) {
-      cluster.sync();
-      int tp, tq;
-      tile_coords(first_tile, num_p, num_q, p.group_p, tp, tq);
-      const float* mine = reinterpret_cast<const float*>(smem);
-      const int c0 = BN * rank / split, c1 = BN * (rank + 1) / split;
-      for (int i = c0 * BM + threadIdx.x; i < c1 * BM; i += THREADS) {
-        float v = 0.f;
-        for (int s = 0; s < split; ++s) v += *cluster.map_shared_rank(mine + i, s);
-        const long long row = (long long)tp * BM + (i & (BM - 1)), col = (long long)tq * BN + (i >> 7);
-        if (row < p.rows_p && col < p.rows_q) put(p, col * p.ldc + row, v);
-      }
-      cluster.sync();  // the others have read this CTA's share
+    // each CTA of the cluster joins and writes some of the columns
+    if (split > 1) cluster.sync();
+    int tp, tq;
+    tile_coords(first_tile, num_p, num_q, p.group_p, tp, tq);
+    const int cols = min(BN, p.rows_q - tq * BN);
+    const int c0 = cols * rank / split, c1 = cols * (rank + 1) / split;
+    for (int i = c0 * BM + threadIdx.x; i < c1 * BM; i += THREADS) {
+      const long long row = (long long)tp * BM + (i & (BM - 1));
+      if (row >= p.rows_p) continue;
+      const float* mine = reinterpret_cast<const float*>(smem) + (i >> 7) * PART + (i & (BM - 1));
+      float v = 0.f;
+      if (split == 1) v = *mine;
+      else
+        for (int s = 0; s < split; ++s) v += *cluster.map_shared_rank(mine, s);
+      put(p, (long long)(tq * BN + (i >> 7)) * p.ldc + row, v);
     }
+    if (split > 1) cluster.sync();  // the others have read this CTA's share
   }
 }
 
@@ -656,7 +666,7 @@ tsp_status run(const Operand& op, const Operand& oq, int64_t k, Params p, int sp
   const int cluster = PAIR ? 2 : split;
   const int64_t tiles = ((op.rows + tile_p - 1) / tile_p) * ((oq.rows + BN - 1) / BN);
   if (tiles * cluster > (1ll << 30)) return fail(TSP_ERR_UNSUPPORTED, "tsp_matmul_e4m3: too many tiles");
-  const int64_t clusters = split > 1 ? tiles : std::min<int64_t>(tiles, std::max(1, sm_count() / cluster));
+  const int64_t clusters = TURNED ? tiles : std::min<int64_t>(tiles, std::max(1, sm_count() / cluster));
   return launch<BN, COLS, TURNED, PAIR>(tp, tq, tc, p, (int)(clusters * cluster), cluster, s);
 }
 
@@ -724,8 +734,9 @@ tsp_status tsp_matmul_e4m3(int64_t m, int64_t n, int64_t k, const uint8_t* a, in
   }
   const int bn = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
   const int64_t tiles = ((n + BM - 1) / BM) * ((m + bn - 1) / bn);
+  const int64_t slots = (bn <= 32 ? 2 : 1) * sm_count();
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= 2 * sm_count() && nkb >= split * 4) split *= 2;
+  while (split < 8 && tiles * (split + 1) <= slots && nkb >= (split + 1) * 2) ++split;
   switch (bn) {
     case 16: return run<16, true, true, false>(ob, oa, k, p, split, s);
     case 32: return run<32, true, true, false>(ob, oa, k, p, split, s);

@@ -5,7 +5,7 @@
 //   columns    yt [width][rows]: the transpose, a scale for 128 rows of one column
 //   tiles      one scale for 128 x 128 values: y and its transpose hold the same values
 //
-// Bound: HBM. x is read once, whatever is written. The rows alone are a warp's work each, 128
+// Bound: HBM. x is read once, whatever is written. The rows alone are eight lanes' work, 128
 // columns at a time. What needs a column's largest value or a transpose takes a tile of 128 x 128
 // per CTA: each warp holds 16 rows in registers, the columns' maxima meet in shared memory, and
 // the transposed bytes go through a 16 KB tile there (16-byte chunks, swizzled by their column) so
@@ -33,29 +33,6 @@ struct QuantParams {
 
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(fabsf(v)); }
 
-// Four columns c to c + 3 of a row (zeros behind the width).
-template <bool F32, bool VEC>
-__device__ __forceinline__ void load4(const void* x, long long at, long long left, float (&v)[4]) {
-  if constexpr (VEC) {
-    if (left <= 0) {
-      v[0] = v[1] = v[2] = v[3] = 0.f;
-    } else if constexpr (F32) {
-      const float4 u = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(x) + at));
-      v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-    } else {
-      const uint2 u = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(x) + at));
-      v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = 0.f;
-      if (e < left)
-        v[e] = F32 ? static_cast<const float*>(x)[at + e] : __bfloat162float(static_cast<const __nv_bfloat16*>(x)[at + e]);
-    }
-  }
-}
-
 __device__ __forceinline__ uint32_t quantize4(const Quotient& by, const float (&v)[4]) {
   float a = v[0], b = v[1], c = v[2], d = v[3];
   by.pair(a, b);
@@ -64,7 +41,7 @@ __device__ __forceinline__ uint32_t quantize4(const Quotient& by, const float (&
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store4(uint8_t* y, long long left, uint32_t q) {
+__device__ __forceinline__ void store4(uint8_t* y, int left, uint32_t q) {
   if constexpr (VEC) {
     if (left > 0) *reinterpret_cast<uint32_t*>(y) = q;
   } else {
@@ -74,77 +51,223 @@ __device__ __forceinline__ void store4(uint8_t* y, long long left, uint32_t q) {
   }
 }
 
-// One warp per row and 128 columns, four of them at a time. VEC: the width is a multiple of 4 and
-// every row starts on 16 (fp32) or 8 (bf16) bytes, in y on 4.
-template <bool F32, bool VEC>
+// Rows that start on 16 bytes: eight lanes per block of 128 columns, 16 values each (two runs of 8 in bf16,
+// four of 4 in fp32), so that a scale and its reciprocal are worked out for 16 values at once. A warp takes
+// eight blocks.
+template <bool F32>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantParams p) {
-  constexpr int U = 4;
-  const int lane = threadIdx.x & 31;
-  const long long groups = (p.width + kBlock - 1) / kBlock;
-  const long long blocks = p.rows * groups;
-  const long long first = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * U;
+  constexpr int U = 2, PER = F32 ? 4 : 8, RUNS = 16 / PER;
+  const int lane = threadIdx.x & 31, sub = lane & 7;
+  const uint32_t groups = (uint32_t)((p.width + kBlock - 1) / kBlock);
+  const uint32_t blocks = (uint32_t)p.rows * groups;  // below 2^31: checked by the caller
+  const uint32_t first = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * (4 * U) + (lane >> 3);
   dependents_may_start();
   prior_kernel_done();
-  float v[U][4];
-  long long row[U], left[U];
-  int group[U];
+  uint4 raw[U][RUNS];
+  uint32_t row[U];
+  int col[U];  // of the block
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const long long b = first + i;
-    row[i] = b / groups;
-    group[i] = (int)(b - row[i] * groups);
-    const long long col = (long long)group[i] * kBlock + 4 * lane;
-    left[i] = b < blocks ? p.width - col : 0;
-    load4<F32, VEC>(p.x, row[i] * p.ld_x + col, left[i], v[i]);
+  for (int u = 0; u < U; ++u) {
+    const uint32_t b = first + 4 * u;
+    row[u] = b / groups;
+    col[u] = (int)(b - row[u] * groups) * kBlock;
+    const int es = F32 ? 4 : 2;
+    const uint8_t* from = static_cast<const uint8_t*>(p.x) + ((long long)row[u] * p.ld_x + col[u]) * es;
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k) {
+      const int c = PER * (8 * k + sub);
+      raw[u][k] = make_uint4(0u, 0u, 0u, 0u);
+      if (b < blocks && col[u] + c < p.width) raw[u][k] = __ldcs(reinterpret_cast<const uint4*>(from + c * es));
+    }
   }
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    if (first + i >= blocks) break;
-    const uint32_t top = __reduce_max_sync(
-        0xffffffffu, max(max(magnitude(v[i][0]), magnitude(v[i][1])), max(magnitude(v[i][2]), magnitude(v[i][3]))));
+  for (int u = 0; u < U; ++u) {
+    const uint32_t b = first + 4 * u;
+    uint32_t top = 0u;
+    float v[16];
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k) {
+      const uint32_t w[4] = {raw[u][k].x, raw[u][k].y, raw[u][k].z, raw[u][k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (F32) {
+          v[4 * k + e] = __uint_as_float(w[e]);
+          top = max(top, w[e] & 0x7fffffffu);
+        } else {
+          v[8 * k + 2 * e] = bf16_lo(w[e]);
+          v[8 * k + 2 * e + 1] = bf16_hi(w[e]);
+          top = __vmaxu2(top, w[e] & 0x7fff7fffu);  // the two halves apart
+        }
+      }
+    }
+    if constexpr (!F32) top = max(top << 16, top & 0xffff0000u);
+#pragma unroll
+    for (int o = 4; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (b >= blocks) continue;
     const float scale = e4m3_scale(top);
-    if (lane == 0) p.scales[first + i] = scale;
-    store4<VEC>(p.y + row[i] * p.ld_y + (long long)group[i] * kBlock + 4 * lane, left[i], quantize4(Quotient(scale), v[i]));
+    const Quotient by(scale);
+    if (sub == 0) p.scales[b] = scale;
+    uint8_t* to = p.y + (long long)row[u] * p.ld_y + col[u];
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k) {
+      const int c = PER * (8 * k + sub);
+      if (col[u] + c >= p.width) continue;
+      const float four[4] = {v[PER * k], v[PER * k + 1], v[PER * k + 2], v[PER * k + 3]};
+      const uint32_t lo = quantize4(by, four);
+      if constexpr (F32) {
+        *reinterpret_cast<uint32_t*>(to + c) = lo;
+      } else {
+        const float more[4] = {v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]};
+        *reinterpret_cast<uint2*>(to + c) = make_uint2(lo, quantize4(by, more));
+      }
+    }
   }
 }
 
-// One CTA per tile of 128 x 128. TILE: one scale for all of it. VEC as above; VEC_T: yt's rows start
-// on 16 bytes.
-template <bool F32, bool TILE, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) quantize_tile_kernel(const QuantParams p, int vec_t) {
-  __shared__ __align__(16) uint8_t turned[kBlock * kBlock];
-  __shared__ __align__(16) uint32_t tops[kThreads / 32][kBlock];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long tiles_w = (p.width + kBlock - 1) / kBlock, tiles_r = (p.rows + kBlock - 1) / kBlock;
-  const long long tr = blockIdx.x / tiles_w, tc = blockIdx.x - tr * tiles_w;
-  const long long row0 = tr * kBlock + 16 * warp, col = tc * kBlock + 4 * lane;
+// Other rows: one warp per row and 128 columns, four single values per lane.
+template <bool F32>
+__global__ void __launch_bounds__(kThreads) quantize_any_rows_kernel(const QuantParams p) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t groups = (uint32_t)((p.width + kBlock - 1) / kBlock);
+  const uint32_t blocks = (uint32_t)p.rows * groups;
+  const uint32_t b = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   dependents_may_start();
   prior_kernel_done();
-  float v[16][4];
+  if (b >= blocks) return;
+  const uint32_t row = b / groups;
+  const int col = (int)(b - row * groups) * kBlock + lane;
+  float v[4];
+  uint32_t top = 0u;
 #pragma unroll
-  for (int r = 0; r < 16; ++r)
-    load4<F32, VEC>(p.x, (row0 + r) * p.ld_x + col, row0 + r < p.rows ? p.width - col : 0, v[r]);
+  for (int e = 0; e < 4; ++e) {
+    v[e] = 0.f;
+    if (col + 32 * e < p.width) {
+      const long long at = (long long)row * p.ld_x + col + 32 * e;
+      v[e] = F32 ? static_cast<const float*>(p.x)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.x)[at]);
+    }
+    top = max(top, magnitude(v[e]));
+  }
+  const float scale = e4m3_scale(__reduce_max_sync(0xffffffffu, top));
+  if (lane == 0) p.scales[b] = scale;
+  const uint32_t q = quantize4(Quotient(scale), v);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (col + 32 * e < p.width) p.y[(long long)row * p.ld_y + col + 32 * e] = (uint8_t)(q >> (8 * e));
+}
 
-  uint32_t top[4] = {0u, 0u, 0u, 0u};  // of this lane's columns over this warp's rows
+// The scale and the constants of a quotient by it, worked out once for a row or column of a tile.
+struct __align__(16) Divisor {
+  float up, inv, sc, scale;
+};
+__device__ __forceinline__ Divisor divisor(uint32_t top) {
+  const float scale = e4m3_scale(top);
+  const Quotient by(scale);
+  return {by.up, by.inv, by.sc, scale};
+}
+__device__ __forceinline__ Quotient quotient(const Divisor& d) {
+  Quotient by(1.f);
+  by.up = d.up, by.inv = d.inv, by.sc = d.sc;
+  return by;
+}
+
+// One CTA per tile of 128 x 128. TILE: one scale for all of it. VEC: the width is a multiple of 4 and every
+// row starts on 16 (fp32) or 8 (bf16) bytes, in y on 4. A warp holds 16 rows, a lane four columns of
+// them as they are stored; the rows' and columns' largest values meet in shared memory, where one
+// thread each makes the divisors. vec_t: yt's rows start on 16 bytes.
+template <bool F32, bool TILE, bool VEC>
+__global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) quantize_tile_kernel(const QuantParams p, int vec_t) {
+  __shared__ __align__(16) uint8_t turned[kBlock * kBlock];
+  __shared__ __align__(16) uint32_t col_tops[kThreads / 32][kBlock];
+  __shared__ uint32_t row_tops[kBlock];
+  __shared__ Divisor row_div[kBlock], col_div[kBlock];
+  constexpr int WORDS = F32 ? 4 : 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t tiles_w = (uint32_t)((p.width + kBlock - 1) / kBlock), tiles_r = (uint32_t)((p.rows + kBlock - 1) / kBlock);
+  const uint32_t tr = blockIdx.x / tiles_w, tc = blockIdx.x - tr * tiles_w;
+  const long long row0 = (long long)tr * kBlock + 16 * warp, col = (long long)tc * kBlock + 4 * lane;
+  const int left = (int)min(p.width - col, 4ll), rows_left = (int)min(p.rows - row0, 16ll);
+  dependents_may_start();
+  prior_kernel_done();
+  uint32_t raw[16][WORDS];
 #pragma unroll
-  for (int r = 0; r < 16; ++r)
+  for (int r = 0; r < 16; ++r) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top[e] = max(top[e], magnitude(v[r][e]));
+    for (int e = 0; e < WORDS; ++e) raw[r][e] = 0u;
+    if (r >= rows_left || left <= 0) continue;
+    const long long at = (row0 + r) * p.ld_x + col;
+    if constexpr (VEC && F32) {
+      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(static_cast<const float*>(p.x) + at));
+      raw[r][0] = u.x, raw[r][1] = u.y, raw[r][2] = u.z, raw[r][3] = u.w;
+    } else if constexpr (VEC) {
+      const uint2 u = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.x) + at));
+      raw[r][0] = u.x, raw[r][1] = u.y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < left) {
+          if constexpr (F32) raw[r][e] = static_cast<const uint32_t*>(p.x)[at + e];
+          else raw[r][e >> 1] |= (uint32_t)static_cast<const uint16_t*>(p.x)[at + e] << (16 * (e & 1));
+        }
+    }
+  }
+  auto four = [&](int r, float (&v)[4]) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(raw[r][e]);
+    } else {
+      v[0] = bf16_lo(raw[r][0]), v[1] = bf16_hi(raw[r][0]), v[2] = bf16_lo(raw[r][1]), v[3] = bf16_hi(raw[r][1]);
+    }
+  };
+  auto one = [&](int r, int e) {
+    if constexpr (F32) return __uint_as_float(raw[r][e]);
+    else return (e & 1) ? bf16_hi(raw[r][e >> 1]) : bf16_lo(raw[r][e >> 1]);
+  };
+
+  // largest magnitudes, as bits: of each row (not for TILE), and of this lane's columns
+  uint32_t tops[WORDS];
+#pragma unroll
+  for (int e = 0; e < WORDS; ++e) tops[e] = 0u;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    uint32_t of_row = 0u;
+#pragma unroll
+    for (int e = 0; e < WORDS; ++e) {
+      const uint32_t m = raw[r][e] & (F32 ? 0x7fffffffu : 0x7fff7fffu);
+      tops[e] = F32 ? max(tops[e], m) : __vmaxu2(tops[e], m);
+      of_row = F32 ? max(of_row, m) : __vmaxu2(of_row, m);
+    }
+    if constexpr (!TILE) {
+      if constexpr (!F32) of_row = max(of_row << 16, of_row & 0xffff0000u);
+      of_row = __reduce_max_sync(0xffffffffu, of_row);
+      if (lane == r) row_tops[16 * warp + r] = of_row;
+    }
+  }
+  uint32_t top[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    top[e] = F32 ? tops[F32 ? e : 0] : (e & 1) ? tops[e >> 1] & 0xffff0000u : tops[e >> 1] << 16;
   if constexpr (TILE) {
     const uint32_t t = __reduce_max_sync(0xffffffffu, max(max(top[0], top[1]), max(top[2], top[3])));
-    if (lane == 0) tops[0][warp] = t;
-    __syncthreads();
-    const float scale = e4m3_scale(__reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? tops[0][lane] : 0u));
-    const Quotient by(scale);
+    if (lane == 0) row_tops[warp] = t;
+  } else {
+    *reinterpret_cast<uint4*>(&col_tops[warp][4 * lane]) = make_uint4(top[0], top[1], top[2], top[3]);
+  }
+  __syncthreads();
+  if constexpr (TILE) {
+    const Quotient by(e4m3_scale(__reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? row_tops[lane] : 0u)));
     if (threadIdx.x == 0) {
-      if (p.y) p.scales[tr * tiles_w + tc] = scale;
-      if (p.yt) p.scales_t[tc * tiles_r + tr] = scale;
+      const float scale = e4m3_scale(max(max(max(row_tops[0], row_tops[1]), max(row_tops[2], row_tops[3])),
+                                         max(max(row_tops[4], row_tops[5]), max(row_tops[6], row_tops[7]))));
+      if (p.y) p.scales[(long long)tr * tiles_w + tc] = scale;
+      if (p.yt) p.scales_t[(long long)tc * tiles_r + tr] = scale;
     }
     uint32_t q[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      q[r] = quantize4(by, v[r]);
-      if (p.y && row0 + r < p.rows) store4<VEC>(p.y + (row0 + r) * p.ld_y + col, p.width - col, q[r]);
+      float v[4];
+      four(r, v);
+      q[r] = quantize4(by, v);
+      if (p.y && r < rows_left) store4<VEC>(p.y + (row0 + r) * p.ld_y + col, left, q[r]);
     }
     if (!p.yt) return;
 #pragma unroll
@@ -161,34 +284,37 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_tile_kernel(const QuantP
           make_uint4(w[0], w[1], w[2], w[3]);
     }
   } else {
+    const int i = threadIdx.x & (kBlock - 1);
+    if (threadIdx.x < kBlock) {
+      const Divisor d = divisor(row_tops[i]);
+      row_div[i] = d;
+      if (p.y && (long long)tr * kBlock + i < p.rows) p.scales[((long long)tr * kBlock + i) * tiles_w + tc] = d.scale;
+    } else {
+      uint32_t t = col_tops[0][i];
+#pragma unroll
+      for (int k = 1; k < kThreads / 32; ++k) t = max(t, col_tops[k][i]);
+      const Divisor d = divisor(t);
+      col_div[i] = d;
+      if ((long long)tc * kBlock + i < p.width) p.scales_t[((long long)tc * kBlock + i) * tiles_r + tr] = d.scale;
+    }
+    __syncthreads();
     if (p.y) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        if (row0 + r >= p.rows) break;
-        const uint32_t t = __reduce_max_sync(
-            0xffffffffu, max(max(magnitude(v[r][0]), magnitude(v[r][1])), max(magnitude(v[r][2]), magnitude(v[r][3]))));
-        const float scale = e4m3_scale(t);
-        if (lane == 0) p.scales[(row0 + r) * tiles_w + tc] = scale;
-        store4<VEC>(p.y + (row0 + r) * p.ld_y + col, p.width - col, quantize4(Quotient(scale), v[r]));
+        if (r >= rows_left) break;
+        float v[4];
+        four(r, v);
+        store4<VEC>(p.y + (row0 + r) * p.ld_y + col, left, quantize4(quotient(row_div[16 * warp + r]), v));
       }
-    }
-    *reinterpret_cast<uint4*>(&tops[warp][4 * lane]) = make_uint4(top[0], top[1], top[2], top[3]);
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kThreads / 32; ++k) {
-      const uint4 t = *reinterpret_cast<const uint4*>(&tops[k][4 * lane]);
-      top[0] = max(top[0], t.x), top[1] = max(top[1], t.y), top[2] = max(top[2], t.z), top[3] = max(top[3], t.w);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float scale = e4m3_scale(top[e]);
-      const Quotient by(scale);
-      if (warp == 0 && col + e < p.width) p.scales_t[(col + e) * tiles_r + tr] = scale;
+      const Quotient by = quotient(col_div[4 * lane + e]);
       uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float four[4] = {v[4 * k][e], v[4 * k + 1][e], v[4 * k + 2][e], v[4 * k + 3][e]};
-        w[k] = quantize4(by, four);
+        const float v[4] = {one(4 * k, e), one(4 * k + 1, e), one(4 * k + 2, e), one(4 * k + 3, e)};
+        w[k] = quantize4(by, v);
       }
       *reinterpret_cast<uint4*>(turned + (4 * lane + e) * kBlock + ((warp ^ (lane & 7)) << 4)) =
           make_uint4(w[0], w[1], w[2], w[3]);
@@ -199,10 +325,10 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_tile_kernel(const QuantP
 #pragma unroll
   for (int i = 0; i < kBlock / 32; ++i) {
     const int c = (threadIdx.x >> 3) + 32 * i, chunk = threadIdx.x & 7;
-    const long long row = tr * kBlock + 16 * chunk;
-    if (tc * kBlock + c >= p.width || row >= p.rows) continue;
+    const long long row = (long long)tr * kBlock + 16 * chunk;
+    if ((long long)tc * kBlock + c >= p.width || row >= p.rows) continue;
     const uint8_t* from = turned + c * kBlock + ((chunk ^ ((c >> 2) & 7)) << 4);
-    uint8_t* to = p.yt + (tc * kBlock + c) * p.ld_yt + row;
+    uint8_t* to = p.yt + ((long long)tc * kBlock + c) * p.ld_yt + row;
     if (vec_t && row + 16 <= p.rows) {
       *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
     } else {
@@ -212,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 2) quantize_tile_kernel(const QuantP
 }
 
 template <bool F32, bool VEC>
-tsp_status launch(const QuantParams& p, int block, bool vec_t, cudaStream_t s) {
+tsp_status launch(const QuantParams& p, int block, bool vec16, bool vec_t, cudaStream_t s) {
   const long long tiles = ((p.rows + kBlock - 1) / kBlock) * ((p.width + kBlock - 1) / kBlock);
   cudaError_t e;
   if (block == kBlock) {
@@ -220,9 +346,11 @@ tsp_status launch(const QuantParams& p, int block, bool vec_t, cudaStream_t s) {
   } else if (p.yt) {
     e = launch_early(quantize_tile_kernel<F32, false, VEC>, (unsigned)tiles, kThreads, 0, s, p, (int)vec_t);
   } else {
-    const long long per_cta = kThreads / 32 * 4;
-    const long long ctas = (p.rows * ((p.width + kBlock - 1) / kBlock) + per_cta - 1) / per_cta;
-    e = launch_early(quantize_rows_kernel<F32, VEC>, (unsigned)ctas, kThreads, 0, s, p);
+    const long long blocks = p.rows * ((p.width + kBlock - 1) / kBlock);
+    const long long per_cta = kThreads / 32 * (vec16 ? 8 : 1);
+    const unsigned ctas = (unsigned)((blocks + per_cta - 1) / per_cta);
+    if (vec16) e = launch_early(quantize_rows_kernel<F32>, ctas, kThreads, 0, s, p);
+    else e = launch_early(quantize_any_rows_kernel<F32>, ctas, kThreads, 0, s, p);
   }
   return e == cudaSuccess ? TSP_OK : cuda_fail(e, "quantize: launch");
 }
@@ -259,18 +387,21 @@ tsp_status tsp_quantize_e4m3(int64_t rows, int64_t width, const void* x, int x_f
     return fail(TSP_ERR_UNSUPPORTED, n + ": row stride too large");
   if (x == y || x == yt || (y && y == yt) || (scales && scales == scales_t))
     return fail(TSP_ERR_INVALID_ARG, n + ": an output aliases another buffer");
-  // one CTA per 32 groups of a row, or per tile
+  // blocks are counted in 32 bits, and a tile is a CTA
   const int64_t groups = (width + kBlock - 1) / kBlock;
-  if (rows * groups > 32 * most || ((rows + kBlock - 1) / kBlock) * groups > most)
+  if (rows * groups > most || ((rows + kBlock - 1) / kBlock) * groups > most)
     return fail(TSP_ERR_UNSUPPORTED, n + ": too many blocks");
   const QuantParams p{rows, width, x, ld_x, y, ld_y, scales, yt, ld_yt, scales_t};
   // 4 columns at a time where every row of x and y starts on their boundary
   const bool vec = width % 4 == 0 && ld_x % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * es) == 0 &&
                    (!y || (ld_y % 4 == 0 && reinterpret_cast<uintptr_t>(y) % 4 == 0));
+  // or, rows alone, 16 bytes of x and as many values of y
+  const bool vec16 = width % (16 / es) == 0 && ld_x % (16 / es) == 0 && al16(x) && ld_y % 8 == 0 &&
+                     reinterpret_cast<uintptr_t>(y) % 8 == 0;
   const bool vec_t = ld_yt % 16 == 0 && al16(yt);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (x_f32) return vec ? launch<true, true>(p, block, vec_t, s) : launch<true, false>(p, block, vec_t, s);
-  return vec ? launch<false, true>(p, block, vec_t, s) : launch<false, false>(p, block, vec_t, s);
+  if (x_f32) return vec ? launch<true, true>(p, block, vec16, vec_t, s) : launch<true, false>(p, block, vec16, vec_t, s);
+  return vec ? launch<false, true>(p, block, vec16, vec_t, s) : launch<false, false>(p, block, vec16, vec_t, s);
   TSP_GUARD_END
 }
 
