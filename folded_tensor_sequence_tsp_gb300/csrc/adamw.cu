@@ -7,7 +7,8 @@
 //
 // Bound: HBM. Every value is read once and written once, clipping included (the factor is formed
 // from the norm here, so the gradients are not scaled in a pass of their own). As in grad_clip.cu
-// the list travels in the kernels' parameters, cut into chunks that persistent CTAs take in turn.
+// the list travels in the kernels' parameters, cut into chunks of a CTA each (persistent CTAs that take
+// them in turn: 202M weights with masters 941 us, one CTA each 866).
 //
 // Roundings. All arithmetic is fp32 on the values that the states stand for. 8-bit states are
 // rounded stochastically, up with the probability of the distance from the lower neighbour: one
@@ -74,6 +75,12 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   return x ^ (x >> 16);
 }
 
+// 32 random bits for an element; high: of the upper half of its number, the same for all of a chunk.
+__device__ __forceinline__ uint32_t random_bits(uint32_t key, uint32_t element, uint32_t high) {
+  return mix((element ^ key) + high);
+}
+__device__ __forceinline__ uint32_t high_bits(unsigned long long chunk_at) { return (uint32_t)(chunk_at >> 32) * 0x9E3779B1u; }
+
 __device__ __forceinline__ void make_shared(const Step& a, Shared& s) {
   const long long t = a.device_t ? *a.device_t : a.t;
   s.rate = a.rate, s.root = a.root, s.shrink = a.shrink;
@@ -93,13 +100,41 @@ __device__ __forceinline__ void make_shared(const Step& a, Shared& s) {
   }
 }
 
-// |q| <= 448 to a neighbouring e4m3 value: 16 random bits of the 20 that the value lacks are added
-// before they are cut off. Below 2^-6 the values are 2^-9 apart.
-__device__ __forceinline__ float stochastic8(float q, uint32_t r16) {
-  const float a = fabsf(q);
-  const float normal = __uint_as_float((__float_as_uint(a) + (r16 << 4)) & 0xFFF00000u);
-  const float small = floorf(fmaf(a, 512.f, (float)r16 * (1.f / 65536.f))) * (1.f / 512.f);
-  return copysignf(fminf(a >= 0.015625f ? normal : small, kE4m3Max), q);
+// The byte `b` of each of four words.
+__device__ __forceinline__ uint32_t bytes_of(const uint32_t (&x)[4], int b) {
+  return __byte_perm(__byte_perm(x[0], x[1], b | ((4 + b) << 4)), __byte_perm(x[2], x[3], b | ((4 + b) << 4)), 0x5410);
+}
+
+// The e4m3 codes of four quotients x * inv, |x * inv| <= 448 but for its rounding, each rounded to a neighbouring
+// value: 16 random bits of the 20 that a value lacks are added before they are cut off. Below 2^-6 the
+// values are 2^-9 apart: floor(512 |q| + u), the floor by an addition that rounds down. Conversions between
+// integers and floating point, and roundings by instructions of their own, run at a fourth of this
+// arithmetic's rate or less. SQUARES: x is not negative, small quotients are common (not looked for), and
+// what is above zero stays so.
+template <bool SQUARES>
+__device__ __forceinline__ uint32_t stochastic8(const float (&x)[4], float inv, const uint32_t (&r16)[4]) {
+  uint32_t code[4], q[4];  // the code in the third byte
+  uint32_t least = 0xffffffffu;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float product = x[e] * inv;
+    q[e] = __float_as_uint(fminf(SQUARES ? product : fabsf(product), kE4m3Max));
+    code[e] = (q[e] >> 4) + r16[e] - (120u << 19);
+    least = min(least, q[e]);
+  }
+  if (SQUARES || least < 0x3c800000u) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float u = __uint_as_float(0x3f800000u | (r16[e] << 7)) - 1.f;  // r16 / 65536
+      uint32_t c = __float_as_uint(__fadd_rd(fmaf(__uint_as_float(q[e]), 512.f, u), 8388608.f)) & 15u;
+      if (SQUARES) c = max(c, min(__float_as_uint(x[e]), 1u));
+      if (q[e] < 0x3c800000u) code[e] = c << 16;
+    }
+  }
+  const uint32_t codes = bytes_of(code, 2);
+  if (SQUARES) return codes;
+  const uint32_t bits[4] = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+  return codes | (bytes_of(bits, 3) & 0x80808080u);
 }
 
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
@@ -107,15 +142,14 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
   return __half22float2(__half2(h));
 }
 
-// Four elements of a tensor per thread: consecutive ones where everything is aligned, else a
-// warp's width apart.
-template <bool VEC>
+// Four elements of a tensor per thread: consecutive ones where everything is aligned (VEC), else a
+// warp's width apart. FULL: all of them exist.
+template <bool VEC, bool FULL>
 struct Four {
-  unsigned long long at;  // of the first
-  int n;                  // elements that exist from the block's start
-  int lane;
-  __device__ __forceinline__ bool has(int e) const { return (VEC ? 4 * lane + e : lane + 32 * e) < n; }
-  __device__ __forceinline__ unsigned long long of(int e) const { return VEC ? at + e : at + 32 * e; }
+  unsigned long long at;  // the first
+  int left;               // elements from it to the end of the chunk (FULL: enough)
+  __device__ __forceinline__ bool has(int e) const { return FULL || (VEC ? e : 32 * e) < left; }
+  __device__ __forceinline__ unsigned long long of(int e) const { return at + (VEC ? e : 32 * e); }
 
   __device__ __forceinline__ void load32(const void* p, float (&x)[4]) const {
     const float* f = static_cast<const float*>(p);
@@ -149,10 +183,9 @@ struct Four {
     }
     const float2 lo = from_e4m3x2(u & 0xffffu), hi = from_e4m3x2(u >> 16);
     x[0] = lo.x * scale, x[1] = lo.y * scale, x[2] = hi.x * scale, x[3] = hi.y * scale;
-    // what does not exist is zero whatever the scale
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (!has(e)) x[e] = 0.f;
+      if (!has(e)) x[e] = 0.f;  // whatever the scale
   }
   __device__ __forceinline__ void store32(void* p, const float (&x)[4]) const {
     float* f = static_cast<float*>(p);
@@ -186,79 +219,97 @@ struct Four {
   }
 };
 
-__device__ __forceinline__ float block_scale(const float (&x)[4]) {
+__device__ __forceinline__ uint32_t largest(const float (&x)[4]) {
   uint32_t top = 0u;
 #pragma unroll
   for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(fabsf(x[e])));
-  return e4m3_scale(__reduce_max_sync(0xffffffffu, top));
+  return top;
 }
 
-// 128 elements of a tensor per warp and pass: the block of an 8-bit state.
-template <int N, bool STATE8, bool VEC>
+// m, v and p from the gradient g. Every product of m and v is rounded by itself: a state's bits follow from
+// the formula alone, and with them the border at which its 8 bits are rounded up. The update takes an
+// approximate root and quotient, off by two units each; the root of a v below 2^-126 is 0 (it would be under
+// 1.1e-19, far below any eps).
+__device__ __forceinline__ void update(const Step& a, const Shared& s, float (&p)[4], const float (&g)[4], float (&m)[4],
+                                       float (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float x = __fmul_rn(g[e], s.factor);
+    m[e] = __fadd_rn(__fmul_rn(a.beta1, m[e]), __fmul_rn(a.one_beta1, x));
+    v[e] = __fadd_rn(__fmul_rn(a.beta2, v[e]), __fmul_rn(a.one_beta2, __fmul_rn(x, x)));
+    float root;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(v[e]));
+    float quotient;
+    asm("div.approx.ftz.f32 %0, %1, %2;" : "=f"(quotient) : "f"(s.rate * m[e]), "f"(fmaf(root, s.root, a.eps)));
+    p[e] -= fmaf(s.shrink, p[e], quotient);
+  }
+}
+
+template <int N, class F>
+__device__ __forceinline__ void load_weight(const Table<N>& t, int i, const F& f, float (&p)[4], float (&g)[4]) {
+  if (t.kind[i] & PARAM_BF16) f.load16(t.p[i], p);
+  else f.load32(t.p[i], p);
+  if (t.kind[i] & GRAD_BF16) f.load16(t.g[i], g);
+  else f.load32(t.g[i], g);
+}
+
+template <int N, class F>
+__device__ __forceinline__ void store_weight(const Table<N>& t, int i, const F& f, uint32_t key, uint32_t high,
+                                             float (&p)[4]) {
+  if (t.kind[i] & PARAM_BF16) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t r = random_bits(key, (uint32_t)f.of(e), high), u = __float_as_uint(p[e]);
+      if ((u & 0x7f800000u) != 0x7f800000u) p[e] = __uint_as_float((u + (r & 0xffffu)) & 0xffff0000u);
+    }
+    f.store16(t.p[i], p);
+  } else {
+    f.store32(t.p[i], p);
+    if (t.kind[i] & MASTER) f.store16(t.p16[i], p);
+  }
+}
+
+// A chunk, 128 elements per warp and pass. FULL: it is whole. scales: of the chunk's m and v, old ones in, new
+// ones out.
+template <int N, bool STATE8, bool VEC, bool FULL>
 __device__ __forceinline__ void update_chunk(const Table<N>& t, int i, unsigned long long chunk_at, int n,
-                                             const Step& a, const Shared& s) {
+                                             const Step& a, const Shared& s, float (*scales)[kChunk / 128]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned char kind = t.kind[i];
   const uint32_t tensor_key = mix(s.key + (unsigned int)(t.index0 + i));
-  const uint32_t state_key = mix(tensor_key), weight_key = mix(tensor_key + 1u);
-  for (int b = warp * 128; b < n; b += kThreads / 32 * 128) {
-    Four<VEC> f;
-    f.lane = lane;
-    f.n = n - b;
-    f.at = chunk_at + b + (VEC ? 4 * lane : lane);
-    const unsigned long long block = (chunk_at + b) >> 7;
+  const uint32_t state_key = mix(tensor_key), weight_key = mix(tensor_key + 1u), high = high_bits(chunk_at);
+#pragma unroll 1
+  for (int pass = 0; pass < kChunk / (4 * kThreads); ++pass) {
+    const int b = warp * 128 + pass * 4 * kThreads;
+    if (!FULL && b >= n) break;
+    const int first = b + (VEC ? 4 * lane : lane);
+    const Four<VEC, FULL> f{chunk_at + first, n - first};
+    const int block = b >> 7;
     float p[4], g[4], m[4], v[4];
-    if (kind & PARAM_BF16) f.load16(t.p[i], p);
-    else f.load32(t.p[i], p);
-    if (kind & GRAD_BF16) f.load16(t.g[i], g);
-    else f.load32(t.g[i], g);
+    load_weight(t, i, f, p, g);
     if constexpr (STATE8) {
-      f.load8(t.m[i], t.ms[i][block], m);
-      f.load8(t.v[i], t.vs[i][block], v);
+      f.load8(t.m[i], scales[0][block], m);
+      f.load8(t.v[i], scales[1][block], v);
     } else {
       f.load32(t.m[i], m);
       f.load32(t.v[i], v);
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // every product rounded by itself: a state's bits follow from the formula alone, and with
-      // them the border at which its 8 bits are rounded up
-      const float x = __fmul_rn(g[e], s.factor);
-      m[e] = __fadd_rn(__fmul_rn(a.beta1, m[e]), __fmul_rn(a.one_beta1, x));
-      v[e] = __fadd_rn(__fmul_rn(a.beta2, v[e]), __fmul_rn(a.one_beta2, __fmul_rn(x, x)));
-      float root;
-      asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v[e]));
-      p[e] -= fmaf(s.shrink, p[e], __fdividef(s.rate * m[e], fmaf(root, s.root, a.eps)));
-    }
-    if (kind & PARAM_BF16) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const unsigned long long el = f.of(e);
-        const uint32_t r = mix(((uint32_t)el ^ weight_key) + (uint32_t)(el >> 32) * 0x9E3779B1u);
-        const uint32_t u = __float_as_uint(p[e]);
-        if ((u & 0x7f800000u) != 0x7f800000u) p[e] = __uint_as_float((u + (r & 0xffffu)) & 0xffff0000u);
-      }
-      f.store16(t.p[i], p);
-    } else {
-      f.store32(t.p[i], p);
-      if (kind & MASTER) f.store16(t.p16[i], p);
-    }
+    update(a, s, p, g, m, v);
+    store_weight(t, i, f, weight_key, high, p);
     if constexpr (STATE8) {
-      const float m_scale = block_scale(m), v_scale = block_scale(v);
-      const float m_inv = __frcp_rn(m_scale), v_inv = __frcp_rn(v_scale);
+      const float m_scale = e4m3_scale(__reduce_max_sync(0xffffffffu, largest(m)));
+      const float v_scale = e4m3_scale(__reduce_max_sync(0xffffffffu, largest(v)));
+      uint32_t low[4], up[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const unsigned long long el = f.of(e);
-        const uint32_t r = mix(((uint32_t)el ^ state_key) + (uint32_t)(el >> 32) * 0x9E3779B1u);
-        m[e] = stochastic8(m[e] * m_inv, r & 0xffffu);
-        const float q = stochastic8(v[e] * v_inv, r >> 16);
-        v[e] = v[e] > 0.f ? fmaxf(q, 0.001953125f) : q;
+        const uint32_t r = random_bits(state_key, (uint32_t)f.of(e), high);
+        low[e] = r & 0xffffu;
+        up[e] = r >> 16;
       }
-      f.store8(t.m[i], to_e4m3x4(m[0], m[1], m[2], m[3]));
-      f.store8(t.v[i], to_e4m3x4(v[0], v[1], v[2], v[3]));
-      if (lane == 0) {
-        t.ms[i][block] = m_scale;
-        t.vs[i][block] = v_scale;
+      f.store8(t.m[i], stochastic8<false>(m, __frcp_rn(m_scale), low));
+      f.store8(t.v[i], stochastic8<true>(v, __frcp_rn(v_scale), up));
+      if (lane == 0) {  // read above by this warp alone
+        scales[0][block] = m_scale;
+        scales[1][block] = v_scale;
       }
     } else {
       f.store32(t.m[i], m);
@@ -267,25 +318,42 @@ __device__ __forceinline__ void update_chunk(const Table<N>& t, int i, unsigned 
   }
 }
 
+// Six CTAs per SM: with 56 registers and four of them 8-bit states take 646 us instead of 632.
 template <int N, bool STATE8>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<N> t,
+__global__ void __launch_bounds__(kThreads, 6) adamw_kernel(const __grid_constant__ Table<N> t,
                                                          const __grid_constant__ Step a) {
   __shared__ Shared shared;
   if (threadIdx.x == 0) make_shared(a, shared);
   __syncthreads();
   const Shared s = shared;
-  const unsigned int chunks = t.first[t.count];
-  for (unsigned int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    int lo = 0, hi = t.count - 1;
-    while (lo < hi) {  // the last tensor whose first chunk is not behind c
-      const int mid = (lo + hi + 1) >> 1;
-      if (t.first[mid] <= c) lo = mid;
-      else hi = mid - 1;
+  int lo = 0, hi = t.count - 1;
+  while (lo < hi) {  // the last tensor whose first chunk is not behind this one
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first[mid] <= blockIdx.x) lo = mid;
+    else hi = mid - 1;
+  }
+  const unsigned long long at = (unsigned long long)(blockIdx.x - t.first[lo]) * kChunk;
+  const int n = (int)min((unsigned long long)kChunk, t.n[lo] - at);
+  // The chunk's scales are read and written by one warp each, a line at a time. Where each warp read and wrote its
+  // blocks' own, lines were read while their neighbours' values were on their way to them, and a step of
+  // 202M weights with masters took 860 us instead of 632.
+  __shared__ float scales[2][kChunk / 128];
+  float* scale = nullptr;
+  if constexpr (STATE8) {
+    const int w = threadIdx.x >> 5, block = threadIdx.x & 31;
+    static_assert(kChunk / 128 == 32, "a lane for each block");
+    if (w < 2 && block * 128 < n) {
+      scale = (w ? t.vs : t.ms)[lo] + (at >> 7) + block;
+      scales[w][block] = *scale;
     }
-    const unsigned long long at = (unsigned long long)(c - t.first[lo]) * kChunk;
-    const int n = (int)min((unsigned long long)kChunk, t.n[lo] - at);
-    if (t.kind[lo] & ALIGNED) update_chunk<N, STATE8, true>(t, lo, at, n, a, s);
-    else update_chunk<N, STATE8, false>(t, lo, at, n, a, s);
+    __syncthreads();
+  }
+  if (!(t.kind[lo] & ALIGNED)) update_chunk<N, STATE8, false, false>(t, lo, at, n, a, s, scales);
+  else if (n == kChunk) update_chunk<N, STATE8, true, true>(t, lo, at, n, a, s, scales);
+  else update_chunk<N, STATE8, true, false>(t, lo, at, n, a, s, scales);
+  if constexpr (STATE8) {
+    __syncthreads();
+    if (scale) *scale = scales[threadIdx.x >> 5][threadIdx.x & 31];
   }
 }
 
@@ -330,7 +398,7 @@ tsp_status check_list(const char* what, const List& l) {
         off(l.master(i), 4) || off(l.m[i], sa) || off(l.v[i], sa) || (l.bits == 8 && (off(l.ms[i], 4) || off(l.vs[i], 4))))
       return fail(TSP_ERR_INVALID_ARG, w + ": tensor not aligned to its element");
   }
-  if (total > (1ll << 31)) return fail(TSP_ERR_UNSUPPORTED, w + ": too many elements");
+  if (total >= (1ll << 31)) return fail(TSP_ERR_UNSUPPORTED, w + ": too many elements");
   return TSP_OK;
 }
 
@@ -377,8 +445,7 @@ tsp_status run(const List& l, const Step& a, cudaStream_t s) {
   auto flush = [&](unsigned int chunks) -> tsp_status {
     if (t.count == 0) return TSP_OK;
     t.first[t.count] = chunks;
-    const unsigned int ctas = std::min(chunks, 8u * (unsigned)sm_count());
-    adamw_kernel<N, STATE8><<<ctas, kThreads, 0, s>>>(t, a);
+    adamw_kernel<N, STATE8><<<chunks, kThreads, 0, s>>>(t, a);
     const cudaError_t e = cudaGetLastError();
     t.count = 0;
     return e == cudaSuccess ? TSP_OK : cuda_fail(e, "adamw: launch");
