@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(THREADS, Config<BN, PAIR>::CTAS)
   // needs a fourth of them from shared memory.
   constexpr bool QUAD = COLS && BN >= 64;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // an offset, not a pointer made from a number: the compiler goes on knowing that this is shared memory
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint8_t* s_p = smem;
   uint8_t* s_q = smem + STAGES * P_BYTES;
   uint8_t* s_out = smem + STAGES * cfg::STAGE_BYTES;
@@ -309,24 +310,41 @@ __global__ void __launch_bounds__(THREADS, Config<BN, PAIR>::CTAS)
           ok = __all_sync(0xffffffffu, mbar_wait_short(&scale_empty[slot], phase ^ 1u, wb, SITE_E4M3_PRODUCER));
           if (!ok) break;
           float* to = s_scale + slot * cfg::SCALES + (of_p ? 0 : BM);
-          for (int i = lane; i < count; i += 32) {
-            const long long r = row0 + (of_p || COLS ? i : i * BM);
-            const float* from = base + (min(r, (long long)rows - 1) >> shift) * ld + kb;
+          // of four rows at once, so that eight loads are under way; pairs have few registers here, and wait
+          // for something else
+          constexpr int AT_ONCE = PAIR ? 1 : 4;
+          for (int i0 = lane; i0 < count; i0 += 32 * AT_ONCE) {
+            float4 v[AT_ONCE][KS / 4];
 #pragma unroll
-            for (int k = 0; k < KS; k += 4) {
-              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (vec && kb + k + 4 <= kb1) {
-                v = *reinterpret_cast<const float4*>(from + k);
-              } else {
-                if (kb + k < kb1) v.x = from[k];
-                if (kb + k + 1 < kb1) v.y = from[k + 1];
-                if (kb + k + 2 < kb1) v.z = from[k + 2];
-                if (kb + k + 3 < kb1) v.w = from[k + 3];
+            for (int j = 0; j < AT_ONCE; ++j) {
+              const int i = min(i0 + 32 * j, count - 1);
+              const long long r = row0 + (of_p || COLS ? i : i * BM);
+              const float* from = base + (min(r, (long long)rows - 1) >> shift) * ld + kb;
+#pragma unroll
+              for (int k = 0; k < KS; k += 4) {
+                float4& x = v[j][k / 4];
+                x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (vec && kb + k + 4 <= kb1) {
+                  x = *reinterpret_cast<const float4*>(from + k);
+                } else {
+                  if (kb + k < kb1) x.x = from[k];
+                  if (kb + k + 1 < kb1) x.y = from[k + 1];
+                  if (kb + k + 2 < kb1) x.z = from[k + 2];
+                  if (kb + k + 3 < kb1) x.w = from[k + 3];
+                }
               }
-              to[k * (BM + BN) + i] = v.x;
-              to[(k + 1) * (BM + BN) + i] = v.y;
-              to[(k + 2) * (BM + BN) + i] = v.z;
-              to[(k + 3) * (BM + BN) + i] = v.w;
+            }
+#pragma unroll
+            for (int j = 0; j < AT_ONCE; ++j) {
+              const int i = i0 + 32 * j;
+              if (i >= count) break;
+#pragma unroll
+              for (int k = 0; k < KS; k += 4) {
+                to[k * (BM + BN) + i] = v[j][k / 4].x;
+                to[(k + 1) * (BM + BN) + i] = v[j][k / 4].y;
+                to[(k + 2) * (BM + BN) + i] = v[j][k / 4].z;
+                to[(k + 3) * (BM + BN) + i] = v[j][k / 4].w;
+              }
             }
           }
           __syncwarp();
