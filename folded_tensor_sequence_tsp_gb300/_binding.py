@@ -684,7 +684,7 @@ def _launch(name, device, stream, *args):
         raw = torch._C._cuda_getCurrentRawStream(device)
     else:
         raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if device == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():  # there is a CUDA tensor, so CUDA is initialised
         status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -899,25 +899,36 @@ class TensorList:
 
     def __init__(self, tensors, name, dtypes=_GRAD_TYPES):
         self.n = len(tensors)
-        self.given = [t is not None for t in tensors]
-        some = [t for t in tensors if t is not None]
-        devices = {t.get_device() for t in some}
+        self.given = None  # all of them
+        try:
+            devices = set(map(torch.Tensor.get_device, tensors))
+        except TypeError:  # None among them
+            self.given = [t is not None for t in tensors]
+            devices = {t.get_device() for t in tensors if t is not None}
         if len(devices) > 1 or min(devices, default=0) < 0:
             raise ValueError(f"{name} must be on one CUDA device")
         self.device = devices.pop() if devices else None
-        if not all([t.is_contiguous() for t in some]):
+        some = tensors if self.given is None else [t for t in tensors if t is not None]
+        if not all(map(torch.Tensor.is_contiguous, some)):
             raise ValueError(f"{name} must be contiguous")
-        types = [0 if t is None else dtypes.get(t.dtype, -1) for t in tensors]
+        types = [dtypes.get(t.dtype, -1) for t in some]
         if -1 in types:
             raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}")
-        self.types = array.array("i", types)
-        self.pointers = array.array("q", [0 if t is None else t.data_ptr() for t in tensors])
-        self.sizes = array.array("q", [0 if t is None else t.numel() for t in tensors])
+        values = [list(map(torch.Tensor.data_ptr, some)), list(map(torch.Tensor.numel, some)), types]
+        if self.given is not None:  # zeros in the gaps
+            left = [iter(x) for x in values]
+            values = [[next(x) if g else 0 for g in self.given] for x in left]
+        self.pointers, self.sizes = array.array("q", values[0]), array.array("q", values[1])
+        self.types = array.array("i", values[2])
 
     def like(self, other, name, blocks=False):
         """Check that the tensors hold as many elements as the other list's, or one per 128 of them."""
         want = [-(-n // 128) for n in other.sizes] if blocks else other.sizes
-        if self.n != other.n or any([a != b and given for given, a, b in zip(self.given, self.sizes, want)]):
+        if self.given is None:
+            same = self.sizes == (array.array("q", want) if blocks else want)
+        else:
+            same = self.n == other.n and not any([g and a != b for g, a, b in zip(self.given, self.sizes, want)])
+        if not same:
             raise ValueError(f"{name} must match the weights in number and size")
         if self.device is not None and other.device is not None and self.device != other.device:
             raise ValueError(f"{name} must be on the weights' device")

@@ -29,13 +29,12 @@ constexpr int BK = 128;
 constexpr int THREADS = 384;
 constexpr int EPI_WARPS = 8;
 constexpr uint32_t P_BYTES = BM * BK;
-constexpr int KS = 8;  // blocks of K whose scales are fetched together
 // Row stride of the sums in shared memory: a quarter warp's accesses to two columns' rows hit all banks
 constexpr int PART = BM + 4;
 
 // PAIR: two CTAs on a tile of 256 x BN, each with 128 rows of P, half of Q's in its shared memory, and
 // BN columns of sums.
-template <int BN, bool PAIR>
+template <int BN, bool COLS, bool PAIR>
 struct Config {
   static constexpr uint32_t Q_BYTES = (PAIR ? BN / 2 : BN) * BK;
   static constexpr uint32_t STAGE_BYTES = P_BYTES + Q_BYTES;
@@ -43,8 +42,11 @@ struct Config {
   static constexpr int CTAS = BN <= 32 ? 2 : 1;
   static constexpr int STAGES = PAIR ? 4 : BN == 128 ? 5 : BN == 64 ? 8 : 5;
   static constexpr uint32_t TMEM_COLS = 2 * BN;
-  // scales of some blocks of K: of P's rows, and of Q's rows or of its (one or two) blocks of 128
-  static constexpr int SCALES = KS * (BM + BN);
+  // Scales of KS blocks of K are fetched together, BM + QS for each: of P's rows, and of Q's rows or of its one or
+  // two blocks of 128. (Tile scales, 8192 x 8192 x 4096: 4 blocks 230 us, 8 206 us, 16 205 us, 32 225 us.)
+  static constexpr int KS = COLS ? 8 : 16;
+  static constexpr int QS = COLS ? BN : 4;
+  static constexpr int SCALES = KS * (BM + QS);
   static constexpr size_t SCALE_BYTES = 2 * SCALES * 4;
   static constexpr size_t OUT_BYTES = PAIR ? 65536 : 0;  // a pair's sums on their way out: 32 KB for each warpgroup
   static constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * STAGE_BYTES + OUT_BYTES + SCALE_BYTES + 256;
@@ -100,11 +102,11 @@ __device__ __forceinline__ void put(const Params& p, long long at, float v) {
 // COLS: Q has a scale for every row (a column of the tile), else one for 128 rows.
 // TURNED: P = B and Q = A, C[q][p]; else C[p][q].
 template <int BN, bool COLS, bool TURNED, bool PAIR>
-__global__ void __launch_bounds__(THREADS, Config<BN, PAIR>::CTAS)
+__global__ void __launch_bounds__(THREADS, Config<BN, COLS, PAIR>::CTAS)
     matmul_e4m3_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_c, const Params p) {
-  using cfg = Config<BN, PAIR>;
-  constexpr int STAGES = cfg::STAGES, HALF = BN / 2;
+  using cfg = Config<BN, COLS, PAIR>;
+  constexpr int STAGES = cfg::STAGES, HALF = BN / 2, KS = cfg::KS, QS = cfg::QS;
   constexpr int CH = BN == 16 ? 8 : 16;  // columns per tensor memory load
   // Where columns have a scale each, and there are enough: a thread holds four rows of every fourth pair of columns, so that it
   // needs a fourth of them from shared memory.
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(THREADS, Config<BN, PAIR>::CTAS)
   uint8_t* s_p = smem;
   uint8_t* s_q = smem + STAGES * P_BYTES;
   uint8_t* s_out = smem + STAGES * cfg::STAGE_BYTES;
-  float* s_scale = reinterpret_cast<float*>(s_out + cfg::OUT_BYTES);  // [2][KS][BM + BN]
+  float* s_scale = reinterpret_cast<float*>(s_out + cfg::OUT_BYTES);  // [2][KS][BM + QS]
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(s_scale) + cfg::SCALE_BYTES);
   uint64_t* full = bars;                   // [STAGES] TMA landed
   uint64_t* empty = bars + STAGES;         // [STAGES] MMAs reading the stage are done
@@ -340,10 +342,10 @@ __global__ void __launch_bounds__(THREADS, Config<BN, PAIR>::CTAS)
               if (i >= count) break;
 #pragma unroll
               for (int k = 0; k < KS; k += 4) {
-                to[k * (BM + BN) + i] = v[j][k / 4].x;
-                to[(k + 1) * (BM + BN) + i] = v[j][k / 4].y;
-                to[(k + 2) * (BM + BN) + i] = v[j][k / 4].z;
-                to[(k + 3) * (BM + BN) + i] = v[j][k / 4].w;
+                to[k * (BM + QS) + i] = v[j][k / 4].x;
+                to[(k + 1) * (BM + QS) + i] = v[j][k / 4].y;
+                to[(k + 2) * (BM + QS) + i] = v[j][k / 4].z;
+                to[(k + 3) * (BM + QS) + i] = v[j][k / 4].w;
               }
             }
           }
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, Config<BN, PAIR>::CTAS)
           scales = s_scale + slot * cfg::SCALES;
           if (kb + 1 < kb1) ok = mbar_wait_short(&scale_full[slot], slot_phase, wb, SITE_E4M3_EPILOGUE);
         } else {
-          scales += BM + BN;
+          scales += BM + QS;
         }
         if (kb + 1 < kb1) {
           ready = mbar_try_wait(&acc_full[acc], acc_phase);
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(THREADS, Config<BN, PAIR>::CTAS)
         row_scales();
       }
       for (int kb = kb0; ok && kb < kb1; ++kb) {
-        if (!ready) ok = mbar_wait_short(&acc_full[acc], acc_phase, wb, SITE_E4M3_EPILOGUE);
+        if (!ready) ok = mbar_wait_poll(&acc_full[acc], acc_phase, wb, SITE_E4M3_EPILOGUE);
         if (!ok) break;
         tc_fence_after();
         const uint32_t from = lanes + (uint32_t)(acc * BN);
@@ -591,20 +593,33 @@ __global__ void __launch_bounds__(THREADS, Config<BN, PAIR>::CTAS)
             }
           } else {
             // row by row, a column per lane
-            for (int i = 0; i < 32; ++i) {
-              const int r = warp_in * 32 + i;
-              if (first_row + r >= p.rows_p) break;
-              const long long at = (long long)(first_row + r) * p.ldc;
-              for (int c = lane; c < (p.c_f32 ? 64 : 128); c += 32) {
-                if (first_col + c >= p.rows_q) break;
-                if (p.c_f32) {
-                  const float x = *reinterpret_cast<const float*>(out + (c >> 5) * 16384 + r * 128 +
-                                                                  ((((c & 31) >> 2) ^ (r & 7)) << 4) + (c & 3) * 4);
-                  put(p, at + first_col + c, x);
-                } else {
-                  const __nv_bfloat16 x = *reinterpret_cast<const __nv_bfloat16*>(
-                      out + (c >> 6) * 16384 + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 7) * 2);
-                  static_cast<__nv_bfloat16*>(p.c)[at + first_col + c] = x;
+            const int columns = p.rows_q - first_col, rows = p.rows_p - (first_row + warp_in * 32);
+            const long long at = (long long)(first_row + warp_in * 32) * p.ldc + first_col + lane;
+            const uint8_t* from = out + warp_in * 32 * 128;
+            if (p.c_f32) {
+              float* to = static_cast<float*>(p.c) + at;
+#pragma unroll 8
+              for (int i = 0; i < 32; ++i) {
+                if (i >= rows) break;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                  if (lane + 32 * b >= columns) continue;
+                  const float x = *reinterpret_cast<const float*>(from + b * 16384 + i * 128 +
+                                                                  (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4);
+                  float* c = to + i * p.ldc + 32 * b;
+                  *c = p.accumulate ? *c + x : x;
+                }
+              }
+            } else {
+              __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.c) + at;
+#pragma unroll 8
+              for (int i = 0; i < 32; ++i) {
+                if (i >= rows) break;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                  if (lane + 32 * b >= columns) continue;
+                  to[i * p.ldc + 32 * b] = *reinterpret_cast<const __nv_bfloat16*>(
+                      from + (b >> 1) * 16384 + i * 128 + (((4 * (b & 1) + (lane >> 3)) ^ (i & 7)) << 4) + (lane & 7) * 2);
                 }
               }
             }
@@ -647,7 +662,7 @@ __global__ void __launch_bounds__(THREADS, Config<BN, PAIR>::CTAS)
 template <int BN, bool COLS, bool TURNED, bool PAIR>
 tsp_status launch(const CUtensorMap& tp, const CUtensorMap& tq, const CUtensorMap& tc, const Params& p, int ctas, int cluster, cudaStream_t s) {
   auto kernel = matmul_e4m3_kernel<BN, COLS, TURNED, PAIR>;
-  constexpr size_t smem = Config<BN, PAIR>::SMEM_BYTES;
+  constexpr size_t smem = Config<BN, COLS, PAIR>::SMEM_BYTES;
   TSP_TRY(ensure_smem_limit(reinterpret_cast<const void*>(kernel), (int)smem, "matmul_e4m3: cudaFuncSetAttribute"));
   const cudaError_t e = launch_early_cluster(kernel, ctas, THREADS, smem, s, cluster, tp, tq, tc, p);
   return e == cudaSuccess ? TSP_OK : cuda_fail(e, "matmul_e4m3: launch");
@@ -743,18 +758,25 @@ tsp_status tsp_matmul_e4m3(int64_t m, int64_t n, int64_t k, const uint8_t* a, in
   p.status = status_of(ws);
   p.limit_ns = wait_limit_ns();
 
-  const int64_t large = ((m + BM - 1) / BM) * ((n + 255) / 256);
-  if (m > 128 && large >= sm_count() / 2) {
+  // Which kernel, by estimates in tenths of a microsecond of what each takes: so many per block of K and wave of
+  // CTAs, and so many around. Measured on both sides (us, pairs / turned): 512 x 4096 x 4096 19.7 / 21.3,
+  // 256 x 4096 x 4096 19.4 / 18.1, 2048^3 13.8 / 28.4, 1024 x 1024 x 8192 with a scale per row of both 46.9 / 24.6,
+  // 256 x 256 x 8192 43 / 10, 2816 x 1024 x 1000 14.5 / 21.4. Up to 128 rows a pair's tile would be half empty.
+  const int64_t sms = sm_count();
+  const int bn = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
+  const int64_t tiles = ((n + BM - 1) / BM) * ((m + bn - 1) / bn);
+  const int64_t slots = (bn <= 32 ? 2 : 1) * sms;
+  int split = 1;  // as many CTAs as there is room for at once (more waves: 48 x 11008 x 4096 17 -> 23 us)
+  while (split < 8 && tiles * (split + 1) <= slots && nkb >= (split + 1) * 2) ++split;
+  const int64_t turned = (tiles * split + slots - 1) / slots * (6 * ((nkb + split - 1) / split) + 10) + (split > 1 ? 60 : 40);
+  const int64_t pair_tiles = ((m + 255) / 256) * ((n + 255) / 256);
+  const int64_t pairs = (pair_tiles + sms / 2 - 1) / std::max<int64_t>(1, sms / 2) * ((b_block == 1 ? 13 : 9) * nkb / 2 + 10) + 40;
+  if (m > 128 && pairs <= turned) {
     // about 32 MB of A's row blocks walk down each column block of B together where B does not fit the L2 well
-    const int64_t g = n * k <= (48ll << 20) ? 1 : (32ll << 20) / (BM * k);
+    const int64_t g = n * k <= (48ll << 20) ? 1 : (32ll << 20) / (2 * BM * k);
     p.group_p = (int)std::max<int64_t>(1, g);
     return b_block == 1 ? run<256, true, false, true>(oa, ob, k, p, 1, s) : run<256, false, false, true>(oa, ob, k, p, 1, s);
   }
-  const int bn = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
-  const int64_t tiles = ((n + BM - 1) / BM) * ((m + bn - 1) / bn);
-  const int64_t slots = (bn <= 32 ? 2 : 1) * sm_count();
-  int split = 1;
-  while (split < 8 && tiles * (split + 1) <= slots && nkb >= (split + 1) * 2) ++split;
   switch (bn) {
     case 16: return run<16, true, true, false>(ob, oa, k, p, split, s);
     case 32: return run<32, true, true, false>(ob, oa, k, p, split, s);
