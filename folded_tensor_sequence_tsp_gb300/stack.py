@@ -1,4 +1,4 @@
-"""A stack of pre-norm TSP layers: forward, training forward, backward and clipping.
+"""A stack of pre-norm TSP layers: forward, training forward, backward, clipping and AdamW steps.
 
 Per layer, on the sharded activations ([D, S/D, H], or [D, batch, S/D, H]):
     a = Attn(norm(h) w_attn),  h += a
@@ -19,7 +19,7 @@ from ._binding import (TSP_OK, TSPError, tsp_attention_bwd, tsp_attention_fwd, t
                        tsp_device_status, tsp_last_error, tsp_mlp_bwd, tsp_mlp_fwd, tsp_pack_weights,
                        tsp_packed_weight_bytes, tsp_plan, tsp_plan_batched, tsp_workspace_bytes,
                        tsp_workspace_init)
-from .operators import TSPGradClip, TSPRMSNorm, _device, _not_in_a_capture, _ready
+from .operators import TSPAdamW, TSPGradClip, TSPRMSNorm, _device, _not_in_a_capture, _ready
 
 __all__ = ["TSPStack"]
 
@@ -157,6 +157,27 @@ class TSPStack:
         """Scale backward()'s grads in place to a global norm of at most max_norm; returns the
         norm as one float32 on the device. The packed layout's padding holds zeros."""
         return self.clipper.clip(grads, max_norm)
+
+    @_on_its_device
+    def enable_updates(self, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, state_bits=32, seed=0):
+        """Make what step() needs: fp32 masters of the weights as they are now, and the states (fp32, or e4m3
+        with state_bits 8). Weight decay is for the matrices; the norm weights, which are the caller's
+        tensors and updated in place, have none."""
+        params = (self.wpack, self.norms)
+        self.masters = [[p.float() for p in ps] for ps in params]
+        self.optimizers = [TSPAdamW(ps, masters=ms, betas=betas, eps=eps, weight_decay=decay, state_bits=state_bits,
+                                    seed=seed + i, device=self.device)
+                           for i, (ps, ms, decay) in enumerate(zip(params, self.masters, (weight_decay, 0.0)))]
+
+    @_on_its_device
+    def step(self, grads, lr, max_norm=float("inf"), t=None):
+        """One AdamW step with backward()'s grads, scaled on the way to a global norm of at most max_norm;
+        returns the norm as one float32 on the device. grads are left as they are. lr and t as in TSPAdamW.step."""
+        norm = self.clipper.norm(grads)
+        n = len(self.wpack)
+        for optimizer, part in zip(self.optimizers, (grads[:n], grads[n:])):
+            optimizer.step(part, lr, norm=norm, max_norm=max_norm, t=t)
+        return norm
 
     @_on_its_device
     def check(self):
