@@ -6,7 +6,9 @@
 // or e4m3 with an fp32 scale for each 128 elements of a tensor.
 //
 // Bound: HBM. Every value is read once and written once, clipping included (the factor is formed
-// from the norm here, so the gradients are not scaled in a pass of their own). As in grad_clip.cu
+// from the norm here, so the gradients are not scaled in a pass of their own). 202M bf16 weights with fp32
+// masters: 868 us with 32-bit states (7.0 TB/s), 632 with 8-bit ones (5.8 TB/s; 100 instructions an element,
+// 0.8 per cycle and scheduler, bind as much). As in grad_clip.cu
 // the list travels in the kernels' parameters, cut into chunks of a CTA each (persistent CTAs that take
 // them in turn: 202M weights with masters 941 us, one CTA each 866).
 //

@@ -5,11 +5,17 @@
 //   columns    yt [width][rows]: the transpose, a scale for 128 rows of one column
 //   tiles      one scale for 128 x 128 values: y and its transpose hold the same values
 //
-// Bound: HBM. x is read once, whatever is written. The rows alone are eight lanes' work, 128
-// columns at a time. What needs a column's largest value or a transpose takes a tile of 128 x 128
-// per CTA: each warp holds 16 rows in registers, the columns' maxima meet in shared memory, and
-// the transposed bytes go through a 16 KB tile there (16-byte chunks, swizzled by their column) so
-// that both layouts are written in runs of 128 bytes.
+// Bound: HBM for rows and tiles (16384 x 4096 bf16 rows: 31 us, 0.95 of the copy rate; 11008 x 4096 fp32 tiles in
+// both layouts: 43 us, 0.92), the arithmetic of two quotients a value for both layouts with scales of their own
+// (16384 x 4096 bf16: 54 us, 0.74). x is read once, whatever is written. In rows eight lanes hold a block, 16
+// values each, so that a divisor is worked out for 16 values (with four per lane: 104 us). What needs a
+// column's largest value or a transpose takes a tile of 128 x 128 per CTA: each warp holds 16 rows as they are
+// stored, the rows' and columns' maxima meet in shared memory, where one thread each makes the divisors (in
+// every lane: 135 us for 16384 x 4096), and the transposed bytes go through a 16 KB tile there (16-byte chunks,
+// swizzled by their column) so that both layouts are written in runs of 128 bytes. With quotients of six
+// operations for two values in place of QuickQuotient's two: 34, 51 and 67 us.
+#include <type_traits>
+
 #include "e4m3.cuh"
 #include "tsp_internal.h"
 
@@ -33,7 +39,8 @@ struct QuantParams {
 
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(fabsf(v)); }
 
-__device__ __forceinline__ uint32_t quantize4(const Quotient& by, const float (&v)[4]) {
+template <class Q>
+__device__ __forceinline__ uint32_t quantize4(const Q& by, const float (&v)[4]) {
   float a = v[0], b = v[1], c = v[2], d = v[3];
   by.pair(a, b);
   by.pair(c, d);
@@ -103,24 +110,27 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantPara
     if constexpr (!F32) top = max(top << 16, top & 0xffff0000u);
 #pragma unroll
     for (int o = 4; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (b >= blocks) continue;
     const float scale = e4m3_scale(top);
-    const Quotient by(scale);
-    if (sub == 0) p.scales[b] = scale;
+    const QuickQuotient quick(scale);
+    if (sub == 0 && b < blocks) p.scales[b] = scale;
     uint8_t* to = p.y + (long long)row[u] * p.ld_y + col[u];
+    auto write = [&](const auto& by) {
 #pragma unroll
-    for (int k = 0; k < RUNS; ++k) {
-      const int c = PER * (8 * k + sub);
-      if (col[u] + c >= p.width) continue;
-      const float four[4] = {v[PER * k], v[PER * k + 1], v[PER * k + 2], v[PER * k + 3]};
-      const uint32_t lo = quantize4(by, four);
-      if constexpr (F32) {
-        *reinterpret_cast<uint32_t*>(to + c) = lo;
-      } else {
-        const float more[4] = {v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]};
-        *reinterpret_cast<uint2*>(to + c) = make_uint2(lo, quantize4(by, more));
+      for (int k = 0; k < RUNS; ++k) {
+        const int c = PER * (8 * k + sub);
+        if (b >= blocks || col[u] + c >= p.width) continue;
+        const float four[4] = {v[PER * k], v[PER * k + 1], v[PER * k + 2], v[PER * k + 3]};
+        const uint32_t lo = quantize4(by, four);
+        if constexpr (F32) {
+          *reinterpret_cast<uint32_t*>(to + c) = lo;
+        } else {
+          const float more[4] = {v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]};
+          *reinterpret_cast<uint2*>(to + c) = make_uint2(lo, quantize4(by, more));
+        }
       }
-    }
+    };
+    if (__all_sync(0xffffffffu, quick.ok)) write(quick);
+    else write(Quotient(scale));
   }
 }
 
@@ -155,27 +165,41 @@ __global__ void __launch_bounds__(kThreads) quantize_any_rows_kernel(const Quant
     if (col + 32 * e < p.width) p.y[(long long)row * p.ld_y + col + 32 * e] = (uint8_t)(q >> (8 * e));
 }
 
-// The scale and the constants of a quotient by it, worked out once for a row or column of a tile.
+// The scale of a row or column of a tile and the constants of a quick quotient by it, worked out once; lo is
+// negative where that quotient will not do.
 struct __align__(16) Divisor {
-  float up, inv, sc, scale;
+  float hi, lo, scale;
 };
 __device__ __forceinline__ Divisor divisor(uint32_t top) {
   const float scale = e4m3_scale(top);
-  const Quotient by(scale);
-  return {by.up, by.inv, by.sc, scale};
+  const QuickQuotient quick(scale);
+  return {quick.hi, quick.ok ? quick.lo : -1.f, scale};
 }
-__device__ __forceinline__ Quotient quotient(const Divisor& d) {
-  Quotient by(1.f);
-  by.up = d.up, by.inv = d.inv, by.sc = d.sc;
-  return by;
+// The quotient by it, of either kind.
+template <bool QUICK>
+__device__ __forceinline__ auto quotient(const Divisor& d) {
+  if constexpr (QUICK) {
+    QuickQuotient by(1.f);
+    by.hi = d.hi, by.lo = d.lo;
+    return by;
+  } else {
+    return Quotient(d.scale);
+  }
+}
+// One branch for all of a warp's divisors: f(std::true_type) where a quick quotient does for each lane's.
+template <class F>
+__device__ __forceinline__ void with_quotients(bool ok, F f) {
+  if (__all_sync(0xffffffffu, ok)) f(std::true_type());
+  else f(std::false_type());
 }
 
 // One CTA per tile of 128 x 128. TILE: one scale for all of it. VEC: the width is a multiple of 4 and every
 // row starts on 16 (fp32) or 8 (bf16) bytes, in y on 4. A warp holds 16 rows, a lane four columns of
 // them as they are stored; the rows' and columns' largest values meet in shared memory, where one
-// thread each makes the divisors. vec_t: yt's rows start on 16 bytes.
+// thread each makes the divisors. CTAs per SM as measured: bf16 2, 3 and 4: 69, 61 and 54 us for 16384 x 4096; fp32
+// with a scale per row and column 2 and 3: 80 and 108 us. vec_t: yt's rows start on 16 bytes.
 template <bool F32, bool TILE, bool VEC>
-__global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) quantize_tile_kernel(const QuantParams p, int vec_t) {
+__global__ void __launch_bounds__(kThreads, F32 ? (TILE ? 3 : 2) : 4) quantize_tile_kernel(const QuantParams p, int vec_t) {
   __shared__ __align__(16) uint8_t turned[kBlock * kBlock];
   __shared__ __align__(16) uint32_t col_tops[kThreads / 32][kBlock];
   __shared__ uint32_t row_tops[kBlock];
@@ -254,21 +278,22 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) quantize_tile_kernel(co
   }
   __syncthreads();
   if constexpr (TILE) {
-    const Quotient by(e4m3_scale(__reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? row_tops[lane] : 0u)));
+    const Divisor by = divisor(__reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? row_tops[lane] : 0u));
     if (threadIdx.x == 0) {
-      const float scale = e4m3_scale(max(max(max(row_tops[0], row_tops[1]), max(row_tops[2], row_tops[3])),
-                                         max(max(row_tops[4], row_tops[5]), max(row_tops[6], row_tops[7]))));
-      if (p.y) p.scales[(long long)tr * tiles_w + tc] = scale;
-      if (p.yt) p.scales_t[(long long)tc * tiles_r + tr] = scale;
+      if (p.y) p.scales[(long long)tr * tiles_w + tc] = by.scale;
+      if (p.yt) p.scales_t[(long long)tc * tiles_r + tr] = by.scale;
     }
     uint32_t q[16];
+    with_quotients(by.lo >= 0.f, [&](auto quick) {
+      const auto divide = quotient<quick.value>(by);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      float v[4];
-      four(r, v);
-      q[r] = quantize4(by, v);
-      if (p.y && r < rows_left) store4<VEC>(p.y + (row0 + r) * p.ld_y + col, left, q[r]);
-    }
+      for (int r = 0; r < 16; ++r) {
+        float v[4];
+        four(r, v);
+        q[r] = quantize4(divide, v);
+        if (p.y && r < rows_left) store4<VEC>(p.y + (row0 + r) * p.ld_y + col, left, q[r]);
+      }
+    });
     if (!p.yt) return;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -299,26 +324,31 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) quantize_tile_kernel(co
     }
     __syncthreads();
     if (p.y) {
+      with_quotients(row_div[16 * warp + (lane & 15)].lo >= 0.f, [&](auto quick) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        if (r >= rows_left) break;
-        float v[4];
-        four(r, v);
-        store4<VEC>(p.y + (row0 + r) * p.ld_y + col, left, quantize4(quotient(row_div[16 * warp + r]), v));
-      }
+        for (int r = 0; r < 16; ++r) {
+          if (r >= rows_left) break;
+          float v[4];
+          four(r, v);
+          store4<VEC>(p.y + (row0 + r) * p.ld_y + col, left, quantize4(quotient<quick.value>(row_div[16 * warp + r]), v));
+        }
+      });
     }
+    const Divisor by[4] = {col_div[4 * lane], col_div[4 * lane + 1], col_div[4 * lane + 2], col_div[4 * lane + 3]};
+    with_quotients(min(min(by[0].lo, by[1].lo), min(by[2].lo, by[3].lo)) >= 0.f, [&](auto quick) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const Quotient by = quotient(col_div[4 * lane + e]);
-      uint32_t w[4];
+      for (int e = 0; e < 4; ++e) {
+        const auto divide = quotient<quick.value>(by[e]);
+        uint32_t w[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float v[4] = {one(4 * k, e), one(4 * k + 1, e), one(4 * k + 2, e), one(4 * k + 3, e)};
-        w[k] = quantize4(by, v);
+        for (int k = 0; k < 4; ++k) {
+          const float v[4] = {one(4 * k, e), one(4 * k + 1, e), one(4 * k + 2, e), one(4 * k + 3, e)};
+          w[k] = quantize4(divide, v);
+        }
+        *reinterpret_cast<uint4*>(turned + (4 * lane + e) * kBlock + ((warp ^ (lane & 7)) << 4)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
       }
-      *reinterpret_cast<uint4*>(turned + (4 * lane + e) * kBlock + ((warp ^ (lane & 7)) << 4)) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    });
   }
   __syncthreads();
   // 16 rows of x of one column per thread and step

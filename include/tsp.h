@@ -788,8 +788,8 @@ tsp_status tsp_quantize_e4m3(int64_t rows, int64_t width, const void* x, int x_f
  *
  * Rows of a and b start on 16 bytes (base and ld_a, ld_b multiples of 16), those of c anywhere on its
  * element; what lies behind a row's end is neither read into the result nor written. m, n, k in
- * [0, 2^30]; k 0 gives zeros. c may not overlap an input. Sums are in a fixed order that goes by m, n and
- * k alone. ws: tsp_matmul_e4m3_workspace_bytes() bytes, 256-byte aligned, initialised once by
+ * [0, 2^30]; k 0 gives zeros. c may not overlap an input. Sums are in a fixed order, which goes by
+ * m, n, k, b_block and the device alone. ws: tsp_matmul_e4m3_workspace_bytes() bytes, 256-byte aligned, initialised once by
  * tsp_status_init; calls may share it.
  */
 size_t tsp_matmul_e4m3_workspace_bytes(void);

@@ -116,6 +116,35 @@ def test_what_is_not_finite_stays_in_its_blocks(block, bad):
     assert torch.equal(y.cpu()[~rows], codes[~rows])
 
 
+@pytest.mark.parametrize("block", [1, 128])
+def test_quotients_next_to_ties(block):
+    """Scales whose mantissas are within some units of a multiple of 2^19, and values whose quotients by them are
+    within some units of halfway between two e4m3 values: where an approximate quotient would round wrongly."""
+    g = torch.Generator().manual_seed(3)
+    rows = []
+    for near in (0, 1, 2, 5, 11, 15, 16, 17, 18, 40):
+        for sign in (1, -1):
+            for j in (16, 17, 21, 26, 31):
+                s = torch.tensor((j << 19) + sign * near, dtype=torch.float64) * 2.0 ** -30
+                top = (s * 448).float()
+                scale = (top.double() / 448).float().double()  # what the block's largest value makes of it
+                # ties: 1.0001 to 1.1111 in binary, and between subnormal values
+                t = (2 * torch.randint(8, 16, (63,), generator=g) + 1).double() * 2.0 ** torch.randint(-10, 4, (63,), generator=g)
+                t = torch.cat([t, (2 * torch.randint(0, 8, (64,), generator=g) + 1).double() * 2.0 ** -10])
+                ulp = 2.0 ** (torch.floor(torch.log2(t)) - 23)
+                x = (scale * (t + ulp * torch.randint(-3, 4, (127,), generator=g) / 2)).float()
+                bits = x.view(torch.int32) + torch.randint(-1, 2, (127,), generator=g, dtype=torch.int32)
+                x = bits.view(torch.float32) * (torch.randint(0, 2, (127,), generator=g) * 2 - 1)
+                rows.append(torch.cat([top[None], x]))
+    x = torch.stack(rows)
+    if block == 1:
+        check(x.cuda(), 1)
+        check(x.t().contiguous().cuda(), 1)
+    else:
+        for i in range(0, len(rows), 10):  # one largest value to a tile
+            check(x[i:i + 1].repeat(128, 1).cuda(), 128)
+
+
 def test_empty():
     for rows, w in ((0, 5), (5, 0), (0, 0)):
         x = torch.zeros(rows, w, device="cuda")
