@@ -74,7 +74,7 @@ struct Params {
   void* c;
   long long ldc;
   int c_f32, accumulate;
-  int tma_out;  // pairs: C is written by TMA (rows start on 16 bytes, nothing is added)
+  int tma_out;  // pairs: C is written by TMA (rows start and end on 16 bytes, nothing is added)
   int group_p;  // tile order of the persistent walk
   DevStatus* status;
   unsigned long long limit_ns;
@@ -765,7 +765,8 @@ tsp_status tsp_matmul_e4m3(int64_t m, int64_t n, int64_t k, const uint8_t* a, in
   p.ldc = ld_c;
   p.c_f32 = c_f32;
   p.accumulate = accumulate;
-  p.tma_out = !accumulate && al16(c) && (ld_c * es) % 16 == 0;
+  // TMA writes whole 16 bytes: a row that ends inside them would take what lies behind it along
+  p.tma_out = !accumulate && al16(c) && (ld_c * es) % 16 == 0 && (n * es) % 16 == 0;
   p.group_p = 1;
   p.status = status_of(ws);
   p.limit_ns = wait_limit_ns();

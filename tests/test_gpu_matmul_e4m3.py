@@ -88,6 +88,21 @@ def test_products(m, n, k, dtype, b_block, ws):
     run(m, n, k, b_block, dtype, ws, seed=m + n + k)
 
 
+# K split over clusters of 3, 5, 6, 7 and 8; tiles that walk in groups of rows (b above 48 MB)
+@pytest.mark.parametrize("m, n, k", [(4, 11000, 1024), (2, 7680, 1280), (30, 6400, 1536), (9, 5500, 1800), (50, 2400, 2048),
+                                     (600, 13000, 4096)])
+def test_splits_and_tile_orders(m, n, k, ws):
+    run(m, n, k, 128, torch.bfloat16, ws, seed=n)
+
+
+@pytest.mark.parametrize("dtype, n, pad", [(torch.bfloat16, 1, 7), (torch.bfloat16, 9, 7), (torch.float32, 3, 1),
+                                           (torch.float32, 1, 3), (torch.bfloat16, 130, 6)])
+def test_narrow_outputs_of_many_rows(dtype, n, pad, ws):
+    """Rows that end inside 16 bytes: what lies behind them stays."""
+    for b_block in (1, 128):
+        run(30000, n, 256, b_block, dtype, ws, pad_c=pad)
+
+
 @pytest.mark.parametrize("m, n, k", [(5, 300, 4096), (700, 4096, 256), (1, 1, 1)])
 def test_adding_to_the_output(m, n, k, ws):
     run(m, n, k, 1, torch.float32, ws, accumulate=True)
@@ -252,6 +267,32 @@ def test_another_stream_and_batched_shapes():
     got = layer.forward(x, w, stream=s)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_layers_on_two_streams_at_once():
+    """An object each: their calls overlap."""
+    tokens, n, k = 300, 1000, 2000
+    x, dy = normal(tokens, k, seed=2).bfloat16(), normal(tokens, n, seed=3).bfloat16()
+    layers = [tsp.TSPLinearE4M3(tokens, n, k) for _ in range(2)]
+    w = layers[0].quantize_weight(0.05 * normal(n, k, seed=1))
+    y, saved = layers[0].forward_train(x, w)
+    want = (y, *layers[0].backward(saved, dy, w))
+    for layer in layers:
+        layer.enable_backward()
+    streams = [torch.cuda.Stream() for _ in layers]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for layer, s, out in zip(layers, streams, got):
+            y, saved = layer.forward_train(x, w, stream=s)
+            out.append((y, *layer.backward(saved, dy, w, stream=s)))
+    torch.cuda.synchronize()
+    for out in got:
+        for result in out:
+            assert all(torch.equal(a, b) for a, b in zip(result, want))
+        del out[:]
+    for layer in layers:
+        layer.check()
 
 
 def test_no_tokens():
