@@ -322,7 +322,7 @@ class TSPLinearE4M3:
 
     def forward(self, x, weight, scales=None, out=None, stream=None):
         """y [..., out] in bfloat16. x [..., in]: bfloat16, or e4m3 [rows, in] with scales [rows, ceil(in / 128)]
-        as TSPRMSNorm.forward_e4m3 (group 128) and tsp_quantize_e4m3 leave them."""
+        as TSPRMSNorm.forward_e4m3 (group 128) and tsp_quantize_e4m3 leave them, in rows that start on 16 bytes."""
         n, k = self.out_features, self.in_features
         device = _same_device((x, scales, *weight[:2], out, self.ws))
         out = self._out(out, (*x.shape[:-1], n), torch.bfloat16, stream, "out")
