@@ -502,7 +502,9 @@ tsp_status tsp_adamw_step(int n, void* const* params, const int* types, void* co
   const tsp_adamw& h = *step;
   if (!(h.beta1 >= 0. && h.beta1 < 1.) || !(h.beta2 >= 0. && h.beta2 < 1.))
     return fail(TSP_ERR_INVALID_ARG, w + ": betas in [0, 1)");
-  if (!((float)h.eps > 0.f) || !std::isfinite(h.eps)) return fail(TSP_ERR_INVALID_ARG, w + ": eps must be positive and finite");
+  // the quotient by it flushes what is smaller, and 0 / 0 is NaN
+  if (!((float)h.eps >= 1.17549435e-38f) || !std::isfinite(h.eps))
+    return fail(TSP_ERR_INVALID_ARG, w + ": eps must be finite and at least 2^-126");
   if (!h.device_lr && !(h.lr >= 0. && std::isfinite(h.lr))) return fail(TSP_ERR_INVALID_ARG, w + ": lr must be finite, not negative");
   if (!(h.weight_decay >= 0.) || !std::isfinite(h.weight_decay))
     return fail(TSP_ERR_INVALID_ARG, w + ": weight_decay must be finite, not negative");

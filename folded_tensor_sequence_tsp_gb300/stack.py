@@ -59,6 +59,7 @@ class TSPStack:
         self.norms = [w[k] for w in weights for k in _NORMS] + [last_norm]
         self.norm = TSPRMSNorm(self.plan.info.tokens, hidden, eps, device=self.device)
         self.clipper = TSPGradClip(len(self.wpack) + len(self.norms), device=self.device)
+        self.masters = self.optimizers = None  # enable_updates()
 
     @_on_its_device
     def _pack(self, weights):
@@ -173,6 +174,8 @@ class TSPStack:
     def step(self, grads, lr, max_norm=float("inf"), t=None):
         """One AdamW step with backward()'s grads, scaled on the way to a global norm of at most max_norm;
         returns the norm as one float32 on the device. grads are left as they are. lr and t as in TSPAdamW.step."""
+        if self.optimizers is None:
+            raise RuntimeError("TSPStack.step() needs enable_updates()")
         norm = self.clipper.norm(grads)
         n = len(self.wpack)
         for optimizer, part in zip(self.optimizers, (grads[:n], grads[n:])):

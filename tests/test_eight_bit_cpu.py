@@ -84,7 +84,7 @@ def adamw(lib, n=1, types=(0,), sizes=(300,), grad_types=None, masters=None, bit
 def test_adamw_refusals(lib):
     for kw, code, word in [
             (dict(beta1=1.0), BAD, "betas"), (dict(beta2=-0.1), BAD, "betas"), (dict(beta1=math.nan), BAD, "betas"),
-            (dict(eps=0.0), BAD, "eps"), (dict(eps=math.inf), BAD, "eps"), (dict(eps=1e-60), BAD, "eps"),
+            (dict(eps=0.0), BAD, "eps"), (dict(eps=math.inf), BAD, "eps"), (dict(eps=1e-60), BAD, "eps"), (dict(eps=1e-38), BAD, "eps"),
             (dict(lr=-1.0), BAD, "lr"), (dict(lr=math.nan), BAD, "lr"), (dict(weight_decay=-1.0), BAD, "weight_decay"),
             (dict(weight_decay=math.inf), BAD, "weight_decay"), (dict(t=0), BAD, "count from 1"),
             (dict(norm=P(9), max_norm=-1.0), BAD, "max_norm"), (dict(norm=P(9), max_norm=math.nan), BAD, "max_norm"),

@@ -211,10 +211,11 @@ def test_from_zero_states():
         assert torch.allclose(p, -LR * g.sign(), rtol=1e-5)
 
 
-def test_zero_gradients_and_states_leave_the_weights():
+@pytest.mark.parametrize("eps", [1e-8, 1.2e-38])
+def test_zero_gradients_and_states_leave_the_weights(eps):
     p = torch.randn(1000, device="cuda")
     before = p.clone()
-    opt = tsp.TSPAdamW([p], state_bits=8)
+    opt = tsp.TSPAdamW([p], eps=eps, state_bits=8)
     opt.step([torch.zeros(1000, device="cuda")], LR)
     assert torch.equal(p, before) and bool((opt.m_scales[0] == 1).all()) and bool((opt.v_scales[0] == 1).all())
 
