@@ -312,10 +312,15 @@ class TSPLinearE4M3:
         return p, ld if rows > 1 else _up16(width), _matrix(scales, "weight scales", (_blocks(rows), _blocks(width)),
                                                             (torch.float32,))
 
+    def _new(self, shape, dtype, stream):
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with _on(stream, self.device):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
     def _out(self, out, shape, dtype, stream, name):
         if out is None:
-            with _on(stream, self.device):
-                out = torch.empty(shape, dtype=dtype, device=self.device)
+            out = self._new(shape, dtype, stream)
         elif out.dtype != dtype or out.shape != shape or not out.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
         return out
@@ -351,26 +356,25 @@ class TSPLinearE4M3:
         out = self._out(out, (*x.shape[:-1], n), torch.bfloat16, stream, "out")
         w = self._weight(*weight[:2], n, k)
         m, xp, ldx = self._input(x, k, "x")
-        with _on(stream, self.device):
-            saved = (torch.empty(k, _up16(m), dtype=torch.float8_e4m3fn, device=self.device)[:, :m],
-                     torch.empty(k, _blocks(m), device=self.device))
+        # the values [in, rows in a multiple of 16], then their scales [in, ceil(rows / 128)]
+        kept = self._new((k * (_up16(m) + 4 * _blocks(m)),), torch.uint8, stream)
         if m:
-            ws = self.ws.data_ptr()
+            ws, xt = self.ws.data_ptr(), kept.data_ptr()
             a, ld_a, sa = ws + self._at[0][0], _up16(k), ws + self._at[0][1]
-            _launch("tsp_quantize_e4m3", device, stream, m, k, xp, 0, ldx, 1, a, ld_a, sa, saved[0].data_ptr(),
-                    _up16(m), saved[1].data_ptr())
+            _launch("tsp_quantize_e4m3", device, stream, m, k, xp, 0, ldx, 1, a, ld_a, sa, xt, _up16(m), xt + k * _up16(m))
             _launch("tsp_matmul_e4m3", device, stream, m, n, k, a, ld_a, sa, *w, 128, out.data_ptr(), n, 0, 0, ws)
-        return out, saved
+        return out, (kept, m)
 
     def backward(self, saved, dy, weight, dx=None, dw=None, accumulate=False, stream=None):
         """(dx, dw) of forward_train's saved and the gradient dy [..., out] of y (bfloat16): dx in bfloat16, dw
         in float32, added to the given dw with accumulate."""
         self.enable_backward()
         n, k = self.out_features, self.in_features
-        device = _same_device((dy, *saved, *weight[2:], dx, dw, self.ws))
+        kept, rows = saved
+        device = _same_device((dy, kept, *weight[2:], dx, dw, self.ws))
         m, gp, ldg = self._input(dy, n, "dy")
-        if saved[0].shape != (k, m):
-            raise ValueError(f"saved belongs to {saved[0].shape[1]} rows, dy has {m}")
+        if rows != m or kept.numel() != k * (_up16(m) + 4 * _blocks(m)):
+            raise ValueError(f"saved belongs to {rows} rows of another layer or call, dy has {m}")
         wt = self._weight(*(weight[2:] or (None, None)), k, n)
         if accumulate and dw is None:
             raise ValueError("accumulate needs a dw to add to")
@@ -381,8 +385,9 @@ class TSPLinearE4M3:
         if m:
             _launch("tsp_quantize_e4m3", device, stream, m, n, gp, 0, ldg, 1, g, _up16(n), sg, gt, _up16(m), sgt)
             _launch("tsp_matmul_e4m3", device, stream, m, k, n, g, _up16(n), sg, *wt, 128, dx.data_ptr(), k, 0, 0, ws)
-        _launch("tsp_matmul_e4m3", device, stream, n, k, m, gt, _up16(m), sgt, saved[0].data_ptr(), _up16(m),
-                saved[1].data_ptr(), 1, dw.data_ptr(), k, 1, int(accumulate), ws)
+        xt = kept.data_ptr()
+        _launch("tsp_matmul_e4m3", device, stream, n, k, m, gt, _up16(m), sgt, xt, _up16(m), xt + k * _up16(m), 1,
+                dw.data_ptr(), k, 1, int(accumulate), ws)
         return dx, dw
 
     def check(self, stream=None):
