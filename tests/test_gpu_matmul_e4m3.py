@@ -295,6 +295,29 @@ def test_layers_on_two_streams_at_once():
         layer.check()
 
 
+def test_a_layer_refuses_what_does_not_fit():
+    layer = tsp.TSPLinearE4M3(10, 64, 48)
+    w = layer.quantize_weight(normal(64, 48, seed=1))
+    x, dy = normal(6, 48, seed=2).bfloat16(), normal(6, 64, seed=3).bfloat16()
+    _, saved = layer.forward_train(x, w)
+    out = torch.empty(6, 64, device="cuda")
+    x8 = torch.zeros(6, 40, dtype=torch.uint8, device="cuda").view(E4M3)
+    for match, call in [
+            ("made for 10", lambda: layer.forward(normal(11, 48, seed=2).bfloat16(), w)),
+            ("shape", lambda: layer.forward(x[:, :40].contiguous(), w)),
+            ("bfloat16", lambda: layer.forward(x.float(), w)),
+            ("out must be", lambda: layer.forward(x, w, out=out)),
+            ("weight must have shape", lambda: layer.forward(x, tsp.TSPLinearE4M3(1, 48, 64).quantize_weight(normal(48, 64, seed=1)))),
+            ("x must have shape", lambda: layer.forward(x8, w, scales=torch.ones(6, 1, device="cuda"))),
+            ("expected a weight", lambda: layer.quantize_weight(normal(48, 64, seed=1))),
+            ("transpose", lambda: layer.backward(saved, dy, w[:2])),
+            ("saved belongs", lambda: layer.backward(saved, dy[:5].contiguous(), w)),
+            ("saved belongs", lambda: layer.backward((saved[0][:-1], 6), dy, w)),
+            ("needs a dw", lambda: layer.backward(saved, dy, w, accumulate=True))]:
+        with pytest.raises(ValueError, match=match):
+            call()
+
+
 def test_no_tokens():
     layer = tsp.TSPLinearE4M3(10, 64, 32)
     w = layer.quantize_weight(normal(64, 32, seed=1))
