@@ -30,6 +30,7 @@
 
 #include <algorithm>
 
+#include "tile_walk.h"
 #include "tsp_device.cuh"
 #include "tsp_internal.h"
 
@@ -79,15 +80,6 @@ struct Params {
   DevStatus* status;
   unsigned long long limit_ns;
 };
-
-__device__ __forceinline__ void tile_coords(int tile, int num_p, int num_q, int group_p, int& tp, int& tq) {
-  const int span = group_p * num_q;
-  const int g = tile / span, r = tile - g * span;
-  const int first = g * group_p;
-  const int gm = min(group_p, num_p - first);
-  tp = first + r % gm;
-  tq = r / gm;
-}
 
 template <int CH>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[CH]) {
@@ -783,9 +775,7 @@ tsp_status tsp_matmul_e4m3(int64_t m, int64_t n, int64_t k, const uint8_t* a, in
   const int64_t pair_tiles = ((m + 255) / 256) * ((n + 255) / 256);
   const int64_t pairs = (pair_tiles + sms / 2 - 1) / std::max<int64_t>(1, sms / 2) * ((b_block == 1 ? 13 : 9) * nkb / 2 + 10) + 40;
   if (m > 128 && pairs <= turned) {
-    // about 32 MB of A's row blocks walk down each column block of B together where B does not fit the L2 well
-    const int64_t g = n * k <= (48ll << 20) ? 1 : (32ll << 20) / (2 * BM * k);
-    p.group_p = (int)std::max<int64_t>(1, g);
+    p.group_p = walk_group(m, n, k, 2 * BM);
     return b_block == 1 ? run<256, true, false, true>(oa, ob, k, p, 1, s) : run<256, false, false, true>(oa, ob, k, p, 1, s);
   }
   switch (bn) {
