@@ -295,12 +295,18 @@ class TSPLinearE4M3:
         tsp_quantize_e4m3(w, *out, block=128, stream=stream)
         return out
 
+    @staticmethod
+    def _as_rows(x, width, name):
+        """A [..., width] tensor as a matrix."""
+        if x.dim() == 2:
+            return x
+        if x.dim() < 1 or x.shape[-1] != width:
+            raise ValueError(f"{name}: expected rows of {width}, got shape {tuple(x.shape)}")
+        return x.view(-1, width)
+
     def _input(self, x, width, name):
         """(rows, address, row stride) of a bfloat16 [..., width] tensor."""
-        if x.dim() != 2:
-            if x.dim() < 1 or x.shape[-1] != width:
-                raise ValueError(f"{name}: expected rows of {width}, got shape {tuple(x.shape)}")
-            x = x.view(-1, width)
+        x = self._as_rows(x, width, name)
         if x.shape[0] > self.tokens:
             raise ValueError(f"{x.shape[0]} rows; the object was made for {self.tokens}")
         return x.shape[0], *_rows(x, name, (x.shape[0], width), (torch.bfloat16,))
@@ -339,8 +345,9 @@ class TSPLinearE4M3:
                 a, ld_a, sa = ws + self._at[0][0], _up16(k), ws + self._at[0][1]
                 _launch("tsp_quantize_e4m3", device, stream, m, k, xp, 0, ldx, 1, a, ld_a, sa, None, 0, None)
         else:
-            m = x.numel() // k if x.dim() else 0
-            a, ld_a = _rows(x if x.dim() == 2 else x.view(-1, k), "x", (m, k))
+            x = self._as_rows(x, k, "x")
+            m = x.shape[0]
+            a, ld_a = _rows(x, "x", (m, k))
             ld_a = ld_a if m > 1 else _up16(k)
             sa = _matrix(scales, "scales", (m, _blocks(k)), (torch.float32,))
         if m:

@@ -244,3 +244,20 @@ def test_a_master_belongs_beside_bfloat16(monkeypatch):
         tsp.TSPAdamW([torch.zeros(5)], masters=[torch.zeros(5)])
     with pytest.raises(ValueError, match="scales belong"):
         tsp.TSPAdamW([torch.zeros(5)]).resume(3, [torch.zeros(5)], [torch.zeros(5)], [torch.zeros(1)], [torch.zeros(1)])
+
+
+@pytest.mark.parametrize("shape", [(2, 3, 64), (64,), (2, 2, 2, 16), (3, 32, 1)])
+def test_an_input_in_8_bits_has_rows_of_the_layers_width(monkeypatch, shape):
+    """As many values as rows of 32 have, in other rows: out is made for x's own rows, so nothing may be launched."""
+    Fakes(monkeypatch)
+    launched = []
+    monkeypatch.setattr(operators, "_same_device", lambda tensors: 0)
+    monkeypatch.setattr(operators, "_launch", lambda *args: launched.append(args))
+    layer = tsp.TSPLinearE4M3(100, 48, 32)
+    weight = (torch.zeros(48, 32, dtype=torch.float8_e4m3fn), torch.ones(1, 1))
+    x = torch.zeros(shape, dtype=torch.float8_e4m3fn)
+    with pytest.raises(ValueError, match="rows of 32"):
+        layer.forward(x, weight, scales=torch.ones(x.numel() // 32, 1))
+    assert not launched
+    y = layer.forward(torch.zeros(2, 3, 32, dtype=torch.float8_e4m3fn), weight, scales=torch.ones(6, 1))
+    assert y.shape == (2, 3, 48) and launched[0][3:6] == (6, 48, 32)
