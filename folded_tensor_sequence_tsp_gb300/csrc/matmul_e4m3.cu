@@ -223,16 +223,24 @@ __global__ void __launch_bounds__(THREADS, Config<BN, COLS, PAIR>::CTAS)
           }
         }
       }
-      // Do not leave while a TMA copy into this CTA's shared memory is in flight. Those of a pair's
-      // second CTA count on the first one's barriers: its sums have waited for MMAs on all of them,
-      // or, when a wait gave up, it gives them a millisecond.
+      // Do not leave while something is on its way to this CTA's shared memory: a TMA copy or, from the MMA warp of a
+      // pair's first CTA, an arrival of a commit. A stage whose empty barrier is through the phase of its last copy has
+      // neither (its MMAs have read the copy), the sums have seen every product, and the drain is the last
+      // commit. Where a wait gave up, copies of the first CTA are waited for at their own barriers, and the
+      // second one gives its copies, which count there, a millisecond.
       WaitBound wd{p.status, p.limit_ns, nullptr};
+      if constexpr (PAIR) {
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s)
+          if (ok && last_parity[s] >= 0) ok = mbar_wait(&empty[s], (uint32_t)last_parity[s], wb, SITE_DRAIN);
+        if (rank != 0) mbar_wait(drain, 0, wd, SITE_DRAIN);
+      }
       if (PAIR && rank != 0) {
         if (!ok) {
           const unsigned long long t0 = global_ns();
           while (global_ns() - t0 < 1000000ull) __nanosleep(1000);
         }
-      } else {
+      } else if (!PAIR || !ok) {
 #pragma unroll
         for (int s = 0; s < STAGES; ++s)
           if (last_parity[s] >= 0) mbar_wait(&full[s], (uint32_t)last_parity[s], wd, SITE_DRAIN);
