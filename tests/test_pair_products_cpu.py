@@ -32,3 +32,17 @@ def test_the_second_cta_stays_for_the_first_ones_commits(text):
     assert re.search(r"last_parity\[s\] >= 0\) ok = mbar_wait\(&empty\[s\], \(uint32_t\)last_parity\[s\], wb", leaving)
     sums = text[text.index("setmaxnreg.inc"):]
     assert re.search(r"mbar_wait_poll\(&acc_full\[acc\], acc_phase", sums)
+
+
+def test_lanes_of_the_sums_stay_together_when_a_wait_gives_up(text):
+    """A lane whose wait gave up must not leave the others in a tensor memory load of the whole warp: what it goes
+    through does not depend on its own waits, and the warp meets between a wait and the loads."""
+    sums = text[text.index("setmaxnreg.inc"):]
+    loop = re.search(r"for \(int kb = kb0; ([^;]*); \+\+kb\) \{(.*?)tc_fence_after\(\);", sums, flags=re.S)
+    assert loop.group(1) == "kb < kb1" and "break" not in loop.group(2)
+    assert re.search(r"if \(ok && !ready\) ok = mbar_wait_poll\(&acc_full.*?;\s*__syncwarp\(\);\s*$", loop.group(2), flags=re.S)
+    # `ok` guards waits and arrivals alone
+    uses = re.findall(r"if \(([^()]*\bok\b[^()]*)\)\s*(\{|\w+[^;]*;)", sums[:sums.index("if constexpr (TURNED)")])
+    assert {u[0] for u in uses} == {"ok && !ready", "lane == 0 && ok", "ok && kb + 1 < kb1", "ok && kb0 < kb1"}
+    # a lane that gave up arrives nowhere
+    assert not re.search(r"if \(lane == 0\)", sums[:sums.index("if constexpr (TURNED)")])
