@@ -228,6 +228,12 @@ __device__ __forceinline__ uint32_t largest(const float (&x)[4]) {
   return top;
 }
 
+// The scale of a block of a state: NaN where one of its values is infinite or NaN. An infinite scale would leave those
+// that are above zero infinite, and their weights standing still.
+__device__ __forceinline__ float state_scale(uint32_t top) {
+  return top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : e4m3_scale(top);
+}
+
 // m, v and p from the gradient g. Every product of m and v is rounded by itself: a state's bits follow from
 // the formula alone, and with them the border at which its 8 bits are rounded up. The update takes an
 // approximate root and quotient, off by two units each; the root of a v below 2^-126 is 0 (it would be under
@@ -298,8 +304,8 @@ __device__ __forceinline__ void update_chunk(const Table<N>& t, int i, unsigned 
     update(a, s, p, g, m, v);
     store_weight(t, i, f, weight_key, high, p);
     if constexpr (STATE8) {
-      const float m_scale = e4m3_scale(__reduce_max_sync(0xffffffffu, largest(m)));
-      const float v_scale = e4m3_scale(__reduce_max_sync(0xffffffffu, largest(v)));
+      const float m_scale = state_scale(__reduce_max_sync(0xffffffffu, largest(m)));
+      const float v_scale = state_scale(__reduce_max_sync(0xffffffffu, largest(v)));
       uint32_t low[4], up[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {

@@ -814,7 +814,9 @@ tsp_status tsp_matmul_e4m3(int64_t m, int64_t n, int64_t k, const uint8_t* a, in
  * 8-bit states, and bf16 weights without a master, are rounded stochastically: to the upper
  * neighbour with the probability of the distance from the lower one, by random bits that are a
  * function of seed, t, the tensor's place in the list and the element. A v above zero is not
- * rounded to zero. A block of a state that holds a NaN or an infinity is NaN from then on.
+ * rounded to zero. A block of an 8-bit state that comes to hold a NaN or an infinity (the square of a gradient may
+ * overflow) has a NaN as its scale: all of it is NaN from then on, and with the next step its weights are. In 32 bits such
+ * a value stays with its element.
  *
  * The lists are HOST arrays, read during the call; norm, device_lr and device_t are on the device.
  * device_lr and device_t, where given, are read instead of lr and t when the kernel runs: a captured step
