@@ -236,8 +236,10 @@ __device__ __forceinline__ float state_scale(uint32_t top) {
 
 // m, v and p from the gradient g. Every product of m and v is rounded by itself: a state's bits follow from
 // the formula alone, and with them the border at which its 8 bits are rounded up. The update takes an
-// approximate root and quotient, off by two units each; the root of a v below 2^-126 is 0 (it would be under
-// 1.1e-19, far below any eps).
+// approximate root and quotient, off by two units each. FULL_RANGE: they take numbers below 2^-126 as they are.
+// Without, such a v counts as 0 in the root (it would be under 2^-63), and so does such a numerator: see
+// tsp_adamw_step for where that is done.
+template <bool FULL_RANGE>
 __device__ __forceinline__ void update(const Step& a, const Shared& s, float (&p)[4], const float (&g)[4], float (&m)[4],
                                        float (&v)[4]) {
 #pragma unroll
@@ -245,10 +247,12 @@ __device__ __forceinline__ void update(const Step& a, const Shared& s, float (&p
     const float x = __fmul_rn(g[e], s.factor);
     m[e] = __fadd_rn(__fmul_rn(a.beta1, m[e]), __fmul_rn(a.one_beta1, x));
     v[e] = __fadd_rn(__fmul_rn(a.beta2, v[e]), __fmul_rn(a.one_beta2, __fmul_rn(x, x)));
-    float root;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(v[e]));
-    float quotient;
-    asm("div.approx.ftz.f32 %0, %1, %2;" : "=f"(quotient) : "f"(s.rate * m[e]), "f"(fmaf(root, s.root, a.eps)));
+    float root, quotient;
+    if constexpr (FULL_RANGE) asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v[e]));
+    else asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(v[e]));
+    const float above = s.rate * m[e], below = fmaf(root, s.root, a.eps);
+    if constexpr (FULL_RANGE) asm("div.approx.f32 %0, %1, %2;" : "=f"(quotient) : "f"(above), "f"(below));
+    else asm("div.approx.ftz.f32 %0, %1, %2;" : "=f"(quotient) : "f"(above), "f"(below));
     p[e] -= fmaf(s.shrink, p[e], quotient);
   }
 }
@@ -279,7 +283,7 @@ __device__ __forceinline__ void store_weight(const Table<N>& t, int i, const F& 
 
 // A chunk, 128 elements per warp and pass. FULL: it is whole. scales: of the chunk's m and v, old ones in, new
 // ones out.
-template <int N, bool STATE8, bool VEC, bool FULL>
+template <int N, bool STATE8, bool FULL_RANGE, bool VEC, bool FULL>
 __device__ __forceinline__ void update_chunk(const Table<N>& t, int i, unsigned long long chunk_at, int n,
                                              const Step& a, const Shared& s, float (*scales)[kChunk / 128]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -301,7 +305,7 @@ __device__ __forceinline__ void update_chunk(const Table<N>& t, int i, unsigned 
       f.load32(t.m[i], m);
       f.load32(t.v[i], v);
     }
-    update(a, s, p, g, m, v);
+    update<FULL_RANGE>(a, s, p, g, m, v);
     store_weight(t, i, f, weight_key, high, p);
     if constexpr (STATE8) {
       const float m_scale = state_scale(__reduce_max_sync(0xffffffffu, largest(m)));
@@ -327,7 +331,7 @@ __device__ __forceinline__ void update_chunk(const Table<N>& t, int i, unsigned 
 }
 
 // Six CTAs per SM: with 56 registers and four of them 8-bit states take 646 us instead of 632.
-template <int N, bool STATE8>
+template <int N, bool STATE8, bool FULL_RANGE>
 __global__ void __launch_bounds__(kThreads, 6) adamw_kernel(const __grid_constant__ Table<N> t,
                                                          const __grid_constant__ Step a) {
   __shared__ Shared shared;
@@ -356,9 +360,9 @@ __global__ void __launch_bounds__(kThreads, 6) adamw_kernel(const __grid_constan
     }
     __syncthreads();
   }
-  if (!(t.kind[lo] & ALIGNED)) update_chunk<N, STATE8, false, false>(t, lo, at, n, a, s, scales);
-  else if (n == kChunk) update_chunk<N, STATE8, true, true>(t, lo, at, n, a, s, scales);
-  else update_chunk<N, STATE8, true, false>(t, lo, at, n, a, s, scales);
+  if (!(t.kind[lo] & ALIGNED)) update_chunk<N, STATE8, FULL_RANGE, false, false>(t, lo, at, n, a, s, scales);
+  else if (n == kChunk) update_chunk<N, STATE8, FULL_RANGE, true, true>(t, lo, at, n, a, s, scales);
+  else update_chunk<N, STATE8, FULL_RANGE, true, false>(t, lo, at, n, a, s, scales);
   if constexpr (STATE8) {
     __syncthreads();
     if (scale) *scale = scales[threadIdx.x >> 5][threadIdx.x & 31];
@@ -445,7 +449,7 @@ tsp_status check_overlap(const char* what, const List& l) {
   return TSP_OK;
 }
 
-template <int N, bool STATE8>
+template <int N, bool STATE8, bool FULL_RANGE>
 tsp_status run(const List& l, const Step& a, cudaStream_t s) {
   static_assert(sizeof(Table<N>) + sizeof(Step) <= 32 * 1024 - 4, "kernel parameters");
   Table<N> t;
@@ -453,7 +457,7 @@ tsp_status run(const List& l, const Step& a, cudaStream_t s) {
   auto flush = [&](unsigned int chunks) -> tsp_status {
     if (t.count == 0) return TSP_OK;
     t.first[t.count] = chunks;
-    adamw_kernel<N, STATE8><<<chunks, kThreads, 0, s>>>(t, a);
+    adamw_kernel<N, STATE8, FULL_RANGE><<<chunks, kThreads, 0, s>>>(t, a);
     const cudaError_t e = cudaGetLastError();
     t.count = 0;
     return e == cudaSuccess ? TSP_OK : cuda_fail(e, "adamw: launch");
@@ -508,7 +512,7 @@ tsp_status tsp_adamw_step(int n, void* const* params, const int* types, void* co
   const tsp_adamw& h = *step;
   if (!(h.beta1 >= 0. && h.beta1 < 1.) || !(h.beta2 >= 0. && h.beta2 < 1.))
     return fail(TSP_ERR_INVALID_ARG, w + ": betas in [0, 1)");
-  // the quotient by it flushes what is smaller, and 0 / 0 is NaN
+  // the approximate quotient takes no smaller divisor
   if (!((float)h.eps >= 1.17549435e-38f) || !std::isfinite(h.eps))
     return fail(TSP_ERR_INVALID_ARG, w + ": eps must be finite and at least 2^-126");
   if (!h.device_lr && !(h.lr >= 0. && std::isfinite(h.lr))) return fail(TSP_ERR_INVALID_ARG, w + ": lr must be finite, not negative");
@@ -528,8 +532,14 @@ tsp_status tsp_adamw_step(int n, void* const* params, const int* types, void* co
                (float)(h.lr * h.weight_decay), (float)h.max_norm, h.lr, h.weight_decay, log1, log2, (long long)h.t,
                h.seed, h.norm, h.device_lr, reinterpret_cast<const long long*>(h.device_t)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (n <= kSmall) return state_bits == 8 ? run<kSmall, true>(l, a, s) : run<kSmall, false>(l, a, s);
-  return state_bits == 8 ? run<kLarge, true>(l, a, s) : run<kLarge, false>(l, a, s);
+  // With 8-bit states, whose kernel is bound by its instructions, numbers below 2^-126 count as 0 in root and quotient
+  // where eps is so far above that it does not show: the root, at most 2^-63 / sqrt(1 - beta2^t), is below 2^-24 of eps,
+  // and a step that is lost, below 2^-126 / eps, below 2^-87. 202M weights with masters 632 us, and 655 with a smaller
+  // eps. With 32-bit states every number counts: 866 us either way.
+  const bool full = !(h.eps >= std::ldexp(1. / std::sqrt(1. - h.beta2), -39));
+  auto small = state_bits == 32 ? run<kSmall, false, true> : full ? run<kSmall, true, true> : run<kSmall, true, false>;
+  auto large = state_bits == 32 ? run<kLarge, false, true> : full ? run<kLarge, true, true> : run<kLarge, true, false>;
+  return (n <= kSmall ? small : large)(l, a, s);
   TSP_GUARD_END
 }
 

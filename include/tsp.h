@@ -802,8 +802,8 @@ tsp_status tsp_matmul_e4m3(int64_t m, int64_t n, int64_t k, const uint8_t* a, in
  *     g' = g * min(1, max_norm / (norm + 1e-6)) where norm is given (tsp_grad_norm's), else g
  *     m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
  *     p = p - lr (weight_decay p + (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps))
- * in fp32: the clipping factor is one fp32 quotient, and each product and sum of m and v is rounded; the root
- * of a v below 2^-126 counts as 0. eps is at least 2^-126, betas are in [0, 1).
+ * in fp32: the clipping factor is one fp32 quotient, and each product and sum of m and v is rounded (a g'^2 below
+ * 2^-150 is 0; where v is 0, the step goes by m / eps). eps is at least 2^-126, betas are in [0, 1).
  * params[i] is fp32 or bf16 (types[i]); a bf16 weight may have an fp32 master (masters[i], else
  * NULL; masters itself may be NULL): the master is updated and the weight is the master rounded to nearest.
  * grads[i] is fp32 or bf16 (grad_types[i]); a tensor whose grads[i] is NULL or whose size is 0 is left

@@ -72,3 +72,32 @@ def test_an_overflow_in_32_bits_stays_with_its_element(kind):
         assert torch.equal(a[~hit], b[~hit])
     assert opt.v[0][5] == math.inf and p[0][5] == before[5]  # m / infinity
     assert bool(p[0][[300, 999]].isnan().all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-8, 1e-15, 1e-25, 1e-30])
+def test_roots_of_second_moments_below_the_normal_numbers(eps, bits):
+    """v = (1 - beta2) g^2 from 2^-116 down to 300 steps of 2^-149: its root counts beside a small eps, as the rule has it.
+    g^2 and v are rounded to steps of 2^-149, half of one each; the root takes half of v's relative error."""
+    n = 4000
+    b1, b2 = BETAS
+    sign = gradient(n, 3).sign()
+    g = (10 ** torch.linspace(-20.5, -17, n, dtype=torch.float64)).float().cuda() * sign
+    p = torch.zeros(n, device="cuda")
+    tsp_opt = tsp.TSPAdamW([p], betas=BETAS, eps=eps, state_bits=bits)
+    tsp_opt.step([g], LR)
+    g = g.double()
+    v = (1 - b2) * g * g
+    want = -LR * g / ((v / (1 - b2)).sqrt() + eps)  # m is corrected to g
+    error = 20 * U + 0.5 * 2.0 ** -150 * (1 + (1 - b2)) / v
+    assert bool(((p.double() - want).abs() <= error * want.abs()).all()), float(((p.double() - want).abs() / want.abs() / error).max())
+
+
+def test_steps_whose_parts_are_below_the_normal_numbers():
+    """g^2 is 0 in fp32, so the step is rate * m / eps; rate * m, which takes half a step of 2^-149, is not lost."""
+    n, eps = 1000, 2e-37
+    g = torch.linspace(1e-37, 9e-37, n, device="cuda")
+    p = torch.zeros(n, device="cuda")
+    tsp.TSPAdamW([p], betas=BETAS, eps=eps).step([g], LR)
+    want = -LR * g.double() / eps
+    assert bool(((p.double() - want).abs() <= 20 * U * want.abs() + 2.0 ** -149 / eps).all())
