@@ -34,7 +34,7 @@ __all__ = [
     "tsp_packed_attention_workspace_bytes", "tsp_status_init", "tsp_packed_attention_fwd",
     "tsp_packed_attention_bwd", "tsp_rmsnorm_fwd", "tsp_rmsnorm_fwd_e4m3", "tsp_rmsnorm_workspace_bytes", "tsp_rmsnorm_bwd",
     "tsp_grad_workspace_bytes", "tsp_grad_norm", "tsp_grad_clip", "tsp_quantize_e4m3",
-    "tsp_matmul_e4m3_workspace_bytes", "tsp_matmul_e4m3", "tsp_adamw_step",
+    "tsp_matmul_e4m3_workspace_bytes", "tsp_matmul_e4m3", "tsp_adamw_step", "tsp_adamw_check",
 ]
 
 TSP_OK, TSP_ERR_INVALID_ARG, TSP_ERR_UNSUPPORTED, TSP_ERR_CUDA, TSP_ERR_TIMEOUT = range(5)
@@ -158,6 +158,7 @@ _SIGS = {
     "tsp_matmul_e4m3_workspace_bytes": (ctypes.c_size_t, []),
     "tsp_matmul_e4m3": (_I, [_L, _L, _L, _P, _L, _P, _P, _L, _P, _I, _P, _L, _I, _I, _P, _P]),
     "tsp_adamw_step": (_I, [_I] + [_P] * 10 + [_I, ctypes.POINTER(AdamW), _P]),
+    "tsp_adamw_check": (_I, [_I] + [_P] * 10 + [_I, ctypes.POINTER(AdamW)]),
 }
 
 
@@ -956,21 +957,30 @@ def _adamw_lists(params, masters, m, v, m_scales, v_scales):
     return lists
 
 
-def _adamw_launch(lists, grads, step, stream):
+def _adamw_call(lists, grads, step):
+    """(device, the library's arguments but for the stream, what they point into), checked by the binding; no
+    device: nothing to do."""
     p, masters, m, v, ms, vs = lists
     g = TensorList(grads, "gradients").like(p, "gradients")
     at = lambda x: None if x is None else _at(x.pointers)  # noqa: E731
-    if p.device is None:
-        return
-    _launch("tsp_adamw_step", p.device, stream, p.n, at(p), _at(p.types), at(masters), at(g), _at(g.types), at(m),
-            at(v), at(ms), at(vs), _at(p.sizes), 32 if ms is None else 8, ctypes.byref(step))
+    return p.device, (p.n, at(p), _at(p.types), at(masters), at(g), _at(g.types), at(m), at(v), at(ms), at(vs), _at(p.sizes),
+                      32 if ms is None else 8, ctypes.byref(step)), (lists, g, step)
 
 
-def tsp_adamw_step(params, grads, m, v, lr, t, masters=None, m_scales=None, v_scales=None, betas=(0.9, 0.999),
-                   eps=1e-8, weight_decay=0.0, norm=None, max_norm=float("inf"), seed=0, stream=None):
-    """One AdamW step over lists of tensors, in place; see TSPAdamW, which keeps the states. m and v
-    are float32, or float8_e4m3fn with m_scales and v_scales. grads and masters may hold None. lr and t
-    are numbers, or one float32 and one int64 value on the device, read when the kernel runs."""
+def _adamw_launch(call, stream):
+    device, args, _ = call
+    if device is not None:
+        _launch("tsp_adamw_step", device, stream, *args)
+
+
+def _adamw_check(call):
+    device, args, _ = call
+    if device is not None:
+        _check(load_library().tsp_adamw_check(*args), "tsp_adamw_check")
+
+
+def _adamw_arguments(params, grads, m, v, lr, t, masters=None, m_scales=None, v_scales=None, betas=(0.9, 0.999),
+                     eps=1e-8, weight_decay=0.0, norm=None, max_norm=float("inf"), seed=0):
     lists = _adamw_lists(params, masters, m, v, m_scales, v_scales)
     device = lists[0].device
     dev = lambda x: isinstance(x, torch.Tensor)  # noqa: E731
@@ -978,7 +988,21 @@ def tsp_adamw_step(params, grads, m, v, lr, t, masters=None, m_scales=None, v_sc
                  seed & 0xFFFFFFFF, _scalar(norm, "norm", torch.float32, device),
                  _scalar(lr, "lr", torch.float32, device) if dev(lr) else None,
                  _scalar(t, "t", torch.int64, device) if dev(t) else None)
-    _adamw_launch(lists, grads, step, stream)
+    return _adamw_call(lists, grads, step)
+
+
+def tsp_adamw_step(params, grads, m, v, lr, t, masters=None, m_scales=None, v_scales=None, betas=(0.9, 0.999),
+                   eps=1e-8, weight_decay=0.0, norm=None, max_norm=float("inf"), seed=0, stream=None):
+    """One AdamW step over lists of tensors, in place; see TSPAdamW, which keeps the states. m and v
+    are float32, or float8_e4m3fn with m_scales and v_scales. grads and masters may hold None. lr and t
+    are numbers, or one float32 and one int64 value on the device, read when the kernel runs."""
+    _adamw_launch(_adamw_arguments(params, grads, m, v, lr, t, masters, m_scales, v_scales, betas, eps, weight_decay, norm,
+                                   max_norm, seed), stream)
+
+
+def tsp_adamw_check(params, grads, m, v, lr, t, **kwargs):
+    """Raise what tsp_adamw_step would refuse with these arguments (but for stream), without a step."""
+    _adamw_check(_adamw_arguments(params, grads, m, v, lr, t, **kwargs))
 
 
 # ------------------------------------------------------------------ packed attention

@@ -499,14 +499,10 @@ tsp_status run(const List& l, const Step& a, cudaStream_t s) {
 
 using namespace tsp;
 
-extern "C" {
+namespace tsp {
+namespace {
 
-tsp_status tsp_adamw_step(int n, void* const* params, const int* types, void* const* masters,
-                          const void* const* grads, const int* grad_types, void* const* m, void* const* v,
-                          float* const* m_scales, float* const* v_scales, const int64_t* sizes, int state_bits,
-                          const tsp_adamw* step, void* stream) {
-  TSP_GUARD_BEGIN
-  const char* what = "tsp_adamw_step";
+tsp_status check_step(const char* what, const tsp_adamw* step, const List& l) {
   const std::string w(what);
   if (!step) return fail(TSP_ERR_INVALID_ARG, w + ": null step");
   const tsp_adamw& h = *step;
@@ -523,9 +519,33 @@ tsp_status tsp_adamw_step(int n, void* const* params, const int* types, void* co
   if (reinterpret_cast<uintptr_t>(h.norm) % 4 || reinterpret_cast<uintptr_t>(h.device_lr) % 4 ||
       reinterpret_cast<uintptr_t>(h.device_t) % 8)
     return fail(TSP_ERR_INVALID_ARG, w + ": norm, device_lr or device_t is misaligned");
-  const List l{n, params, types, masters, grads, grad_types, m, v, m_scales, v_scales, sizes, state_bits};
   TSP_TRY(check_list(what, l));
-  TSP_TRY(check_overlap(what, l));
+  return check_overlap(what, l);
+}
+
+}  // namespace
+}  // namespace tsp
+
+extern "C" {
+
+tsp_status tsp_adamw_check(int n, void* const* params, const int* types, void* const* masters,
+                           const void* const* grads, const int* grad_types, void* const* m, void* const* v,
+                           float* const* m_scales, float* const* v_scales, const int64_t* sizes, int state_bits,
+                           const tsp_adamw* step) {
+  TSP_GUARD_BEGIN
+  return check_step("tsp_adamw_check", step,
+                    {n, params, types, masters, grads, grad_types, m, v, m_scales, v_scales, sizes, state_bits});
+  TSP_GUARD_END
+}
+
+tsp_status tsp_adamw_step(int n, void* const* params, const int* types, void* const* masters,
+                          const void* const* grads, const int* grad_types, void* const* m, void* const* v,
+                          float* const* m_scales, float* const* v_scales, const int64_t* sizes, int state_bits,
+                          const tsp_adamw* step, void* stream) {
+  TSP_GUARD_BEGIN
+  const List l{n, params, types, masters, grads, grad_types, m, v, m_scales, v_scales, sizes, state_bits};
+  TSP_TRY(check_step("tsp_adamw_step", step, l));
+  const tsp_adamw& h = *step;
   const double log1 = std::log(h.beta1), log2 = std::log(h.beta2);
   const Step a{(float)h.beta1, (float)h.beta2, (float)(1. - h.beta1), (float)(1. - h.beta2), (float)h.eps,
                (float)(h.lr / -std::expm1((double)h.t * log1)), (float)(1. / std::sqrt(-std::expm1((double)h.t * log2))),

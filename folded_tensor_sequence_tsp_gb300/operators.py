@@ -16,7 +16,7 @@ from typing import NamedTuple
 
 import torch
 
-from ._binding import (AdamW, TSP_OK, TSPError, _adamw_launch, _adamw_lists, _launch, _matrix, _rows, _same_device,
+from ._binding import (AdamW, TSP_OK, TSPError, _adamw_call, _adamw_check, _adamw_launch, _adamw_lists, _launch, _matrix, _rows, _same_device,
                        _scalar, tsp_device_status, tsp_grad_clip, tsp_grad_norm,
                        tsp_grad_workspace_bytes, tsp_last_error, tsp_matmul_e4m3_workspace_bytes, tsp_packed_attention_bwd,
                        tsp_packed_attention_fwd,
@@ -444,13 +444,7 @@ class TSPAdamW:
         self.t, self.m, self.v, self.m_scales, self.v_scales = t, m, v, m_scales, v_scales
         self._lists = lists
 
-    def step(self, grads, lr, norm=None, max_norm=float("inf"), t=None, stream=None):
-        """One step with the gradients of all weights (None: that weight is left as it is).
-
-        norm: the gradients' global norm, one float32 on the device (TSPGradClip.norm); they are
-        then scaled to a norm of at most max_norm on the way. lr may be one float32 on the device,
-        and t one int64, this step's number from 1, in place of the object's own count: a captured
-        step is then replayed with their values of that moment."""
+    def _call(self, grads, lr, norm, max_norm, t):
         device = self.device.index
         step = AdamW(0.0, *self.betas, self.eps, self.weight_decay, max_norm, self.t + 1, self.seed & 0xFFFFFFFF,
                      _scalar(norm, "norm", torch.float32, device), None, None)
@@ -460,6 +454,27 @@ class TSPAdamW:
             step.lr = lr
         if t is not None:
             step.device_t = _scalar(t, "t", torch.int64, device)
-        _adamw_launch(self._lists, grads, step, stream)
+        return _adamw_call(self._lists, grads, step)
+
+    def _run(self, call, t, stream):
+        _adamw_launch(call, stream)
         if t is None:
             self.t += 1
+
+    def step(self, grads, lr, norm=None, max_norm=float("inf"), t=None, stream=None):
+        """One step with the gradients of all weights (None: that weight is left as it is).
+
+        norm: the gradients' global norm, one float32 on the device (TSPGradClip.norm); they are
+        then scaled to a norm of at most max_norm on the way. lr may be one float32 on the device,
+        and t one int64, this step's number from 1, in place of the object's own count: a captured
+        step is then replayed with their values of that moment."""
+        self._run(self._call(grads, lr, norm, max_norm, t), t, stream)
+
+
+def _step_together(optimizers, parts, lr, norm, max_norm, t, stream=None):
+    """A step of each optimizer with its part of the gradients, or, where one refuses, of none."""
+    calls = [o._call(part, lr, norm, max_norm, t) for o, part in zip(optimizers, parts)]
+    for call in calls[1:]:  # the first step refuses before anything runs
+        _adamw_check(call)
+    for optimizer, call in zip(optimizers, calls):
+        optimizer._run(call, t, stream)

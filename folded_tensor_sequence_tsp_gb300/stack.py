@@ -19,7 +19,7 @@ from ._binding import (TSP_OK, TSPError, tsp_attention_bwd, tsp_attention_fwd, t
                        tsp_device_status, tsp_last_error, tsp_mlp_bwd, tsp_mlp_fwd, tsp_pack_weights,
                        tsp_packed_weight_bytes, tsp_plan, tsp_plan_batched, tsp_workspace_bytes,
                        tsp_workspace_init)
-from .operators import TSPAdamW, TSPGradClip, TSPRMSNorm, _device, _not_in_a_capture, _ready
+from .operators import TSPAdamW, TSPGradClip, TSPRMSNorm, _device, _not_in_a_capture, _ready, _step_together
 
 __all__ = ["TSPStack"]
 
@@ -173,13 +173,13 @@ class TSPStack:
     @_on_its_device
     def step(self, grads, lr, max_norm=float("inf"), t=None):
         """One AdamW step with backward()'s grads, scaled on the way to a global norm of at most max_norm;
-        returns the norm as one float32 on the device. grads are left as they are. lr and t as in TSPAdamW.step."""
+        returns the norm as one float32 on the device. grads are left as they are. lr and t as in TSPAdamW.step. What
+        is refused leaves every weight and state as it was."""
         if self.optimizers is None:
             raise RuntimeError("TSPStack.step() needs enable_updates()")
         norm = self.clipper.norm(grads)
         n = len(self.wpack)
-        for optimizer, part in zip(self.optimizers, (grads[:n], grads[n:])):
-            optimizer.step(part, lr, norm=norm, max_norm=max_norm, t=t)
+        _step_together(self.optimizers, (grads[:n], grads[n:]), lr, norm, max_norm, t)
         return norm
 
     @_on_its_device

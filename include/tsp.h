@@ -839,6 +839,15 @@ tsp_status tsp_adamw_step(int n, void* const* params, const int* types, void* co
                           const tsp_adamw* step, void* stream);
 
 /*
+ * tsp_adamw_check - the refusals of tsp_adamw_step without the step: a program whose weights are in several lists
+ * checks every list before it steps the first. Runs on the host alone.
+ */
+tsp_status tsp_adamw_check(int n, void* const* params, const int* types, void* const* masters,
+                           const void* const* grads, const int* grad_types, void* const* m, void* const* v,
+                           float* const* m_scales, float* const* v_scales, const int64_t* sizes, int state_bits,
+                           const tsp_adamw* step);
+
+/*
  * tsp_device_status - synchronise `stream`, then read and clear the workspace
  * status word. Returns TSP_OK, TSP_ERR_TIMEOUT (a bounded device wait gave up; the
  * outputs of the affected call are undefined), TSP_ERR_UNSUPPORTED (a kernel whose

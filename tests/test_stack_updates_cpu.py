@@ -1,0 +1,97 @@
+"""TSPStack's AdamW steps on the host: what a refused step leaves, seeds, masters. No GPU: what allocates or
+launches is replaced, the library's checks run."""
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+tsp = pytest.importorskip("folded_tensor_sequence_tsp_gb300")
+B = tsp._binding
+operators, stack_module = tsp.operators, tsp.stack
+
+
+@pytest.fixture
+def host(monkeypatch):
+    """CPU tensors pass for those of device 0; launches are listed by name."""
+    import os
+    if not os.path.exists(B.library_path()):
+        import __graft_entry__
+        __graft_entry__.build()
+    launched = []
+
+    class Device:
+        def __init__(self, device):
+            pass
+
+        def __enter__(self):
+            pass
+
+        def __exit__(self, *exc):
+            pass
+
+    def get_device(t):
+        if t is None:
+            raise TypeError  # as the method itself does
+        return 0
+
+    device = SimpleNamespace(index=0)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.Tensor, "get_device", get_device)
+    monkeypatch.setattr(torch.Tensor, "device", device)
+    monkeypatch.setattr(operators, "_device", lambda d: device)
+    monkeypatch.setattr(operators, "_not_in_a_capture", lambda *a: None)
+    monkeypatch.setattr(operators, "_ready", lambda d: None)
+    zeros = torch.zeros
+    monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **k: zeros(*a, **k))
+    monkeypatch.setattr(B, "_launch", lambda name, *args: launched.append(name))
+    return SimpleNamespace(launched=launched, device=device)
+
+
+def made(host, **kw):
+    stack = object.__new__(tsp.TSPStack)
+    stack.device = host.device
+    stack.wpack = [torch.randn(300).bfloat16(), torch.randn(257).bfloat16()]
+    stack.norms = [torch.ones(64).bfloat16() for _ in range(5)]
+    stack.clipper = SimpleNamespace(norm=lambda grads: torch.ones(()))
+    stack.masters = stack.optimizers = None
+    stack.enable_updates(**kw)
+    return stack
+
+
+def gradients(stack):
+    return [torch.ones(p.numel()) for p in stack.wpack + stack.norms]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("wrong", ["short", "long", "a norm's size", "a norm's type", "over a norm's master", "a norm itself",
+                                   "max_norm", "a matrix's size"])
+def test_a_refused_step_steps_nothing(host, wrong, bits):
+    stack = made(host, state_bits=bits)
+    grads, kw = gradients(stack), {}
+    n = len(stack.wpack)
+    if wrong == "short":
+        grads = grads[:-1]
+    elif wrong == "long":
+        grads.append(torch.ones(64))
+    elif wrong == "a norm's size":
+        grads[n + 1] = torch.ones(63)
+    elif wrong == "a norm's type":
+        grads[-1] = torch.ones(64, dtype=torch.float64)
+    elif wrong == "over a norm's master":
+        grads[-1] = stack.masters[1][-1]
+    elif wrong == "a norm itself":
+        grads[-1] = stack.norms[-1]
+    elif wrong == "max_norm":
+        kw["max_norm"] = -1.0
+    else:
+        grads[0] = torch.ones(301)
+    with pytest.raises((ValueError, B.TSPError)):
+        stack.step(grads, 1e-3, **kw)
+    assert host.launched == []
+    assert [o.t for o in stack.optimizers] == [0, 0]
+
+
+def test_a_step_steps_both_lists(host):
+    stack = made(host)
+    stack.step(gradients(stack), 1e-3, max_norm=1.0)
+    assert host.launched == ["tsp_adamw_step"] * 2 and [o.t for o in stack.optimizers] == [1, 1]
