@@ -167,8 +167,10 @@ class TSPStack:
         params = (self.wpack, self.norms)
         self.masters = [[p.float() for p in ps] for ps in params]
         self.optimizers = [TSPAdamW(ps, masters=ms, betas=betas, eps=eps, weight_decay=decay, state_bits=state_bits,
-                                    seed=seed + i, device=self.device)
-                           for i, (ps, ms, decay) in enumerate(zip(params, self.masters, (weight_decay, 0.0)))]
+                                    seed=s, device=self.device)
+                           for ps, ms, decay, s in zip(params, self.masters, (weight_decay, 0.0),
+                                                       # random bits go by seed + t: no step of one has the other's
+                                                       (seed, seed ^ 0x80000000))]
 
     @_on_its_device
     def step(self, grads, lr, max_norm=float("inf"), t=None):

@@ -95,3 +95,12 @@ def test_a_step_steps_both_lists(host):
     stack = made(host)
     stack.step(gradients(stack), 1e-3, max_norm=1.0)
     assert host.launched == ["tsp_adamw_step"] * 2 and [o.t for o in stack.optimizers] == [1, 1]
+
+
+@pytest.mark.parametrize("seed", [0, 5, (1 << 32) - 1, -3])
+def test_the_lists_random_bits_do_not_meet(host, seed):
+    """A step's key goes by seed + t in 32 bits: the two lists' are 2^31 apart, so that no step of one has the key of a
+    step of the other."""
+    a, b = made(host, seed=seed).optimizers
+    assert a.seed & 0xFFFFFFFF == seed & 0xFFFFFFFF
+    assert (a.seed - b.seed) & 0xFFFFFFFF == 1 << 31
