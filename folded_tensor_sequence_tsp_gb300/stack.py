@@ -163,9 +163,18 @@ class TSPStack:
     def enable_updates(self, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, state_bits=32, seed=0):
         """Make what step() needs: fp32 masters of the weights as they are now, and the states (fp32, or e4m3
         with state_bits 8). Weight decay is for the matrices; the norm weights, which are the caller's
-        tensors and updated in place, have none."""
+        tensors and updated in place, have none.
+
+        Called again, it makes new states and keeps the masters, but for weights that have been written since: those
+        are their masters' new values. A step that was captured before is not replayed after it."""
+        _not_in_a_capture(self.device, "TSPStack.enable_updates()")
         params = (self.wpack, self.norms)
-        self.masters = [[p.float() for p in ps] for ps in params]
+        if self.masters is None:
+            self.masters = [[p.float() for p in ps] for ps in params]
+        else:
+            for ps, ms in zip(params, self.masters):
+                for p, m in zip(ps, ms):
+                    m.copy_(torch.where(m.bfloat16() == p, m, p.float()))
         self.optimizers = [TSPAdamW(ps, masters=ms, betas=betas, eps=eps, weight_decay=decay, state_bits=state_bits,
                                     seed=s, device=self.device)
                            for ps, ms, decay, s in zip(params, self.masters, (weight_decay, 0.0),

@@ -48,3 +48,19 @@ def test_a_refused_step_leaves_everything(bits):
     assert all(torch.equal(a, b) for a, b in zip(before, everything(stack))) and [o.t for o in stack.optimizers] == [1, 1]
     stack.step(grads, 1e-3)
     assert not any(torch.equal(a, b) for a, b in zip(before[:9], everything(stack))) and [o.t for o in stack.optimizers] == [2, 2]
+
+
+def test_updates_enabled_again_go_on_from_the_masters():
+    stack, grads = made()
+    for _ in range(3):
+        stack.step(grads, 1e-4)
+    masters = [m.clone() for ms in stack.masters for m in ms]
+    assert not all(torch.equal(p.float(), m) for p, m in zip(stack.wpack + stack.norms, masters))
+    stack.norms[0].fill_(0.75)
+    stack.enable_updates(state_bits=8)
+    written = masters[len(stack.wpack)]
+    written[written.bfloat16() != 0.75] = 0.75  # what the others hold beyond the weight stays
+    assert all(torch.equal(a, b) for a, b in zip(masters, [m for ms in stack.masters for m in ms]))
+    stack.step(grads, 1e-4)
+    assert [o.t for o in stack.optimizers] == [1, 1]
+    assert all(torch.equal(p, m.bfloat16()) for p, m in zip(stack.wpack + stack.norms, [m for ms in stack.masters for m in ms]))

@@ -39,7 +39,8 @@ def host(monkeypatch):
     monkeypatch.setattr(torch.Tensor, "get_device", get_device)
     monkeypatch.setattr(torch.Tensor, "device", device)
     monkeypatch.setattr(operators, "_device", lambda d: device)
-    monkeypatch.setattr(operators, "_not_in_a_capture", lambda *a: None)
+    for module in (operators, stack_module):
+        monkeypatch.setattr(module, "_not_in_a_capture", lambda *a: None)
     monkeypatch.setattr(operators, "_ready", lambda d: None)
     zeros = torch.zeros
     monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **k: zeros(*a, **k))
@@ -104,3 +105,38 @@ def test_the_lists_random_bits_do_not_meet(host, seed):
     a, b = made(host, seed=seed).optimizers
     assert a.seed & 0xFFFFFFFF == seed & 0xFFFFFFFF
     assert (a.seed - b.seed) & 0xFFFFFFFF == 1 << 31
+
+
+def test_updates_enabled_again_keep_what_the_masters_hold(host):
+    """States begin anew, the masters do not: they hold more than the bfloat16 weights. A weight that has been written
+    since is its master's new value."""
+    stack = made(host, seed=1)
+    masters = [m for ms in stack.masters for m in ms]
+    with torch.no_grad():
+        for m in masters:
+            m.mul_(1 + 2.0 ** -12)  # less than half a step of bfloat16
+    for p, m in zip(stack.wpack + stack.norms, masters):
+        p.copy_(m)
+    stack.wpack[1][7:9] = 3.0
+    stack.norms[2].fill_(0.5)
+    want = [m.clone() for m in masters]
+    want[1][7:9], want[len(stack.wpack) + 2][:] = 3.0, 0.5
+    stack.step(gradients(stack), 1e-3)
+    stack.enable_updates(seed=2, state_bits=8)
+    again = [m for ms in stack.masters for m in ms]
+    assert all(torch.equal(a, b) for a, b in zip(again, want)) and all(a is b for a, b in zip(again, masters))
+    assert [o.t for o in stack.optimizers] == [0, 0] and [o.state_bits for o in stack.optimizers] == [8, 8]
+    assert all(a is b for o, ms in zip(stack.optimizers, stack.masters) for a, b in zip(o.masters, ms))
+
+
+def test_updates_are_not_enabled_in_a_capture(host, monkeypatch):
+    stack = made(host)
+    before = stack.masters, stack.optimizers
+
+    def capturing(device, what):
+        raise RuntimeError(f"{what} cannot be captured")
+    monkeypatch.setattr(stack_module, "_not_in_a_capture", capturing)
+    monkeypatch.setattr(torch, "where", lambda *a: pytest.fail("work before the refusal"))
+    with pytest.raises(RuntimeError, match="enable_updates"):
+        stack.enable_updates()
+    assert stack.masters is before[0] and stack.optimizers is before[1]
