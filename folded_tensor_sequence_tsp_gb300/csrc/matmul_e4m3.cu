@@ -30,6 +30,7 @@
 
 #include <algorithm>
 
+#include "extent.h"
 #include "tile_walk.h"
 #include "tsp_device.cuh"
 #include "tsp_internal.h"
@@ -752,10 +753,11 @@ tsp_status tsp_matmul_e4m3(int64_t m, int64_t n, int64_t k, const uint8_t* a, in
     return fail(TSP_ERR_INVALID_ARG, w + ": row stride of a or b");
   if (reinterpret_cast<uintptr_t>(a_scales) % 4 || reinterpret_cast<uintptr_t>(b_scales) % 4)
     return fail(TSP_ERR_INVALID_ARG, w + ": scales not aligned to their element");
-  if (c == static_cast<const void*>(a) || c == static_cast<const void*>(b) || c == static_cast<const void*>(a_scales) ||
-      c == static_cast<const void*>(b_scales))
-    return fail(TSP_ERR_INVALID_ARG, w + ": c aliases an input");
   const int64_t nkb = (k + BK - 1) / BK;
+  const int64_t sa = m * nkb * 4, sb = (b_block == 1 ? n : (n + 127) / 128) * nkb * 4;
+  const Extent out = extent(c, m, n * es, ld_c * es);
+  for (const Extent& in : {extent(a, m, k, ld_a), extent(b, n, k, ld_b), extent(a_scales, 1, sa, sa), extent(b_scales, 1, sb, sb)})
+    if (overlaps(out, in)) return fail(TSP_ERR_INVALID_ARG, w + ": c aliases an input");
   const Operand oa{a, m, ld_a, a_scales, nkb, 0};
   const Operand ob{b, n, ld_b, b_scales, nkb, b_block == 1 ? 0 : 7};
   Params p{};

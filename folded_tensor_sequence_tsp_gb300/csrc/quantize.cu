@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "e4m3.cuh"
+#include "extent.h"
 #include "tsp_internal.h"
 
 namespace tsp {
@@ -415,12 +416,17 @@ tsp_status tsp_quantize_e4m3(int64_t rows, int64_t width, const void* x, int x_f
     return fail(TSP_ERR_INVALID_ARG, n + ": row stride below the row's length");
   if (ld_x > (1ll << 40) || ld_y > (1ll << 40) || ld_yt > (1ll << 40))
     return fail(TSP_ERR_UNSUPPORTED, n + ": row stride too large");
-  if (x == y || x == yt || (y && y == yt) || (scales && scales == scales_t))
-    return fail(TSP_ERR_INVALID_ARG, n + ": an output aliases another buffer");
+  const int64_t groups = (width + kBlock - 1) / kBlock, groups_t = (rows + kBlock - 1) / kBlock;
   // blocks are counted in 32 bits, and a tile is a CTA
-  const int64_t groups = (width + kBlock - 1) / kBlock;
   if (rows * groups > most || ((rows + kBlock - 1) / kBlock) * groups > most)
     return fail(TSP_ERR_UNSUPPORTED, n + ": too many blocks");
+  const int64_t rs = y ? (block == 1 ? rows : groups_t) * groups * 4 : 0;
+  const int64_t ts = yt ? (block == 1 ? width : groups) * groups_t * 4 : 0;
+  const Extent all[5] = {extent(x, rows, width * es, ld_x * es), extent(y, y ? rows : 0, width, ld_y), extent(scales, 1, rs, rs),
+                         extent(yt, yt ? width : 0, rows, ld_yt), extent(scales_t, 1, ts, ts)};
+  for (int i = 1; i < 5; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlaps(all[i], all[j])) return fail(TSP_ERR_INVALID_ARG, n + ": an output aliases another buffer");
   const QuantParams p{rows, width, x, ld_x, y, ld_y, scales, yt, ld_yt, scales_t};
   // 4 columns at a time where every row of x and y starts on their boundary
   const bool vec = width % 4 == 0 && ld_x % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * es) == 0 &&

@@ -769,7 +769,8 @@ tsp_status tsp_grad_clip(int n, const void* const* grads, void* const* outs, con
  *              transpose of the same values, scales_t that of the same scales.
  * Either of y (with scales) and yt (with scales_t) may be NULL. Short blocks at the edges are
  * blocks like the others; bytes behind a row's end are left as they were. Row strides are in elements;
- * products want those of y and yt to be multiples of 16. Outputs may not overlap x or one another.
+ * products want those of y and yt to be multiples of 16. Outputs may not overlap x or one another; rows of two of
+ * them may lie between one another where their strides are the same number of bytes.
  */
 tsp_status tsp_quantize_e4m3(int64_t rows, int64_t width, const void* x, int x_f32, int64_t ld_x, int block,
                              uint8_t* y, int64_t ld_y, float* scales, uint8_t* yt, int64_t ld_yt, float* scales_t,
@@ -788,9 +789,9 @@ tsp_status tsp_quantize_e4m3(int64_t rows, int64_t width, const void* x, int x_f
  *
  * Rows of a and b start on 16 bytes (base and ld_a, ld_b multiples of 16), those of c anywhere on its
  * element; what lies behind a row's end is neither read into the result nor written. m, n, k in
- * [0, 2^30]; k 0 gives zeros. c may not overlap an input. Sums are in a fixed order, which goes by
- * m, n, k, b_block and the device alone. ws: tsp_matmul_e4m3_workspace_bytes() bytes, 256-byte aligned, initialised once by
- * tsp_status_init; calls may share it.
+ * [0, 2^30]; k 0 gives zeros. c may not overlap an input (rows in between as for the quantiser). Sums are in a fixed
+ * order, which goes by m, n, k, b_block and the device alone. ws: tsp_matmul_e4m3_workspace_bytes() bytes, 256-byte
+ * aligned, initialised once by tsp_status_init; calls may share it.
  */
 size_t tsp_matmul_e4m3_workspace_bytes(void);
 tsp_status tsp_matmul_e4m3(int64_t m, int64_t n, int64_t k, const uint8_t* a, int64_t ld_a, const float* a_scales,
