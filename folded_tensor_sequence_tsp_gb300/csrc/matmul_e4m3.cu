@@ -379,9 +379,12 @@ __global__ void __launch_bounds__(THREADS, Config<BN, COLS, PAIR>::CTAS)
     uint32_t acc_phase = 0, slot_phase = 0;
     // Every warp goes through every tile, and every lane through every block, also after a wait gave up: the warps
     // meet at barriers below, and the loads are the whole warp's, while each lane waits, and can give up, by
-    // itself. It then waits and arrives no more; what it adds is of no use. (A vote of the warp in each
-    // block instead: 8192 x 8192 x 4096 with a scale per row of both 314 us, not 310.)
-    bool ok = true;
+    // itself. It then waits and arrives no more; what it adds is of no use. (8192 x 8192 x 4096 with a scale per row of
+    // both: 306 us, 311 with `ok` tested at each wait and arrival of a block, 314 with a vote of the warp there.)
+    bool ok = true, arrives = lane == 0;
+    auto waited = [&](bool done) {
+      if (!done) ok = arrives = false;
+    };
     for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
       int tp, tq;
       tile_coords(tile, num_p, num_q, p.group_p, tp, tq);
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(THREADS, Config<BN, COLS, PAIR>::CTAS)
       // Shared memory is busy with the operands, and an access to it takes some 150 cycles: the scales of
       // a block's rows are read, and its product is first asked for, while the block before it is added.
       const float* scales = s_scale + slot * cfg::SCALES;
-      bool ready = false;
+      bool ready;
       float f[QUAD ? 4 : 1];
       auto row_scales = [&]() {
         if constexpr (QUAD) {
@@ -406,7 +409,7 @@ __global__ void __launch_bounds__(THREADS, Config<BN, COLS, PAIR>::CTAS)
       auto taken = [&](int kb) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && ok) {
+        if (arrives) {
           if constexpr (PAIR) mbar_arrive_cluster(acc ? taken1 : taken0);
           else mbar_arrive(&acc_empty[acc]);
         }
@@ -414,23 +417,24 @@ __global__ void __launch_bounds__(THREADS, Config<BN, COLS, PAIR>::CTAS)
         if (acc == 0) acc_phase ^= 1u;
         const int done = kb + 1 - kb0;
         if (kb + 1 == kb1 || (done & (KS - 1)) == 0) {
-          if (lane == 0 && ok) mbar_arrive(&scale_empty[slot]);
+          if (arrives) mbar_arrive(&scale_empty[slot]);
           slot ^= 1;
           if (slot == 0) slot_phase ^= 1u;
           scales = s_scale + slot * cfg::SCALES;
-          if (ok && kb + 1 < kb1) ok = mbar_wait_short(&scale_full[slot], slot_phase, wb, SITE_E4M3_EPILOGUE);
+          if (ok && kb + 1 < kb1) waited(mbar_wait_short(&scale_full[slot], slot_phase, wb, SITE_E4M3_EPILOGUE));
         } else {
           scales += BM + QS;
         }
         if (kb + 1 < kb1) {
-          ready = mbar_try_wait(&acc_full[acc], acc_phase);
+          ready = mbar_try_wait(&acc_full[acc], acc_phase) || !ok;
           row_scales();
         }
       };
-      if (ok && kb0 < kb1) ok = mbar_wait_short(&scale_full[slot], slot_phase, wb, SITE_E4M3_EPILOGUE);
+      if (ok && kb0 < kb1) waited(mbar_wait_short(&scale_full[slot], slot_phase, wb, SITE_E4M3_EPILOGUE));
+      ready = !ok;
       row_scales();
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (ok && !ready) ok = mbar_wait_poll(&acc_full[acc], acc_phase, wb, SITE_E4M3_EPILOGUE);
+        if (!ready) waited(mbar_wait_poll(&acc_full[acc], acc_phase, wb, SITE_E4M3_EPILOGUE));
         __syncwarp();
         tc_fence_after();
         const uint32_t from = lanes + (uint32_t)(acc * BN);

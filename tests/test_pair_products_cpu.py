@@ -40,9 +40,12 @@ def test_lanes_of_the_sums_stay_together_when_a_wait_gives_up(text):
     sums = text[text.index("setmaxnreg.inc"):]
     loop = re.search(r"for \(int kb = kb0; ([^;]*); \+\+kb\) \{(.*?)tc_fence_after\(\);", sums, flags=re.S)
     assert loop.group(1) == "kb < kb1" and "break" not in loop.group(2)
-    assert re.search(r"if \(ok && !ready\) ok = mbar_wait_poll\(&acc_full.*?;\s*__syncwarp\(\);\s*$", loop.group(2), flags=re.S)
-    # `ok` guards waits and arrivals alone
-    uses = re.findall(r"if \(([^()]*\bok\b[^()]*)\)\s*(\{|\w+[^;]*;)", sums[:sums.index("if constexpr (TURNED)")])
-    assert {u[0] for u in uses} == {"ok && !ready", "lane == 0 && ok", "ok && kb + 1 < kb1", "ok && kb0 < kb1"}
-    # a lane that gave up arrives nowhere
-    assert not re.search(r"if \(lane == 0\)", sums[:sums.index("if constexpr (TURNED)")])
+    assert re.search(r"if \(!ready\) waited\(mbar_wait_poll\(&acc_full[^;]*;\s*__syncwarp\(\);\s*$", loop.group(2), flags=re.S)
+    # a lane that gave up waits for nothing and arrives nowhere, and nothing else goes by it
+    sums = sums[:sums.index("if constexpr (TURNED)")]
+    assert re.search(r"if \(!done\) ok = arrives = false;", sums)
+    assert len(re.findall(r"mbar_wait_\w+\(", sums)) == len(re.findall(r"waited\(mbar_wait_\w+\(", sums)) == 3
+    conditions = set(re.findall(r"if \(([^()]*\b(?:ok|ready|arrives)\b[^()]*)\)", sums))
+    assert conditions == {"!ready", "arrives", "ok && kb + 1 < kb1", "ok && kb0 < kb1"}
+    assert re.findall(r"\bready = ([^;]*);", sums) == ["mbar_try_wait(&acc_full[acc], acc_phase) || !ok", "!ok"]
+    assert not re.search(r"if \(lane == 0\)", sums)
