@@ -261,3 +261,21 @@ def test_an_input_in_8_bits_has_rows_of_the_layers_width(monkeypatch, shape):
     assert not launched
     y = layer.forward(torch.zeros(2, 3, 32, dtype=torch.float8_e4m3fn), weight, scales=torch.ones(6, 1))
     assert y.shape == (2, 3, 48) and launched[0][3:6] == (6, 48, 32)
+
+
+def test_adamw_check_refuses_what_the_step_does(lib):
+    """The same lists with and without a stream."""
+    kw = dict(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, weight_decay=0.1, max_norm=1.0, t=1, seed=0)
+    ptr = lambda *x: (B._P * len(x))(*x)  # noqa: E731
+    ints = lambda *x: (ctypes.c_int * len(x))(*x)  # noqa: E731
+
+    def check(g=P(1), n=1, bits=32, **change):
+        return lib.tsp_adamw_check(n, ptr(P(0)), ints(0), None, ptr(g), ints(0), ptr(P(2)), ptr(P(3)), None, None,
+                                   (ctypes.c_int64 * 1)(300), bits, ctypes.byref(B.AdamW(**{**kw, **change})))
+    assert check() == B.TSP_OK
+    expect(check(g=P(0) + 400), BAD, "overlaps")
+    expect(check(bits=16), NO, "32 or 8")
+    expect(check(beta1=1.0), BAD, "betas")
+    expect(check(t=0), BAD, "count from 1")
+    expect(check(g=P(1) + 2), BAD, "aligned")
+    assert lib.tsp_adamw_check(0, *[None] * 10, 32, None) == BAD
