@@ -7,10 +7,12 @@
 //
 // Bound: HBM. Every value is read once and written once, clipping included (the factor is formed
 // from the norm here, so the gradients are not scaled in a pass of their own). 202M bf16 weights with fp32
-// masters: 868 us with 32-bit states (7.0 TB/s), 632 with 8-bit ones (5.8 TB/s; 100 instructions an element,
-// 0.8 per cycle and scheduler, bind as much). As in grad_clip.cu
+// masters: 866 us with 32-bit states (7.0 TB/s), 632 to 637 with 8-bit ones (5.8 TB/s; 100 instructions an element,
+// 0.8 per cycle and scheduler, bind as much); fp32 weights 803 and 600. bf16 weights without masters are the one form
+// that 8 bits make slower, 640 and 684 (3.0 TB/s): each element takes a second hash. As in grad_clip.cu
 // the list travels in the kernels' parameters, cut into chunks of a CTA each (persistent CTAs that take
-// them in turn: 202M weights with masters 941 us, one CTA each 866).
+// them in turn: 202M weights with masters 941 us, one CTA each 866). A tensor without a gradient between two others
+// ends a launch.
 //
 // Roundings. All arithmetic is fp32 on the values that the states stand for. 8-bit states are
 // rounded stochastically, up with the probability of the distance from the lower neighbour: one

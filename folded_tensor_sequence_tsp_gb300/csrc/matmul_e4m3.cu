@@ -17,10 +17,12 @@
 // pair loads half of Q, so a block brings 32 KB to an SM instead of 48; at 64 bytes per cycle into an SM, and
 // at the rate of its shared memory, the 48 would take half as long again as the 512 cycles of the MMAs. The
 // sums leave through shared memory by TMA under the next tile.
-//   8192 x 8192 x 4096, scales for tiles, bf16 out: 205 us, 2680 TFLOP/s (tensor pipe 56 % active). Bound by
-//   the warps that add: a block takes them 860 cycles (tensor memory loads, barriers and scales among busy
-//   shared memory, 256 cycles of fp32 FMAs). The same loads and MMAs without the sums: 167 us.
-//   The same with a scale per row of both and fp32 out: 304 us; 512 cycles of FMA, and 268 MB to write.
+//   8192 x 8192 x 4096, scales for tiles, bf16 out: 205 to 215 us from box to box, 2560 to 2680 TFLOP/s (tensor
+//   pipe 55 % active). Bound by the warps that add: a block takes them 860 cycles (tensor memory loads, barriers
+//   and scales among busy shared memory, 256 cycles of fp32 FMAs). The same loads and MMAs without the sums: 167 us.
+//   The same with a scale per row of both and fp32 out: 305 us; 512 cycles of FMA, and 268 MB to write.
+//   Added to what C holds, the sums are written by the warps, in the open: 11008 x 4096 x 8192 (dw) 725 us, and 400
+//   without the addition, whose sums leave by TMA; 2816 x 1024 x 1000 47 and 15 us.
 // Few rows or few tiles: P = B, Q = A, so that 16 to 128 rows of A fill a tile; a tile per CTA or, with the
 // blocks of K split, per cluster of CTAs, which join their sums through distributed shared memory in a
 // fixed order.

@@ -4,10 +4,10 @@ does not bring.
 
 One object serves one stream at a time: its calls share its workspace, so calls that may
 overlap (two streams, two captured graphs that replay at the same time) need an object
-each. The workspace is never replaced, so a captured graph stays valid as long as its
-object lives. An object may serve another stream than the one it was made on: its workspace is
-ready when the constructor returns. Like any tensor, it is deleted once the streams it served
-are done with it.
+each. A workspace that a captured graph may use is kept as long as its object lives, also where
+TSPLinearE4M3.enable_backward() puts a larger one in its place. An object may serve another
+stream than the one it was made on: its workspace is ready when the constructor returns. Like
+any tensor, it is deleted once the streams it served are done with it.
 """
 from __future__ import annotations
 
